@@ -47,8 +47,9 @@ typedef enum {
 } wb_status;
 
 /* Element types of one precision site (showcase site, "The Approach": a
- * PrecisionConfig assigns weight and activation precision per layer site). */
-typedef enum { WB_BF16 = 0, WB_E4M3 = 1 } wb_dtype;
+ * PrecisionConfig assigns weight and activation precision per layer site).  WB_F16 and WB_F32 are
+ * types of the training LayerNorm below only; a precision site is WB_BF16 or WB_E4M3. */
+typedef enum { WB_BF16 = 0, WB_E4M3 = 1, WB_F16 = 2, WB_F32 = 3 } wb_dtype;
 
 /* The three encoder layer sites of the showcase site's precision table
  * ("The Approach"): encoder_attn_qkv, encoder_attn_out, encoder_ffn (FC1 and
@@ -374,6 +375,34 @@ wb_status wb_rmsnorm(const void* x, const void* residual, const float* g, int ro
  * (1 when amax = 0). */
 wb_status wb_quantize_e5m2(const void* x, int64_t n, uint8_t* q, float* scale, void* stream);
 wb_status wb_dequantize_e5m2(const uint8_t* q, const float* scale, int64_t n, void* y, void* stream);
+
+/* --- training: LayerNorm with its backward pass ---------------------------------
+ * The source pages have no counterpart: they run the model forward only.  These are for adapting
+ * what stands behind the encoder (and the encoder's own norms).
+ *
+ * wb_layernorm_forward: t = x + residual rounded to the tensors' type (t = x without a residual),
+ * y = (t - mean) * rstd * g + b, rstd = 1 / sqrt(var + eps), biased variance, per row of width d.
+ * Unlike wb_layernorm it takes any width 1 <= d <= 10240, writes stats[row] = (mean, rstd)
+ * (float32 [rows][2]) for the backward pass, and normalises the rounded sum, so that the backward
+ * pass can read it back from `total`.  dtype is WB_BF16, WB_F16 or WB_F32 and holds for x,
+ * residual, y and total, all [rows, d]; g, b: float32 [d].  residual and total are both given or
+ * both NULL.
+ *
+ * wb_layernorm_backward: with h = (x - mean) rstd and u = g dy (x being the forward pass's `total`,
+ * or its x without a residual):
+ *   dx = rstd (u - mean(u) - h mean(u h)) + dtotal,  dg = sum over rows of dy h,  db = sum of dy.
+ * dtotal (or NULL) is the gradient that reaches t past the norm, along the residual branch.  dx is
+ * the gradient of x and of residual alike.  dg and db (float32 [d], overwritten) are both given or
+ * both NULL; NULL leaves them out and needs no workspace.  The sums run in a fixed order: the same
+ * call gives the same bits.  dx may be the buffer of dy, x or dtotal.
+ * Statistics and sums are float32.  rows = 0 writes zeros to dg and db.
+ * WB_EUNSUPPORTED for another dtype, WB_EINVAL for bad sizes, pointers or alignment. */
+wb_status wb_layernorm_forward(const void* x, const void* residual, const float* g, const float* b, int rows, int d,
+                               float eps, int dtype, void* y, void* total, float* stats, void* stream);
+size_t wb_layernorm_backward_workspace_bytes(int rows, int d);
+wb_status wb_layernorm_backward(const void* dy, const void* x, const float* g, const float* stats, const void* dtotal,
+                                int rows, int d, int dtype, void* dx, float* dg, float* db, void* workspace,
+                                size_t workspace_bytes, void* stream);
 
 /* --- kernel timing (benchmarks) -------------------------------------------------
  * Between wb_profile_begin() and wb_profile_end() every kernel that libwb

@@ -14,7 +14,7 @@ from . import build as _build
 LIB_PATH = _build.LIB
 
 WB_OK, WB_EINVAL, WB_ECUDA, WB_EUNSUPPORTED, WB_ETIMEOUT, WB_EWORKSPACE, WB_EBOUNDS = 0, -1, -2, -3, -4, -5, -6
-WB_BF16, WB_E4M3 = 0, 1
+WB_BF16, WB_E4M3, WB_F16, WB_F32 = 0, 1, 2, 3
 WB_LOGMEL_STATIC_MAX_CHUNKS = 2   # include/wb.h
 WB_SELFTEST_WAIT_SITE = 0x7F      # include/wb.h
 WB_SELFTEST_BOUNDS_SITE = 0x7E    # include/wb.h
@@ -91,6 +91,11 @@ SIGNATURES = {
     "wb_rmsnorm": (c_int, [c_void, c_void, c_void, c_int, c_int, c_float, c_void, c_void, c_void]),
     "wb_quantize_e5m2": (c_int, [c_void, c_i64, c_void, c_void, c_void]),
     "wb_dequantize_e5m2": (c_int, [c_void, c_void, c_i64, c_void, c_void]),
+    "wb_layernorm_forward": (c_int, [c_void, c_void, c_void, c_void, c_int, c_int, c_float, c_int, c_void, c_void,
+                                     c_void, c_void]),
+    "wb_layernorm_backward_workspace_bytes": (c_size, [c_int, c_int]),
+    "wb_layernorm_backward": (c_int, [c_void, c_void, c_void, c_void, c_void, c_int, c_int, c_int, c_void, c_void,
+                                      c_void, c_void, c_size, c_void]),
     "wb_profile_begin": (c_int, []),
     "wb_profile_end": (c_int, [c_int, P(ctypes.c_char_p), P(ctypes.c_double), P(ctypes.c_int64)]),
 }

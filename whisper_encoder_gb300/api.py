@@ -6,13 +6,14 @@ current torch CUDA stream.  All arithmetic happens in libwb's kernels.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 
 import torch
 
 from . import _lib
-from ._lib import WB_BF16, WB_E4M3, WB_ETIMEOUT, WB_OK, WbError, call, load
+from ._lib import WB_BF16, WB_E4M3, WB_ETIMEOUT, WB_F16, WB_F32, WB_OK, WbError, call, load
 
 CHUNK_SAMPLES = 480000
 N_FRAMES = 3000
@@ -262,6 +263,86 @@ def cross_kv(enc_out: torch.Tensor, dims, layers: list, stream=None) -> torch.Te
     ds = dims_struct(dims)
     call("wb_cross_kv", _p(enc_out), batch, ctypes.byref(ds), len(layers), arr, _p(kv), _stream(stream))
     return kv
+
+
+# --------------------------------- training -----------------------------------
+_LN_TYPES = {torch.bfloat16: WB_BF16, torch.float16: WB_F16, torch.float32: WB_F32}
+
+
+def _place(stream, first, *rest):
+    """Where a training call runs: the device of its tensors (which must agree) and ``stream``.
+
+    Outputs and workspaces are allocated inside, so that on a side stream the allocator hands their
+    memory out again in that stream's order; inputs of other streams are marked as in use on it."""
+    dev = first.device
+    for t in rest:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}: one device expected")
+    if stream is None:
+        return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    if stream.device != dev:
+        raise ValueError(f"stream on {stream.device}, tensors on {dev}")
+    if stream != torch.cuda.current_stream(dev):
+        for t in (first, *rest):
+            if t is not None:
+                t.record_stream(stream)
+    return torch.cuda.stream(stream)
+
+
+def _need_shape(t, dtype, shape, name):
+    _need(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _ln_rows(x, name):
+    if not isinstance(x, torch.Tensor) or x.dtype not in _LN_TYPES or x.dim() == 0:
+        raise ValueError(f"{name}: expected a bf16, f16 or f32 tensor [..., d]")
+    _need(x, x.dtype, name)
+    d = x.shape[-1]
+    return (x.numel() // d if d else 0), d, _LN_TYPES[x.dtype]
+
+
+def layernorm_forward(x, g, b, eps: float = 1e-5, residual=None, stream=None):
+    """LayerNorm that keeps what its backward pass needs: (y, total, stats).
+
+    x [..., d] of bf16, f16 or f32, 1 <= d <= 10240; total = x + residual rounded to x's type (x itself
+    without a residual); stats f32 [rows, 2] = (mean, rstd) of total's rows."""
+    rows, d, ty = _ln_rows(x, "x")
+    _need_shape(g, torch.float32, (d,), "g")
+    _need_shape(b, torch.float32, (d,), "b")
+    if residual is not None:
+        _need_shape(residual, x.dtype, x.shape, "residual")
+    with _place(stream, x, g, b, residual):
+        y = torch.empty_like(x)
+        total = torch.empty_like(x) if residual is not None else None
+        stats = torch.empty((rows, 2), dtype=torch.float32, device=x.device)
+        call("wb_layernorm_forward", _p(x), _p(residual), _p(g), _p(b), rows, d, eps, ty, _p(y), _p(total), _p(stats),
+             _stream())
+    return y, (x if total is None else total), stats
+
+
+def layernorm_backward(dy, x, g, stats, dtotal=None, need_params: bool = True, stream=None):
+    """Gradients of layernorm_forward: (dx, dg, db) from dy, the forward pass's ``total`` and ``stats``.
+
+    dx is the gradient of x and of residual alike; dtotal, if given, is the gradient that reaches total
+    past the norm and is added to it.  dg, db: f32 [d] (None without need_params)."""
+    rows, d, ty = _ln_rows(x, "x")
+    _need_shape(dy, x.dtype, x.shape, "dy")
+    _need_shape(g, torch.float32, (d,), "g")
+    _need_shape(stats, torch.float32, (rows, 2), "stats")
+    if dtotal is not None:
+        _need_shape(dtotal, x.dtype, x.shape, "dtotal")
+    with _place(stream, x, dy, g, stats, dtotal):
+        dx = torch.empty_like(x)
+        dg = db = ws = None
+        if need_params:
+            dg = torch.empty_like(g)
+            db = torch.empty_like(g)
+            ws = _workspace(load().wb_layernorm_backward_workspace_bytes(rows, d), x.device)
+        call("wb_layernorm_backward", _p(dy), _p(x), _p(g), _p(stats), _p(dtotal), rows, d, ty, _p(dx), _p(dg), _p(db),
+             _p(ws), ws.numel() if need_params else 0, _stream())
+    return dx, dg, db
 
 
 def profile_begin() -> None:

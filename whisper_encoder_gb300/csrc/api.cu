@@ -101,13 +101,10 @@ bool o_map(CUtensorMap* m, const void* base, uint64_t n, uint64_t rows, uint64_t
 // ------------------------------ kernel timing -------------------------------
 // While enabled, every libwb launch is bracketed by two CUDA events recorded
 // on its own stream; wb_profile_end() sums the elapsed times per kernel class.
-enum ProfClass {
-  PC_LOGMEL_PREP, PC_LOGMEL_DFT, PC_LOGMEL_MEL, PC_LOGMEL_POST, PC_STEM_PREP, PC_STEM_CONV1, PC_STEM_CONV2,
-  PC_ENC_LN, PC_ENC_QUANT, PC_ENC_QKV, PC_ENC_ATTN, PC_ENC_OUT, PC_ENC_FC1, PC_ENC_FC2, PC_OTHER, PC_COUNT
-};
 const char* const kProfNames[PC_COUNT] = {
     "logmel.prep", "logmel.dft", "logmel.mel", "logmel.post", "stem.prep", "stem.conv1", "stem.conv2",
-    "enc.layernorm", "enc.quantize", "enc.qkv", "enc.attention", "enc.out_proj", "enc.fc1", "enc.fc2", "other"};
+    "enc.layernorm", "enc.quantize", "enc.qkv", "enc.attention", "enc.out_proj", "enc.fc1", "enc.fc2", "other",
+    "train.layernorm"};
 
 struct ProfRec {
   int cls, kernels;
@@ -128,43 +125,7 @@ cudaEvent_t prof_event() {
   return e;
 }
 
-struct Prof {
-  int cls, kernels;
-  cudaStream_t s;
-  cudaEvent_t a = nullptr;
-  Prof(int c, cudaStream_t st, int k = 1) : cls(c), kernels(k), s(st) {
-    if (!g_prof_on) return;
-    std::lock_guard<std::mutex> lk(g_mu);
-    a = prof_event();
-    if (a) cudaEventRecord(a, s);
-  }
-  ~Prof() {
-    if (!a) return;
-    std::lock_guard<std::mutex> lk(g_mu);
-    cudaEvent_t b = prof_event();
-    if (!b) return;
-    cudaEventRecord(b, s);
-    g_prof_recs.push_back(ProfRec{cls, kernels, a, b});
-  }
-};
-
 // ------------------------------ helpers ------------------------------------
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Carver {
-  size_t off = 0;
-  size_t take(size_t bytes) {
-    const size_t o = off;
-    off += (bytes + 255) & ~static_cast<size_t>(255);
-    return o;
-  }
-};
-
-#define WB_CUDA(x)                         \
-  do {                                     \
-    if ((x) != cudaSuccess) return WB_ECUDA; \
-  } while (0)
-
 GemmParams base_params() {
   GemmParams p;
   std::memset(&p, 0, sizeof(p));
@@ -322,6 +283,33 @@ wb_status run_attention(const __nv_bfloat16* q, const __nv_bfloat16* k, long lon
 }
 
 }  // namespace
+
+namespace wb {
+
+uint32_t* tc_err_ptr() { return err_ptr(); }
+
+bool tma_map_bf16(CUtensorMap* m, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+                  const uint32_t* box, CUtensorMapSwizzle swz) {
+  return make_map(m, false, rank, base, dims, strides, box, swz);
+}
+
+Prof::Prof(int c, cudaStream_t st, int k) : cls(c), kernels(k), s(st) {
+  if (!g_prof_on) return;
+  std::lock_guard<std::mutex> lk(g_mu);
+  a = prof_event();
+  if (a) cudaEventRecord(a, s);
+}
+
+Prof::~Prof() {
+  if (!a) return;
+  std::lock_guard<std::mutex> lk(g_mu);
+  cudaEvent_t b = prof_event();
+  if (!b) return;
+  cudaEventRecord(b, s);
+  g_prof_recs.push_back(ProfRec{cls, kernels, a, b});
+}
+
+}  // namespace wb
 
 // ============================================================================
 extern "C" {
