@@ -404,6 +404,54 @@ wb_status wb_layernorm_backward(const void* dy, const void* x, const float* g, c
                                 int rows, int d, int dtype, void* dx, float* dg, float* db, void* workspace,
                                 size_t workspace_bytes, void* stream);
 
+/* --- training: losses of a vocabulary head --------------------------------------
+ * The source pages have no counterpart (they decode with trained weights only).  A head is a
+ * projection matrix w (bf16 [V, d], the layout of wb_linear's w) applied to hidden states x (bf16
+ * [M, d]); its logits s = x w^T, M x V of them, are never stored.  d: a multiple of 8 up to 65536;
+ * V any size from 1 to 2^24; M from 0 to 2^24.
+ *
+ * wb_linear_cross_entropy: with e = label_smoothing (0 <= e < 1), per row i
+ *   lse[i] = log sum_v exp s[i, v],  loss[i] = lse[i] - (1 - e) s[i, label] - e mean_v s[i, v].
+ * A row with a negative label takes no part: loss 0, lse 0, no gradient, and its x may hold anything.
+ * A label >= V is a mistake: the row's loss is NaN and it takes no further part.  labels: int64 [M];
+ * loss, lse: float32 [M].
+ * wb_linear_cross_entropy_backward: from dloss[i] (float32 [M]; read only for rows that take part)
+ * and the forward pass's lse, the gradients dx (bf16 [M, d], zeros for rows that take no part) and dw
+ * (bf16 [V, d]), both overwritten; either may be NULL.  The logits are computed again, a piece of the
+ * vocabulary at a time.
+ *
+ * wb_linear_distill: each row has k (1 to 1024) of a teacher's logits, top (float32, bf16 or f16
+ * [M, k]) at the vocabulary entries index (int64 [M, k]).  At temperature T, with p the softmax of
+ * top / T over the row's entries and q the softmax of s / T over the whole vocabulary,
+ *   loss[i] = T^2 sum_j p_j (log p_j - log q_j),  lse[i] = log sum_v exp(s[i, v] / T).
+ * An entry with a negative index or a logit of -infinity is not there; an index that comes twice
+ * counts with both entries' p.  A row without entries takes no part, as above; a row with an index
+ * >= V is a mistake, as above.
+ * wb_linear_distill_backward: as wb_linear_cross_entropy_backward.
+ *
+ * Sums, softmax statistics and losses are float32.  softmax - target is rounded to bf16 once, as a
+ * factor of the two gradient products, and so is x dloss / max|dloss| for dw.  All sums run in a
+ * fixed order: the same call gives the same bits.  Two calls that may overlap on the GPU need a
+ * workspace each.  x, w: 16-byte aligned.  WB_EINVAL for bad sizes, pointers or alignment,
+ * WB_EUNSUPPORTED for another top_dtype, WB_EWORKSPACE for a missing or small workspace. */
+size_t wb_linear_cross_entropy_workspace_bytes(int M, int d, int V);
+wb_status wb_linear_cross_entropy(const void* x, const void* w, const int64_t* labels, int M, int d, int V,
+                                  float label_smoothing, float* loss, float* lse, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+size_t wb_linear_cross_entropy_backward_workspace_bytes(int M, int d, int V);
+wb_status wb_linear_cross_entropy_backward(const float* dloss, const void* x, const void* w, const int64_t* labels,
+                                           const float* lse, int M, int d, int V, float label_smoothing, void* dx,
+                                           void* dw, void* workspace, size_t workspace_bytes, void* stream);
+size_t wb_linear_distill_workspace_bytes(int M, int d, int V, int k);
+wb_status wb_linear_distill(const void* x, const void* w, const void* top, int top_dtype, const int64_t* index, int M,
+                            int d, int V, int k, float temperature, float* loss, float* lse, void* workspace,
+                            size_t workspace_bytes, void* stream);
+size_t wb_linear_distill_backward_workspace_bytes(int M, int d, int V, int k);
+wb_status wb_linear_distill_backward(const float* dloss, const void* x, const void* w, const void* top, int top_dtype,
+                                     const int64_t* index, const float* lse, int M, int d, int V, int k,
+                                     float temperature, void* dx, void* dw, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
 /* --- kernel timing (benchmarks) -------------------------------------------------
  * Between wb_profile_begin() and wb_profile_end() every kernel that libwb
  * launches is bracketed by two CUDA events recorded on its launch stream.

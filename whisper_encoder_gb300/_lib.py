@@ -96,6 +96,18 @@ SIGNATURES = {
     "wb_layernorm_backward_workspace_bytes": (c_size, [c_int, c_int]),
     "wb_layernorm_backward": (c_int, [c_void, c_void, c_void, c_void, c_void, c_int, c_int, c_int, c_void, c_void,
                                       c_void, c_void, c_size, c_void]),
+    "wb_linear_cross_entropy_workspace_bytes": (c_size, [c_int, c_int, c_int]),
+    "wb_linear_cross_entropy": (c_int, [c_void, c_void, c_void, c_int, c_int, c_int, c_float, c_void, c_void, c_void,
+                                        c_size, c_void]),
+    "wb_linear_cross_entropy_backward_workspace_bytes": (c_size, [c_int, c_int, c_int]),
+    "wb_linear_cross_entropy_backward": (c_int, [c_void, c_void, c_void, c_void, c_void, c_int, c_int, c_int, c_float,
+                                                 c_void, c_void, c_void, c_size, c_void]),
+    "wb_linear_distill_workspace_bytes": (c_size, [c_int, c_int, c_int, c_int]),
+    "wb_linear_distill": (c_int, [c_void, c_void, c_void, c_int, c_void, c_int, c_int, c_int, c_int, c_float, c_void,
+                                  c_void, c_void, c_size, c_void]),
+    "wb_linear_distill_backward_workspace_bytes": (c_size, [c_int, c_int, c_int, c_int]),
+    "wb_linear_distill_backward": (c_int, [c_void, c_void, c_void, c_void, c_int, c_void, c_void, c_int, c_int, c_int,
+                                           c_int, c_float, c_void, c_void, c_void, c_size, c_void]),
     "wb_profile_begin": (c_int, []),
     "wb_profile_end": (c_int, [c_int, P(ctypes.c_char_p), P(ctypes.c_double), P(ctypes.c_int64)]),
 }

@@ -345,6 +345,94 @@ def layernorm_backward(dy, x, g, stats, dtotal=None, need_params: bool = True, s
     return dx, dg, db
 
 
+def _head_shape(x, w):
+    _need(x, torch.bfloat16, "x")
+    _need(w, torch.bfloat16, "w")
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
+        raise ValueError(f"x and w: expected [M, d] and [V, d], got {tuple(x.shape)} and {tuple(w.shape)}")
+    return x.shape[0], x.shape[1], w.shape[0]
+
+
+def _head_workspace(workspace, query, device, *shape):
+    if workspace is None:
+        return _workspace(getattr(load(), query)(*shape), device)
+    _need(workspace, torch.uint8, "workspace")
+    return workspace
+
+
+def _teacher(top, index, M):
+    if not isinstance(top, torch.Tensor) or top.dtype not in _LN_TYPES or top.dim() != 2:
+        raise ValueError("top: expected a f32, bf16 or f16 tensor [M, k]")
+    _need_shape(top, top.dtype, (M, top.shape[1]), "top")
+    _need_shape(index, torch.int64, top.shape, "index")
+    return top.shape[1], _LN_TYPES[top.dtype]
+
+
+def linear_cross_entropy(x, w, labels, label_smoothing: float = 0.0, workspace=None, stream=None):
+    """Softmax cross entropy of the logits x w^T against labels, without storing the logits: (loss, lse).
+
+    x bf16 [M, d], w bf16 [V, d], labels int64 [M]; loss and lse f32 [M].  Rows with a negative label
+    take no part (loss 0); a label >= V gives a loss of NaN."""
+    M, d, V = _head_shape(x, w)
+    _need_shape(labels, torch.int64, (M,), "labels")
+    with _place(stream, x, w, labels, workspace):
+        loss, lse = torch.empty((2, M), dtype=torch.float32, device=x.device)
+        ws = _head_workspace(workspace, "wb_linear_cross_entropy_workspace_bytes", x.device, M, d, V)
+        call("wb_linear_cross_entropy", _p(x), _p(w), _p(labels), M, d, V, label_smoothing, _p(loss), _p(lse), _p(ws),
+             ws.numel(), _stream())
+    return loss, lse
+
+
+def linear_cross_entropy_backward(dloss, x, w, labels, lse, label_smoothing: float = 0.0, need_dx: bool = True,
+                                  need_dw: bool = True, workspace=None, stream=None):
+    """Gradients (dx bf16 [M, d], dw bf16 [V, d]) of linear_cross_entropy from dloss f32 [M] and its lse;
+    None for one that is not needed."""
+    M, d, V = _head_shape(x, w)
+    _need_shape(labels, torch.int64, (M,), "labels")
+    _need_shape(dloss, torch.float32, (M,), "dloss")
+    _need_shape(lse, torch.float32, (M,), "lse")
+    with _place(stream, x, w, labels, dloss, lse, workspace):
+        dx = torch.empty_like(x) if need_dx else None
+        dw = torch.empty_like(w) if need_dw else None
+        ws = _head_workspace(workspace, "wb_linear_cross_entropy_backward_workspace_bytes", x.device, M, d, V)
+        call("wb_linear_cross_entropy_backward", _p(dloss), _p(x), _p(w), _p(labels), _p(lse), M, d, V,
+             label_smoothing, _p(dx), _p(dw), _p(ws), ws.numel(), _stream())
+    return dx, dw
+
+
+def linear_distill(x, w, top, index, temperature: float = 1.0, workspace=None, stream=None):
+    """T^2 KL(teacher || student) of the logits x w^T, the teacher given by its top logits: (loss, lse).
+
+    x bf16 [M, d], w bf16 [V, d]; top f32, bf16 or f16 [M, k] are teacher logits of the vocabulary
+    entries index int64 [M, k] (negative: not there).  loss and lse f32 [M]; rows without entries take
+    no part (loss 0)."""
+    M, d, V = _head_shape(x, w)
+    k, ty = _teacher(top, index, M)
+    with _place(stream, x, w, top, index, workspace):
+        loss, lse = torch.empty((2, M), dtype=torch.float32, device=x.device)
+        ws = _head_workspace(workspace, "wb_linear_distill_workspace_bytes", x.device, M, d, V, k)
+        call("wb_linear_distill", _p(x), _p(w), _p(top), ty, _p(index), M, d, V, k, temperature, _p(loss), _p(lse),
+             _p(ws), ws.numel(), _stream())
+    return loss, lse
+
+
+def linear_distill_backward(dloss, x, w, top, index, lse, temperature: float = 1.0, need_dx: bool = True,
+                            need_dw: bool = True, workspace=None, stream=None):
+    """Gradients (dx bf16 [M, d], dw bf16 [V, d]) of linear_distill from dloss f32 [M] and its lse; None
+    for one that is not needed."""
+    M, d, V = _head_shape(x, w)
+    k, ty = _teacher(top, index, M)
+    _need_shape(dloss, torch.float32, (M,), "dloss")
+    _need_shape(lse, torch.float32, (M,), "lse")
+    with _place(stream, x, w, top, index, dloss, lse, workspace):
+        dx = torch.empty_like(x) if need_dx else None
+        dw = torch.empty_like(w) if need_dw else None
+        ws = _head_workspace(workspace, "wb_linear_distill_backward_workspace_bytes", x.device, M, d, V, k)
+        call("wb_linear_distill_backward", _p(dloss), _p(x), _p(w), _p(top), ty, _p(index), _p(lse), M, d, V, k,
+             temperature, _p(dx), _p(dw), _p(ws), ws.numel(), _stream())
+    return dx, dw
+
+
 def profile_begin() -> None:
     """Start timing every libwb kernel launch (CUDA events on the launch stream)."""
     call("wb_profile_begin")

@@ -49,8 +49,8 @@ bool encoder_fn() {
 }
 
 // rank-dimensional tiled map; strides in bytes for dims 1..rank-1; 128-byte swizzle.
-bool make_map(CUtensorMap* m, bool u8, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
-              const uint32_t* box, CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B, bool f16 = false) {
+bool make_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base, const uint64_t* dims,
+              const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B) {
   if (!encoder_fn()) return false;
   cuuint64_t gd[5];
   cuuint64_t gs[4];
@@ -61,12 +61,17 @@ bool make_map(CUtensorMap* m, bool u8, int rank, const void* base, const uint64_
     es[i] = 1;
   }
   for (int i = 0; i < rank - 1; ++i) gs[i] = strides[i];
-  CUresult r = g_encode(m, u8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                        static_cast<cuuint32_t>(rank), const_cast<void*>(base), gd, gs, bx, es,
+  CUresult r = g_encode(m, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), gd, gs, bx, es,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+bool make_map(CUtensorMap* m, bool u8, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+              const uint32_t* box, CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B, bool f16 = false) {
+  return make_map(m, u8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                              : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                  rank, base, dims, strides, box, swz);
 }
 
 // A operand view: (k, row, part, batch) with box (BK, 128, 1, 1).
@@ -104,7 +109,8 @@ bool o_map(CUtensorMap* m, const void* base, uint64_t n, uint64_t rows, uint64_t
 const char* const kProfNames[PC_COUNT] = {
     "logmel.prep", "logmel.dft", "logmel.mel", "logmel.post", "stem.prep", "stem.conv1", "stem.conv2",
     "enc.layernorm", "enc.quantize", "enc.qkv", "enc.attention", "enc.out_proj", "enc.fc1", "enc.fc2", "other",
-    "train.layernorm"};
+    "train.layernorm", "train.head_rows", "train.head_lse", "train.head_finish", "train.head_dlogits", "train.head_dx",
+    "train.head_dw"};
 
 struct ProfRec {
   int cls, kernels;
@@ -288,9 +294,14 @@ namespace wb {
 
 uint32_t* tc_err_ptr() { return err_ptr(); }
 
+bool tma_map_f32(CUtensorMap* m, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+                 const uint32_t* box, CUtensorMapSwizzle swz) {
+  return make_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, rank, base, dims, strides, box, swz);
+}
+
 bool tma_map_bf16(CUtensorMap* m, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
                   const uint32_t* box, CUtensorMapSwizzle swz) {
-  return make_map(m, false, rank, base, dims, strides, box, swz);
+  return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, base, dims, strides, box, swz);
 }
 
 Prof::Prof(int c, cudaStream_t st, int k) : cls(c), kernels(k), s(st) {

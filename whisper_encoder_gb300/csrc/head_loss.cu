@@ -1,0 +1,842 @@
+// Losses of a vocabulary head straight from hidden states and the projection matrix: softmax cross
+// entropy and distillation from a teacher's top logits, forward and backward, without keeping the
+// logits.
+//
+// Both are one operator with sparse targets.  Row i has target entries (v_j, P_j) (cross entropy: its
+// label with weight 1 - e, and e / V everywhere), s = x w^T / T, lse_i = log sum_v exp s_iv:
+//   loss_i = T^2 sum_j P_j (log P_j - s_ij + lse_i)      D_iv = exp(s_iv - lse_i) - P_iv
+//   dx_i = T dloss_i sum_v D_iv w_v                      dw_v = T sum_i dloss_i D_iv x_i
+// Rows without a target take no part: they are taken out first (rows_kernel), so they cost no product,
+// and whatever their x holds reaches nothing.  head_gemm.cuh has the products.
+//
+// Precision: s, lse, losses and every sum are float32.  D is rounded to bf16 once, as a factor of the
+// two gradient products; |D| <= 1, and dloss stays outside of it (applied to the float32 sums of dx,
+// and to x' = dloss / max|dloss| x for dw, exactly 1 where all dloss are equal), so that one rounding of
+// dloss is not shared by all of a row's or all of dw's entries.
+#include <mutex>
+
+#include "../../include/wb.h"
+#include "internal.h"
+#include "head_gemm.cuh"
+
+namespace wb {
+namespace {
+
+constexpr int HEAD_MAX_K = 1024;
+constexpr int ROWS_THREADS = 256;
+constexpr int FIN_ROWS = 32, FIN_SLICES = 16;
+
+// ---------------------------------------------------------------------------
+// Teacher entries of one row per block: softmax of the stored logits at the temperature, equal indices
+// merged, sorted by index.  cnt: entries, 0 for a row without any, -2 for a row with an index >= V.
+// ---------------------------------------------------------------------------
+template <typename T>
+__device__ __forceinline__ float teacher_f32(T v);
+template <>
+__device__ __forceinline__ float teacher_f32(float v) { return v; }
+template <>
+__device__ __forceinline__ float teacher_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ float teacher_f32(__half v) { return __half2float(v); }
+
+constexpr int LIST_THREADS = 128;
+
+__device__ __forceinline__ float block_reduce(float v, bool is_max, float* sm) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float w = __shfl_xor_sync(0xffffffffu, v, o);
+    v = is_max ? fmaxf(v, w) : v + w;
+  }
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = sm[0];
+  for (int i = 1; i < LIST_THREADS / 32; ++i) v = is_max ? fmaxf(v, sm[i]) : v + sm[i];
+  return v;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(LIST_THREADS)
+    target_lists_kernel(const T* __restrict__ top, const int64_t* __restrict__ index, int M, int k, int V,
+                        float inv_t, int* __restrict__ out_idx, float* __restrict__ out_p, int* __restrict__ out_cnt,
+                        uint32_t* err) {
+  extern __shared__ int sm_list[];
+  int* id = sm_list;                                       // [k]
+  float* pr = reinterpret_cast<float*>(sm_list + k);       // [k]
+  float* merged = pr + k;                                  // [k]
+  __shared__ float sm[LIST_THREADS / 32];
+  __shared__ int n_bad, n_out;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const long long n_el = static_cast<long long>(M) * k;
+  const int row = blockIdx.x;
+  const long long base = static_cast<long long>(row) * k;
+  if (threadIdx.x == 0) n_bad = n_out = 0;
+  __syncthreads();
+  float mx = -INFINITY;
+  for (int j = threadIdx.x; j < k; j += LIST_THREADS) {
+    if (!in_bounds(err, base + j, 1, n_el, SITE_HEAD_LIST)) { id[j] = -1; continue; }
+    const long long v = index[base + j];
+    const float t = teacher_f32<T>(top[base + j]) * inv_t;
+    if (v >= V) atomicAdd(&n_bad, 1);
+    const bool on = v >= 0 && v < V && !(t == -INFINITY);
+    id[j] = on ? static_cast<int>(v) : -1;
+    pr[j] = on ? t : -INFINITY;
+    if (on) mx = fmaxf(mx, t);
+  }
+  mx = block_reduce(mx, true, sm);
+  float sum = 0.0f;
+  for (int j = threadIdx.x; j < k; j += LIST_THREADS) {
+    if (id[j] < 0) continue;
+    pr[j] = expf(pr[j] - mx);
+    sum += pr[j];
+  }
+  sum = block_reduce(sum, false, sm);
+  // entry j stands for its index if no earlier entry has it; it then has the sum of all of them
+  for (int j = threadIdx.x; j < k; j += LIST_THREADS) {
+    float p = -1.0f;
+    if (id[j] >= 0) {
+      bool first = true;
+      p = 0.0f;
+      for (int q = 0; q < k; ++q) {
+        if (id[q] != id[j]) continue;
+        if (q < j) first = false;
+        p += pr[q];
+      }
+      p = first && !(p == 0.0f) ? p / sum : -1.0f;
+    }
+    merged[j] = p;
+  }
+  __syncthreads();
+  for (int j = threadIdx.x; j < k; j += LIST_THREADS) {
+    if (merged[j] == -1.0f) continue;
+    int rank = 0;
+    for (int q = 0; q < k; ++q) rank += merged[q] != -1.0f && id[q] < id[j];
+    if (in_bounds(err, base + rank, 1, n_el, SITE_HEAD_LIST)) {
+      out_idx[base + rank] = id[j];
+      out_p[base + rank] = merged[j];
+    }
+    atomicAdd(&n_out, 1);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && in_bounds(err, row, 1, M, SITE_HEAD_LIST)) out_cnt[row] = n_bad ? -2 : n_out;
+}
+
+// ---------------------------------------------------------------------------
+// Rows that take part, in order: row_src, their x (and x'), what the others get.
+// ---------------------------------------------------------------------------
+struct RowsArgs {
+  const int64_t* labels;     // cross entropy: 0 <= label < V takes part
+  const int* cnt;            // distillation: cnt > 0 takes part
+  int M, V, d, rows_per_block;
+  const __nv_bfloat16* x;
+  __nv_bfloat16* xc;         // compacted
+  int* row_src;
+  int* n_rows;
+  int* label32;              // by source row (cross entropy)
+  // forward: what the rows without a target get
+  float* loss;
+  float* lse;
+  // backward
+  const float* dloss;
+  const float* g_max;
+  __nv_bfloat16* xs;         // compacted x' (null: not wanted)
+  __nv_bfloat16* dx;         // rows without a target: zeros (null: not wanted)
+  uint32_t* err;
+};
+
+__device__ __forceinline__ int row_state(const RowsArgs& a, int i) {   // 1 takes part, 0 not, -1 a mistake
+  if (a.labels) {
+    const long long v = a.labels[i];
+    return v < 0 ? 0 : v < a.V ? 1 : -1;
+  }
+  const int c = a.cnt[i];
+  return c > 0 ? 1 : c == 0 ? 0 : -1;
+}
+
+__global__ void __launch_bounds__(ROWS_THREADS) rows_kernel(const __grid_constant__ RowsArgs a) {
+  __shared__ int warp_sum[ROWS_THREADS / 32];
+  __shared__ int at[ROWS_THREADS];           // compact index of the block's rows, or -1 / -2
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int r0 = blockIdx.x * a.rows_per_block;
+  const int r1 = min(r0 + a.rows_per_block, a.M);
+  // rows that take part before this block's
+  int before = 0;
+  for (int i = threadIdx.x; i < r0; i += ROWS_THREADS) before += row_state(a, i) == 1;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+  if (lane == 0) warp_sum[warp] = before;
+  __syncthreads();
+  before = 0;
+#pragma unroll
+  for (int w = 0; w < ROWS_THREADS / 32; ++w) before += warp_sum[w];
+  __syncthreads();
+  // the block's own rows, one a thread
+  const int row = r0 + threadIdx.x;
+  const int st = row < r1 ? row_state(a, row) : 0;
+  const unsigned ball = __ballot_sync(0xffffffffu, st == 1);
+  if (lane == 0) warp_sum[warp] = __popc(ball);
+  __syncthreads();
+  int off = before, all = before;
+#pragma unroll
+  for (int w = 0; w < ROWS_THREADS / 32; ++w) {
+    if (w < warp) off += warp_sum[w];
+    all += warp_sum[w];
+  }
+  off += __popc(ball & ((1u << lane) - 1u));
+  if (row < r1) {
+    at[threadIdx.x] = st == 1 ? off : -1;
+    if (st == 1 && in_bounds(a.err, off, 1, a.M, SITE_HEAD_ROWS)) a.row_src[off] = row;
+    if (a.labels && a.label32) a.label32[row] = st == 1 ? static_cast<int>(a.labels[row]) : -1;
+    if (st != 1 && a.loss) {
+      a.loss[row] = st == 0 ? 0.0f : __int_as_float(0x7fc00000);
+      a.lse[row] = 0.0f;
+    }
+  }
+  if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) *a.n_rows = all;
+  __syncthreads();
+  const float g = a.xs ? *a.g_max : 0.0f;
+  const int nv = a.d / 8;
+  const long long n_el = static_cast<long long>(a.M) * a.d;
+  for (int i = r0 + warp; i < r1; i += ROWS_THREADS / 32) {
+    const int dst = at[i - r0];
+    if (dst < 0) {
+      if (a.dx)
+        for (int v = lane; v < nv; v += 32)
+          if (in_bounds(a.err, static_cast<long long>(i) * a.d + 8 * v, 8, n_el, SITE_HEAD_DX))
+            *reinterpret_cast<uint4*>(a.dx + static_cast<long long>(i) * a.d + 8 * v) = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    const uint4* src = reinterpret_cast<const uint4*>(a.x + static_cast<long long>(i) * a.d);
+    uint4* to = reinterpret_cast<uint4*>(a.xc + static_cast<long long>(dst) * a.d);
+    const float r = a.xs ? (g > 0.0f ? a.dloss[i] / g : a.dloss[i]) : 0.0f;   // g = 0: all zero (or not a number)
+    for (int v = lane; v < nv; v += 32) {
+      if (!in_bounds(a.err, static_cast<long long>(dst) * a.d + 8 * v, 8, n_el, SITE_HEAD_X)) continue;
+      const uint4 u = src[v];
+      to[v] = u;
+      if (a.xs) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          o[q] = pack_bf16(__uint_as_float(w[q] << 16) * r, __uint_as_float(w[q] & 0xffff0000u) * r);
+        *reinterpret_cast<uint4*>(a.xs + static_cast<long long>(dst) * a.d + 8 * v) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+  }
+  // x' up to the next whole block of 64 rows is a factor of the sum over rows: zeros
+  if (a.xs && blockIdx.x == gridDim.x - 1) {
+    const int end = min(max((all + 63) / 64 * 64, 64), a.M);
+    for (long long v = static_cast<long long>(all) * nv + threadIdx.x; v < static_cast<long long>(end) * nv;
+         v += ROWS_THREADS)
+      if (in_bounds(a.err, v * 8, 8, n_el, SITE_HEAD_X)) reinterpret_cast<uint4*>(a.xs)[v] = make_uint4(0, 0, 0, 0);
+  }
+}
+
+// Largest |dloss| of the rows that take part (one block).
+__global__ void __launch_bounds__(1024) dloss_max_kernel(const __grid_constant__ RowsArgs a, float* g_max) {
+  __shared__ float sm[32];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  float g = 0.0f;
+  for (int i = threadIdx.x; i < a.M; i += 1024)
+    if (row_state(a, i) == 1) g = fmaxf(g, fabsf(a.dloss[i]));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = g;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    g = sm[threadIdx.x];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+    if (threadIdx.x == 0) *g_max = g;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Row losses from the tiles' (max, sum): 32 rows a block, 16 interleaved slices of the column tiles.
+// ---------------------------------------------------------------------------
+struct FinishArgs {
+  const int* n_rows;
+  const int* row_src;
+  int M, V, n_tiles, k;
+  const float2* part;
+  const float* part_sum;
+  long long part_ld;
+  const float* tgt_s;        // by compact row
+  const float* tgt_p;        // by source row; null: cross entropy
+  const int* tgt_cnt;
+  float inv_t, smoothing;
+  float* loss;
+  float* lse;
+  uint32_t* err;
+};
+
+__global__ void __launch_bounds__(FIN_ROWS* FIN_SLICES) head_finish_kernel(const __grid_constant__ FinishArgs a) {
+  __shared__ float sm[3][FIN_SLICES][FIN_ROWS + 1];
+  __shared__ float row_lse[FIN_ROWS];
+  const int rx = threadIdx.x & 31, sl = threadIdx.x >> 5;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int n = min(max(*a.n_rows, 0), a.M);
+  for (int r0 = blockIdx.x * FIN_ROWS; r0 < n; r0 += gridDim.x * FIN_ROWS) {
+    const int row = r0 + rx;
+    const bool on = row < n;
+    float m = -INFINITY, l = 0.0f, s = 0.0f;
+    if (on) {
+#pragma unroll 4
+      for (int t = sl; t < a.n_tiles; t += FIN_SLICES) {
+        const long long i = static_cast<long long>(t) * a.part_ld + row;
+        if (!in_bounds(a.err, i, 1, static_cast<long long>(a.n_tiles) * a.part_ld, SITE_HEAD_PART)) continue;
+        const float2 q = a.part[i];
+        const float mn = fmaxf(m, q.x), mo = mn == -INFINITY ? 0.0f : mn;
+        l = l * exp2f(m - mo) + q.y * exp2f(q.x - mo);
+        m = mn;
+        if (a.part_sum) s += a.part_sum[i];
+      }
+    }
+    sm[0][sl][rx] = m;
+    sm[1][sl][rx] = l;
+    sm[2][sl][rx] = s;
+    __syncthreads();
+    if (sl == 0 && on) {
+#pragma unroll
+      for (int q = 1; q < FIN_SLICES; ++q) m = fmaxf(m, sm[0][q][rx]);
+      const float mo = m == -INFINITY ? 0.0f : m;
+      l = 0.0f;
+      s = 0.0f;
+#pragma unroll
+      for (int q = 0; q < FIN_SLICES; ++q) {
+        l += sm[1][q][rx] * exp2f(sm[0][q][rx] - mo);
+        s += sm[2][q][rx];
+      }
+      const float lse = fmaf(mo, 0.69314718055994531f, logf(l));
+      row_lse[rx] = lse;
+      const int src = in_bounds(a.err, row, 1, a.M, SITE_HEAD_ROWS) ? a.row_src[row] : 0;
+      if (in_bounds(a.err, src, 1, a.M, SITE_HEAD_ROWS)) {
+        a.lse[src] = lse;
+        if (!a.tgt_p) {
+          const float sy = a.tgt_s[row];
+          a.loss[src] = a.smoothing > 0.0f
+                            ? (1.0f - a.smoothing) * (lse - sy) + a.smoothing * (lse - s / static_cast<float>(a.V))
+                            : lse - sy;
+        }
+      }
+    }
+    __syncthreads();
+    if (a.tgt_p) {       // distillation: a warp per row over its entries
+      for (int r = sl; r < FIN_ROWS && r0 + r < n; r += FIN_SLICES) {
+        const int src = a.row_src[r0 + r];
+        if (!in_bounds(a.err, src, 1, a.M, SITE_HEAD_ROWS)) continue;
+        const float lse = row_lse[r];
+        const int cnt = a.tgt_cnt[src];
+        float t = 0.0f;
+        for (int j = rx; j < cnt; j += 32) {
+          const long long i = static_cast<long long>(src) * a.k + j, is = static_cast<long long>(r0 + r) * a.k + j;
+          if (!in_bounds(a.err, i, 1, static_cast<long long>(a.M) * a.k, SITE_HEAD_TARGET)) continue;
+          const float p = a.tgt_p[i];
+          t += p * (logf(p) - a.tgt_s[is] * a.inv_t + lse);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+        if (rx == 0) a.loss[src] = t / (a.inv_t * a.inv_t);
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// dx of the rows that take part: the slabs' sum times T dloss, rounded once.
+__global__ void __launch_bounds__(256)
+    head_dx_kernel(const int* __restrict__ n_rows, const int* __restrict__ row_src, int M, int d, int splits,
+                   const float* __restrict__ slab, const float* __restrict__ dloss, float temperature,
+                   __nv_bfloat16* __restrict__ dx, uint32_t* err) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int n = min(max(*n_rows, 0), M);
+  const int nv = d / 8;
+  const long long per_slab = static_cast<long long>(M) * d;
+  const long long work = static_cast<long long>(n) * nv;
+  for (long long w = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; w < work;
+       w += static_cast<long long>(gridDim.x) * 256) {
+    const int row = static_cast<int>(w / nv), v = static_cast<int>(w % nv);
+    const int src = row_src[row];
+    if (!in_bounds(err, src, 1, M, SITE_HEAD_ROWS)) continue;
+    const float f = dloss[src] * temperature;
+    float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int q = 0; q < splits; ++q) {
+      const long long i = q * per_slab + static_cast<long long>(row) * d + 8 * v;
+      if (!in_bounds(err, i, 8, splits * per_slab, SITE_HEAD_SLAB)) continue;
+      const float4 a = *reinterpret_cast<const float4*>(slab + i), b = *reinterpret_cast<const float4*>(slab + i + 4);
+      s[0] += a.x; s[1] += a.y; s[2] += a.z; s[3] += a.w;
+      s[4] += b.x; s[5] += b.y; s[6] += b.z; s[7] += b.w;
+    }
+    const long long o = static_cast<long long>(src) * d + 8 * v;
+    if (in_bounds(err, o, 8, per_slab, SITE_HEAD_DX))
+      *reinterpret_cast<uint4*>(dx + o) = make_uint4(pack_bf16(s[0] * f, s[1] * f), pack_bf16(s[2] * f, s[3] * f),
+                                                     pack_bf16(s[4] * f, s[5] * f), pack_bf16(s[6] * f, s[7] * f));
+  }
+}
+
+// ------------------------------ host side ------------------------------
+constexpr int kSms = 152;      // sizes of workspaces do not depend on the device that asks
+
+struct HeadShape {
+  int M, d, V, k;              // k = 0: cross entropy
+  int n_tiles() const { return (V + HEAD_BN - 1) / HEAD_BN; }
+  int entries() const { return k > 0 ? k : 1; }
+};
+
+bool shape_ok(int M, int d, int V) {
+  return M >= 0 && M <= (1 << 24) && d >= 8 && d <= (1 << 16) && d % 8 == 0 && V >= 1 && V <= (1 << 24);
+}
+
+// Targets and row map, shared by both passes.
+struct RowsLayout {
+  size_t n_rows, row_src, label32, idx, p, cnt, xc;
+};
+
+RowsLayout rows_layout(Carver& c, const HeadShape& h) {
+  RowsLayout L;
+  const size_t m = static_cast<size_t>(h.M);
+  L.n_rows = c.take(256);
+  L.row_src = c.take(m * sizeof(int));
+  L.label32 = L.idx = L.p = L.cnt = 0;
+  if (h.k > 0) {
+    L.idx = c.take(m * h.k * sizeof(int));
+    L.p = c.take(m * h.k * sizeof(float));
+    L.cnt = c.take(m * sizeof(int));
+  } else {
+    L.label32 = c.take(m * sizeof(int));
+  }
+  L.xc = c.take(m * h.d * 2);
+  return L;
+}
+
+struct FwdLayout {
+  RowsLayout r;
+  size_t part, part_sum, tgt_s, total;
+  long long part_ld;
+};
+
+FwdLayout fwd_layout(const HeadShape& h) {
+  Carver c;
+  FwdLayout L;
+  L.r = rows_layout(c, h);
+  L.part_ld = (static_cast<long long>(h.M) + 31) / 32 * 32;
+  L.part = c.take(static_cast<size_t>(h.n_tiles()) * L.part_ld * sizeof(float2));
+  L.part_sum = h.k > 0 ? 0 : c.take(static_cast<size_t>(h.n_tiles()) * L.part_ld * sizeof(float));
+  L.tgt_s = c.take(static_cast<size_t>(h.M) * h.entries() * sizeof(float));
+  L.total = c.off;
+  return L;
+}
+
+struct BwdLayout {
+  RowsLayout r;
+  size_t g_max, xs, dl, slab, total;
+  int piece, splits;           // vocabulary rows per piece (a multiple of 256), slabs of dx
+};
+
+// A piece's D takes at most about this much memory.
+constexpr long long PIECE_BYTES = 256ll << 20;
+
+BwdLayout bwd_layout(const HeadShape& h) {
+  Carver c;
+  BwdLayout L;
+  L.r = rows_layout(c, h);
+  const long long v256 = (static_cast<long long>(h.V) + 255) / 256 * 256;
+  long long piece = PIECE_BYTES / (2ll * h.M) / 256 * 256;
+  if (piece < 256) piece = 256;
+  if (piece > v256) piece = v256;
+  L.piece = static_cast<int>(piece);
+  // too few dx tiles for the device: the sum over the piece is split over slabs
+  const long long tiles = static_cast<long long>((h.M + HEAD_BM - 1) / HEAD_BM) * ((h.d + HEAD_BN - 1) / HEAD_BN);
+  const long long kb = piece / HEAD_BK;
+  long long splits = kSms / tiles;
+  if (splits > kb / 4) splits = kb / 4;
+  if (splits < 1) splits = 1;
+  L.splits = static_cast<int>(splits);
+  const size_t m = static_cast<size_t>(h.M);
+  L.g_max = c.take(256);
+  L.xs = c.take(m * h.d * 2);
+  L.dl = c.take(m * L.piece * 2);
+  L.slab = c.take(static_cast<size_t>(L.splits) * m * h.d * sizeof(float));
+  L.total = c.off;
+  return L;
+}
+
+bool map2(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t ld, uint32_t bx, uint32_t by,
+          CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B) {
+  const uint64_t dims[2] = {inner, rows};
+  const uint64_t str[1] = {ld * 2};
+  const uint32_t box[2] = {bx, by};
+  return tma_map_bf16(m, 2, base, dims, str, box, swz);
+}
+
+std::mutex g_head_mu;
+
+template <int KIND>
+cudaError_t launch_head(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o, const HeadParams& p,
+                        cudaStream_t s) {
+  static uint64_t attr_done = 0;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  {
+    // once per device, so that launches stay legal inside a graph capture
+    std::lock_guard<std::mutex> lk(g_head_mu);
+    if (dev < 0 || dev > 63) return cudaErrorInvalidDevice;
+    if (!(attr_done & (1ull << dev))) {
+      e = cudaFuncSetAttribute(head_gemm_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, HeadSmem::TOTAL);
+      if (e != cudaSuccess) return e;
+      attr_done |= 1ull << dev;
+    }
+  }
+  const long long rows = (p.m_cap + HEAD_BM - 1) / HEAD_BM;
+  const long long vm = (p.vc + HEAD_BM - 1) / HEAD_BM, vn = (p.vc + HEAD_BN - 1) / HEAD_BN,
+                  dn = (p.d + HEAD_BN - 1) / HEAD_BN;
+  const long long tiles = KIND == HEAD_DW ? vm * dn : KIND == HEAD_DX ? rows * dn * p.k_splits : rows * vn;
+  const int sms = sm_count();
+  const int grid = tiles < sms ? static_cast<int>(tiles) : sms;
+  return launch_pdl(head_gemm_kernel<KIND>, dim3(grid), dim3(GEMM_THREADS), HeadSmem::TOTAL, s, a, b, o, p);
+}
+
+struct Targets {
+  const int64_t* labels;       // cross entropy
+  float smoothing;
+  const void* top;             // distillation
+  int top_type;
+  const int64_t* index;
+  float temperature;
+};
+
+cudaError_t launch_lists(const HeadShape& h, const Targets& t, int* idx, float* p, int* cnt, uint32_t* err,
+                         cudaStream_t s) {
+  const size_t smem = static_cast<size_t>(h.k) * 12;
+  const float inv_t = 1.0f / t.temperature;
+  const dim3 grid(h.M), block(LIST_THREADS);
+  if (t.top_type == WB_F32)
+    return launch_pdl(target_lists_kernel<float>, grid, block, smem, s, static_cast<const float*>(t.top), t.index, h.M,
+                      h.k, h.V, inv_t, idx, p, cnt, err);
+  if (t.top_type == WB_BF16)
+    return launch_pdl(target_lists_kernel<__nv_bfloat16>, grid, block, smem, s,
+                      static_cast<const __nv_bfloat16*>(t.top), t.index, h.M, h.k, h.V, inv_t, idx, p, cnt, err);
+  return launch_pdl(target_lists_kernel<__half>, grid, block, smem, s, static_cast<const __half*>(t.top), t.index, h.M,
+                    h.k, h.V, inv_t, idx, p, cnt, err);
+}
+
+// Fewer rows a block while there are few (the copy wants many blocks); each block counts the rows
+// before its own, which grows with the square of the blocks, so at most about a thousand of them.
+int rows_per_block(int M) {
+  int r = 8;
+  while (r < ROWS_THREADS && M > 1216 * r) r *= 2;
+  return r;
+}
+
+struct HeadBase {
+  HeadShape h;
+  uint8_t* ws;
+  uint32_t* err;
+  const int* row_src;
+  const int* n_rows;
+  const int* tgt_idx;
+  const float* tgt_p;
+  const int* tgt_cnt;
+  __nv_bfloat16* xc;
+};
+
+HeadParams head_params(const HeadBase& b, const Targets& t) {
+  HeadParams p = {};
+  p.n_rows = b.n_rows;
+  p.m_cap = b.h.M;
+  p.V = b.h.V;
+  p.d = b.h.d;
+  p.vc = b.h.V;
+  p.panel = 8;
+  p.k_splits = 1;
+  p.scale_log2 = 1.4426950408889634f / t.temperature;
+  p.row_src = b.row_src;
+  p.tgt_idx = b.tgt_idx;
+  p.tgt_p = b.tgt_p;
+  p.tgt_cnt = b.tgt_cnt;
+  p.k = b.h.entries();
+  p.label_p = 1.0f - t.smoothing;
+  p.smooth = t.smoothing / static_cast<float>(b.h.V);
+  p.err = b.err;
+  return p;
+}
+
+HeadBase head_base(const HeadShape& h, uint8_t* ws, const RowsLayout& L, uint32_t* err) {
+  HeadBase b;
+  b.h = h;
+  b.ws = ws;
+  b.err = err;
+  b.row_src = reinterpret_cast<int*>(ws + L.row_src);
+  b.n_rows = reinterpret_cast<int*>(ws + L.n_rows);
+  b.tgt_idx = reinterpret_cast<int*>(ws + (h.k > 0 ? L.idx : L.label32));
+  b.tgt_p = h.k > 0 ? reinterpret_cast<float*>(ws + L.p) : nullptr;
+  b.tgt_cnt = h.k > 0 ? reinterpret_cast<int*>(ws + L.cnt) : nullptr;
+  b.xc = reinterpret_cast<__nv_bfloat16*>(ws + L.xc);
+  return b;
+}
+
+RowsArgs rows_args(const HeadBase& b, const Targets& t, const RowsLayout& L, const void* x) {
+  RowsArgs a = {};
+  a.labels = t.labels;
+  a.cnt = b.tgt_cnt;
+  a.M = b.h.M;
+  a.V = b.h.V;
+  a.d = b.h.d;
+  a.rows_per_block = rows_per_block(b.h.M);
+  a.x = static_cast<const __nv_bfloat16*>(x);
+  a.xc = b.xc;
+  a.row_src = reinterpret_cast<int*>(b.ws + L.row_src);
+  a.n_rows = reinterpret_cast<int*>(b.ws + L.n_rows);
+  a.label32 = b.h.k > 0 ? nullptr : reinterpret_cast<int*>(b.ws + L.label32);
+  a.err = b.err;
+  return a;
+}
+
+cudaError_t launch_rows(const RowsArgs& a, cudaStream_t s) {
+  return launch_pdl(rows_kernel, dim3((a.M + a.rows_per_block - 1) / a.rows_per_block), dim3(ROWS_THREADS), 0, s, a);
+}
+
+wb_status head_forward(const HeadShape& h, const Targets& t, const void* x, const void* w, float* loss, float* lse,
+                       void* workspace, cudaStream_t s) {
+  uint32_t* err = tc_err_ptr();
+  if (!err) return WB_ECUDA;
+  const FwdLayout L = fwd_layout(h);
+  const HeadBase b = head_base(h, static_cast<uint8_t*>(workspace), L.r, err);
+  {
+    Prof pr(PC_HEAD_ROWS, s, h.k > 0 ? 2 : 1);
+    if (h.k > 0)
+      WB_CUDA(launch_lists(h, t, reinterpret_cast<int*>(b.ws + L.r.idx), reinterpret_cast<float*>(b.ws + L.r.p),
+                           reinterpret_cast<int*>(b.ws + L.r.cnt), err, s));
+    RowsArgs a = rows_args(b, t, L.r, x);
+    a.loss = loss;
+    a.lse = lse;
+    WB_CUDA(launch_rows(a, s));
+  }
+  HeadParams p = head_params(b, t);
+  p.part = reinterpret_cast<float2*>(b.ws + L.part);
+  p.part_sum = t.smoothing > 0.0f ? reinterpret_cast<float*>(b.ws + L.part_sum) : nullptr;
+  p.part_ld = L.part_ld;
+  p.tgt_s = reinterpret_cast<float*>(b.ws + L.tgt_s);
+  CUtensorMap am, bm;
+  if (!map2(&am, b.xc, h.d, h.M, h.d, HEAD_BK, HEAD_BM) || !map2(&bm, w, h.d, h.V, h.d, HEAD_BK, HEAD_BN))
+    return WB_ECUDA;
+  {
+    Prof pr(PC_HEAD_LSE, s);
+    WB_CUDA(launch_head<HEAD_LSE>(am, bm, am, p, s));
+  }
+  FinishArgs f = {};
+  f.n_rows = b.n_rows;
+  f.row_src = b.row_src;
+  f.M = h.M;
+  f.V = h.V;
+  f.n_tiles = h.n_tiles();
+  f.k = h.entries();
+  f.part = p.part;
+  f.part_sum = p.part_sum;
+  f.part_ld = L.part_ld;
+  f.tgt_s = p.tgt_s;
+  f.tgt_p = b.tgt_p;
+  f.tgt_cnt = b.tgt_cnt;
+  f.inv_t = 1.0f / t.temperature;
+  f.smoothing = t.smoothing;
+  f.loss = loss;
+  f.lse = lse;
+  f.err = err;
+  {
+    Prof pr(PC_HEAD_FINISH, s);
+    const int blocks = (h.M + FIN_ROWS - 1) / FIN_ROWS;
+    WB_CUDA(launch_pdl(head_finish_kernel, dim3(blocks < 8 * kSms ? blocks : 8 * kSms), dim3(FIN_ROWS * FIN_SLICES), 0,
+                       s, f));
+  }
+  return WB_OK;
+}
+
+wb_status head_backward(const HeadShape& h, const Targets& t, const float* dloss, const void* x, const void* w,
+                        const float* lse, void* dx, void* dw, void* workspace, cudaStream_t s) {
+  uint32_t* err = tc_err_ptr();
+  if (!err) return WB_ECUDA;
+  const BwdLayout L = bwd_layout(h);
+  const HeadBase b = head_base(h, static_cast<uint8_t*>(workspace), L.r, err);
+  auto* g_max = reinterpret_cast<float*>(b.ws + L.g_max);
+  auto* xs = reinterpret_cast<__nv_bfloat16*>(b.ws + L.xs);
+  auto* dl = reinterpret_cast<__nv_bfloat16*>(b.ws + L.dl);
+  auto* slab = reinterpret_cast<float*>(b.ws + L.slab);
+  {
+    Prof pr(PC_HEAD_ROWS, s, (h.k > 0 ? 2 : 1) + (dw ? 1 : 0));
+    if (h.k > 0)
+      WB_CUDA(launch_lists(h, t, reinterpret_cast<int*>(b.ws + L.r.idx), reinterpret_cast<float*>(b.ws + L.r.p),
+                           reinterpret_cast<int*>(b.ws + L.r.cnt), err, s));
+    RowsArgs a = rows_args(b, t, L.r, x);
+    a.dloss = dloss;
+    a.g_max = g_max;
+    a.xs = dw ? xs : nullptr;
+    a.dx = static_cast<__nv_bfloat16*>(dx);
+    if (dw) WB_CUDA(launch_pdl(dloss_max_kernel, dim3(1), dim3(1024), 0, s, a, g_max));
+    WB_CUDA(launch_rows(a, s));
+  }
+  HeadParams p = head_params(b, t);
+  p.lse = lse;
+  p.g_scale = g_max;
+  p.out_scale = t.temperature;
+  p.k_splits = L.splits;
+  CUtensorMap xa, wb, dlo, dla, wk, slo, dlt, xk, dwo;
+  const uint64_t ld = L.piece;
+  bool ok = map2(&xa, b.xc, h.d, h.M, h.d, HEAD_BK, HEAD_BM) && map2(&wb, w, h.d, h.V, h.d, HEAD_BK, HEAD_BN) &&
+            map2(&dlo, dl, ld, h.M, ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (dx) {
+    const uint64_t dims[3] = {static_cast<uint64_t>(h.d), static_cast<uint64_t>(h.M), static_cast<uint64_t>(L.splits)};
+    const uint64_t str[2] = {static_cast<uint64_t>(h.d) * 4, static_cast<uint64_t>(h.d) * 4 * h.M};
+    const uint32_t box[3] = {16, 32, 1};
+    ok = ok && map2(&dla, dl, ld, h.M, ld, HEAD_BK, HEAD_BM) && map2(&wk, w, h.d, h.V, h.d, 64, HEAD_BK) &&
+         tma_map_f32(&slo, 3, slab, dims, str, box, CU_TENSOR_MAP_SWIZZLE_64B);
+  }
+  if (dw)
+    ok = ok && map2(&dlt, dl, ld, h.M, ld, 64, HEAD_BK) && map2(&xk, xs, h.d, h.M, h.d, 64, HEAD_BK) &&
+         map2(&dwo, dw, h.d, h.V, h.d, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (!ok) return WB_ECUDA;
+  for (int v0 = 0; v0 < h.V; v0 += L.piece) {
+    p.v0 = v0;
+    p.vc = h.V - v0 < L.piece ? h.V - v0 : L.piece;
+    p.first_piece = v0 == 0;
+    {
+      Prof pr(PC_HEAD_DLOGITS, s);
+      WB_CUDA(launch_head<HEAD_DLOGITS>(xa, wb, dlo, p, s));
+    }
+    if (dx) {
+      Prof pr(PC_HEAD_DX, s);
+      WB_CUDA(launch_head<HEAD_DX>(dla, wk, slo, p, s));
+    }
+    if (dw) {
+      Prof pr(PC_HEAD_DW, s);
+      WB_CUDA(launch_head<HEAD_DW>(dlt, xk, dwo, p, s));
+    }
+  }
+  if (dx) {
+    Prof pr(PC_HEAD_FINISH, s);
+    const long long work = static_cast<long long>(h.M) * (h.d / 8);
+    const long long blocks = (work + 255) / 256;
+    WB_CUDA(launch_pdl(head_dx_kernel, dim3(static_cast<unsigned>(blocks < 16 * kSms ? blocks : 16 * kSms)), dim3(256),
+                       0, s, b.n_rows, b.row_src, h.M, h.d, L.splits, static_cast<const float*>(slab), dloss,
+                       t.temperature, static_cast<__nv_bfloat16*>(dx), err));
+  }
+  return WB_OK;
+}
+
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+wb_status check_forward(const HeadShape& h, const void* x, const void* w, const float* loss, const float* lse,
+                        const void* ws, size_t ws_bytes) {
+  if (!x || !w || !loss || !lse || !aligned16(x) || !aligned16(w) || !aligned4(loss) || !aligned4(lse))
+    return WB_EINVAL;
+  if (!ws || !aligned16(ws) || ws_bytes < fwd_layout(h).total) return WB_EWORKSPACE;
+  return WB_OK;
+}
+
+wb_status check_backward(const HeadShape& h, const float* dloss, const void* x, const void* w, const float* lse,
+                         const void* dx, const void* dw, const void* ws, size_t ws_bytes) {
+  if (!dloss || !x || !w || !lse || !aligned16(x) || !aligned16(w) || !aligned4(dloss) || !aligned4(lse) ||
+      (dx && !aligned16(dx)) || (dw && !aligned16(dw)))
+    return WB_EINVAL;
+  if (!ws || !aligned16(ws) || ws_bytes < bwd_layout(h).total) return WB_EWORKSPACE;
+  return WB_OK;
+}
+
+bool top_ok(int type) { return type == WB_BF16 || type == WB_F16 || type == WB_F32; }
+bool positive(float t) { return t > 0.0f && t < INFINITY; }
+
+}  // namespace
+}  // namespace wb
+
+using namespace wb;
+
+extern "C" {
+
+size_t wb_linear_cross_entropy_workspace_bytes(int M, int d, int V) {
+  return shape_ok(M, d, V) && M > 0 ? fwd_layout(HeadShape{M, d, V, 0}).total : 0;
+}
+size_t wb_linear_cross_entropy_backward_workspace_bytes(int M, int d, int V) {
+  return shape_ok(M, d, V) && M > 0 ? bwd_layout(HeadShape{M, d, V, 0}).total : 0;
+}
+size_t wb_linear_distill_workspace_bytes(int M, int d, int V, int k) {
+  return shape_ok(M, d, V) && M > 0 && k >= 1 && k <= HEAD_MAX_K ? fwd_layout(HeadShape{M, d, V, k}).total : 0;
+}
+size_t wb_linear_distill_backward_workspace_bytes(int M, int d, int V, int k) {
+  return shape_ok(M, d, V) && M > 0 && k >= 1 && k <= HEAD_MAX_K ? bwd_layout(HeadShape{M, d, V, k}).total : 0;
+}
+
+wb_status wb_linear_cross_entropy(const void* x, const void* w, const int64_t* labels, int M, int d, int V,
+                                  float label_smoothing, float* loss, float* lse, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  if (!shape_ok(M, d, V) || !(label_smoothing >= 0.0f && label_smoothing < 1.0f)) return WB_EINVAL;
+  if (M == 0) return WB_OK;
+  if (!labels || !aligned8(labels)) return WB_EINVAL;
+  const HeadShape h{M, d, V, 0};
+  const wb_status st = check_forward(h, x, w, loss, lse, workspace, workspace_bytes);
+  if (st != WB_OK) return st;
+  const Targets t{labels, label_smoothing, nullptr, 0, nullptr, 1.0f};
+  return head_forward(h, t, x, w, loss, lse, workspace, static_cast<cudaStream_t>(stream));
+}
+
+wb_status wb_linear_cross_entropy_backward(const float* dloss, const void* x, const void* w, const int64_t* labels,
+                                           const float* lse, int M, int d, int V, float label_smoothing, void* dx,
+                                           void* dw, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!shape_ok(M, d, V) || !(label_smoothing >= 0.0f && label_smoothing < 1.0f)) return WB_EINVAL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M == 0) {
+    if (dw && !aligned16(dw)) return WB_EINVAL;
+    if (dw) WB_CUDA(cudaMemsetAsync(dw, 0, static_cast<size_t>(V) * d * 2, s));
+    return WB_OK;
+  }
+  if (!labels || !aligned8(labels)) return WB_EINVAL;
+  const HeadShape h{M, d, V, 0};
+  const wb_status st = check_backward(h, dloss, x, w, lse, dx, dw, workspace, workspace_bytes);
+  if (st != WB_OK) return st;
+  if (!dx && !dw) return WB_OK;
+  const Targets t{labels, label_smoothing, nullptr, 0, nullptr, 1.0f};
+  return head_backward(h, t, dloss, x, w, lse, dx, dw, workspace, s);
+}
+
+wb_status wb_linear_distill(const void* x, const void* w, const void* top, int top_dtype, const int64_t* index, int M,
+                            int d, int V, int k, float temperature, float* loss, float* lse, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  if (!top_ok(top_dtype)) return WB_EUNSUPPORTED;
+  if (!shape_ok(M, d, V) || k < 1 || k > HEAD_MAX_K || !positive(temperature)) return WB_EINVAL;
+  if (M == 0) return WB_OK;
+  if (!top || !index || !aligned16(top) || !aligned8(index)) return WB_EINVAL;
+  const HeadShape h{M, d, V, k};
+  const wb_status st = check_forward(h, x, w, loss, lse, workspace, workspace_bytes);
+  if (st != WB_OK) return st;
+  const Targets t{nullptr, 0.0f, top, top_dtype, index, temperature};
+  return head_forward(h, t, x, w, loss, lse, workspace, static_cast<cudaStream_t>(stream));
+}
+
+wb_status wb_linear_distill_backward(const float* dloss, const void* x, const void* w, const void* top, int top_dtype,
+                                     const int64_t* index, const float* lse, int M, int d, int V, int k,
+                                     float temperature, void* dx, void* dw, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+  if (!top_ok(top_dtype)) return WB_EUNSUPPORTED;
+  if (!shape_ok(M, d, V) || k < 1 || k > HEAD_MAX_K || !positive(temperature)) return WB_EINVAL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M == 0) {
+    if (dw && !aligned16(dw)) return WB_EINVAL;
+    if (dw) WB_CUDA(cudaMemsetAsync(dw, 0, static_cast<size_t>(V) * d * 2, s));
+    return WB_OK;
+  }
+  if (!top || !index || !aligned16(top) || !aligned8(index)) return WB_EINVAL;
+  const HeadShape h{M, d, V, k};
+  const wb_status st = check_backward(h, dloss, x, w, lse, dx, dw, workspace, workspace_bytes);
+  if (st != WB_OK) return st;
+  if (!dx && !dw) return WB_OK;
+  const Targets t{nullptr, 0.0f, top, top_dtype, index, temperature};
+  return head_backward(h, t, dloss, x, w, lse, dx, dw, workspace, s);
+}
+
+}  // extern "C"

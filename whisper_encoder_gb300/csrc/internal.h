@@ -86,9 +86,12 @@ inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, siz
 // ---- host helpers of the entry points (api.cu) ----
 // Device error word of the tensor-core and training kernels (per device); null if it cannot be found.
 uint32_t* tc_err_ptr();
-// Tiled map of a bf16 tensor; strides in bytes for dims 1..rank-1.
+// Tiled map of a bf16 / float32 tensor; strides in bytes for dims 1..rank-1.
 bool tma_map_bf16(CUtensorMap* m, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
                   const uint32_t* box, CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B);
+
+bool tma_map_f32(CUtensorMap* m, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+                 const uint32_t* box, CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -110,7 +113,7 @@ struct Carver {
 enum ProfClass {
   PC_LOGMEL_PREP, PC_LOGMEL_DFT, PC_LOGMEL_MEL, PC_LOGMEL_POST, PC_STEM_PREP, PC_STEM_CONV1, PC_STEM_CONV2,
   PC_ENC_LN, PC_ENC_QUANT, PC_ENC_QKV, PC_ENC_ATTN, PC_ENC_OUT, PC_ENC_FC1, PC_ENC_FC2, PC_OTHER,
-  PC_TRAIN_LN, PC_COUNT
+  PC_TRAIN_LN, PC_HEAD_ROWS, PC_HEAD_LSE, PC_HEAD_FINISH, PC_HEAD_DLOGITS, PC_HEAD_DX, PC_HEAD_DW, PC_COUNT
 };
 struct Prof {
   int cls, kernels;

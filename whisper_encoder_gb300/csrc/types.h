@@ -115,7 +115,8 @@ struct AttnParams {
 };
 
 // Sites (bits 8..15 of the error word) of the debug bounds checks: 0x20-0x3F the SIMT kernels,
-// 0x40-0x4F the GEMM epilogues, 0x50-0x5F the attention epilogue, 0x60-0x6F the LayerNorm of training.
+// 0x40-0x4F the GEMM epilogues, 0x50-0x5F the attention epilogue, 0x60-0x67 the LayerNorm of training,
+// 0x68-0x6F the vocabulary losses.
 enum : uint32_t {
   SITE_PAD_SPLIT = 0x20, SITE_DFT_BASIS, SITE_MEL_FB, SITE_LOGMEL_POST, SITE_STEM_T_IN, SITE_STEM_T_OUT,
   SITE_ZERO_ROWS, SITE_PACK_CONV, SITE_LN_X, SITE_LN_Y, SITE_LN_GB, SITE_STATS_X, SITE_STATS_OUT,
@@ -125,7 +126,8 @@ enum : uint32_t {
   SITE_GEMM_RESID = 0x40, SITE_GEMM_BIAS, SITE_GEMM_LNSTATS, SITE_GEMM_POS, SITE_GEMM_VT, SITE_GEMM_POWER,
   SITE_GEMM_MEL, SITE_GEMM_AMAX, SITE_GEMM_LNPART,
   SITE_ATT_OUT = 0x50, SITE_ATT_AMAX,
-  SITE_LNT_X = 0x60, SITE_LNT_Y, SITE_LNT_TOTAL, SITE_LNT_STATS, SITE_LNT_PART, SITE_LNT_GRAD
+  SITE_LNT_X = 0x60, SITE_LNT_Y, SITE_LNT_TOTAL, SITE_LNT_STATS, SITE_LNT_PART, SITE_LNT_GRAD,
+  SITE_HEAD_ROWS = 0x68, SITE_HEAD_TARGET, SITE_HEAD_PART, SITE_HEAD_X, SITE_HEAD_LIST, SITE_HEAD_SLAB, SITE_HEAD_DX
 };
 
 }  // namespace wb
