@@ -399,7 +399,7 @@ wb_status wb_dequantize_e5m2(const uint8_t* q, const float* scale, int64_t n, vo
  * WB_EUNSUPPORTED for another dtype, WB_EINVAL for bad sizes, pointers or alignment. */
 wb_status wb_layernorm_forward(const void* x, const void* residual, const float* g, const float* b, int rows, int d,
                                float eps, int dtype, void* y, void* total, float* stats, void* stream);
-size_t wb_layernorm_backward_workspace_bytes(int rows, int d);
+size_t wb_layernorm_backward_workspace_bytes(int rows, int d, int dtype);
 wb_status wb_layernorm_backward(const void* dy, const void* x, const float* g, const float* stats, const void* dtotal,
                                 int rows, int d, int dtype, void* dx, float* dg, float* db, void* workspace,
                                 size_t workspace_bytes, void* stream);

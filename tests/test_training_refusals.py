@@ -46,13 +46,15 @@ def test_layernorm_train_refusals(lib):
     assert bwd(dt=ODD) == L.WB_EINVAL
     assert bwd(dg=None) == L.WB_EINVAL                  # one parameter gradient without the other
     assert bwd(ws=None) == L.WB_EWORKSPACE
-    need = lib.wb_layernorm_backward_workspace_bytes(4, 64)
+    need = lib.wb_layernorm_backward_workspace_bytes(4, 64, L.WB_F32)
     assert need >= 2 * 64 * 4
     assert bwd(n=need - 1) == L.WB_EWORKSPACE
-    assert lib.wb_layernorm_backward_workspace_bytes(0, 64) == 0
-    assert lib.wb_layernorm_backward_workspace_bytes(4, 20000) == 0
+    assert lib.wb_layernorm_backward_workspace_bytes(0, 64, L.WB_F32) == 0
+    assert lib.wb_layernorm_backward_workspace_bytes(4, 20000, L.WB_F32) == 0
+    assert lib.wb_layernorm_backward_workspace_bytes(4, 64, L.WB_E4M3) == 0
     # the partial rows of the parameter gradients stop growing with the rows
-    assert lib.wb_layernorm_backward_workspace_bytes(1 << 20, 1280) == lib.wb_layernorm_backward_workspace_bytes(1 << 21, 1280)
+    assert (lib.wb_layernorm_backward_workspace_bytes(1 << 20, 1280, L.WB_BF16)
+            == lib.wb_layernorm_backward_workspace_bytes(1 << 21, 1280, L.WB_BF16))
 
 
 def test_head_loss_refusals(lib):

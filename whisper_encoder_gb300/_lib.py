@@ -93,7 +93,7 @@ SIGNATURES = {
     "wb_dequantize_e5m2": (c_int, [c_void, c_void, c_i64, c_void, c_void]),
     "wb_layernorm_forward": (c_int, [c_void, c_void, c_void, c_void, c_int, c_int, c_float, c_int, c_void, c_void,
                                      c_void, c_void]),
-    "wb_layernorm_backward_workspace_bytes": (c_size, [c_int, c_int]),
+    "wb_layernorm_backward_workspace_bytes": (c_size, [c_int, c_int, c_int]),
     "wb_layernorm_backward": (c_int, [c_void, c_void, c_void, c_void, c_void, c_int, c_int, c_int, c_void, c_void,
                                       c_void, c_void, c_size, c_void]),
     "wb_linear_cross_entropy_workspace_bytes": (c_size, [c_int, c_int, c_int]),

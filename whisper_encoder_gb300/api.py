@@ -339,7 +339,7 @@ def layernorm_backward(dy, x, g, stats, dtotal=None, need_params: bool = True, s
         if need_params:
             dg = torch.empty_like(g)
             db = torch.empty_like(g)
-            ws = _workspace(load().wb_layernorm_backward_workspace_bytes(rows, d), x.device)
+            ws = _workspace(load().wb_layernorm_backward_workspace_bytes(rows, d, ty), x.device)
         call("wb_layernorm_backward", _p(dy), _p(x), _p(g), _p(stats), _p(dtotal), rows, d, ty, _p(dx), _p(dg), _p(db),
              _p(ws), ws.numel() if need_params else 0, _stream())
     return dx, dg, db
