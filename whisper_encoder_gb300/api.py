@@ -279,7 +279,7 @@ def _place(stream, first, *rest):
         if t is not None and t.device != dev:
             raise ValueError(f"tensors on {dev} and {t.device}: one device expected")
     if stream is None:
-        return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+        return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
     if stream.device != dev:
         raise ValueError(f"stream on {stream.device}, tensors on {dev}")
     if stream != torch.cuda.current_stream(dev):
@@ -287,6 +287,18 @@ def _place(stream, first, *rest):
             if t is not None:
                 t.record_stream(stream)
     return torch.cuda.stream(stream)
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _raw_stream(t) -> int:
+    """The current stream of t's device as an address (torch.cuda.current_stream builds an object: 6 us)."""
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def _a(t):
+    return None if t is None else t.data_ptr()
 
 
 def _need_shape(t, dtype, shape, name):
@@ -317,8 +329,8 @@ def layernorm_forward(x, g, b, eps: float = 1e-5, residual=None, stream=None):
         y = torch.empty_like(x)
         total = torch.empty_like(x) if residual is not None else None
         stats = torch.empty((rows, 2), dtype=torch.float32, device=x.device)
-        call("wb_layernorm_forward", _p(x), _p(residual), _p(g), _p(b), rows, d, eps, ty, _p(y), _p(total), _p(stats),
-             _stream())
+        call("wb_layernorm_forward", _a(x), _a(residual), _a(g), _a(b), rows, d, eps, ty, _a(y), _a(total), _a(stats),
+             _raw_stream(x))
     return y, (x if total is None else total), stats
 
 
@@ -340,8 +352,8 @@ def layernorm_backward(dy, x, g, stats, dtotal=None, need_params: bool = True, s
             dg = torch.empty_like(g)
             db = torch.empty_like(g)
             ws = _workspace(load().wb_layernorm_backward_workspace_bytes(rows, d, ty), x.device)
-        call("wb_layernorm_backward", _p(dy), _p(x), _p(g), _p(stats), _p(dtotal), rows, d, ty, _p(dx), _p(dg), _p(db),
-             _p(ws), ws.numel() if need_params else 0, _stream())
+        call("wb_layernorm_backward", _a(dy), _a(x), _a(g), _a(stats), _a(dtotal), rows, d, ty, _a(dx), _a(dg), _a(db),
+             _a(ws), ws.numel() if need_params else 0, _raw_stream(x))
     return dx, dg, db
 
 
@@ -376,10 +388,11 @@ def linear_cross_entropy(x, w, labels, label_smoothing: float = 0.0, workspace=N
     M, d, V = _head_shape(x, w)
     _need_shape(labels, torch.int64, (M,), "labels")
     with _place(stream, x, w, labels, workspace):
-        loss, lse = torch.empty((2, M), dtype=torch.float32, device=x.device)
+        loss = torch.empty(M, dtype=torch.float32, device=x.device)
+        lse = torch.empty(M, dtype=torch.float32, device=x.device)
         ws = _head_workspace(workspace, "wb_linear_cross_entropy_workspace_bytes", x.device, M, d, V)
-        call("wb_linear_cross_entropy", _p(x), _p(w), _p(labels), M, d, V, label_smoothing, _p(loss), _p(lse), _p(ws),
-             ws.numel(), _stream())
+        call("wb_linear_cross_entropy", _a(x), _a(w), _a(labels), M, d, V, label_smoothing, _a(loss), _a(lse), _a(ws),
+             ws.numel(), _raw_stream(x))
     return loss, lse
 
 
@@ -395,8 +408,8 @@ def linear_cross_entropy_backward(dloss, x, w, labels, lse, label_smoothing: flo
         dx = torch.empty_like(x) if need_dx else None
         dw = torch.empty_like(w) if need_dw else None
         ws = _head_workspace(workspace, "wb_linear_cross_entropy_backward_workspace_bytes", x.device, M, d, V)
-        call("wb_linear_cross_entropy_backward", _p(dloss), _p(x), _p(w), _p(labels), _p(lse), M, d, V,
-             label_smoothing, _p(dx), _p(dw), _p(ws), ws.numel(), _stream())
+        call("wb_linear_cross_entropy_backward", _a(dloss), _a(x), _a(w), _a(labels), _a(lse), M, d, V,
+             label_smoothing, _a(dx), _a(dw), _a(ws), ws.numel(), _raw_stream(x))
     return dx, dw
 
 
@@ -409,10 +422,11 @@ def linear_distill(x, w, top, index, temperature: float = 1.0, workspace=None, s
     M, d, V = _head_shape(x, w)
     k, ty = _teacher(top, index, M)
     with _place(stream, x, w, top, index, workspace):
-        loss, lse = torch.empty((2, M), dtype=torch.float32, device=x.device)
+        loss = torch.empty(M, dtype=torch.float32, device=x.device)
+        lse = torch.empty(M, dtype=torch.float32, device=x.device)
         ws = _head_workspace(workspace, "wb_linear_distill_workspace_bytes", x.device, M, d, V, k)
-        call("wb_linear_distill", _p(x), _p(w), _p(top), ty, _p(index), M, d, V, k, temperature, _p(loss), _p(lse),
-             _p(ws), ws.numel(), _stream())
+        call("wb_linear_distill", _a(x), _a(w), _a(top), ty, _a(index), M, d, V, k, temperature, _a(loss), _a(lse),
+             _a(ws), ws.numel(), _raw_stream(x))
     return loss, lse
 
 
@@ -428,8 +442,8 @@ def linear_distill_backward(dloss, x, w, top, index, lse, temperature: float = 1
         dx = torch.empty_like(x) if need_dx else None
         dw = torch.empty_like(w) if need_dw else None
         ws = _head_workspace(workspace, "wb_linear_distill_backward_workspace_bytes", x.device, M, d, V, k)
-        call("wb_linear_distill_backward", _p(dloss), _p(x), _p(w), _p(top), ty, _p(index), _p(lse), M, d, V, k,
-             temperature, _p(dx), _p(dw), _p(ws), ws.numel(), _stream())
+        call("wb_linear_distill_backward", _a(dloss), _a(x), _a(w), _a(top), ty, _a(index), _a(lse), M, d, V, k,
+             temperature, _a(dx), _a(dw), _a(ws), ws.numel(), _raw_stream(x))
     return dx, dw
 
 
