@@ -109,8 +109,8 @@ bool o_map(CUtensorMap* m, const void* base, uint64_t n, uint64_t rows, uint64_t
 const char* const kProfNames[PC_COUNT] = {
     "logmel.prep", "logmel.dft", "logmel.mel", "logmel.post", "stem.prep", "stem.conv1", "stem.conv2",
     "enc.layernorm", "enc.quantize", "enc.qkv", "enc.attention", "enc.out_proj", "enc.fc1", "enc.fc2", "other",
-    "train.layernorm", "train.head_rows", "train.head_lse", "train.head_finish", "train.head_dlogits", "train.head_dx",
-    "train.head_dw"};
+    "train.layernorm", "train.head_rows", "train.head_lse", "train.head_finish", "train.head_dlogits",
+    "train.head_grads"};
 
 struct ProfRec {
   int cls, kernels;

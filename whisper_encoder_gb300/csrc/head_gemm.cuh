@@ -4,55 +4,70 @@
 // matrix w (bf16 [V, d]), logits s = x w^T that are never stored:
 //   HEAD_LSE      s tile by tile -> per row and tile (max, sum 2^(s c - max)) and the targets' logits
 //   HEAD_DLOGITS  s again for a piece of the vocabulary -> D = softmax - target, bf16 [n, piece]
-//   HEAD_DX       D w      for the piece, added to float32 slabs
-//   HEAD_DW       D^T x'   for the piece's rows of dw
+//   HEAD_GRADS    for the piece, in one launch: D w, added to float32 slabs of dx, and D^T x', the
+//                 piece's rows of dw
 // D stays a piece (the workspace bounds it), so memory does not grow with n V; recomputing s costs one
-// of the four products.  All three operands are read where they lie: w and x' as MN-major B tiles,
-// D as an MN-major A tile for dw, so nothing is transposed in memory.
+// of the four products.  All operands are read where they lie: w and x' as MN-major B tiles, D as an
+// MN-major A tile for dw, so nothing is transposed in memory.
 //
-// Roles as in the other GEMMs of this library: warp 0 lane 0 loads a ring of 4 stages with TMA
-// (128 x 64 of A, 64 x 256 of B), warp 1 lane 0 issues the MMAs into one of two 256-column TMEM
-// accumulators, warps 2-17 run the epilogue of the tile before: warp w has TMEM lane quarter w % 4 and
-// 64 of the 256 columns.  Every wait is bounded.  The rows that take part are only known on the
-// device (*n_rows); all roles read them and walk the same tiles.
+// Two forms.  PAIR: two CTAs (a cluster, one SM each) make one tile of 256 rows x up to 256 columns: each
+// loads 128 rows of A and half of B's columns, so that a byte from L2 feeds twice the MMAs.  Single: one
+// CTA, 128 rows.  The pair keeps the tensor cores busier where the operands come from L2 for long
+// (@@); the single form has the finer rows, starts sooner and wins where a product is short.
+// Per CTA, as in the other GEMMs of this library: warp 0 lane 0 loads a ring of stages with TMA; warp 1
+// lane 0 (of the pair's first CTA) issues the MMAs into one of two 256-column TMEM accumulators; warps 2-17
+// run the epilogue of the tile before on their CTA's 128 rows: warp w has TMEM lane quarter w % 4 and a
+// quarter of the columns.  Every wait is bounded.  The rows that take part are only known on the device
+// (*n_rows); all roles read them and walk the same tiles.
 #pragma once
 #include "gemm.cuh"
 
 namespace wb {
 
-enum HeadKind : int { HEAD_LSE, HEAD_DLOGITS, HEAD_DX, HEAD_DW };
+enum HeadKind : int { HEAD_LSE, HEAD_DLOGITS, HEAD_GRADS };
 
-constexpr int HEAD_BM = 128, HEAD_BN = 256, HEAD_BK = 64;
+constexpr int HEAD_BN = 256, HEAD_BK = 64;   // widest tile, elements of k per stage
+constexpr int head_bm(bool pair) { return pair ? 256 : 128; }
 
+template <bool PAIR>
 struct HeadSmem {
-  static constexpr int A_BYTES = HEAD_BM * HEAD_BK * 2;
-  static constexpr int B_BYTES = HEAD_BN * HEAD_BK * 2;
+  static constexpr int A_BYTES = 128 * HEAD_BK * 2;
+  static constexpr int B_BYTES = (PAIR ? HEAD_BN / 2 : HEAD_BN) * HEAD_BK * 2;
   static constexpr int MN_BLOCK = 64 * HEAD_BK * 2;      // 64 M / N elements x 64 k of an MN-major tile
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = 4;
+  static constexpr int STAGES = PAIR ? 6 : 4;
   static constexpr int BOX_BYTES = 32 * 64;              // 32 rows x 64 bytes per epilogue warp (64-byte swizzle)
   static constexpr int OFF_EPI = STAGES * STAGE_BYTES;
   static constexpr int OFF_BAR = OFF_EPI + GEMM_EPI_WARPS * BOX_BYTES;
   static constexpr int TOTAL = 1024 + OFF_BAR + 512;
 };
-static_assert(HeadSmem::TOTAL <= 227 * 1024, "one CTA per SM");
+static_assert(HeadSmem<true>::TOTAL <= 227 * 1024 && HeadSmem<false>::TOTAL <= 227 * 1024, "one CTA per SM");
+
+struct HeadMaps {
+  CUtensorMap a0, a1;        // x (LSE, DLOGITS); D for dx (K-major), D for dw (MN-major)
+  CUtensorMap b0, b1;        // w (K-major); w for dx (MN-major), x' for dw (MN-major)
+  CUtensorMap o0, o1;        // D; slabs of dx, dw
+};
 
 struct HeadParams {
-  const int* n_rows;         // device: rows that take part, at most m_cap
+  const int* n_rows;         // device: rows that take part, at most m_cap; null: all of them
   int m_cap;                 // rows of the call
   int V, d;
   int v0, vc;                // this piece of the vocabulary (LSE: all of it)
+  int bn;                    // columns of a tile, a multiple of 32
   int panel;                 // column tiles walked together (LSE, DLOGITS)
-  int k_splits;              // DX: slabs
-  int first_piece;           // DX: store instead of add
+  int dx_splits;             // GRADS: slabs, 0 without dx
+  int want_dw;
+  int first_piece;           // dx: store instead of add
   float scale_log2;          // log2(e) / temperature
-  // targets of compact row i: entries [src(i) * k, + cnt(src(i))) sorted by index, src = row_src
-  const int* row_src;
-  const int* tgt_idx;
-  const float* tgt_p;        // null: every entry weighs label_p
-  const int* tgt_cnt;        // null: k entries
+  // by row of x: its label (cross entropy), or its source row and the number of its sorted entries
+  const int64_t* labels;     // LSE without compaction: the labels themselves
+  const int* row_tgt;        // null without compaction: the row itself
+  const int* row_cnt;        // null: cross entropy
+  const int* tgt_idx;        // distillation: [source row][k], sorted
+  const float* tgt_p;
   int k;
-  float label_p;
+  float label_p;             // cross entropy: weight of the label
   float smooth;              // what every column's target has on top (label smoothing / V)
   // LSE out
   float2* part;              // [column tile][part_ld]: (max, sum) in log2 units
@@ -60,31 +75,29 @@ struct HeadParams {
   long long part_ld;
   float* tgt_s;              // [row][k]: logits at the targets
   // DLOGITS in
-  const float* lse;          // by source row, natural units
-  // DW
+  const float* row_lse2;     // by compact row, log2 units
+  // dw
   const float* g_scale;      // device scalar that x' was divided by
   float out_scale;
   uint32_t* err;
 };
 
-template <int KIND>
+template <int KIND, bool PAIR>
 __global__ void __launch_bounds__(GEMM_THREADS, 1)
-    head_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
-                     const __grid_constant__ CUtensorMap omap, const __grid_constant__ HeadParams p) {
-  using S = HeadSmem;
+    head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadParams p) {
+  using S = HeadSmem<PAIR>;
+  constexpr int BM = head_bm(PAIR);
   constexpr int STAGES = S::STAGES;
-  constexpr bool A_MN = KIND == HEAD_DW, B_MN = KIND == HEAD_DX || KIND == HEAD_DW;
-  constexpr uint32_t IDESC =
-      make_idesc(HEAD_BM, HEAD_BN, 1u) | (A_MN ? IDESC_A_MN : 0u) | (B_MN ? IDESC_B_MN : 0u);
+  constexpr bool LOGITS = KIND != HEAD_GRADS;
   constexpr uint32_t TMEM_COLS = 2 * HEAD_BN;
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base_u32 = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base_u32 - smem_u32(smem_raw));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);   // [STAGES]
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);   // [STAGES], the first CTA's count both
   uint64_t* empty = full + STAGES;                                   // [STAGES]
   uint64_t* tfull = empty + STAGES;                                  // [2]
-  uint64_t* tempty = tfull + 2;                                      // [2]
+  uint64_t* tempty = tfull + 2;                                      // [2], the first CTA's count both
   uint64_t* red_full = tempty + 2;                                   // [2][4]: LSE partials of a quarter
   uint64_t* mma_done = red_full + 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
@@ -92,6 +105,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 
   const int warp = warp_id();
   const int lane = lane_id();
+  const uint32_t rank = PAIR ? cluster_rank() : 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -99,164 +113,201 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], GEMM_EPI_WARPS);
+      mbar_init(&tempty[a], (PAIR ? 2 : 1) * GEMM_EPI_WARPS);
       for (int q = 0; q < 4; ++q) mbar_init(&red_full[4 * a + q], 3);
     }
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(tmem_slot, TMEM_COLS);
+  if (warp == 1) {
+    if (PAIR) tmem_alloc_pair(tmem_slot, TMEM_COLS);
+    else tmem_alloc(tmem_slot, TMEM_COLS);
+  }
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync();      // the peer's barriers are set up too
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   grid_dependency_wait();
   grid_dependents_launch();
 
-  // ---- tiles: the same walk in every role ----
-  int n = *p.n_rows;
+  // ---- tiles: the same walk in every role of both CTAs ----
+  int n = p.n_rows ? *p.n_rows : p.m_cap;
   n = n < 0 ? 0 : n > p.m_cap ? p.m_cap : n;
-  const int row_tiles = n > 0 ? (n + HEAD_BM - 1) / HEAD_BM : 1;     // with no rows: one tile of zeros
-  const int v_tiles_m = (p.vc + HEAD_BM - 1) / HEAD_BM;
-  const int m_tiles = KIND == HEAD_DW ? v_tiles_m : row_tiles;
-  const int n_tiles = KIND == HEAD_LSE || KIND == HEAD_DLOGITS ? (p.vc + HEAD_BN - 1) / HEAD_BN
-                                                               : (p.d + HEAD_BN - 1) / HEAD_BN;
-  const int kb_all = KIND == HEAD_DX ? (p.vc + HEAD_BK - 1) / HEAD_BK
-                     : KIND == HEAD_DW ? ((n > 0 ? n : 1) + HEAD_BK - 1) / HEAD_BK
-                                       : (p.d + HEAD_BK - 1) / HEAD_BK;
-  const int splits = KIND == HEAD_DX ? p.k_splits : 1;
-  const long long per_split = static_cast<long long>(m_tiles) * n_tiles;
-  const long long total = per_split * splits;
+  const int bn = p.bn;
+  const int row_tiles = n > 0 ? (n + BM - 1) / BM : 1;     // with no rows: one tile of zeros
+  const int n_tiles = ((LOGITS ? p.vc : p.d) + bn - 1) / bn;
+  const int kb_d = (p.d + HEAD_BK - 1) / HEAD_BK, kb_v = (p.vc + HEAD_BK - 1) / HEAD_BK,
+            kb_n = ((n > 0 ? n : 1) + HEAD_BK - 1) / HEAD_BK;
+  const long long dw_tiles = LOGITS || !p.want_dw ? 0 : static_cast<long long>((p.vc + BM - 1) / BM) * n_tiles;
+  const long long dx_tiles = static_cast<long long>(row_tiles) * n_tiles;
+  const long long total = LOGITS ? dx_tiles : dw_tiles + dx_tiles * p.dx_splits;
   struct Tile {
     int mt, nt, split, kb0, kb1;
+    bool dw;
   };
   auto tile_at = [&](long long t) -> Tile {
     Tile r;
-    if (KIND == HEAD_LSE || KIND == HEAD_DLOGITS) {
+    r.split = 0;
+    r.kb0 = 0;
+    r.dw = false;
+    if (LOGITS) {
       // panels of column tiles, all rows through each: a panel of w is read once from memory and the
       // rows again from L2 (they are the smaller side)
-      const long long per_panel = static_cast<long long>(m_tiles) * p.panel;
+      const long long per_panel = static_cast<long long>(row_tiles) * p.panel;
       const int pn = static_cast<int>(t / per_panel);
       const long long q = t - pn * per_panel;
       const int left = n_tiles - pn * p.panel;
       const int w = left < p.panel ? left : p.panel;
       r.mt = static_cast<int>(q / w);
       r.nt = pn * p.panel + static_cast<int>(q % w);
-      r.split = 0;
+      r.kb1 = kb_d;
+    } else if (t < dw_tiles) {
+      r.dw = true;
+      r.mt = static_cast<int>(t / n_tiles);
+      r.nt = static_cast<int>(t % n_tiles);
+      r.kb1 = kb_n;
     } else {
-      r.split = static_cast<int>(t / per_split);
-      const long long q = t - r.split * per_split;
+      const long long u = t - dw_tiles;
+      r.split = static_cast<int>(u / dx_tiles);
+      const long long q = u - r.split * dx_tiles;
       r.mt = static_cast<int>(q / n_tiles);
       r.nt = static_cast<int>(q % n_tiles);
+      r.kb0 = static_cast<int>(static_cast<long long>(kb_v) * r.split / p.dx_splits);
+      r.kb1 = static_cast<int>(static_cast<long long>(kb_v) * (r.split + 1) / p.dx_splits);
     }
-    r.kb0 = static_cast<int>(static_cast<long long>(kb_all) * r.split / splits);
-    r.kb1 = static_cast<int>(static_cast<long long>(kb_all) * (r.split + 1) / splits);
     return r;
   };
+  const long long t_first = PAIR ? blockIdx.x >> 1 : blockIdx.x, t_step = PAIR ? gridDim.x >> 1 : gridDim.x;
 
   if (warp == 0) {
     // ------------------------------ TMA producer ---------------------------
     if (lane == 0) {
-      tma_prefetch_desc(&amap);
-      tma_prefetch_desc(&bmap);
       int stage = 0;
-      uint32_t phase = 0, issued_mask = 0, last_parity = 0;
+      uint32_t phase = 0;
       bool ok = true;
-      for (long long t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const int half = PAIR ? bn / 2 : bn;         // this CTA's columns of B
+      const int mn_loads = (half + 63) / 64;
+      const uint32_t b_bytes = LOGITS ? half * 128 : mn_loads * S::MN_BLOCK;
+      auto load = [&](uint8_t* dst, const CUtensorMap* m, int stg, int c0, int c1) {
+        if (PAIR) tma_load_2d_pair(dst, m, cluster_addr(&full[stg], 0), c0, c1);
+        else tma_load_2d(dst, m, &full[stg], c0, c1);
+      };
+      for (long long t = t_first; t < total && ok; t += t_step) {
         const Tile tl = tile_at(t);
+        const int row0 = tl.mt * BM + static_cast<int>(rank) * (128);
+        const int col0 = tl.nt * bn + static_cast<int>(rank) * half;
         for (int kb = tl.kb0; kb < tl.kb1; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, p.err, abort_flag, 24)) { ok = false; break; }
-          mbar_arrive_expect_tx(&full[stage], S::STAGE_BYTES);
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * (S::A_BYTES + b_bytes));
           uint8_t* sa = smem + stage * S::STAGE_BYTES;
           uint8_t* sb = sa + S::A_BYTES;
-          if constexpr (A_MN) {
-            for (int j = 0; j < HEAD_BM / 64; ++j)
-              tma_load_2d(sa + j * S::MN_BLOCK, &amap, &full[stage], tl.mt * HEAD_BM + 64 * j, kb * HEAD_BK);
+          if (LOGITS) {
+            load(sa, &maps.a0, stage, kb * HEAD_BK, row0);
+            load(sb, &maps.b0, stage, kb * HEAD_BK, p.v0 + col0);
+          } else if (tl.dw) {
+            for (int j = 0; j < 2; ++j)
+              load(sa + j * S::MN_BLOCK, &maps.a1, stage, row0 + 64 * j, kb * HEAD_BK);
+            for (int j = 0; j < mn_loads; ++j)
+              load(sb + j * S::MN_BLOCK, &maps.b1, stage, col0 + 64 * j, kb * HEAD_BK);
           } else {
-            tma_load_2d(sa, &amap, &full[stage], kb * HEAD_BK, tl.mt * HEAD_BM);
+            load(sa, &maps.a0, stage, kb * HEAD_BK, row0);
+            for (int j = 0; j < mn_loads; ++j)
+              load(sb + j * S::MN_BLOCK, &maps.b0, stage, col0 + 64 * j, p.v0 + kb * HEAD_BK);
           }
-          if constexpr (B_MN) {
-            const int k_row = kb * HEAD_BK + (KIND == HEAD_DX ? p.v0 : 0);
-            for (int j = 0; j < HEAD_BN / 64; ++j)
-              tma_load_2d(sb + j * S::MN_BLOCK, &bmap, &full[stage], tl.nt * HEAD_BN + 64 * j, k_row);
-          } else {
-            tma_load_2d(sb, &bmap, &full[stage], kb * HEAD_BK, p.v0 + tl.nt * HEAD_BN);
-          }
-          issued_mask |= 1u << stage;
-          last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
-      if (!ok) {  // let every copy already in flight land before the CTA exits
-        for (int s = 0; s < STAGES; ++s)
-          if (issued_mask & (1u << s)) mbar_drain(&full[s], (last_parity >> s) & 1u);
+      if (!ok) {  // copies already in flight land long before this (their barrier may never be counted out)
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 10000000ull) {
+        }
       }
     }
   } else if (warp == 1) {
     // ------------------------------ MMA issuer -----------------------------
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
       int local = 0;
-      for (long long t = blockIdx.x; t < total && ok; t += gridDim.x, ++local) {
+      auto commit = [&](uint64_t* bar) {
+        if (PAIR) mma_commit_pair(bar);
+        else mma_commit(bar);
+      };
+      const uint32_t idesc0 = make_idesc(BM, bn, 1u) | (LOGITS ? 0u : IDESC_B_MN);
+      for (long long t = t_first; t < total && ok; t += t_step, ++local) {
         const Tile tl = tile_at(t);
         const int acc = local & 1;
         if (!mbar_wait(&tempty[acc], ((local >> 1) & 1) ^ 1u, p.err, abort_flag, 25)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * HEAD_BN;
+        const uint32_t idesc = idesc0 | (tl.dw ? IDESC_A_MN : 0u);
         for (int kb = tl.kb0; kb < tl.kb1; ++kb) {
           if (!mbar_wait(&full[stage], phase, p.err, abort_flag, 26)) { ok = false; break; }
           tc_fence_after();
           const uint32_t sa = smem_u32(smem + stage * S::STAGE_BYTES);
           const uint32_t sb = sa + S::A_BYTES;
+          // a descriptor advances by the byte offset / 16 (addresses stay below 256 KB): K-major 32 bytes a
+          // K16 step, MN-major 2048
+          const uint64_t ad = tl.dw ? sw128_mn_desc(sa, S::MN_BLOCK) : sw128_desc(sa);
+          const uint64_t bd = LOGITS ? sw128_desc(sb) : sw128_mn_desc(sb, S::MN_BLOCK);
+          const uint64_t a_step = tl.dw ? 128 : 2;
+          constexpr uint64_t b_step = LOGITS ? 2 : 128;
 #pragma unroll
-          for (int k = 0; k < HEAD_BK / 16; ++k) {
-            const uint64_t ad = A_MN ? sw128_mn_desc(sa + k * 2048, S::MN_BLOCK) : sw128_desc(sa + k * 32);
-            const uint64_t bd = B_MN ? sw128_mn_desc(sb + k * 2048, S::MN_BLOCK) : sw128_desc(sb + k * 32);
-            mma_bf16(d_tmem, ad, bd, IDESC, kb != tl.kb0 || k != 0);
-          }
-          mma_commit(&empty[stage]);
+          for (int k = 0; k < HEAD_BK / 16; ++k)
+            if (PAIR) mma_bf16_pair(d_tmem, ad + k * a_step, bd + k * b_step, idesc, kb != tl.kb0 || k != 0);
+            else mma_bf16(d_tmem, ad + k * a_step, bd + k * b_step, idesc, kb != tl.kb0 || k != 0);
+          commit(&empty[stage]);
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
-        if (ok) mma_commit(&tfull[acc]);
+        if (ok) commit(&tfull[acc]);
       }
-      mma_commit(mma_done);     // no MMA reads smem or writes TMEM any more when the CTA leaves
-      mbar_drain(mma_done, 0);
+      commit(mma_done);
     }
   } else {
     // ------------------------------- epilogue ------------------------------
-    constexpr int COLS = HEAD_BN / 4;
     const int ew = warp - 2;
     const int quarter = warp & 3;                // TMEM lane quarter this warp may access
     const int cg = ew >> 2;                      // column group
+    const int ch0 = bn / 32 * cg / 4, ch1 = bn / 32 * (cg + 1) / 4;   // its chunks of 32 columns: 0 to 2
     uint8_t* box = smem + S::OFF_EPI + ew * S::BOX_BYTES;
-    // LSE: (max, sum, plain sum) of this warp's 64 columns for the quarter's first warp, two tiles deep
+    // LSE: (max, sum, plain sum) of a warp's columns for the quarter's first warp, two tiles deep
     float* red = reinterpret_cast<float*>(smem + S::OFF_EPI);        // [2][4 quarters][3][4 groups][32]
+    auto release = [&](int a) {                  // one lane a warp: this warp has read accumulator a
+      if (PAIR) mbar_arrive_cluster(cluster_addr(&tempty[a], 0));
+      else mbar_arrive(&tempty[a]);
+    };
     const float c = p.scale_log2;
-    const float g_out = KIND == HEAD_DW ? *p.g_scale * p.out_scale : 1.0f;
+    const float g_out = KIND == HEAD_GRADS && p.want_dw ? *p.g_scale * p.out_scale : 1.0f;
     bool ok = true;
     int local = 0;
-    for (long long t = blockIdx.x; t < total && ok; t += gridDim.x, ++local) {
+    for (long long t = t_first; t < total && ok; t += t_step, ++local) {
       const Tile tl = tile_at(t);
       const int acc = local & 1;
       const uint32_t acc_phase = (local >> 1) & 1;
-      const int m0 = tl.mt * HEAD_BM + quarter * 32;   // first row of this warp's slab
+      const int m0 = tl.mt * BM + static_cast<int>(rank) * (128) + quarter * 32;   // first row of this warp
       const int m = m0 + lane;
       const bool row_ok = m < n;
-      const int ncol0 = tl.nt * HEAD_BN + cg * COLS;   // first column inside the piece / the width
+      const int ncol0 = tl.nt * bn + ch0 * 32;         // first column inside the piece / the width
       // the row's next target at or after this warp's first column, found while the MMAs run
       const int lo = p.v0 + ncol0;
-      int pos = 0, cnt = 0, next = 0x7fffffff, src = 0;
+      int pos = 0, cnt = 0, next = 0x7fffffff;
       long long tb = 0;
       float lse2 = 0.0f, smooth = 0.0f;
-      if ((KIND == HEAD_LSE || KIND == HEAD_DLOGITS) && row_ok &&
-          in_bounds(p.err, m, 1, p.m_cap, SITE_HEAD_ROWS)) {
-        src = p.row_src[m];
-        if (in_bounds(p.err, src, 1, p.m_cap, SITE_HEAD_ROWS)) {
-          tb = static_cast<long long>(src) * p.k;
-          cnt = p.tgt_cnt ? p.tgt_cnt[src] : p.k;
+      if (LOGITS && row_ok && in_bounds(p.err, m, 1, p.m_cap, SITE_HEAD_ROWS)) {
+        if (KIND == HEAD_DLOGITS) {
+          lse2 = p.row_lse2[m];
+          smooth = p.smooth;
+        }
+        const long long tl64 = p.labels ? p.labels[m] : p.row_tgt ? p.row_tgt[m] : m;
+        const int tgt = tl64 < 0 || tl64 > 0x7ffffffe ? -1 : static_cast<int>(tl64);
+        if (!p.row_cnt) {
+          if (tgt >= lo && tgt < p.V) next = tgt;
+        } else if (in_bounds(p.err, tgt, 1, p.m_cap, SITE_HEAD_ROWS)) {
+          tb = static_cast<long long>(tgt) * p.k;
+          cnt = max(p.row_cnt[m], 0);
           int hi = cnt;
           while (pos < hi) {
             const int mid = (pos + hi) >> 1;
@@ -264,37 +315,30 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             else hi = mid;
           }
           if (pos < cnt) next = p.tgt_idx[tb + pos];
-          if (KIND == HEAD_DLOGITS) {
-            lse2 = p.lse[src] * 1.4426950408889634f;
-            smooth = p.smooth;
-          }
         }
       }
       if (!mbar_wait(&tfull[acc], acc_phase, p.err, abort_flag, 27)) { ok = false; break; }
       tc_fence_after();
-      const uint32_t t_cols = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * HEAD_BN + cg * COLS;
+      const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * HEAD_BN;
 
       if constexpr (KIND == HEAD_LSE) {
         float mx = -INFINITY, l = 0.0f, sum = 0.0f;
-#pragma unroll
-        for (int ch = 0; ch < COLS / 32; ++ch) {
-          const int n0 = ncol0 + ch * 32;
-          if (n0 >= p.vc) continue;
+        for (int ch = ch0; ch < ch1; ++ch) {
+          const int n0 = tl.nt * bn + ch * 32;
+          if (n0 >= p.vc) break;
           float v[32];
-          tmem_ld32(t_cols + ch * 32, v);
+          tmem_ld32(t_row + ch * 32, v);
           tmem_ld_wait();
           // targets in these 32 columns are rare: one column at a time, read again for all lanes
-          const int end = lo + (ch + 1) * 32;
           while (true) {
-            const unsigned pend = __ballot_sync(0xffffffffu, next < end);
+            const unsigned pend = __ballot_sync(0xffffffffu, next < n0 + 32);
             if (!pend) break;
-            const int col = __shfl_sync(0xffffffffu, next, __ffs(pend) - 1) - lo;
-            const float s = tmem_ld1(t_cols + col);
+            const int col = __shfl_sync(0xffffffffu, next, __ffs(pend) - 1) - n0;
+            const float s = tmem_ld1(t_row + ch * 32 + col);
             tmem_ld_wait();
-            if (next - lo == col) {
-              if (in_bounds(p.err, static_cast<long long>(m) * p.k + pos, 1, static_cast<long long>(p.m_cap) * p.k,
-                            SITE_HEAD_TARGET))
-                p.tgt_s[static_cast<long long>(m) * p.k + pos] = s;
+            if (next - n0 == col) {
+              const long long ti = static_cast<long long>(m) * p.k + pos;
+              if (in_bounds(p.err, ti, 1, static_cast<long long>(p.m_cap) * p.k, SITE_HEAD_TARGET)) p.tgt_s[ti] = s;
               ++pos;
               next = pos < cnt ? p.tgt_idx[tb + pos] : 0x7fffffff;
             }
@@ -337,7 +381,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&red_full[4 * acc + quarter]);
-            mbar_arrive(&tempty[acc]);
+            release(acc);
           }
         } else {
           if (!__all_sync(0xffffffffu, mbar_wait(&red_full[4 * acc + quarter], acc_phase, p.err, abort_flag, 28))) {
@@ -357,7 +401,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
           // the accumulator goes back only now: the tile after next then finds the exchange area read
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&tempty[acc]);
+          if (lane == 0) release(acc);
           const long long pi = static_cast<long long>(tl.nt) * p.part_ld + m;
           if (row_ok && in_bounds(p.err, pi, 1, static_cast<long long>(n_tiles) * p.part_ld, SITE_HEAD_PART)) {
             p.part[pi] = make_float2(mm, l);
@@ -365,18 +409,17 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
           }
         }
       } else {
-#pragma unroll
-        for (int ch = 0; ch < COLS / 32; ++ch) {
-          const int n0 = ncol0 + ch * 32;
+        for (int ch = ch0; ch < ch1; ++ch) {
+          const int n0 = tl.nt * bn + ch * 32;
           float v[32];
-          tmem_ld32(t_cols + ch * 32, v);
+          tmem_ld32(t_row + ch * 32, v);
           tmem_ld_wait();
-          if (ch == COLS / 32 - 1) {
+          if (ch == ch1 - 1) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&tempty[acc]);
+            if (lane == 0) release(acc);
           }
-          if constexpr (KIND == HEAD_DX) {
+          if (KIND == HEAD_GRADS && !tl.dw) {
             if (n0 >= p.d || m0 >= p.m_cap) continue;
             if (tl.kb0 == tl.kb1) {          // a short last piece can leave a split without any k
 #pragma unroll
@@ -394,61 +437,66 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
               fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0) {
-                if (p.first_piece) tma_store_3d(&omap, box, n0 + 16 * hf, m0, tl.split);
-                else tma_reduce_add_3d(&omap, box, n0 + 16 * hf, m0, tl.split);
+                if (p.first_piece) tma_store_3d(&maps.o0, box, n0 + 16 * hf, m0, tl.split);
+                else tma_reduce_add_3d(&maps.o0, box, n0 + 16 * hf, m0, tl.split);
                 bulk_commit();
               }
             }
-          } else {
-            if constexpr (KIND == HEAD_DLOGITS) {
-              const uint64_t c2 = f32x2_pack(c, c), l2 = f32x2_pack(-lse2, -lse2);
+            continue;
+          }
+          if constexpr (KIND == HEAD_DLOGITS) {
+            const uint64_t c2 = f32x2_pack(c, c), l2 = f32x2_pack(-lse2, -lse2);
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                float a, b;
-                fma_f32x2(a, b, v[i], v[i + 1], c2, l2);
-                v[i] = ex2_approx(a) - smooth;
-                v[i + 1] = ex2_approx(b) - smooth;
-              }
-              const int end = lo + (ch + 1) * 32;
-              while (__any_sync(0xffffffffu, next < end)) {
-                if (next < end) {
-                  const int col = next - lo - ch * 32;
-                  const float pt = p.tgt_p ? p.tgt_p[tb + pos] : p.label_p;
-#pragma unroll
-                  for (int i = 0; i < 32; ++i)
-                    if (i == col) v[i] -= pt;
-                  ++pos;
-                  next = pos < cnt ? p.tgt_idx[tb + pos] : 0x7fffffff;
-                }
-              }
-              // rows and columns outside are zeros: they are factors of the products that follow
-              if (!row_ok || p.v0 + n0 + 32 > p.V) {
+            for (int i = 0; i < 32; i += 2) {
+              float a, b;
+              fma_f32x2(a, b, v[i], v[i + 1], c2, l2);
+              v[i] = ex2_approx(a) - smooth;
+              v[i + 1] = ex2_approx(b) - smooth;
+            }
+            const int end = p.v0 + n0 + 32;
+            while (__any_sync(0xffffffffu, next < end)) {
+              if (next < end) {
+                const int col = next - (end - 32);
+                const float pt = p.tgt_p ? p.tgt_p[tb + pos] : p.label_p;
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                  if (!row_ok || p.v0 + n0 + i >= p.V) v[i] = 0.0f;
+                  if (i == col) v[i] -= pt;
+                ++pos;
+                next = pos < cnt ? p.tgt_idx[tb + pos] : 0x7fffffff;
               }
-              if (m0 >= p.m_cap) continue;
-            } else {                                        // HEAD_DW
-              if (n0 >= p.d || p.v0 + m0 >= p.V) continue;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] *= g_out;
             }
-            uint32_t pk[16];
+            // rows and columns outside are zeros: they are factors of the products that follow
+            if (!row_ok || end > p.V) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) pk[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-            if (lane == 0) bulk_wait_read0();       // the previous store has read the staging box
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<uint4*>(box + box_off(lane, j)) =
-                  make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_2d(&omap, box, n0, (KIND == HEAD_DW ? p.v0 : 0) + m0);
-              bulk_commit();
+              for (int i = 0; i < 32; ++i)
+                if (!row_ok || p.v0 + n0 + i >= p.V) v[i] = 0.0f;
             }
+            if (m0 >= p.m_cap) continue;
+          } else {                                        // dw
+            if (n0 >= p.d || p.v0 + m0 >= p.V) continue;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] *= g_out;
           }
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) pk[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+          if (lane == 0) bulk_wait_read0();       // the previous store has read the staging box
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(box + box_off(lane, j)) =
+                make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (KIND == HEAD_DLOGITS) tma_store_2d(&maps.o0, box, n0, m0);
+            else tma_store_2d(&maps.o1, box, n0, p.v0 + m0);
+            bulk_commit();
+          }
+        }
+        if (ch0 == ch1) {                         // a narrow tile: no column for this warp
+          __syncwarp();
+          if (lane == 0) release(acc);
         }
       }
     }
@@ -457,8 +505,16 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 
   tc_fence_before();
   __syncthreads();
+  // every MMA is done and has signalled this CTA's barriers (they signal in order); then the peer's
+  // arrivals here are over too
+  if (threadIdx.x == 32) mbar_drain(mma_done, 0);
+  __syncthreads();
+  if (PAIR) cluster_sync();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem_base, TMEM_COLS);
+  if (warp == 1) {
+    if (PAIR) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    else tmem_dealloc(tmem_base, TMEM_COLS);
+  }
 }
 
 }  // namespace wb

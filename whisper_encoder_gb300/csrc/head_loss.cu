@@ -13,6 +13,7 @@
 // two gradient products; |D| <= 1, and dloss stays outside of it (applied to the float32 sums of dx,
 // and to x' = dloss / max|dloss| x for dw, exactly 1 where all dloss are equal), so that one rounding of
 // dloss is not shared by all of a row's or all of dw's entries.
+#include <cstring>
 #include <mutex>
 
 #include "../../include/wb.h"
@@ -24,7 +25,9 @@ namespace {
 
 constexpr int HEAD_MAX_K = 1024;
 constexpr int ROWS_THREADS = 256;
-constexpr int FIN_ROWS = 32, FIN_SLICES = 16;
+constexpr int FIN_ROWS = 32, FIN_SLICES = 32;
+constexpr int HEAD_SMS = 152;    // sizes of workspaces do not depend on the device that asks
+constexpr int OWN_MAX_ROWS = 2048;   // up to here each block of rows_kernel finds max |dloss| itself
 
 // ---------------------------------------------------------------------------
 // Teacher entries of one row per block: softmax of the stored logits at the temperature, equal indices
@@ -132,30 +135,37 @@ struct RowsArgs {
   const __nv_bfloat16* x;
   __nv_bfloat16* xc;         // compacted
   int* row_src;
+  int* row_tgt;              // by compact row: its label (cross entropy); distillation reads row_src and row_cnt
+  int* row_cnt;
+  float* row_lse2;           // by compact row: lse in log2 units (backward)
   int* n_rows;
-  int* label32;              // by source row (cross entropy)
   // forward: what the rows without a target get
   float* loss;
   float* lse;
   // backward
   const float* dloss;
-  const float* g_max;
+  const float* lse_in;
+  float* g_max;              // max |dloss|: found by dloss_max_kernel before, or (own_max) by each block here
+  int own_max;
   __nv_bfloat16* xs;         // compacted x' (null: not wanted)
   __nv_bfloat16* dx;         // rows without a target: zeros (null: not wanted)
   uint32_t* err;
 };
 
-__device__ __forceinline__ int row_state(const RowsArgs& a, int i) {   // 1 takes part, 0 not, -1 a mistake
-  if (a.labels) {
-    const long long v = a.labels[i];
-    return v < 0 ? 0 : v < a.V ? 1 : -1;
+// 1: row i takes part, 0: it does not, -1: its target is a mistake.
+__device__ __forceinline__ int target_state(const int64_t* labels, const int* cnt, int V, int i) {
+  if (labels) {
+    const long long v = labels[i];
+    return v < 0 ? 0 : v < V ? 1 : -1;
   }
-  const int c = a.cnt[i];
+  const int c = cnt[i];
   return c > 0 ? 1 : c == 0 ? 0 : -1;
 }
+__device__ __forceinline__ int row_state(const RowsArgs& a, int i) { return target_state(a.labels, a.cnt, a.V, i); }
 
 __global__ void __launch_bounds__(ROWS_THREADS) rows_kernel(const __grid_constant__ RowsArgs a) {
   __shared__ int warp_sum[ROWS_THREADS / 32];
+  __shared__ float warp_max[ROWS_THREADS / 32];
   __shared__ int at[ROWS_THREADS];           // compact index of the block's rows, or -1 / -2
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dependency_wait();
@@ -188,16 +198,34 @@ __global__ void __launch_bounds__(ROWS_THREADS) rows_kernel(const __grid_constan
   off += __popc(ball & ((1u << lane) - 1u));
   if (row < r1) {
     at[threadIdx.x] = st == 1 ? off : -1;
-    if (st == 1 && in_bounds(a.err, off, 1, a.M, SITE_HEAD_ROWS)) a.row_src[off] = row;
-    if (a.labels && a.label32) a.label32[row] = st == 1 ? static_cast<int>(a.labels[row]) : -1;
+    if (st == 1 && in_bounds(a.err, off, 1, a.M, SITE_HEAD_ROWS)) {
+      a.row_src[off] = row;
+      if (a.labels) a.row_tgt[off] = static_cast<int>(a.labels[row]);
+      else a.row_cnt[off] = a.cnt[row];
+      if (a.lse_in) a.row_lse2[off] = a.lse_in[row] * 1.4426950408889634f;
+    }
     if (st != 1 && a.loss) {
       a.loss[row] = st == 0 ? 0.0f : __int_as_float(0x7fc00000);
       a.lse[row] = 0.0f;
     }
   }
   if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) *a.n_rows = all;
+  float g = 0.0f;
+  if (a.xs && a.own_max) {
+    for (int i = threadIdx.x; i < a.M; i += ROWS_THREADS)
+      if (row_state(a, i) == 1) g = fmaxf(g, fabsf(a.dloss[i]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+    if (lane == 0) warp_max[warp] = g;
+  }
   __syncthreads();
-  const float g = a.xs ? *a.g_max : 0.0f;
+  if (a.xs && a.own_max) {
+#pragma unroll
+    for (int w = 0; w < ROWS_THREADS / 32; ++w) g = fmaxf(g, warp_max[w]);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.g_max = g;
+  } else if (a.xs) {
+    g = *a.g_max;
+  }
   const int nv = a.d / 8;
   const long long n_el = static_cast<long long>(a.M) * a.d;
   for (int i = r0 + warp; i < r1; i += ROWS_THREADS / 32) {
@@ -256,11 +284,12 @@ __global__ void __launch_bounds__(1024) dloss_max_kernel(const __grid_constant__
 }
 
 // ---------------------------------------------------------------------------
-// Row losses from the tiles' (max, sum): 32 rows a block, 16 interleaved slices of the column tiles.
+// Row losses from the tiles' (max, sum): 32 rows a block, 32 interleaved slices of the column tiles.
 // ---------------------------------------------------------------------------
 struct FinishArgs {
-  const int* n_rows;
+  const int* n_rows;         // null (with row_src): every row of the call, those without a target too
   const int* row_src;
+  const int64_t* labels;     // cross entropy, where every row is there
   int M, V, n_tiles, k;
   const float2* part;
   const float* part_sum;
@@ -280,13 +309,13 @@ __global__ void __launch_bounds__(FIN_ROWS* FIN_SLICES) head_finish_kernel(const
   const int rx = threadIdx.x & 31, sl = threadIdx.x >> 5;
   grid_dependency_wait();
   grid_dependents_launch();
-  const int n = min(max(*a.n_rows, 0), a.M);
+  const int n = a.n_rows ? min(max(*a.n_rows, 0), a.M) : a.M;
   for (int r0 = blockIdx.x * FIN_ROWS; r0 < n; r0 += gridDim.x * FIN_ROWS) {
     const int row = r0 + rx;
     const bool on = row < n;
     float m = -INFINITY, l = 0.0f, s = 0.0f;
     if (on) {
-#pragma unroll 4
+#pragma unroll 8
       for (int t = sl; t < a.n_tiles; t += FIN_SLICES) {
         const long long i = static_cast<long long>(t) * a.part_ld + row;
         if (!in_bounds(a.err, i, 1, static_cast<long long>(a.n_tiles) * a.part_ld, SITE_HEAD_PART)) continue;
@@ -314,10 +343,14 @@ __global__ void __launch_bounds__(FIN_ROWS* FIN_SLICES) head_finish_kernel(const
       }
       const float lse = fmaf(mo, 0.69314718055994531f, logf(l));
       row_lse[rx] = lse;
-      const int src = in_bounds(a.err, row, 1, a.M, SITE_HEAD_ROWS) ? a.row_src[row] : 0;
+      const int src = !a.row_src ? row : in_bounds(a.err, row, 1, a.M, SITE_HEAD_ROWS) ? a.row_src[row] : 0;
       if (in_bounds(a.err, src, 1, a.M, SITE_HEAD_ROWS)) {
-        a.lse[src] = lse;
-        if (!a.tgt_p) {
+        int state = 1;                       // as row_state
+        if (!a.row_src) state = target_state(a.labels, a.tgt_cnt, a.V, src);
+        a.lse[src] = state == 1 ? lse : 0.0f;
+        if (state != 1) {
+          a.loss[src] = state == 0 ? 0.0f : __int_as_float(0x7fc00000);
+        } else if (!a.tgt_p) {
           const float sy = a.tgt_s[row];
           a.loss[src] = a.smoothing > 0.0f
                             ? (1.0f - a.smoothing) * (lse - sy) + a.smoothing * (lse - s / static_cast<float>(a.V))
@@ -328,10 +361,11 @@ __global__ void __launch_bounds__(FIN_ROWS* FIN_SLICES) head_finish_kernel(const
     __syncthreads();
     if (a.tgt_p) {       // distillation: a warp per row over its entries
       for (int r = sl; r < FIN_ROWS && r0 + r < n; r += FIN_SLICES) {
-        const int src = a.row_src[r0 + r];
+        const int src = a.row_src ? a.row_src[r0 + r] : r0 + r;
         if (!in_bounds(a.err, src, 1, a.M, SITE_HEAD_ROWS)) continue;
         const float lse = row_lse[r];
         const int cnt = a.tgt_cnt[src];
+        if (cnt <= 0) continue;
         float t = 0.0f;
         for (int j = rx; j < cnt; j += 32) {
           const long long i = static_cast<long long>(src) * a.k + j, is = static_cast<long long>(r0 + r) * a.k + j;
@@ -348,31 +382,50 @@ __global__ void __launch_bounds__(FIN_ROWS* FIN_SLICES) head_finish_kernel(const
   }
 }
 
-// dx of the rows that take part: the slabs' sum times T dloss, rounded once.
+// dx of the rows that take part: the slabs' sum times T dloss, rounded once.  `lanes` (1 to 8) threads
+// share a vector of 8 columns, each adding every lanes-th slab; their sums are added in order.
 __global__ void __launch_bounds__(256)
-    head_dx_kernel(const int* __restrict__ n_rows, const int* __restrict__ row_src, int M, int d, int splits,
+    head_dx_kernel(const int* __restrict__ n_rows, const int* __restrict__ row_src, int M, int d, int splits, int lanes,
                    const float* __restrict__ slab, const float* __restrict__ dloss, float temperature,
                    __nv_bfloat16* __restrict__ dx, uint32_t* err) {
+  __shared__ float sm[256][8];
   grid_dependency_wait();
   grid_dependents_launch();
   const int n = min(max(*n_rows, 0), M);
-  const int nv = d / 8;
+  const int nv = d / 8, per_block = 256 / lanes;
   const long long per_slab = static_cast<long long>(M) * d;
   const long long work = static_cast<long long>(n) * nv;
-  for (long long w = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; w < work;
-       w += static_cast<long long>(gridDim.x) * 256) {
-    const int row = static_cast<int>(w / nv), v = static_cast<int>(w % nv);
+  const int vx = threadIdx.x % per_block, sl = threadIdx.x / per_block;
+  for (long long w0 = static_cast<long long>(blockIdx.x) * per_block; w0 < work;
+       w0 += static_cast<long long>(gridDim.x) * per_block) {
+    const long long w = w0 + vx;
+    const bool on = w < work;
+    const int row = on ? static_cast<int>(w / nv) : 0, v = on ? static_cast<int>(w % nv) : 0;
+    float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (on) {
+#pragma unroll 4
+      for (int q = sl; q < splits; q += lanes) {
+        const long long i = q * per_slab + static_cast<long long>(row) * d + 8 * v;
+        if (!in_bounds(err, i, 8, splits * per_slab, SITE_HEAD_SLAB)) continue;
+        const float4 a = *reinterpret_cast<const float4*>(slab + i), b = *reinterpret_cast<const float4*>(slab + i + 4);
+        s[0] += a.x; s[1] += a.y; s[2] += a.z; s[3] += a.w;
+        s[4] += b.x; s[5] += b.y; s[6] += b.z; s[7] += b.w;
+      }
+    }
+    if (lanes > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sm[threadIdx.x][j] = s[j];
+      __syncthreads();
+      if (sl != 0) continue;
+      for (int q = 1; q < lanes; ++q)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] += sm[q * per_block + vx][j];
+    }
+    if (!on) continue;
     const int src = row_src[row];
     if (!in_bounds(err, src, 1, M, SITE_HEAD_ROWS)) continue;
     const float f = dloss[src] * temperature;
-    float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int q = 0; q < splits; ++q) {
-      const long long i = q * per_slab + static_cast<long long>(row) * d + 8 * v;
-      if (!in_bounds(err, i, 8, splits * per_slab, SITE_HEAD_SLAB)) continue;
-      const float4 a = *reinterpret_cast<const float4*>(slab + i), b = *reinterpret_cast<const float4*>(slab + i + 4);
-      s[0] += a.x; s[1] += a.y; s[2] += a.z; s[3] += a.w;
-      s[4] += b.x; s[5] += b.y; s[6] += b.z; s[7] += b.w;
-    }
     const long long o = static_cast<long long>(src) * d + 8 * v;
     if (in_bounds(err, o, 8, per_slab, SITE_HEAD_DX))
       *reinterpret_cast<uint4*>(dx + o) = make_uint4(pack_bf16(s[0] * f, s[1] * f), pack_bf16(s[2] * f, s[3] * f),
@@ -381,21 +434,52 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------ host side ------------------------------
-constexpr int kSms = 152;      // sizes of workspaces do not depend on the device that asks
+int ceil_div(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
 
 struct HeadShape {
   int M, d, V, k;              // k = 0: cross entropy
-  int n_tiles() const { return (V + HEAD_BN - 1) / HEAD_BN; }
   int entries() const { return k > 0 ? k : 1; }
+  // the pair form of the products (@@)
+  bool pair() const { return M > 2048; }
+  int bm() const { return head_bm(pair()); }
+  int slots() const { return pair() ? HEAD_SMS / 2 : HEAD_SMS; }   // tiles at a time
+  int row_tiles() const { return ceil_div(M, bm()); }
+  // one tile of rows: taking out rows saves no product, so the forward pass reads x as it is
+  bool direct() const { return M <= 128; }
 };
 
 bool shape_ok(int M, int d, int V) {
   return M >= 0 && M <= (1 << 24) && d >= 8 && d <= (1 << 16) && d % 8 == 0 && V >= 1 && V <= (1 << 24);
 }
 
+// Column-tile width of the forward product: the one whose rounds of tiles over the device end first, a
+// tile costing its columns and about 24 more (its fill and drain).  Measured at one row against
+// 51866 x 1280: @@
+int lse_width(const HeadShape& h) {
+  int best = HEAD_BN;
+  long long cost = -1;
+  for (int bn = HEAD_BN; bn >= 64; bn -= 32) {
+    const long long tiles = static_cast<long long>(h.row_tiles()) * ceil_div(h.V, bn);
+    const long long c = (tiles + h.slots() - 1) / h.slots() * (bn + 24);
+    if (cost < 0 || c < cost) {
+      cost = c;
+      best = bn;
+    }
+  }
+  return best;
+}
+
+// Column-tile width of the gradient products: the fewest columns past d (384 = 2 x 192).
+int grad_width(int d) {
+  int best = HEAD_BN;
+  for (int bn = HEAD_BN; bn >= 128; bn -= 32)
+    if (ceil_div(d, bn) * bn < ceil_div(d, best) * best) best = bn;
+  return best;
+}
+
 // Targets and row map, shared by both passes.
 struct RowsLayout {
-  size_t n_rows, row_src, label32, idx, p, cnt, xc;
+  size_t n_rows, row_src, row_tgt, row_cnt, row_lse2, idx, p, cnt, xc;
 };
 
 RowsLayout rows_layout(Carver& c, const HeadShape& h) {
@@ -403,13 +487,15 @@ RowsLayout rows_layout(Carver& c, const HeadShape& h) {
   const size_t m = static_cast<size_t>(h.M);
   L.n_rows = c.take(256);
   L.row_src = c.take(m * sizeof(int));
-  L.label32 = L.idx = L.p = L.cnt = 0;
+  L.row_lse2 = c.take(m * sizeof(float));
+  L.row_tgt = L.row_cnt = L.idx = L.p = L.cnt = 0;
   if (h.k > 0) {
+    L.row_cnt = c.take(m * sizeof(int));
     L.idx = c.take(m * h.k * sizeof(int));
     L.p = c.take(m * h.k * sizeof(float));
     L.cnt = c.take(m * sizeof(int));
   } else {
-    L.label32 = c.take(m * sizeof(int));
+    L.row_tgt = c.take(m * sizeof(int));
   }
   L.xc = c.take(m * h.d * 2);
   return L;
@@ -419,6 +505,7 @@ struct FwdLayout {
   RowsLayout r;
   size_t part, part_sum, tgt_s, total;
   long long part_ld;
+  int bn, n_tiles;
 };
 
 FwdLayout fwd_layout(const HeadShape& h) {
@@ -426,8 +513,10 @@ FwdLayout fwd_layout(const HeadShape& h) {
   FwdLayout L;
   L.r = rows_layout(c, h);
   L.part_ld = (static_cast<long long>(h.M) + 31) / 32 * 32;
-  L.part = c.take(static_cast<size_t>(h.n_tiles()) * L.part_ld * sizeof(float2));
-  L.part_sum = h.k > 0 ? 0 : c.take(static_cast<size_t>(h.n_tiles()) * L.part_ld * sizeof(float));
+  L.bn = lse_width(h);
+  L.n_tiles = ceil_div(h.V, L.bn);
+  L.part = c.take(static_cast<size_t>(L.n_tiles) * L.part_ld * sizeof(float2));
+  L.part_sum = h.k > 0 ? 0 : c.take(static_cast<size_t>(L.n_tiles) * L.part_ld * sizeof(float));
   L.tgt_s = c.take(static_cast<size_t>(h.M) * h.entries() * sizeof(float));
   L.total = c.off;
   return L;
@@ -442,26 +531,59 @@ struct BwdLayout {
 // A piece's D takes at most about this much memory.
 constexpr long long PIECE_BYTES = 256ll << 20;
 
+// Slabs of dx: where its tiles are too few for the device, the sum over the piece is split.
+int dx_splits(const HeadShape& h, int piece) {
+  const long long tiles = static_cast<long long>(h.row_tiles()) * ceil_div(h.d, grad_width(h.d));
+  const int kb = piece / HEAD_BK;
+  long long s = h.slots() / tiles;
+  if (s > kb / 8) s = kb / 8;
+  return s < 1 ? 1 : static_cast<int>(s);
+}
+
+// Time of the products of one piece of vc rows, in blocks of 64 along k of a whole tile (about a quarter
+// of a microsecond): tiles go round the SMs (or pairs), so each product lasts as long as the fullest.
+long long piece_cost(const HeadShape& h, int vc, int splits) {
+  const int kb_d = ceil_div(h.d, HEAD_BK), kb_v = ceil_div(vc, HEAD_BK), kb_n = ceil_div(h.M, HEAD_BK);
+  const long long rt = h.row_tiles(), dt = ceil_div(h.d, grad_width(h.d)), slots = h.slots();
+  const long long logits = (rt * ceil_div(vc, HEAD_BN) + slots - 1) / slots * (kb_d + 4);
+  const long long dw = ceil_div(vc, h.bm()) * dt, all = dw + rt * dt * splits;
+  long long grads = 0;
+  for (int c = 0; c < slots && c < all; ++c) {
+    const long long mine = (all - 1 - c) / slots + 1, mine_dw = c < dw ? (dw - 1 - c) / slots + 1 : 0;
+    const long long t = mine_dw * (kb_n + 4) + (mine - mine_dw) * (ceil_div(kb_v, splits) + 4);
+    if (t > grads) grads = t;
+  }
+  return logits + grads + 32;                  // two launches
+}
+
 BwdLayout bwd_layout(const HeadShape& h) {
   Carver c;
   BwdLayout L;
   L.r = rows_layout(c, h);
   const long long v256 = (static_cast<long long>(h.V) + 255) / 256 * 256;
-  long long piece = PIECE_BYTES / (2ll * h.M) / 256 * 256;
-  if (piece < 256) piece = 256;
-  if (piece > v256) piece = v256;
-  L.piece = static_cast<int>(piece);
-  // too few dx tiles for the device: the sum over the piece is split over slabs
-  const long long tiles = static_cast<long long>((h.M + HEAD_BM - 1) / HEAD_BM) * ((h.d + HEAD_BN - 1) / HEAD_BN);
-  const long long kb = piece / HEAD_BK;
-  long long splits = kSms / tiles;
-  if (splits > kb / 4) splits = kb / 4;
-  if (splits < 1) splits = 1;
-  L.splits = static_cast<int>(splits);
+  long long most = PIECE_BYTES / (2ll * h.M) / 256 * 256;
+  if (most < 256) most = 256;
+  if (most > v256) most = v256;
+  // equal pieces, as many as leave the fewest idle SMs (@@)
+  L.piece = static_cast<int>(most);
+  if (most < v256) {
+    const int fewest = ceil_div(v256, most);
+    long long best = -1;
+    for (int pieces = fewest; pieces <= fewest + 8 && pieces * 256ll <= v256; ++pieces) {
+      const int vc = ceil_div(ceil_div(h.V, pieces), 256) * 256;
+      const int last = h.V - (ceil_div(h.V, vc) - 1) * vc;
+      const long long t = (ceil_div(h.V, vc) - 1) * piece_cost(h, vc, 1) + piece_cost(h, last, 1);
+      if (best < 0 || t < best) {
+        best = t;
+        L.piece = vc;
+      }
+    }
+  }
+  L.splits = dx_splits(h, L.piece);
   const size_t m = static_cast<size_t>(h.M);
   L.g_max = c.take(256);
   L.xs = c.take(m * h.d * 2);
-  L.dl = c.take(m * L.piece * 2);
+  L.dl = c.take(m * static_cast<size_t>(most) * 2);
   L.slab = c.take(static_cast<size_t>(L.splits) * m * h.d * sizeof(float));
   L.total = c.off;
   return L;
@@ -477,10 +599,10 @@ bool map2(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint6
 
 std::mutex g_head_mu;
 
-template <int KIND>
-cudaError_t launch_head(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o, const HeadParams& p,
-                        cudaStream_t s) {
+template <int KIND, bool PAIR>
+cudaError_t launch_form(const HeadMaps& maps, const HeadParams& p, cudaStream_t s) {
   static uint64_t attr_done = 0;
+  constexpr int SMEM = HeadSmem<PAIR>::TOTAL;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -489,18 +611,35 @@ cudaError_t launch_head(const CUtensorMap& a, const CUtensorMap& b, const CUtens
     std::lock_guard<std::mutex> lk(g_head_mu);
     if (dev < 0 || dev > 63) return cudaErrorInvalidDevice;
     if (!(attr_done & (1ull << dev))) {
-      e = cudaFuncSetAttribute(head_gemm_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, HeadSmem::TOTAL);
+      e = cudaFuncSetAttribute(head_gemm_kernel<KIND, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
       if (e != cudaSuccess) return e;
       attr_done |= 1ull << dev;
     }
   }
-  const long long rows = (p.m_cap + HEAD_BM - 1) / HEAD_BM;
-  const long long vm = (p.vc + HEAD_BM - 1) / HEAD_BM, vn = (p.vc + HEAD_BN - 1) / HEAD_BN,
-                  dn = (p.d + HEAD_BN - 1) / HEAD_BN;
-  const long long tiles = KIND == HEAD_DW ? vm * dn : KIND == HEAD_DX ? rows * dn * p.k_splits : rows * vn;
-  const int sms = sm_count();
-  const int grid = tiles < sms ? static_cast<int>(tiles) : sms;
-  return launch_pdl(head_gemm_kernel<KIND>, dim3(grid), dim3(GEMM_THREADS), HeadSmem::TOTAL, s, a, b, o, p);
+  constexpr int BM = head_bm(PAIR), CTAS = PAIR ? 2 : 1;
+  const long long rows = ceil_div(p.m_cap, BM), dn = ceil_div(p.d, p.bn);
+  const long long tiles = KIND != HEAD_GRADS ? rows * ceil_div(p.vc, p.bn)
+                                             : (p.want_dw ? ceil_div(p.vc, BM) * dn : 0) + rows * dn * p.dx_splits;
+  long long slots = sm_count() / CTAS;
+  if (slots < 1) slots = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CTAS;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(CTAS * (tiles < slots ? tiles : slots)));
+  cfg.blockDim = dim3(GEMM_THREADS);
+  cfg.dynamicSmemBytes = SMEM;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, head_gemm_kernel<KIND, PAIR>, maps, p);
+}
+template <int KIND>
+cudaError_t launch_head(const HeadShape& h, const HeadMaps& maps, const HeadParams& p, cudaStream_t s) {
+  return h.pair() ? launch_form<KIND, true>(maps, p, s) : launch_form<KIND, false>(maps, p, s);
 }
 
 struct Targets {
@@ -541,9 +680,12 @@ struct HeadBase {
   uint32_t* err;
   const int* row_src;
   const int* n_rows;
-  const int* tgt_idx;
-  const float* tgt_p;
-  const int* tgt_cnt;
+  int* row_tgt;                // cross entropy
+  int* row_cnt;                // distillation, and the lists by source row
+  float* row_lse2;
+  int* tgt_idx;
+  float* tgt_p;
+  int* tgt_cnt;
   __nv_bfloat16* xc;
 };
 
@@ -554,13 +696,13 @@ HeadParams head_params(const HeadBase& b, const Targets& t) {
   p.V = b.h.V;
   p.d = b.h.d;
   p.vc = b.h.V;
+  p.bn = HEAD_BN;
   p.panel = 8;
-  p.k_splits = 1;
   p.scale_log2 = 1.4426950408889634f / t.temperature;
-  p.row_src = b.row_src;
+  p.row_tgt = b.h.k > 0 ? b.row_src : b.row_tgt;
+  p.row_cnt = b.row_cnt;
   p.tgt_idx = b.tgt_idx;
   p.tgt_p = b.tgt_p;
-  p.tgt_cnt = b.tgt_cnt;
   p.k = b.h.entries();
   p.label_p = 1.0f - t.smoothing;
   p.smooth = t.smoothing / static_cast<float>(b.h.V);
@@ -575,7 +717,10 @@ HeadBase head_base(const HeadShape& h, uint8_t* ws, const RowsLayout& L, uint32_
   b.err = err;
   b.row_src = reinterpret_cast<int*>(ws + L.row_src);
   b.n_rows = reinterpret_cast<int*>(ws + L.n_rows);
-  b.tgt_idx = reinterpret_cast<int*>(ws + (h.k > 0 ? L.idx : L.label32));
+  b.row_tgt = h.k > 0 ? nullptr : reinterpret_cast<int*>(ws + L.row_tgt);
+  b.row_cnt = h.k > 0 ? reinterpret_cast<int*>(ws + L.row_cnt) : nullptr;
+  b.row_lse2 = reinterpret_cast<float*>(ws + L.row_lse2);
+  b.tgt_idx = h.k > 0 ? reinterpret_cast<int*>(ws + L.idx) : nullptr;
   b.tgt_p = h.k > 0 ? reinterpret_cast<float*>(ws + L.p) : nullptr;
   b.tgt_cnt = h.k > 0 ? reinterpret_cast<int*>(ws + L.cnt) : nullptr;
   b.xc = reinterpret_cast<__nv_bfloat16*>(ws + L.xc);
@@ -594,7 +739,9 @@ RowsArgs rows_args(const HeadBase& b, const Targets& t, const RowsLayout& L, con
   a.xc = b.xc;
   a.row_src = reinterpret_cast<int*>(b.ws + L.row_src);
   a.n_rows = reinterpret_cast<int*>(b.ws + L.n_rows);
-  a.label32 = b.h.k > 0 ? nullptr : reinterpret_cast<int*>(b.ws + L.label32);
+  a.row_tgt = b.row_tgt;
+  a.row_cnt = b.row_cnt;
+  a.row_lse2 = b.row_lse2;
   a.err = b.err;
   return a;
 }
@@ -609,34 +756,45 @@ wb_status head_forward(const HeadShape& h, const Targets& t, const void* x, cons
   if (!err) return WB_ECUDA;
   const FwdLayout L = fwd_layout(h);
   const HeadBase b = head_base(h, static_cast<uint8_t*>(workspace), L.r, err);
-  {
-    Prof pr(PC_HEAD_ROWS, s, h.k > 0 ? 2 : 1);
-    if (h.k > 0)
-      WB_CUDA(launch_lists(h, t, reinterpret_cast<int*>(b.ws + L.r.idx), reinterpret_cast<float*>(b.ws + L.r.p),
-                           reinterpret_cast<int*>(b.ws + L.r.cnt), err, s));
-    RowsArgs a = rows_args(b, t, L.r, x);
-    a.loss = loss;
-    a.lse = lse;
-    WB_CUDA(launch_rows(a, s));
+  const bool direct = h.direct();
+  if (h.k > 0 || !direct) {
+    Prof pr(PC_HEAD_ROWS, s, (h.k > 0) + !direct);
+    if (h.k > 0) WB_CUDA(launch_lists(h, t, b.tgt_idx, b.tgt_p, b.tgt_cnt, err, s));
+    if (!direct) {
+      RowsArgs a = rows_args(b, t, L.r, x);
+      a.loss = loss;
+      a.lse = lse;
+      WB_CUDA(launch_rows(a, s));
+    }
   }
   HeadParams p = head_params(b, t);
+  if (direct) {
+    p.n_rows = nullptr;
+    p.labels = t.labels;
+    p.row_tgt = nullptr;
+    p.row_cnt = b.tgt_cnt;
+  }
   p.part = reinterpret_cast<float2*>(b.ws + L.part);
   p.part_sum = t.smoothing > 0.0f ? reinterpret_cast<float*>(b.ws + L.part_sum) : nullptr;
   p.part_ld = L.part_ld;
   p.tgt_s = reinterpret_cast<float*>(b.ws + L.tgt_s);
-  CUtensorMap am, bm;
-  if (!map2(&am, b.xc, h.d, h.M, h.d, HEAD_BK, HEAD_BM) || !map2(&bm, w, h.d, h.V, h.d, HEAD_BK, HEAD_BN))
+  p.bn = L.bn;
+  HeadMaps maps;
+  std::memset(&maps, 0, sizeof(maps));
+  if (!map2(&maps.a0, direct ? x : b.xc, h.d, h.M, h.d, HEAD_BK, 128) ||
+      !map2(&maps.b0, w, h.d, h.V, h.d, HEAD_BK, h.pair() ? L.bn / 2 : L.bn))
     return WB_ECUDA;
   {
     Prof pr(PC_HEAD_LSE, s);
-    WB_CUDA(launch_head<HEAD_LSE>(am, bm, am, p, s));
+    WB_CUDA(launch_head<HEAD_LSE>(h, maps, p, s));
   }
   FinishArgs f = {};
-  f.n_rows = b.n_rows;
-  f.row_src = b.row_src;
+  f.n_rows = direct ? nullptr : b.n_rows;
+  f.row_src = direct ? nullptr : b.row_src;
+  f.labels = t.labels;
   f.M = h.M;
   f.V = h.V;
-  f.n_tiles = h.n_tiles();
+  f.n_tiles = L.n_tiles;
   f.k = h.entries();
   f.part = p.part;
   f.part_sum = p.part_sum;
@@ -652,7 +810,7 @@ wb_status head_forward(const HeadShape& h, const Targets& t, const void* x, cons
   {
     Prof pr(PC_HEAD_FINISH, s);
     const int blocks = (h.M + FIN_ROWS - 1) / FIN_ROWS;
-    WB_CUDA(launch_pdl(head_finish_kernel, dim3(blocks < 8 * kSms ? blocks : 8 * kSms), dim3(FIN_ROWS * FIN_SLICES), 0,
+    WB_CUDA(launch_pdl(head_finish_kernel, dim3(blocks < 1216 ? blocks : 1216), dim3(FIN_ROWS * FIN_SLICES), 0,
                        s, f));
   }
   return WB_OK;
@@ -669,61 +827,63 @@ wb_status head_backward(const HeadShape& h, const Targets& t, const float* dloss
   auto* dl = reinterpret_cast<__nv_bfloat16*>(b.ws + L.dl);
   auto* slab = reinterpret_cast<float*>(b.ws + L.slab);
   {
-    Prof pr(PC_HEAD_ROWS, s, (h.k > 0 ? 2 : 1) + (dw ? 1 : 0));
+    Prof pr(PC_HEAD_ROWS, s, (h.k > 0 ? 2 : 1) + (dw && h.M > OWN_MAX_ROWS ? 1 : 0));
     if (h.k > 0)
-      WB_CUDA(launch_lists(h, t, reinterpret_cast<int*>(b.ws + L.r.idx), reinterpret_cast<float*>(b.ws + L.r.p),
-                           reinterpret_cast<int*>(b.ws + L.r.cnt), err, s));
+      WB_CUDA(launch_lists(h, t, b.tgt_idx, b.tgt_p, b.tgt_cnt, err, s));
     RowsArgs a = rows_args(b, t, L.r, x);
     a.dloss = dloss;
+    a.lse_in = lse;
     a.g_max = g_max;
+    a.own_max = h.M <= OWN_MAX_ROWS;
     a.xs = dw ? xs : nullptr;
     a.dx = static_cast<__nv_bfloat16*>(dx);
-    if (dw) WB_CUDA(launch_pdl(dloss_max_kernel, dim3(1), dim3(1024), 0, s, a, g_max));
+    if (dw && !a.own_max) WB_CUDA(launch_pdl(dloss_max_kernel, dim3(1), dim3(1024), 0, s, a, g_max));
     WB_CUDA(launch_rows(a, s));
   }
   HeadParams p = head_params(b, t);
-  p.lse = lse;
+  p.row_lse2 = b.row_lse2;
   p.g_scale = g_max;
   p.out_scale = t.temperature;
-  p.k_splits = L.splits;
-  CUtensorMap xa, wb, dlo, dla, wk, slo, dlt, xk, dwo;
+  p.dx_splits = dx ? L.splits : 0;
+  p.want_dw = dw != nullptr;
+  HeadMaps lm, gm;
+  std::memset(&lm, 0, sizeof(lm));
+  std::memset(&gm, 0, sizeof(gm));
   const uint64_t ld = L.piece;
-  bool ok = map2(&xa, b.xc, h.d, h.M, h.d, HEAD_BK, HEAD_BM) && map2(&wb, w, h.d, h.V, h.d, HEAD_BK, HEAD_BN) &&
-            map2(&dlo, dl, ld, h.M, ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  bool ok = map2(&lm.a0, b.xc, h.d, h.M, h.d, HEAD_BK, 128) &&
+            map2(&lm.b0, w, h.d, h.V, h.d, HEAD_BK, h.pair() ? HEAD_BN / 2 : HEAD_BN) &&
+            map2(&lm.o0, dl, ld, h.M, ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   if (dx) {
     const uint64_t dims[3] = {static_cast<uint64_t>(h.d), static_cast<uint64_t>(h.M), static_cast<uint64_t>(L.splits)};
     const uint64_t str[2] = {static_cast<uint64_t>(h.d) * 4, static_cast<uint64_t>(h.d) * 4 * h.M};
     const uint32_t box[3] = {16, 32, 1};
-    ok = ok && map2(&dla, dl, ld, h.M, ld, HEAD_BK, HEAD_BM) && map2(&wk, w, h.d, h.V, h.d, 64, HEAD_BK) &&
-         tma_map_f32(&slo, 3, slab, dims, str, box, CU_TENSOR_MAP_SWIZZLE_64B);
+    ok = ok && map2(&gm.a0, dl, ld, h.M, ld, HEAD_BK, 128) && map2(&gm.b0, w, h.d, h.V, h.d, 64, HEAD_BK) &&
+         tma_map_f32(&gm.o0, 3, slab, dims, str, box, CU_TENSOR_MAP_SWIZZLE_64B);
   }
   if (dw)
-    ok = ok && map2(&dlt, dl, ld, h.M, ld, 64, HEAD_BK) && map2(&xk, xs, h.d, h.M, h.d, 64, HEAD_BK) &&
-         map2(&dwo, dw, h.d, h.V, h.d, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+    ok = ok && map2(&gm.a1, dl, ld, h.M, ld, 64, HEAD_BK) && map2(&gm.b1, xs, h.d, h.M, h.d, 64, HEAD_BK) &&
+         map2(&gm.o1, dw, h.d, h.V, h.d, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   if (!ok) return WB_ECUDA;
   for (int v0 = 0; v0 < h.V; v0 += L.piece) {
     p.v0 = v0;
     p.vc = h.V - v0 < L.piece ? h.V - v0 : L.piece;
     p.first_piece = v0 == 0;
+    p.bn = HEAD_BN;
     {
       Prof pr(PC_HEAD_DLOGITS, s);
-      WB_CUDA(launch_head<HEAD_DLOGITS>(xa, wb, dlo, p, s));
+      WB_CUDA(launch_head<HEAD_DLOGITS>(h, lm, p, s));
     }
-    if (dx) {
-      Prof pr(PC_HEAD_DX, s);
-      WB_CUDA(launch_head<HEAD_DX>(dla, wk, slo, p, s));
-    }
-    if (dw) {
-      Prof pr(PC_HEAD_DW, s);
-      WB_CUDA(launch_head<HEAD_DW>(dlt, xk, dwo, p, s));
-    }
+    p.bn = grad_width(h.d);
+    Prof pr(PC_HEAD_GRADS, s);
+    WB_CUDA(launch_head<HEAD_GRADS>(h, gm, p, s));
   }
   if (dx) {
     Prof pr(PC_HEAD_FINISH, s);
-    const long long work = static_cast<long long>(h.M) * (h.d / 8);
+    const int lanes = L.splits >= 8 ? 8 : L.splits >= 4 ? 4 : L.splits >= 2 ? 2 : 1;
+    const long long work = static_cast<long long>(h.M) * (h.d / 8) * lanes;
     const long long blocks = (work + 255) / 256;
-    WB_CUDA(launch_pdl(head_dx_kernel, dim3(static_cast<unsigned>(blocks < 16 * kSms ? blocks : 16 * kSms)), dim3(256),
-                       0, s, b.n_rows, b.row_src, h.M, h.d, L.splits, static_cast<const float*>(slab), dloss,
+    WB_CUDA(launch_pdl(head_dx_kernel, dim3(static_cast<unsigned>(blocks < 2432 ? blocks : 2432)), dim3(256), 0, s,
+                       b.n_rows, b.row_src, h.M, h.d, L.splits, lanes, static_cast<const float*>(slab), dloss,
                        t.temperature, static_cast<__nv_bfloat16*>(dx), err));
   }
   return WB_OK;
