@@ -75,7 +75,8 @@ def _ce_target(labels, V, smooth):
 
 
 CE = [(1, 8, 1), (1, 64, 2), (3, 8, 5), (1, 1280, 5003), (5, 72, 255), (128, 64, 256), (129, 136, 257), (77, 384, 1000),
-      (300, 384, 2049), (1000, 256, 513), (257, 1280, 3001), (64, 2056, 700)]
+      (300, 384, 2049), (1000, 256, 513), (257, 1280, 3001), (64, 2056, 700), (8, 40, 333), (16, 1288, 700), (2, 4104, 300), (17, 768, 900),
+      (450, 768, 1100), (2, 4096, 5000)]
 
 
 @pytest.mark.parametrize("M,d,V", CE)

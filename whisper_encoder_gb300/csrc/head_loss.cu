@@ -19,6 +19,7 @@
 #include "../../include/wb.h"
 #include "internal.h"
 #include "head_gemm.cuh"
+#include "head_gemv.cuh"
 
 namespace wb {
 namespace {
@@ -438,29 +439,38 @@ int ceil_div(long long a, long long b) { return static_cast<int>((a + b - 1) / b
 
 struct HeadShape {
   int M, d, V, k;              // k = 0: cross entropy
+  bool pair;                   // the pair form of the products
   int entries() const { return k > 0 ? k : 1; }
-  // the pair form of the products (@@)
-  bool pair() const { return M > 2048; }
-  int bm() const { return head_bm(pair()); }
-  int slots() const { return pair() ? HEAD_SMS / 2 : HEAD_SMS; }   // tiles at a time
+  int bm() const { return head_bm(pair); }
+  int slots() const { return pair ? HEAD_SMS / 2 : HEAD_SMS; }   // tiles at a time
   int row_tiles() const { return ceil_div(M, bm()); }
   // one tile of rows: taking out rows saves no product, so the forward pass reads x as it is
   bool direct() const { return M <= 128; }
+  // a few rows: w straight to registers (head_gemv.cuh)
+  bool gemv() const { return M <= GEMV_MAX_M && d <= GEMV_MAX_D; }
 };
+
+// The pair form wins where a tile's k is long and there are rows for it.  Device time of the pair and the
+// single form against 51866 entries, us: forward, d = 1280: 64 rows 35 / 32, 448 rows 57 / 62, 14336 rows
+// 1030 / 1128; d = 384: 448 rows 29 / 27, 14336 rows 415 / 374.  Backward, d = 1280: 64 rows 101 / 87, 200
+// rows 117 / 123, 1500 rows 387 / 451; d = 384: 448 rows 77 / 77, 1000 rows 128 / 132, 14336 rows 1556 / 1649.
+HeadShape fwd_shape(int M, int d, int V, int k) { return HeadShape{M, d, V, k, M > 128 && d >= 768}; }
+HeadShape bwd_shape(int M, int d, int V, int k) { return HeadShape{M, d, V, k, M > 128 && (d >= 768 || M > 512)}; }
 
 bool shape_ok(int M, int d, int V) {
   return M >= 0 && M <= (1 << 24) && d >= 8 && d <= (1 << 16) && d % 8 == 0 && V >= 1 && V <= (1 << 24);
 }
 
-// Column-tile width of the forward product: the one whose rounds of tiles over the device end first, a
-// tile costing its columns and about 24 more (its fill and drain).  Measured at one row against
-// 51866 x 1280: @@
+// Column-tile width of the forward product: the one whose rounds of tiles over the device end first.  A tile
+// costs about 100 columns on top of its own (a stage's round trip through the ring bounds narrow tiles):
+// measured at 1500 rows of 1280, 256 / 192 / 128 / 64 columns 127 / 148 / 208 / 383 us.  So 256 nearly always;
+// 192 where it takes as few rounds (one tile of rows, 51866 entries: 31.5 us against 34.7).
 int lse_width(const HeadShape& h) {
   int best = HEAD_BN;
   long long cost = -1;
   for (int bn = HEAD_BN; bn >= 64; bn -= 32) {
     const long long tiles = static_cast<long long>(h.row_tiles()) * ceil_div(h.V, bn);
-    const long long c = (tiles + h.slots() - 1) / h.slots() * (bn + 24);
+    const long long c = (tiles + h.slots() - 1) / h.slots() * (bn + 100);
     if (cost < 0 || c < cost) {
       cost = c;
       best = bn;
@@ -514,7 +524,7 @@ FwdLayout fwd_layout(const HeadShape& h) {
   L.r = rows_layout(c, h);
   L.part_ld = (static_cast<long long>(h.M) + 31) / 32 * 32;
   L.bn = lse_width(h);
-  L.n_tiles = ceil_div(h.V, L.bn);
+  L.n_tiles = h.gemv() ? HEAD_SMS : ceil_div(h.V, L.bn);
   L.part = c.take(static_cast<size_t>(L.n_tiles) * L.part_ld * sizeof(float2));
   L.part_sum = h.k > 0 ? 0 : c.take(static_cast<size_t>(L.n_tiles) * L.part_ld * sizeof(float));
   L.tgt_s = c.take(static_cast<size_t>(h.M) * h.entries() * sizeof(float));
@@ -639,7 +649,27 @@ cudaError_t launch_form(const HeadMaps& maps, const HeadParams& p, cudaStream_t 
 }
 template <int KIND>
 cudaError_t launch_head(const HeadShape& h, const HeadMaps& maps, const HeadParams& p, cudaStream_t s) {
-  return h.pair() ? launch_form<KIND, true>(maps, p, s) : launch_form<KIND, false>(maps, p, s);
+  return h.pair ? launch_form<KIND, true>(maps, p, s) : launch_form<KIND, false>(maps, p, s);
+}
+
+template <int MT>
+cudaError_t launch_gemv(const GemvParams& p, int blocks, cudaStream_t s) {
+  static uint64_t attr_done = 0;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  {
+    std::lock_guard<std::mutex> lk(g_head_mu);
+    if (dev < 0 || dev > 63) return cudaErrorInvalidDevice;
+    if (!(attr_done & (1ull << dev))) {
+      e = cudaFuncSetAttribute(head_gemv_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               8 * MT * gemv_row_bytes(GEMV_MAX_D));
+      if (e != cudaSuccess) return e;
+      attr_done |= 1ull << dev;
+    }
+  }
+  return launch_pdl(head_gemv_kernel<MT>, dim3(blocks), dim3(GEMV_WARPS * 32),
+                    static_cast<size_t>(8 * MT) * gemv_row_bytes(p.d), s, p);
 }
 
 struct Targets {
@@ -767,26 +797,53 @@ wb_status head_forward(const HeadShape& h, const Targets& t, const void* x, cons
       WB_CUDA(launch_rows(a, s));
     }
   }
-  HeadParams p = head_params(b, t);
-  if (direct) {
-    p.n_rows = nullptr;
+  int n_tiles = L.n_tiles;
+  auto* part = reinterpret_cast<float2*>(b.ws + L.part);
+  float* part_sum = t.smoothing > 0.0f ? reinterpret_cast<float*>(b.ws + L.part_sum) : nullptr;
+  auto* tgt_s = reinterpret_cast<float*>(b.ws + L.tgt_s);
+  if (h.gemv()) {
+    GemvParams p = {};
+    p.x = static_cast<const __nv_bfloat16*>(x);
+    p.w = static_cast<const __nv_bfloat16*>(w);
+    p.M = h.M;
+    p.V = h.V;
+    p.d = h.d;
+    p.scale_log2 = 1.4426950408889634f / t.temperature;
     p.labels = t.labels;
-    p.row_tgt = nullptr;
-    p.row_cnt = b.tgt_cnt;
-  }
-  p.part = reinterpret_cast<float2*>(b.ws + L.part);
-  p.part_sum = t.smoothing > 0.0f ? reinterpret_cast<float*>(b.ws + L.part_sum) : nullptr;
-  p.part_ld = L.part_ld;
-  p.tgt_s = reinterpret_cast<float*>(b.ws + L.tgt_s);
-  p.bn = L.bn;
-  HeadMaps maps;
-  std::memset(&maps, 0, sizeof(maps));
-  if (!map2(&maps.a0, direct ? x : b.xc, h.d, h.M, h.d, HEAD_BK, 128) ||
-      !map2(&maps.b0, w, h.d, h.V, h.d, HEAD_BK, h.pair() ? L.bn / 2 : L.bn))
-    return WB_ECUDA;
-  {
+    p.cnt = b.tgt_cnt;
+    p.tgt_idx = b.tgt_idx;
+    p.k = h.entries();
+    p.part = part;
+    p.part_sum = part_sum;
+    p.part_ld = L.part_ld;
+    p.tgt_s = tgt_s;
+    p.err = err;
+    const int groups = ceil_div(h.V, 16);
+    n_tiles = groups < HEAD_SMS ? groups : HEAD_SMS;
     Prof pr(PC_HEAD_LSE, s);
-    WB_CUDA(launch_head<HEAD_LSE>(h, maps, p, s));
+    WB_CUDA(h.M <= 8 ? launch_gemv<1>(p, n_tiles, s) : launch_gemv<2>(p, n_tiles, s));
+  } else {
+    HeadParams p = head_params(b, t);
+    if (direct) {
+      p.n_rows = nullptr;
+      p.labels = t.labels;
+      p.row_tgt = nullptr;
+      p.row_cnt = b.tgt_cnt;
+    }
+    p.part = part;
+    p.part_sum = part_sum;
+    p.part_ld = L.part_ld;
+    p.tgt_s = tgt_s;
+    p.bn = L.bn;
+    HeadMaps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    if (!map2(&maps.a0, direct ? x : b.xc, h.d, h.M, h.d, HEAD_BK, 128) ||
+        !map2(&maps.b0, w, h.d, h.V, h.d, HEAD_BK, h.pair ? L.bn / 2 : L.bn))
+      return WB_ECUDA;
+    {
+      Prof pr(PC_HEAD_LSE, s);
+      WB_CUDA(launch_head<HEAD_LSE>(h, maps, p, s));
+    }
   }
   FinishArgs f = {};
   f.n_rows = direct ? nullptr : b.n_rows;
@@ -794,12 +851,12 @@ wb_status head_forward(const HeadShape& h, const Targets& t, const void* x, cons
   f.labels = t.labels;
   f.M = h.M;
   f.V = h.V;
-  f.n_tiles = L.n_tiles;
+  f.n_tiles = n_tiles;
   f.k = h.entries();
-  f.part = p.part;
-  f.part_sum = p.part_sum;
+  f.part = part;
+  f.part_sum = part_sum;
   f.part_ld = L.part_ld;
-  f.tgt_s = p.tgt_s;
+  f.tgt_s = tgt_s;
   f.tgt_p = b.tgt_p;
   f.tgt_cnt = b.tgt_cnt;
   f.inv_t = 1.0f / t.temperature;
@@ -851,7 +908,7 @@ wb_status head_backward(const HeadShape& h, const Targets& t, const float* dloss
   std::memset(&gm, 0, sizeof(gm));
   const uint64_t ld = L.piece;
   bool ok = map2(&lm.a0, b.xc, h.d, h.M, h.d, HEAD_BK, 128) &&
-            map2(&lm.b0, w, h.d, h.V, h.d, HEAD_BK, h.pair() ? HEAD_BN / 2 : HEAD_BN) &&
+            map2(&lm.b0, w, h.d, h.V, h.d, HEAD_BK, h.pair ? HEAD_BN / 2 : HEAD_BN) &&
             map2(&lm.o0, dl, ld, h.M, ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   if (dx) {
     const uint64_t dims[3] = {static_cast<uint64_t>(h.d), static_cast<uint64_t>(h.M), static_cast<uint64_t>(L.splits)};
@@ -920,16 +977,16 @@ using namespace wb;
 extern "C" {
 
 size_t wb_linear_cross_entropy_workspace_bytes(int M, int d, int V) {
-  return shape_ok(M, d, V) && M > 0 ? fwd_layout(HeadShape{M, d, V, 0}).total : 0;
+  return shape_ok(M, d, V) && M > 0 ? fwd_layout(fwd_shape(M, d, V, 0)).total : 0;
 }
 size_t wb_linear_cross_entropy_backward_workspace_bytes(int M, int d, int V) {
-  return shape_ok(M, d, V) && M > 0 ? bwd_layout(HeadShape{M, d, V, 0}).total : 0;
+  return shape_ok(M, d, V) && M > 0 ? bwd_layout(bwd_shape(M, d, V, 0)).total : 0;
 }
 size_t wb_linear_distill_workspace_bytes(int M, int d, int V, int k) {
-  return shape_ok(M, d, V) && M > 0 && k >= 1 && k <= HEAD_MAX_K ? fwd_layout(HeadShape{M, d, V, k}).total : 0;
+  return shape_ok(M, d, V) && M > 0 && k >= 1 && k <= HEAD_MAX_K ? fwd_layout(fwd_shape(M, d, V, k)).total : 0;
 }
 size_t wb_linear_distill_backward_workspace_bytes(int M, int d, int V, int k) {
-  return shape_ok(M, d, V) && M > 0 && k >= 1 && k <= HEAD_MAX_K ? bwd_layout(HeadShape{M, d, V, k}).total : 0;
+  return shape_ok(M, d, V) && M > 0 && k >= 1 && k <= HEAD_MAX_K ? bwd_layout(bwd_shape(M, d, V, k)).total : 0;
 }
 
 wb_status wb_linear_cross_entropy(const void* x, const void* w, const int64_t* labels, int M, int d, int V,
@@ -938,7 +995,7 @@ wb_status wb_linear_cross_entropy(const void* x, const void* w, const int64_t* l
   if (!shape_ok(M, d, V) || !(label_smoothing >= 0.0f && label_smoothing < 1.0f)) return WB_EINVAL;
   if (M == 0) return WB_OK;
   if (!labels || !aligned8(labels)) return WB_EINVAL;
-  const HeadShape h{M, d, V, 0};
+  const HeadShape h = fwd_shape(M, d, V, 0);
   const wb_status st = check_forward(h, x, w, loss, lse, workspace, workspace_bytes);
   if (st != WB_OK) return st;
   const Targets t{labels, label_smoothing, nullptr, 0, nullptr, 1.0f};
@@ -956,7 +1013,7 @@ wb_status wb_linear_cross_entropy_backward(const float* dloss, const void* x, co
     return WB_OK;
   }
   if (!labels || !aligned8(labels)) return WB_EINVAL;
-  const HeadShape h{M, d, V, 0};
+  const HeadShape h = bwd_shape(M, d, V, 0);
   const wb_status st = check_backward(h, dloss, x, w, lse, dx, dw, workspace, workspace_bytes);
   if (st != WB_OK) return st;
   if (!dx && !dw) return WB_OK;
@@ -971,7 +1028,7 @@ wb_status wb_linear_distill(const void* x, const void* w, const void* top, int t
   if (!shape_ok(M, d, V) || k < 1 || k > HEAD_MAX_K || !positive(temperature)) return WB_EINVAL;
   if (M == 0) return WB_OK;
   if (!top || !index || !aligned16(top) || !aligned8(index)) return WB_EINVAL;
-  const HeadShape h{M, d, V, k};
+  const HeadShape h = fwd_shape(M, d, V, k);
   const wb_status st = check_forward(h, x, w, loss, lse, workspace, workspace_bytes);
   if (st != WB_OK) return st;
   const Targets t{nullptr, 0.0f, top, top_dtype, index, temperature};
@@ -991,7 +1048,7 @@ wb_status wb_linear_distill_backward(const float* dloss, const void* x, const vo
     return WB_OK;
   }
   if (!top || !index || !aligned16(top) || !aligned8(index)) return WB_EINVAL;
-  const HeadShape h{M, d, V, k};
+  const HeadShape h = bwd_shape(M, d, V, k);
   const wb_status st = check_backward(h, dloss, x, w, lse, dx, dw, workspace, workspace_bytes);
   if (st != WB_OK) return st;
   if (!dx && !dw) return WB_OK;
