@@ -274,15 +274,15 @@ def _place(stream, first, *rest):
 
     Outputs and workspaces are allocated inside, so that on a side stream the allocator hands their
     memory out again in that stream's order; inputs of other streams are marked as in use on it."""
-    dev = first.device
+    i = first.get_device()
     for t in rest:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}: one device expected")
+        if t is not None and t.get_device() != i:
+            raise ValueError(f"tensors on {first.device} and {t.device}: one device expected")
     if stream is None:
-        return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-    if stream.device != dev:
-        raise ValueError(f"stream on {stream.device}, tensors on {dev}")
-    if stream != torch.cuda.current_stream(dev):
+        return _HERE if torch._C._cuda_getDevice() == i else torch.cuda.device(i)
+    if stream.device != first.device:
+        raise ValueError(f"stream on {stream.device}, tensors on {first.device}")
+    if stream != torch.cuda.current_stream(first.device):
         for t in (first, *rest):
             if t is not None:
                 t.record_stream(stream)
@@ -294,7 +294,7 @@ _HERE = contextlib.nullcontext()
 
 def _raw_stream(t) -> int:
     """The current stream of t's device as an address (torch.cuda.current_stream builds an object: 6 us)."""
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _a(t):
@@ -302,9 +302,8 @@ def _a(t):
 
 
 def _need_shape(t, dtype, shape, name):
-    _need(t, dtype, name)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or not t.is_contiguous() or t.shape != shape:
+        raise ValueError(f"{name}: expected a contiguous CUDA {dtype} tensor of shape {tuple(shape)}")
 
 
 def _ln_rows(x, name):
@@ -389,7 +388,7 @@ def linear_cross_entropy(x, w, labels, label_smoothing: float = 0.0, workspace=N
     _need_shape(labels, torch.int64, (M,), "labels")
     with _place(stream, x, w, labels, workspace):
         loss = torch.empty(M, dtype=torch.float32, device=x.device)
-        lse = torch.empty(M, dtype=torch.float32, device=x.device)
+        lse = torch.empty_like(loss)
         ws = _head_workspace(workspace, "wb_linear_cross_entropy_workspace_bytes", x.device, M, d, V)
         call("wb_linear_cross_entropy", _a(x), _a(w), _a(labels), M, d, V, label_smoothing, _a(loss), _a(lse), _a(ws),
              ws.numel(), _raw_stream(x))
@@ -423,7 +422,7 @@ def linear_distill(x, w, top, index, temperature: float = 1.0, workspace=None, s
     k, ty = _teacher(top, index, M)
     with _place(stream, x, w, top, index, workspace):
         loss = torch.empty(M, dtype=torch.float32, device=x.device)
-        lse = torch.empty(M, dtype=torch.float32, device=x.device)
+        lse = torch.empty_like(loss)
         ws = _head_workspace(workspace, "wb_linear_distill_workspace_bytes", x.device, M, d, V, k)
         call("wb_linear_distill", _a(x), _a(w), _a(top), ty, _a(index), M, d, V, k, temperature, _a(loss), _a(lse),
              _a(ws), ws.numel(), _raw_stream(x))

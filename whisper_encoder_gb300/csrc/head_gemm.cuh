@@ -29,19 +29,24 @@ enum HeadKind : int { HEAD_LSE, HEAD_DLOGITS, HEAD_GRADS };
 constexpr int HEAD_BN = 256, HEAD_BK = 64;   // widest tile, elements of k per stage
 constexpr int head_bm(bool pair) { return pair ? 256 : 128; }
 
-template <bool PAIR>
+// The single form runs where a product is short, so that its epilogue shows: outside of HEAD_LSE (which
+// stores no boxes) it has two staging boxes a warp for one stage less.
+template <int KIND, bool PAIR>
 struct HeadSmem {
   static constexpr int A_BYTES = 128 * HEAD_BK * 2;
   static constexpr int B_BYTES = (PAIR ? HEAD_BN / 2 : HEAD_BN) * HEAD_BK * 2;
   static constexpr int MN_BLOCK = 64 * HEAD_BK * 2;      // 64 M / N elements x 64 k of an MN-major tile
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = PAIR ? 6 : 4;
-  static constexpr int BOX_BYTES = 32 * 64;              // 32 rows x 64 bytes per epilogue warp (64-byte swizzle)
+  static constexpr int BOXES = PAIR || KIND == HEAD_LSE ? 1 : 2;
+  static constexpr int STAGES = PAIR ? 6 : KIND == HEAD_LSE ? 4 : 3;
+  static constexpr int BOX_BYTES = 32 * 64;              // 32 rows x 64 bytes (64-byte swizzle)
   static constexpr int OFF_EPI = STAGES * STAGE_BYTES;
-  static constexpr int OFF_BAR = OFF_EPI + GEMM_EPI_WARPS * BOX_BYTES;
+  static constexpr int OFF_BAR = OFF_EPI + GEMM_EPI_WARPS * BOXES * BOX_BYTES;
   static constexpr int TOTAL = 1024 + OFF_BAR + 512;
 };
-static_assert(HeadSmem<true>::TOTAL <= 227 * 1024 && HeadSmem<false>::TOTAL <= 227 * 1024, "one CTA per SM");
+static_assert(HeadSmem<HEAD_GRADS, true>::TOTAL <= 227 * 1024 && HeadSmem<HEAD_LSE, false>::TOTAL <= 227 * 1024 &&
+                  HeadSmem<HEAD_GRADS, false>::TOTAL <= 227 * 1024,
+              "one CTA per SM");
 
 struct HeadMaps {
   CUtensorMap a0, a1;        // x (LSE, DLOGITS); D for dx (K-major), D for dw (MN-major)
@@ -85,7 +90,7 @@ struct HeadParams {
 template <int KIND, bool PAIR>
 __global__ void __launch_bounds__(GEMM_THREADS, 1)
     head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadParams p) {
-  using S = HeadSmem<PAIR>;
+  using S = HeadSmem<KIND, PAIR>;
   constexpr int BM = head_bm(PAIR);
   constexpr int STAGES = S::STAGES;
   constexpr bool LOGITS = KIND != HEAD_GRADS;
@@ -272,7 +277,16 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     const int quarter = warp & 3;                // TMEM lane quarter this warp may access
     const int cg = ew >> 2;                      // column group
     const int ch0 = bn / 32 * cg / 4, ch1 = bn / 32 * (cg + 1) / 4;   // its chunks of 32 columns: 0 to 2
-    uint8_t* box = smem + S::OFF_EPI + ew * S::BOX_BYTES;
+    uint8_t* const boxes = smem + S::OFF_EPI + ew * S::BOXES * S::BOX_BYTES;
+    int n_box = 0;
+    auto next_box = [&]() -> uint8_t* {          // a staging box whose last store has read it
+      if (lane == 0) {
+        if (S::BOXES == 2) bulk_wait_read1();
+        else bulk_wait_read0();
+      }
+      __syncwarp();
+      return boxes + (S::BOXES == 2 ? (n_box++ & 1) * S::BOX_BYTES : 0);
+    };
     // LSE: (max, sum, plain sum) of a warp's columns for the quarter's first warp, two tiles deep
     float* red = reinterpret_cast<float*>(smem + S::OFF_EPI);        // [2][4 quarters][3][4 groups][32]
     auto release = [&](int a) {                  // one lane a warp: this warp has read accumulator a
@@ -428,8 +442,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {               // two boxes of 16 float columns
               if (n0 + 16 * hf >= p.d) continue;
-              if (lane == 0) bulk_wait_read0();
-              __syncwarp();
+              uint8_t* box = next_box();
 #pragma unroll
               for (int j = 0; j < 4; ++j)
                 *reinterpret_cast<float4*>(box + box_off(lane, j)) =
@@ -480,8 +493,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) pk[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-          if (lane == 0) bulk_wait_read0();       // the previous store has read the staging box
-          __syncwarp();
+          uint8_t* box = next_box();
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             *reinterpret_cast<uint4*>(box + box_off(lane, j)) =

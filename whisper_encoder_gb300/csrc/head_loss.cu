@@ -445,7 +445,7 @@ struct HeadShape {
   int slots() const { return pair ? HEAD_SMS / 2 : HEAD_SMS; }   // tiles at a time
   int row_tiles() const { return ceil_div(M, bm()); }
   // one tile of rows: taking out rows saves no product, so the forward pass reads x as it is
-  bool direct() const { return M <= 128; }
+  bool direct() const { return row_tiles() <= 1; }
   // a few rows: w straight to registers (head_gemv.cuh)
   bool gemv() const { return M <= GEMV_MAX_M && d <= GEMV_MAX_D; }
 };
@@ -612,7 +612,7 @@ std::mutex g_head_mu;
 template <int KIND, bool PAIR>
 cudaError_t launch_form(const HeadMaps& maps, const HeadParams& p, cudaStream_t s) {
   static uint64_t attr_done = 0;
-  constexpr int SMEM = HeadSmem<PAIR>::TOTAL;
+  constexpr int SMEM = HeadSmem<KIND, PAIR>::TOTAL;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
