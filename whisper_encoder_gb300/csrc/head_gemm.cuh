@@ -29,21 +29,23 @@ enum HeadKind : int { HEAD_LSE, HEAD_DLOGITS, HEAD_GRADS };
 constexpr int HEAD_BN = 256, HEAD_BK = 64;   // widest tile, elements of k per stage
 constexpr int head_bm(bool pair) { return pair ? 256 : 128; }
 
-// The single form runs where a product is short, so that its epilogue shows: outside of HEAD_LSE (which
-// stores no boxes) it has two staging boxes a warp for one stage less.
+// HEAD_LSE stores no tile, only partials: its staging area is the exchange of those, and a stage more fits.
 template <int KIND, bool PAIR>
 struct HeadSmem {
   static constexpr int A_BYTES = 128 * HEAD_BK * 2;
   static constexpr int B_BYTES = (PAIR ? HEAD_BN / 2 : HEAD_BN) * HEAD_BK * 2;
   static constexpr int MN_BLOCK = 64 * HEAD_BK * 2;      // 64 M / N elements x 64 k of an MN-major tile
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int BOXES = PAIR || KIND == HEAD_LSE ? 1 : 2;
-  static constexpr int STAGES = PAIR ? 6 : KIND == HEAD_LSE ? 4 : 3;
-  static constexpr int BOX_BYTES = 32 * 64;              // 32 rows x 64 bytes (64-byte swizzle)
+  static constexpr int STAGES = (PAIR ? 5 : 3) + (KIND == HEAD_LSE);
+  // 32 rows x 128 bytes per epilogue warp (128-byte swizzle): a bulk store goes row by row, and rows of 64
+  // bytes were as slow as these (@@)
+  static constexpr int BOX_BYTES = 32 * 128;
   static constexpr int OFF_EPI = STAGES * STAGE_BYTES;
-  static constexpr int OFF_BAR = OFF_EPI + GEMM_EPI_WARPS * BOXES * BOX_BYTES;
+  static constexpr int OFF_BAR = OFF_EPI + (KIND == HEAD_LSE ? 2 * 4 * 3 * 128 * 4 : GEMM_EPI_WARPS * BOX_BYTES);
   static constexpr int TOTAL = 1024 + OFF_BAR + 512;
 };
+// Byte offset of 16-byte chunk j of row r in such a box.
+__device__ __forceinline__ uint32_t box128_off(int r, int j) { return static_cast<uint32_t>(r * 128 + ((j ^ (r & 7)) << 4)); }
 static_assert(HeadSmem<HEAD_GRADS, true>::TOTAL <= 227 * 1024 && HeadSmem<HEAD_LSE, false>::TOTAL <= 227 * 1024 &&
                   HeadSmem<HEAD_GRADS, false>::TOTAL <= 227 * 1024,
               "one CTA per SM");
@@ -276,16 +278,13 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     const int ew = warp - 2;
     const int quarter = warp & 3;                // TMEM lane quarter this warp may access
     const int cg = ew >> 2;                      // column group
-    const int ch0 = bn / 32 * cg / 4, ch1 = bn / 32 * (cg + 1) / 4;   // its chunks of 32 columns: 0 to 2
-    uint8_t* const boxes = smem + S::OFF_EPI + ew * S::BOXES * S::BOX_BYTES;
-    int n_box = 0;
-    auto next_box = [&]() -> uint8_t* {          // a staging box whose last store has read it
-      if (lane == 0) {
-        if (S::BOXES == 2) bulk_wait_read1();
-        else bulk_wait_read0();
-      }
+    // its chunks of 32 columns, 0 to 2: LSE an even share, the others 64 columns or none
+    const int ch0 = KIND == HEAD_LSE ? bn / 32 * cg / 4 : min(2 * cg, bn / 32);
+    const int ch1 = KIND == HEAD_LSE ? bn / 32 * (cg + 1) / 4 : min(2 * cg + 2, bn / 32);
+    uint8_t* const box = smem + S::OFF_EPI + ew * S::BOX_BYTES;
+    auto box_free = [&]() {                      // its last store has read it
+      if (lane == 0) bulk_wait_read0();
       __syncwarp();
-      return boxes + (S::BOXES == 2 ? (n_box++ & 1) * S::BOX_BYTES : 0);
     };
     // LSE: (max, sum, plain sum) of a warp's columns for the quarter's first warp, two tiles deep
     float* red = reinterpret_cast<float*>(smem + S::OFF_EPI);        // [2][4 quarters][3][4 groups][32]
@@ -439,21 +438,17 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = 0.0f;
             }
+            box_free();
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {               // two boxes of 16 float columns
-              if (n0 + 16 * hf >= p.d) continue;
-              uint8_t* box = next_box();
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<float4*>(box + box_off(lane, j)) =
-                    make_float4(v[16 * hf + 4 * j], v[16 * hf + 4 * j + 1], v[16 * hf + 4 * j + 2], v[16 * hf + 4 * j + 3]);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                if (p.first_piece) tma_store_3d(&maps.o0, box, n0 + 16 * hf, m0, tl.split);
-                else tma_reduce_add_3d(&maps.o0, box, n0 + 16 * hf, m0, tl.split);
-                bulk_commit();
-              }
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<float4*>(box + box128_off(lane, j)) =
+                  make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (p.first_piece) tma_store_3d(&maps.o0, box, n0, m0, tl.split);
+              else tma_reduce_add_3d(&maps.o0, box, n0, m0, tl.split);
+              bulk_commit();
             }
             continue;
           }
@@ -486,23 +481,26 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             }
             if (m0 >= p.m_cap) continue;
           } else {                                        // dw
-            if (n0 >= p.d || p.v0 + m0 >= p.V) continue;
+            if (p.v0 + m0 >= p.V) continue;
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] *= g_out;
           }
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) pk[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-          uint8_t* box = next_box();
+          // two chunks fill the box; the store clips what lies past the width
+          if (ch == ch0) box_free();
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4*>(box + box_off(lane, j)) =
+            *reinterpret_cast<uint4*>(box + box128_off(lane, 4 * (ch - ch0) + j)) =
                 make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+          if (ch + 1 < ch1) continue;
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
-            if (KIND == HEAD_DLOGITS) tma_store_2d(&maps.o0, box, n0, m0);
-            else tma_store_2d(&maps.o1, box, n0, p.v0 + m0);
+          const int b0 = tl.nt * bn + ch0 * 32;
+          if (lane == 0 && (KIND == HEAD_DLOGITS || b0 < p.d)) {
+            if (KIND == HEAD_DLOGITS) tma_store_2d(&maps.o0, box, b0, m0);
+            else tma_store_2d(&maps.o1, box, b0, p.v0 + m0);
             bulk_commit();
           }
         }

@@ -450,12 +450,13 @@ struct HeadShape {
   bool gemv() const { return M <= GEMV_MAX_M && d <= GEMV_MAX_D; }
 };
 
-// The pair form wins where a tile's k is long and there are rows for it.  Device time of the pair and the
-// single form against 51866 entries, us: forward, d = 1280: 64 rows 35 / 32, 448 rows 57 / 62, 14336 rows
-// 1030 / 1128; d = 384: 448 rows 29 / 27, 14336 rows 415 / 374.  Backward, d = 1280: 64 rows 101 / 87, 200
-// rows 117 / 123, 1500 rows 387 / 451; d = 384: 448 rows 77 / 77, 1000 rows 128 / 132, 14336 rows 1556 / 1649.
+// The pair form wins where there are rows for it and, forward, where a tile's k is long.  Device time of the
+// pair and the single form against 51866 entries, us: forward, d = 1280: 64 rows 35 / 32, 448 rows 57 / 62,
+// 14336 rows 1030 / 1128; d = 384: 448 rows 29 / 27, 14336 rows 415 / 374.  Backward, d = 1280: 64 rows
+// 101 / 87, 200 rows 117 / 123, 1500 rows 387 / 451; d = 384: 64 rows 47 / 38, 448 rows 77 / 85, 14336 rows
+// 1556 / 1649.
 HeadShape fwd_shape(int M, int d, int V, int k) { return HeadShape{M, d, V, k, M > 128 && d >= 768}; }
-HeadShape bwd_shape(int M, int d, int V, int k) { return HeadShape{M, d, V, k, M > 128 && (d >= 768 || M > 512)}; }
+HeadShape bwd_shape(int M, int d, int V, int k) { return HeadShape{M, d, V, k, M > 128}; }
 
 bool shape_ok(int M, int d, int V) {
   return M >= 0 && M <= (1 << 24) && d >= 8 && d <= (1 << 16) && d % 8 == 0 && V >= 1 && V <= (1 << 24);
@@ -482,7 +483,7 @@ int lse_width(const HeadShape& h) {
 // Column-tile width of the gradient products: the fewest columns past d (384 = 2 x 192).
 int grad_width(int d) {
   int best = HEAD_BN;
-  for (int bn = HEAD_BN; bn >= 128; bn -= 32)
+  for (int bn = HEAD_BN; bn >= 128; bn -= 64)
     if (ceil_div(d, bn) * bn < ceil_div(d, best) * best) best = bn;
   return best;
 }
@@ -599,12 +600,11 @@ BwdLayout bwd_layout(const HeadShape& h) {
   return L;
 }
 
-bool map2(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t ld, uint32_t bx, uint32_t by,
-          CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B) {
+bool map2(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t ld, uint32_t bx, uint32_t by) {
   const uint64_t dims[2] = {inner, rows};
   const uint64_t str[1] = {ld * 2};
   const uint32_t box[2] = {bx, by};
-  return tma_map_bf16(m, 2, base, dims, str, box, swz);
+  return tma_map_bf16(m, 2, base, dims, str, box);
 }
 
 std::mutex g_head_mu;
@@ -909,17 +909,17 @@ wb_status head_backward(const HeadShape& h, const Targets& t, const float* dloss
   const uint64_t ld = L.piece;
   bool ok = map2(&lm.a0, b.xc, h.d, h.M, h.d, HEAD_BK, 128) &&
             map2(&lm.b0, w, h.d, h.V, h.d, HEAD_BK, h.pair ? HEAD_BN / 2 : HEAD_BN) &&
-            map2(&lm.o0, dl, ld, h.M, ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+            map2(&lm.o0, dl, ld, h.M, ld, 64, 32);
   if (dx) {
     const uint64_t dims[3] = {static_cast<uint64_t>(h.d), static_cast<uint64_t>(h.M), static_cast<uint64_t>(L.splits)};
     const uint64_t str[2] = {static_cast<uint64_t>(h.d) * 4, static_cast<uint64_t>(h.d) * 4 * h.M};
-    const uint32_t box[3] = {16, 32, 1};
+    const uint32_t box[3] = {32, 32, 1};
     ok = ok && map2(&gm.a0, dl, ld, h.M, ld, HEAD_BK, 128) && map2(&gm.b0, w, h.d, h.V, h.d, 64, HEAD_BK) &&
-         tma_map_f32(&gm.o0, 3, slab, dims, str, box, CU_TENSOR_MAP_SWIZZLE_64B);
+         tma_map_f32(&gm.o0, 3, slab, dims, str, box);
   }
   if (dw)
     ok = ok && map2(&gm.a1, dl, ld, h.M, ld, 64, HEAD_BK) && map2(&gm.b1, xs, h.d, h.M, h.d, 64, HEAD_BK) &&
-         map2(&gm.o1, dw, h.d, h.V, h.d, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+         map2(&gm.o1, dw, h.d, h.V, h.d, 64, 32);
   if (!ok) return WB_ECUDA;
   for (int v0 = 0; v0 < h.V; v0 += L.piece) {
     p.v0 = v0;
