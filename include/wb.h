@@ -417,8 +417,8 @@ wb_status wb_layernorm_backward(const void* dy, const void* x, const float* g, c
  * loss, lse: float32 [M].
  * wb_linear_cross_entropy_backward: from dloss[i] (float32 [M]; read only for rows that take part)
  * and the forward pass's lse, the gradients dx (bf16 [M, d], zeros for rows that take no part) and dw
- * (bf16 [V, d]), both overwritten; either may be NULL.  The logits are computed again, a piece of the
- * vocabulary at a time.
+ * (bf16 [V, d]), both overwritten; either may be NULL, and neither may overlap an input.  The logits
+ * are computed again, a piece of the vocabulary at a time.
  *
  * wb_linear_distill: each row has k (1 to 1024) of a teacher's logits, top (float32, bf16 or f16
  * [M, k]) at the vocabulary entries index (int64 [M, k]).  At temperature T, with p the softmax of
@@ -432,7 +432,7 @@ wb_status wb_layernorm_backward(const void* dy, const void* x, const float* g, c
  * Sums, softmax statistics and losses are float32.  softmax - target is rounded to bf16 once, as a
  * factor of the two gradient products, and so is x dloss / max|dloss| for dw.  All sums run in a
  * fixed order: the same call gives the same bits.  Two calls that may overlap on the GPU need a
- * workspace each.  x, w: 16-byte aligned.  WB_EINVAL for bad sizes, pointers or alignment,
+ * workspace each.  x, w, dx, dw: 16-byte aligned; the others to their element.  WB_EINVAL for bad sizes, pointers or alignment,
  * WB_EUNSUPPORTED for another top_dtype, WB_EWORKSPACE for a missing or small workspace. */
 size_t wb_linear_cross_entropy_workspace_bytes(int M, int d, int V);
 wb_status wb_linear_cross_entropy(const void* x, const void* w, const int64_t* labels, int M, int d, int V,

@@ -190,8 +190,9 @@ def test_no_rows(wb):
     assert got["loss"].shape == (0,) and got["dx"].shape == (0, 64) and not got["dw"].any()
 
 
-def test_a_target_past_the_vocabulary_is_a_loss_of_nan(wb):
-    M, d, V = 40, 64, 100
+@pytest.mark.parametrize("M", [12, 40, 300])
+def test_a_target_past_the_vocabulary_is_a_loss_of_nan(wb, M):
+    d, V = 64, 100
     x, w, dloss, g = _data(M, d, V, 8)
     labels = torch.randint(0, V, (M,), generator=g, device=DEV)
     without = labels.clone()
@@ -201,11 +202,41 @@ def test_a_target_past_the_vocabulary_is_a_loss_of_nan(wb):
     assert torch.isnan(got["loss"][5]) and int(torch.isnan(got["loss"]).sum()) == 1
     for n in ("lse", "dx", "dw"):
         assert torch.equal(got[n], ref[n])
+    assert got["lse"][5] == 0
     index = torch.randint(0, V, (M, 4), generator=g, device=DEV)
     index[7, 2] = V + 3
     got = _distill(wb, x, w, torch.randn(M, 4, device=DEV), index, dloss, 1.0)
     assert torch.isnan(got["loss"][7]) and int(torch.isnan(got["loss"]).sum()) == 1
     assert not got["dx"][7].any() and torch.isfinite(got["dw"].float()).all()
+
+
+@pytest.mark.parametrize("M", [6, 60, 400])
+def test_teacher_values_of_absent_entries_do_not_matter(wb, M):
+    d, V, k = 64, 700, 9
+    x, w, dloss, g = _data(M, d, V, 14)
+    index = torch.randint(0, V, (M, k), generator=g, device=DEV)
+    top = torch.randn(M, k, generator=g, device=DEV)
+    gone = torch.rand(M, k, generator=g, device=DEV) < 0.4
+    index[gone] = -5
+    clean = _distill(wb, x, w, top, index, dloss, 1.5)
+    dirty = top.clone()
+    dirty[gone] = torch.tensor([float("nan"), float("inf"), -float("inf")], device=DEV).repeat(M * k)[:int(gone.sum())]
+    for n, v in _distill(wb, x, w, dirty, index, dloss, 1.5).items():
+        assert torch.equal(v, clean[n]), n
+
+
+def test_not_a_number_stays_in_its_row(wb):
+    for M in (7, 50, 400):
+        x, w, dloss, g = _data(M, 64, 700, 15)
+        labels = torch.randint(0, 700, (M,), generator=g, device=DEV)
+        clean = _ce(wb, x, w, labels, dloss, 0.0)
+        x[3, 5] = float("nan")
+        got = _ce(wb, x, w, labels, dloss, 0.0)
+        for n in ("loss", "lse", "dx"):
+            bad = torch.isnan(got[n]).reshape(M, -1)
+            assert bad[3].all() and int(bad.any(1).sum()) == 1
+            keep = torch.arange(M, device=DEV) != 3
+            assert torch.equal(got[n][keep], clean[n][keep])
 
 
 def test_extreme_logits(wb):
@@ -350,9 +381,10 @@ def test_a_training_step_of_a_head(wb):
     l2 = (4 * (torch.special.xlogy(target, target) - target * torch.log_softmax(s / 2, 1)).sum(1))[valid].sum()
     loss64 = (l1 + l2) / int(valid.sum())
     loss64.backward()
+    loss64 = float(loss64.detach())
     # y is rounded to bf16 (2^-8) on its way into the logits; the loss moves by its gradient times that
     got = float(((ce + kl) * dloss).double().sum())
-    assert abs(got - float(loss64)) < 2.0 ** -8 * float(loss64)
+    assert abs(got - loss64) < 2.0 ** -8 * loss64
     # a gradient goes through at most six roundings to bf16 here (y, D, x', dx, their sum, dh), rms 2^-8 / sqrt(3) each
     tol = 6 ** 0.5 * 2.0 ** -8
     for name, a, b in (("dh", dh, t64.grad), ("dw", dw1.double() + dw2.double(), w64.grad), ("dgamma", dgamma, g64.grad), ("dbeta", dbeta, b64.grad)):

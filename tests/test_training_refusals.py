@@ -13,6 +13,7 @@ def lib():
     return _lib.load()
 
 
+OTHER = ctypes.c_void_p(1 << 21)
 FAKE = ctypes.c_void_p(1 << 20)            # aligned, never dereferenced on these paths
 ODD = ctypes.c_void_p((1 << 20) + 2)
 
@@ -64,14 +65,14 @@ def test_head_loss_refusals(lib):
     def ce(x=FAKE, w=FAKE, labels=FAKE, M=8, d=64, V=100, e=0.0, loss=FAKE, lse=FAKE, ws=FAKE, n=BIG):
         return lib.wb_linear_cross_entropy(x, w, labels, M, d, V, e, loss, lse, ws, n, None)
 
-    def ce_bwd(dloss=FAKE, x=FAKE, w=FAKE, labels=FAKE, lse=FAKE, M=8, d=64, V=100, e=0.0, dx=FAKE, dw=FAKE, ws=FAKE, n=BIG):
+    def ce_bwd(dloss=FAKE, x=FAKE, w=FAKE, labels=FAKE, lse=FAKE, M=8, d=64, V=100, e=0.0, dx=OTHER, dw=OTHER, ws=FAKE, n=BIG):
         return lib.wb_linear_cross_entropy_backward(dloss, x, w, labels, lse, M, d, V, e, dx, dw, ws, n, None)
 
     def kl(x=FAKE, w=FAKE, top=FAKE, ty=L.WB_F32, index=FAKE, M=8, d=64, V=100, k=4, T=1.0, loss=FAKE, lse=FAKE, ws=FAKE, n=BIG):
         return lib.wb_linear_distill(x, w, top, ty, index, M, d, V, k, T, loss, lse, ws, n, None)
 
-    def kl_bwd(dloss=FAKE, x=FAKE, w=FAKE, top=FAKE, ty=L.WB_F32, index=FAKE, lse=FAKE, M=8, d=64, V=100, k=4, T=1.0, dx=FAKE,
-               dw=FAKE, ws=FAKE, n=BIG):
+    def kl_bwd(dloss=FAKE, x=FAKE, w=FAKE, top=FAKE, ty=L.WB_F32, index=FAKE, lse=FAKE, M=8, d=64, V=100, k=4, T=1.0, dx=OTHER,
+               dw=OTHER, ws=FAKE, n=BIG):
         return lib.wb_linear_distill_backward(dloss, x, w, top, ty, index, lse, M, d, V, k, T, dx, dw, ws, n, None)
 
     for f in (ce, ce_bwd, kl, kl_bwd):
@@ -84,14 +85,15 @@ def test_head_loss_refusals(lib):
         for name, value in (("labels", None), ("labels", ODD), ("e", -0.5), ("e", 1.0), ("e", float("nan"))):
             assert f(**{name: value}) == L.WB_EINVAL, (f, name, value)
     for f in (kl, kl_bwd):
-        for name, value in (("top", None), ("top", ODD), ("index", None), ("k", 0), ("k", 1025), ("T", 0.0), ("T", -1.0),
+        for name, value in (("top", None), ("top", ODD), ("index", None), ("index", ODD), ("k", 0), ("k", 1025), ("T", 0.0), ("T", -1.0),
                             ("T", float("nan")), ("T", float("inf"))):
             assert f(**{name: value}) == L.WB_EINVAL, (f, name, value)
         assert f(ty=L.WB_E4M3) == L.WB_EUNSUPPORTED
     for f in (ce_bwd, kl_bwd):
         for name, value in (("dloss", None), ("dloss", ODD), ("dx", ODD), ("dw", ODD)):
             assert f(**{name: value}) == L.WB_EINVAL, (f, name, value)
-        assert f(dx=None, dw=None) == L.WB_OK          # nothing wanted, nothing launched
+        assert f(dx=None, dw=None, x=OTHER, w=OTHER) == L.WB_OK       # nothing wanted, nothing launched
+        assert f(dx=OTHER, x=OTHER) == L.WB_EINVAL and f(dw=OTHER, w=OTHER) == L.WB_EINVAL   # a gradient over its input
     assert ce(M=0, x=None, labels=None, ws=None) == L.WB_OK
     assert kl(M=0, x=None, top=None, ws=None) == L.WB_OK
     assert ce_bwd(M=0, x=None, labels=None, ws=None, dw=None) == L.WB_OK

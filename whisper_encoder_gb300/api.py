@@ -311,7 +311,10 @@ def _ln_rows(x, name):
         raise ValueError(f"{name}: expected a bf16, f16 or f32 tensor [..., d]")
     _need(x, x.dtype, name)
     d = x.shape[-1]
-    return (x.numel() // d if d else 0), d, _LN_TYPES[x.dtype]
+    rows = x.numel() // d if d else 0
+    if rows > 0x7FFFFFFF:
+        raise ValueError(f"{name}: more than 2^31 - 1 rows")
+    return rows, d, _LN_TYPES[x.dtype]
 
 
 def layernorm_forward(x, g, b, eps: float = 1e-5, residual=None, stream=None):
@@ -361,6 +364,8 @@ def _head_shape(x, w):
     _need(w, torch.bfloat16, "w")
     if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
         raise ValueError(f"x and w: expected [M, d] and [V, d], got {tuple(x.shape)} and {tuple(w.shape)}")
+    if max(x.shape[0], w.shape[0]) > 1 << 24:
+        raise ValueError("x and w: at most 2^24 rows each")
     return x.shape[0], x.shape[1], w.shape[0]
 
 

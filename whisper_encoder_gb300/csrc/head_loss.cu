@@ -960,12 +960,13 @@ wb_status check_forward(const HeadShape& h, const void* x, const void* w, const 
 wb_status check_backward(const HeadShape& h, const float* dloss, const void* x, const void* w, const float* lse,
                          const void* dx, const void* dw, const void* ws, size_t ws_bytes) {
   if (!dloss || !x || !w || !lse || !aligned16(x) || !aligned16(w) || !aligned4(dloss) || !aligned4(lse) ||
-      (dx && !aligned16(dx)) || (dw && !aligned16(dw)))
+      (dx && !aligned16(dx)) || (dw && !aligned16(dw)) || dx == x || dw == w)
     return WB_EINVAL;
   if (!ws || !aligned16(ws) || ws_bytes < bwd_layout(h).total) return WB_EWORKSPACE;
   return WB_OK;
 }
 
+bool top_aligned(const void* p, int type) { return (reinterpret_cast<uintptr_t>(p) & (type == WB_F32 ? 3u : 1u)) == 0; }
 bool top_ok(int type) { return type == WB_BF16 || type == WB_F16 || type == WB_F32; }
 bool positive(float t) { return t > 0.0f && t < INFINITY; }
 
@@ -1027,7 +1028,7 @@ wb_status wb_linear_distill(const void* x, const void* w, const void* top, int t
   if (!top_ok(top_dtype)) return WB_EUNSUPPORTED;
   if (!shape_ok(M, d, V) || k < 1 || k > HEAD_MAX_K || !positive(temperature)) return WB_EINVAL;
   if (M == 0) return WB_OK;
-  if (!top || !index || !aligned16(top) || !aligned8(index)) return WB_EINVAL;
+  if (!top || !index || !top_aligned(top, top_dtype) || !aligned8(index)) return WB_EINVAL;
   const HeadShape h = fwd_shape(M, d, V, k);
   const wb_status st = check_forward(h, x, w, loss, lse, workspace, workspace_bytes);
   if (st != WB_OK) return st;
@@ -1047,7 +1048,7 @@ wb_status wb_linear_distill_backward(const float* dloss, const void* x, const vo
     if (dw) WB_CUDA(cudaMemsetAsync(dw, 0, static_cast<size_t>(V) * d * 2, s));
     return WB_OK;
   }
-  if (!top || !index || !aligned16(top) || !aligned8(index)) return WB_EINVAL;
+  if (!top || !index || !top_aligned(top, top_dtype) || !aligned8(index)) return WB_EINVAL;
   const HeadShape h = bwd_shape(M, d, V, k);
   const wb_status st = check_backward(h, dloss, x, w, lse, dx, dw, workspace, workspace_bytes);
   if (st != WB_OK) return st;
