@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(lnt_warps(W) * 32)
 // block order: no atomics, the same result every time.  A team's rows come through its own ring of shared
 // memory, filled by one lane with bulk copies, and are read from there twice (for the row's sums, then for
 // dx), so that neither the rows in flight nor the row at hand cost registers.  The arithmetic is on packed
-// pairs.  Measured at 48000 x 1280 bf16 with dt: 104 us (4.7 TB/s); rows held in registers and read directly 274 us
+// pairs.  Measured at 48000 x 1280 bf16 with dt: 98 us (5.0 TB/s); rows held in registers and read directly 274 us
 // (216 registers, 8 warps an SM); four resident blocks a SM instead of one write more partial rows (5120 wide: 77 us against 72 with the forward pass).
 // Widths whose rows do not start on 16 bytes are read directly, element by element.
 constexpr int LNT_WARPS = 8;     // per block of the element-wise kernel, at most
@@ -202,48 +202,12 @@ __device__ __forceinline__ uint64_t pair_of(const Raw& r, int i, T*) {
   return f32x2_pack(to_f32<T>(r.e[2 * i]), to_f32<T>(r.e[2 * i + 1]));
 }
 
-constexpr int lnb_warps(int W) { return W < 8 ? 12 : 8; }     // warps of a block, one an SM: 12 / W teams
+// Warps of a block, one block an SM.  Measured with 8 / 12 / 16: 48000 x 1280 bf16 with dt (W = 1) 108 / 101 / 98 us;
+// both directions of 3001 x 5120 f16 (W = 4) 74 / 70 / 73 us.
+constexpr int lnb_warps(int W) { return W < 4 ? 16 : W == 4 ? 12 : 8; }
 
-// Sums of R pairs of values over the team, as team_sum.  With two pairs the first two shuffle steps halve
-// what a lane keeps: 6 shuffles instead of 20.
-template <int W, int R>
-__device__ __forceinline__ void team_sums(float (&v)[2 * R], float4 (*red)[W], int team, int warp_in_team, int lane,
-                                          int slot) {
-  if (R == 1) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
-      v[1] += __shfl_xor_sync(0xffffffffu, v[1], o);
-    }
-  } else {
-    const bool up = lane & 16, odd = lane & 8;
-    const float a = (up ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16);
-    const float b = (up ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 16);
-    float s = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xffffffffu, s, 8 * i);
-  }
-  if (W == 1) return;
-  if (lane == 0) red[slot][warp_in_team] = make_float4(v[0], v[1], R == 2 ? v[2] : 0.0f, R == 2 ? v[3] : 0.0f);
-  asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(W * 32) : "memory");
-#pragma unroll
-  for (int i = 0; i < 2 * R; ++i) v[i] = 0.0f;
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    const float4 q = red[slot][i];
-    v[0] += q.x;
-    v[1] += q.y;
-    if (R == 2) {
-      v[2] += q.z;
-      v[3] += q.w;
-    }
-  }
-}
-
-// Partial rows part[block] = [dg (d) | db (d)]; null where the caller wants dx alone.  R rows a step.
-template <typename T, int VEC, int NV, int W, int R>
+// Partial rows part[block] = [dg (d) | db (d)]; null where the caller wants dx alone.
+template <typename T, int VEC, int NV, int W>
 __global__ void __launch_bounds__(lnb_warps(W) * 32, 1)
     ln_train_bwd_kernel(const T* __restrict__ dy, const T* __restrict__ x, const float* __restrict__ g,
                         const float2* __restrict__ stats, const T* __restrict__ dt, int rows, int d,
@@ -253,7 +217,7 @@ __global__ void __launch_bounds__(lnb_warps(W) * 32, 1)
   extern __shared__ __align__(16) uint8_t ring[];          // [teams][stages][x, dy, dt][row]; at the end [teams][2 d] sums
   __shared__ uint64_t full[TEAMS][LNT_STAGES];
   __shared__ int abort_flag;
-  __shared__ float4 red[TEAMS][2][W];
+  __shared__ float2 red[TEAMS][2][W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int team = warp / W, wt = warp % W;
   const float inv_d = 1.0f / static_cast<float>(d);
@@ -288,108 +252,73 @@ __global__ void __launch_bounds__(lnb_warps(W) * 32, 1)
   auto stats_of = [&](long long row) {
     return row < rows && in_bounds(err, row, 1, rows, SITE_LNT_STATS) ? __ldg(stats + row) : make_float2(0.0f, 0.0f);
   };
-  float2 ahead[R];                           // statistics of the next step's rows, loaded a step early
-#pragma unroll
-  for (int q = 0; q < R; ++q) ahead[q] = stats_of(first + q * step);
-  int stage = 0, slot = 0;                   // stages is a multiple of R
+  float2 ahead = stats_of(first);            // statistics of the next row, loaded a row early
+  int stage = 0, slot = 0;
   uint32_t parity = 0;
-  for (long long row0 = first; row0 < rows; row0 += R * step, slot ^= 1) {
-    const uint8_t* at[R];
-    uint64_t nm2[R], rs2[R], c1p[R], c2p[R];
-    bool on[R];                              // the last step may have one row less
-#pragma unroll
-    for (int q = 0; q < R; ++q) {
-      const long long row = row0 + q * step;
-      on[q] = row < rows;
-      const float2 st = ahead[q];
-      ahead[q] = stats_of(row + R * step);
-      nm2[q] = f32x2_pack(-st.x, -st.x);
-      rs2[q] = f32x2_pack(st.y, st.y);
-      c1p[q] = c2p[q] = 0;
-      at[q] = mine + static_cast<size_t>(stage + q) * stage_bytes;
-    }
+  for (long long row = first; row < rows; row += step, slot ^= 1) {
+    const long long base = row * d;
+    const float2 st = ahead;
+    ahead = stats_of(row + step);
+    const uint64_t nm2 = f32x2_pack(-st.x, -st.x), rs2 = f32x2_pack(st.y, st.y);
+    const uint8_t* at = mine + static_cast<size_t>(stage) * stage_bytes;
     // a wait that runs out marks the error word and goes on: every thread keeps to the same barriers
-#pragma unroll
-    for (int q = 0; q < R; ++q)
-      if (on[q]) mbar_wait(&full[team][stage + q], parity, err, &abort_flag, 31);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int col = ((i * W + wt) * 32 + lane) * VEC;
-      if (col >= d) continue;
-      float gg[VEC];
-      load_params<VEC>(g + col, gg);
-#pragma unroll
-      for (int q = 0; q < R; ++q) {
-        if (!on[q]) continue;
-        const Raw xv = *reinterpret_cast<const Raw*>(at[q] + col * sizeof(T));
-        const Raw yv = *reinterpret_cast<const Raw*>(at[q] + bytes + col * sizeof(T));
-#pragma unroll
-        for (int j = 0; j < NP; ++j) {
-          const int e = i * NP + j;
-          const uint64_t y2 = pair_of(yv, j, static_cast<T*>(nullptr));
-          const uint64_t h2 = f32x2_mul(f32x2_add(pair_of(xv, j, static_cast<T*>(nullptr)), nm2[q]), rs2[q]);
-          const uint64_t u2 = f32x2_mul(f32x2_pack(gg[2 * j], gg[2 * j + 1]), y2);
-          ag[e] = f32x2_fma(y2, h2, ag[e]);
-          ab[e] = f32x2_add(ab[e], y2);
-          c1p[q] = f32x2_add(c1p[q], u2);
-          c2p[q] = f32x2_fma(u2, h2, c2p[q]);
-        }
-      }
-    }
-    float c[2 * R];
-#pragma unroll
-    for (int q = 0; q < R; ++q) {
-      float lo, hi;
-      f32x2_unpack(c1p[q], lo, hi);
-      c[2 * q] = lo + hi;
-      f32x2_unpack(c2p[q], lo, hi);
-      c[2 * q + 1] = lo + hi;
-    }
-    team_sums<W, R>(c, red[team], team, wt, lane, slot);
-    uint64_t c12[R], c22[R];
-#pragma unroll
-    for (int q = 0; q < R; ++q) {
-      const float m1 = -c[2 * q] * inv_d, m2 = -c[2 * q + 1] * inv_d;
-      c12[q] = f32x2_pack(m1, m1);
-      c22[q] = f32x2_pack(m2, m2);
-    }
+    mbar_wait(&full[team][stage], parity, err, &abort_flag, 31);
+    uint64_t c1p = 0, c2p = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = ((i * W + wt) * 32 + lane) * VEC;
       if (col >= d) continue;
+      const Raw xv = *reinterpret_cast<const Raw*>(at + col * sizeof(T));
+      const Raw yv = *reinterpret_cast<const Raw*>(at + bytes + col * sizeof(T));
       float gg[VEC];
       load_params<VEC>(g + col, gg);
 #pragma unroll
-      for (int q = 0; q < R; ++q) {
-        const long long base = (row0 + q * step) * d;
-        if (!on[q] || !in_bounds(err, base + col, VEC, n_el, SITE_LNT_Y)) continue;
-        const Raw xv = *reinterpret_cast<const Raw*>(at[q] + col * sizeof(T));
-        const Raw yv = *reinterpret_cast<const Raw*>(at[q] + bytes + col * sizeof(T));
-        Raw tv, o;
-        if (dt) tv = *reinterpret_cast<const Raw*>(at[q] + 2 * bytes + col * sizeof(T));
-#pragma unroll
-        for (int j = 0; j < NP; ++j) {
-          const uint64_t h2 = f32x2_mul(f32x2_add(pair_of(xv, j, static_cast<T*>(nullptr)), nm2[q]), rs2[q]);
-          const uint64_t u2 =
-              f32x2_fma(f32x2_pack(gg[2 * j], gg[2 * j + 1]), pair_of(yv, j, static_cast<T*>(nullptr)), c12[q]);
-          const uint64_t in = f32x2_fma(h2, c22[q], u2);
-          float lo, hi;
-          f32x2_unpack(dt ? f32x2_fma(in, rs2[q], pair_of(tv, j, static_cast<T*>(nullptr))) : f32x2_mul(in, rs2[q]), lo, hi);
-          o.e[2 * j] = from_f32<T>(lo);
-          o.e[2 * j + 1] = from_f32<T>(hi);
-        }
-        *reinterpret_cast<Raw*>(dx + base + col) = o;
+      for (int j = 0; j < NP; ++j) {
+        const int e = i * NP + j;
+        const uint64_t y2 = pair_of(yv, j, static_cast<T*>(nullptr));
+        const uint64_t h2 = f32x2_mul(f32x2_add(pair_of(xv, j, static_cast<T*>(nullptr)), nm2), rs2);
+        const uint64_t u2 = f32x2_mul(f32x2_pack(gg[2 * j], gg[2 * j + 1]), y2);
+        ag[e] = f32x2_fma(y2, h2, ag[e]);
+        ab[e] = f32x2_add(ab[e], y2);
+        c1p = f32x2_add(c1p, u2);
+        c2p = f32x2_fma(u2, h2, c2p);
       }
     }
-    // the team has read the stages for the second time: its next rows may come
+    float lo, hi, c1, c2;
+    f32x2_unpack(c1p, lo, hi);
+    c1 = lo + hi;
+    f32x2_unpack(c2p, lo, hi);
+    c2 = lo + hi;
+    const float2 c = team_sum<W>(c1, c2, red[team], team, wt, lane, slot);
+    c1 = -c.x * inv_d;
+    c2 = -c.y * inv_d;
+    const uint64_t c12 = f32x2_pack(c1, c1), c22 = f32x2_pack(c2, c2);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = ((i * W + wt) * 32 + lane) * VEC;
+      if (col >= d || !in_bounds(err, base + col, VEC, n_el, SITE_LNT_Y)) continue;
+      const Raw xv = *reinterpret_cast<const Raw*>(at + col * sizeof(T));
+      const Raw yv = *reinterpret_cast<const Raw*>(at + bytes + col * sizeof(T));
+      float gg[VEC];
+      load_params<VEC>(g + col, gg);
+      Raw tv, o;
+      if (dt) tv = *reinterpret_cast<const Raw*>(at + 2 * bytes + col * sizeof(T));
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const uint64_t h2 = f32x2_mul(f32x2_add(pair_of(xv, j, static_cast<T*>(nullptr)), nm2), rs2);
+        const uint64_t u2 = f32x2_fma(f32x2_pack(gg[2 * j], gg[2 * j + 1]), pair_of(yv, j, static_cast<T*>(nullptr)), c12);
+        const uint64_t in = f32x2_fma(h2, c22, u2);
+        f32x2_unpack(dt ? f32x2_fma(in, rs2, pair_of(tv, j, static_cast<T*>(nullptr))) : f32x2_mul(in, rs2), lo, hi);
+        o.e[2 * j] = from_f32<T>(lo);
+        o.e[2 * j + 1] = from_f32<T>(hi);
+      }
+      *reinterpret_cast<Raw*>(dx + base + col) = o;
+    }
+    // the team has read the stage for the second time: its next row may come
     if (W == 1) __syncwarp();
     else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(W * 32) : "memory");
-    if (feeder)
-#pragma unroll
-      for (int q = 0; q < R; ++q)
-        if (row0 + (q + stages) * step < rows) issue(row0 + (q + stages) * step, stage + q);
-    stage += R;
-    if (stage >= stages) { stage = 0; parity ^= 1u; }
+    if (feeder && row + stages * step < rows) issue(row + stages * step, stage);
+    if (++stage == stages) { stage = 0; parity ^= 1u; }
   }
   if (!part) return;
   float* dst = part + static_cast<long long>(blockIdx.x) * 2 * d;
@@ -537,7 +466,7 @@ Spread spread(int rows, int d, int dtype, int tensors) {
   if (s.vec) {
     s.warps = team_warps(d);
     const int fit = 200 * 1024 / (lnb_warps(s.warps) / s.warps * d * es * tensors);
-    s.stages = fit >= 4 ? 4 : fit >= 2 ? 2 : 1;            // in pairs, where two rows fit
+    s.stages = fit < LNT_STAGES ? fit : LNT_STAGES;
   } else {
     const int need = (d + 32 * LNT_WARPS - 1) / (32 * LNT_WARPS);
     s.nv = need <= 2 ? need : need <= 4 ? 4 : need <= 6 ? 6 : need <= 10 ? 10 : need <= 20 ? 20 : 40;
@@ -588,21 +517,17 @@ cudaError_t ring_attr(K kern, uint64_t* done) {
   return e;
 }
 
-template <typename T, int VEC, int NV, int W, int R>
-cudaError_t go_rows(const BwdArgs<T>& a, const Spread& sp, cudaStream_t s) {
+template <typename T, int VEC, int NV, int W>
+cudaError_t go(const BwdArgs<T>& a, const Spread& sp, cudaStream_t s) {
   static uint64_t done = 0;
-  const cudaError_t e = ring_attr(ln_train_bwd_kernel<T, VEC, NV, W, R>, &done);
+  const cudaError_t e = ring_attr(ln_train_bwd_kernel<T, VEC, NV, W>, &done);
   if (e != cudaSuccess) return e;
   constexpr size_t TEAMS = lnb_warps(W) / W;
   size_t smem = TEAMS * sp.stages * (a.dt ? 3 : 2) * a.d * sizeof(T);
   const size_t sums = TEAMS * 2 * a.d * sizeof(float);
   if (smem < sums) smem = sums;
-  return launch_pdl(ln_train_bwd_kernel<T, VEC, NV, W, R>, dim3(sp.blocks), dim3(lnb_warps(W) * 32), smem, s, a.dy, a.x,
+  return launch_pdl(ln_train_bwd_kernel<T, VEC, NV, W>, dim3(sp.blocks), dim3(lnb_warps(W) * 32), smem, s, a.dy, a.x,
                     a.g, a.stats, a.dt, a.rows, a.d, a.dx, a.part, sp.stages, a.err);
-}
-template <typename T, int VEC, int NV, int W>
-cudaError_t go(const BwdArgs<T>& a, const Spread& sp, cudaStream_t s) {
-  return sp.stages >= 2 ? go_rows<T, VEC, NV, W, 2>(a, sp, s) : go_rows<T, VEC, NV, W, 1>(a, sp, s);
 }
 template <typename T, int NV>
 cudaError_t go_any(const BwdArgs<T>& a, const Spread& sp, cudaStream_t s) {
