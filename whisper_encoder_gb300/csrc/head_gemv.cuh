@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(GEMV_WARPS * 32, 1) head_gemv_kernel(const __g
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[mt][i] = 0.0f;
-    constexpr int U = 5;                                   // blocks of 32 k whose loads are in flight together
+    constexpr int U = 4;                                   // blocks of 32 k whose loads are in flight together
     for (int kb = 0; kb * 4 < d8; kb += U) {
       uint4 a[U], b[U];
 #pragma unroll

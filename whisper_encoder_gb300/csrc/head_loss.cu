@@ -315,6 +315,14 @@ __global__ void __launch_bounds__(FIN_ROWS* FIN_SLICES) head_finish_kernel(const
     const int row = r0 + rx;
     const bool on = row < n;
     float m = -INFINITY, l = 0.0f, s = 0.0f;
+    // what the row's last step needs, asked for before the tiles' values
+    int src = row, state = 1;
+    float sy = 0.0f;
+    if (sl == 0 && on && in_bounds(a.err, row, 1, a.M, SITE_HEAD_ROWS)) {
+      if (a.row_src) src = a.row_src[row];
+      else state = target_state(a.labels, a.tgt_cnt, a.V, row);
+      if (!a.tgt_p) sy = a.tgt_s[row];
+    }
     if (on) {
 #pragma unroll 8
       for (int t = sl; t < a.n_tiles; t += FIN_SLICES) {
@@ -344,15 +352,11 @@ __global__ void __launch_bounds__(FIN_ROWS* FIN_SLICES) head_finish_kernel(const
       }
       const float lse = fmaf(mo, 0.69314718055994531f, logf(l));
       row_lse[rx] = lse;
-      const int src = !a.row_src ? row : in_bounds(a.err, row, 1, a.M, SITE_HEAD_ROWS) ? a.row_src[row] : 0;
       if (in_bounds(a.err, src, 1, a.M, SITE_HEAD_ROWS)) {
-        int state = 1;                       // as row_state
-        if (!a.row_src) state = target_state(a.labels, a.tgt_cnt, a.V, src);
         a.lse[src] = state == 1 ? lse : 0.0f;
         if (state != 1) {
           a.loss[src] = state == 0 ? 0.0f : __int_as_float(0x7fc00000);
         } else if (!a.tgt_p) {
-          const float sy = a.tgt_s[row];
           a.loss[src] = a.smoothing > 0.0f
                             ? (1.0f - a.smoothing) * (lse - sy) + a.smoothing * (lse - s / static_cast<float>(a.V))
                             : lse - sy;
