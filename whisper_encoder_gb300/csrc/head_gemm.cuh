@@ -11,9 +11,12 @@
 // MN-major A tile for dw, so nothing is transposed in memory.
 //
 // Two forms.  PAIR: two CTAs (a cluster, one SM each) make one tile of 256 rows x up to 256 columns: each
-// loads 128 rows of A and half of B's columns, so that a byte from L2 feeds twice the MMAs.  Single: one
-// CTA, 128 rows.  The pair keeps the tensor cores busier where the operands come from L2 for long
-// (@@); the single form has the finer rows, starts sooner and wins where a product is short.
+// loads 128 rows of A and half of B's columns: 32 KB per 64 of k, which an SM's 64 bytes a clock from L2
+// bring in the 512 clocks of its MMAs.  Single: one CTA, 128 rows: 48 KB for the same MMAs.  The tensor pipe
+// was active for 78 % (pair) and 73 % (single) of the SMs' time in HEAD_DLOGITS, 81 % and 72 to 79 % in the
+// gradient products (3000 x 1280 against 20000); with the loads taken out the pair's forward product is 17 %
+// faster, with three of four MMAs taken out 35 %.  The single form has the finer rows, starts sooner and wins
+// where a product is short.
 // Per CTA, as in the other GEMMs of this library: warp 0 lane 0 loads a ring of stages with TMA; warp 1
 // lane 0 (of the pair's first CTA) issues the MMAs into one of two 256-column TMEM accumulators; warps 2-17
 // run the epilogue of the tile before on their CTA's 128 rows: warp w has TMEM lane quarter w % 4 and a
@@ -37,8 +40,8 @@ struct HeadSmem {
   static constexpr int MN_BLOCK = 64 * HEAD_BK * 2;      // 64 M / N elements x 64 k of an MN-major tile
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int STAGES = (PAIR ? 5 : 3) + (KIND == HEAD_LSE);
-  // 32 rows x 128 bytes per epilogue warp (128-byte swizzle): a bulk store goes row by row, and rows of 64
-  // bytes were as slow as these (@@)
+  // 32 rows x 128 bytes per epilogue warp (128-byte swizzle); with rows of 64 bytes and a stage more the
+  // backward pass of 10752 x 1280 took 2.80 ms against 2.71
   static constexpr int BOX_BYTES = 32 * 128;
   static constexpr int OFF_EPI = STAGES * STAGE_BYTES;
   static constexpr int OFF_BAR = OFF_EPI + (KIND == HEAD_LSE ? 2 * 4 * 3 * 128 * 4 : GEMM_EPI_WARPS * BOX_BYTES);

