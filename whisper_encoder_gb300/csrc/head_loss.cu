@@ -64,10 +64,11 @@ __global__ void __launch_bounds__(LIST_THREADS)
     target_lists_kernel(const T* __restrict__ top, const int64_t* __restrict__ index, int M, int k, int V,
                         float inv_t, int* __restrict__ out_idx, float* __restrict__ out_p, int* __restrict__ out_cnt,
                         uint32_t* err) {
-  extern __shared__ int sm_list[];
-  int* id = sm_list;                                       // [k]
-  float* pr = reinterpret_cast<float*>(sm_list + k);       // [k]
-  float* merged = pr + k;                                  // [k]
+  extern __shared__ __align__(16) int sm_list[];
+  const int kp = (k + 3) & ~3;                             // read four at a time
+  int* id = sm_list;                                       // [kp]
+  float* pr = reinterpret_cast<float*>(sm_list + kp);      // [kp]
+  int* lead = sm_list + 2 * kp;                            // [kp]: the index, where the entry stands for it
   __shared__ float sm[LIST_THREADS / 32];
   __shared__ int n_bad, n_out;
   grid_dependency_wait();
@@ -78,8 +79,10 @@ __global__ void __launch_bounds__(LIST_THREADS)
   if (threadIdx.x == 0) n_bad = n_out = 0;
   __syncthreads();
   float mx = -INFINITY;
-  for (int j = threadIdx.x; j < k; j += LIST_THREADS) {
-    if (!in_bounds(err, base + j, 1, n_el, SITE_HEAD_LIST)) { id[j] = -1; continue; }
+  for (int j = threadIdx.x; j < kp; j += LIST_THREADS) {
+    id[j] = -1;
+    pr[j] = 0.0f;
+    if (j >= k || !in_bounds(err, base + j, 1, n_el, SITE_HEAD_LIST)) continue;
     const long long v = index[base + j];
     const float t = teacher_f32<T>(top[base + j]) * inv_t;
     if (v >= V) atomicAdd(&n_bad, 1);
@@ -97,28 +100,42 @@ __global__ void __launch_bounds__(LIST_THREADS)
   }
   sum = block_reduce(sum, false, sm);
   // entry j stands for its index if no earlier entry has it; it then has the sum of all of them
-  for (int j = threadIdx.x; j < k; j += LIST_THREADS) {
-    float p = -1.0f;
-    if (id[j] >= 0) {
-      bool first = true;
-      p = 0.0f;
-      for (int q = 0; q < k; ++q) {
-        if (id[q] != id[j]) continue;
-        if (q < j) first = false;
-        p += pr[q];
-      }
-      p = first && !(p == 0.0f) ? p / sum : -1.0f;
+  constexpr int NONE = 0x7fffffff;
+  for (int j = threadIdx.x; j < kp; j += LIST_THREADS) {
+    const int my = id[j];
+    bool first = my >= 0;
+    float p = 0.0f;
+    for (int q = 0; first && q < kp; q += 4) {
+      const int4 o = *reinterpret_cast<const int4*>(id + q);
+      if (o.x != my && o.y != my && o.z != my && o.w != my) continue;
+      const int e[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (e[u] == my) {
+          first = first && q + u >= j;
+          p += pr[q + u];
+        }
     }
-    merged[j] = p;
+    // a weight of zero is no entry
+    lead[j] = first && !(p == 0.0f) ? my : NONE;
   }
   __syncthreads();
   for (int j = threadIdx.x; j < k; j += LIST_THREADS) {
-    if (merged[j] == -1.0f) continue;
+    const int my = lead[j];
+    if (my == NONE) continue;
     int rank = 0;
-    for (int q = 0; q < k; ++q) rank += merged[q] != -1.0f && id[q] < id[j];
+    float p = 0.0f;
+    for (int q = 0; q < kp; q += 4) {
+      const int4 o = *reinterpret_cast<const int4*>(lead + q), e = *reinterpret_cast<const int4*>(id + q);
+      rank += (o.x < my) + (o.y < my) + (o.z < my) + (o.w < my);
+      if (e.x == my) p += pr[q];
+      if (e.y == my) p += pr[q + 1];
+      if (e.z == my) p += pr[q + 2];
+      if (e.w == my) p += pr[q + 3];
+    }
     if (in_bounds(err, base + rank, 1, n_el, SITE_HEAD_LIST)) {
-      out_idx[base + rank] = id[j];
-      out_p[base + rank] = merged[j];
+      out_idx[base + rank] = my;
+      out_p[base + rank] = p / sum;
     }
     atomicAdd(&n_out, 1);
   }
@@ -173,6 +190,17 @@ __global__ void __launch_bounds__(ROWS_THREADS) rows_kernel(const __grid_constan
   grid_dependents_launch();
   const int r0 = blockIdx.x * a.rows_per_block;
   const int r1 = min(r0 + a.rows_per_block, a.M);
+  // this warp's first row of x is asked for before its place is known
+  constexpr int PRE = 5;
+  const int nv = a.d / 8;
+  uint4 pre[PRE];
+  const uint4* pre_src = reinterpret_cast<const uint4*>(a.x + static_cast<long long>(r0 + warp) * a.d);
+#pragma unroll
+  for (int q = 0; q < PRE; ++q)
+    if (r0 + warp < r1 && lane + 32 * q < nv &&
+        in_bounds(a.err, static_cast<long long>(r0 + warp) * a.d + 8 * (lane + 32 * q), 8,
+                  static_cast<long long>(a.M) * a.d, SITE_HEAD_X))
+      pre[q] = pre_src[lane + 32 * q];
   // rows that take part before this block's
   int before = 0;
   for (int i = threadIdx.x; i < r0; i += ROWS_THREADS) before += row_state(a, i) == 1;
@@ -227,7 +255,6 @@ __global__ void __launch_bounds__(ROWS_THREADS) rows_kernel(const __grid_constan
   } else if (a.xs) {
     g = *a.g_max;
   }
-  const int nv = a.d / 8;
   const long long n_el = static_cast<long long>(a.M) * a.d;
   for (int i = r0 + warp; i < r1; i += ROWS_THREADS / 32) {
     const int dst = at[i - r0];
@@ -241,9 +268,8 @@ __global__ void __launch_bounds__(ROWS_THREADS) rows_kernel(const __grid_constan
     const uint4* src = reinterpret_cast<const uint4*>(a.x + static_cast<long long>(i) * a.d);
     uint4* to = reinterpret_cast<uint4*>(a.xc + static_cast<long long>(dst) * a.d);
     const float r = a.xs ? (g > 0.0f ? a.dloss[i] / g : a.dloss[i]) : 0.0f;   // g = 0: all zero (or not a number)
-    for (int v = lane; v < nv; v += 32) {
-      if (!in_bounds(a.err, static_cast<long long>(dst) * a.d + 8 * v, 8, n_el, SITE_HEAD_X)) continue;
-      const uint4 u = src[v];
+    auto put = [&](int v, uint4 u) {
+      if (!in_bounds(a.err, static_cast<long long>(dst) * a.d + 8 * v, 8, n_el, SITE_HEAD_X)) return;
       to[v] = u;
       if (a.xs) {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -253,7 +279,14 @@ __global__ void __launch_bounds__(ROWS_THREADS) rows_kernel(const __grid_constan
           o[q] = pack_bf16(__uint_as_float(w[q] << 16) * r, __uint_as_float(w[q] & 0xffff0000u) * r);
         *reinterpret_cast<uint4*>(a.xs + static_cast<long long>(dst) * a.d + 8 * v) = make_uint4(o[0], o[1], o[2], o[3]);
       }
+    };
+    int v = lane;
+    if (i == r0 + warp) {
+#pragma unroll
+      for (int q = 0; q < PRE; ++q, v += 32)
+        if (v < nv) put(v, pre[q]);
     }
+    for (; v < nv; v += 32) put(v, src[v]);
   }
   // x' up to the next whole block of 64 rows is a factor of the sum over rows: zeros
   if (a.xs && blockIdx.x == gridDim.x - 1) {
@@ -315,7 +348,13 @@ __global__ void __launch_bounds__(FIN_ROWS* FIN_SLICES) head_finish_kernel(const
     const int row = r0 + rx;
     const bool on = row < n;
     float m = -INFINITY, l = 0.0f, s = 0.0f;
-    // what the row's last step needs, asked for before the tiles' values
+    // what the row's last step needs, asked for before the tiles' values; distillation: this warp's row of it
+    const int tr = r0 + sl;
+    int t_src = tr, t_cnt = 0;
+    if (a.tgt_p && tr < n && in_bounds(a.err, tr, 1, a.M, SITE_HEAD_ROWS)) {
+      if (a.row_src) t_src = a.row_src[tr];
+      if (in_bounds(a.err, t_src, 1, a.M, SITE_HEAD_ROWS)) t_cnt = a.tgt_cnt[t_src];
+    }
     int src = row, state = 1;
     float sy = 0.0f;
     if (sl == 0 && on && in_bounds(a.err, row, 1, a.M, SITE_HEAD_ROWS)) {
@@ -364,24 +403,19 @@ __global__ void __launch_bounds__(FIN_ROWS* FIN_SLICES) head_finish_kernel(const
       }
     }
     __syncthreads();
+    static_assert(FIN_ROWS == FIN_SLICES, "a warp a row");
     if (a.tgt_p) {       // distillation: a warp per row over its entries
-      for (int r = sl; r < FIN_ROWS && r0 + r < n; r += FIN_SLICES) {
-        const int src = a.row_src ? a.row_src[r0 + r] : r0 + r;
-        if (!in_bounds(a.err, src, 1, a.M, SITE_HEAD_ROWS)) continue;
-        const float lse = row_lse[r];
-        const int cnt = a.tgt_cnt[src];
-        if (cnt <= 0) continue;
-        float t = 0.0f;
-        for (int j = rx; j < cnt; j += 32) {
-          const long long i = static_cast<long long>(src) * a.k + j, is = static_cast<long long>(r0 + r) * a.k + j;
-          if (!in_bounds(a.err, i, 1, static_cast<long long>(a.M) * a.k, SITE_HEAD_TARGET)) continue;
-          const float p = a.tgt_p[i];
-          t += p * (logf(p) - a.tgt_s[is] * a.inv_t + lse);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-        if (rx == 0) a.loss[src] = t / (a.inv_t * a.inv_t);
+      const float lse = row_lse[sl];
+      float t = 0.0f;
+      for (int j = rx; j < t_cnt; j += 32) {
+        const long long i = static_cast<long long>(t_src) * a.k + j, is = static_cast<long long>(tr) * a.k + j;
+        if (!in_bounds(a.err, i, 1, static_cast<long long>(a.M) * a.k, SITE_HEAD_TARGET)) continue;
+        const float p = a.tgt_p[i];
+        t += p * (logf(p) - a.tgt_s[is] * a.inv_t + lse);
       }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      if (rx == 0 && t_cnt > 0) a.loss[t_src] = t / (a.inv_t * a.inv_t);
       __syncthreads();
     }
   }
@@ -407,6 +441,12 @@ __global__ void __launch_bounds__(256)
     const bool on = w < work;
     const int row = on ? static_cast<int>(w / nv) : 0, v = on ? static_cast<int>(w % nv) : 0;
     float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    int src = 0;
+    float f = 0.0f;
+    if (on && sl == 0) {
+      src = row_src[row];
+      if (in_bounds(err, src, 1, M, SITE_HEAD_ROWS)) f = dloss[src] * temperature;
+    }
     if (on) {
 #pragma unroll 4
       for (int q = sl; q < splits; q += lanes) {
@@ -428,9 +468,6 @@ __global__ void __launch_bounds__(256)
         for (int j = 0; j < 8; ++j) s[j] += sm[q * per_block + vx][j];
     }
     if (!on) continue;
-    const int src = row_src[row];
-    if (!in_bounds(err, src, 1, M, SITE_HEAD_ROWS)) continue;
-    const float f = dloss[src] * temperature;
     const long long o = static_cast<long long>(src) * d + 8 * v;
     if (in_bounds(err, o, 8, per_slab, SITE_HEAD_DX))
       *reinterpret_cast<uint4*>(dx + o) = make_uint4(pack_bf16(s[0] * f, s[1] * f), pack_bf16(s[2] * f, s[3] * f),
@@ -466,15 +503,15 @@ bool shape_ok(int M, int d, int V) {
   return M >= 0 && M <= (1 << 24) && d >= 8 && d <= (1 << 16) && d % 8 == 0 && V >= 1 && V <= (1 << 24);
 }
 
-// Column-tile width of the forward product: the one whose rounds of tiles over the device end first.  A tile
+// Column-tile width of the products x w^T: the one whose rounds of tiles over the device end first.  A tile
 // costs about 100 columns on top of its own (a stage's round trip through the ring bounds narrow tiles):
 // measured at 1500 rows of 1280, 256 / 192 / 128 / 64 columns 127 / 148 / 208 / 383 us.  So 256 nearly always;
 // 192 where it takes as few rounds (one tile of rows, 51866 entries: 31.5 us against 34.7).
-int lse_width(const HeadShape& h) {
+int logits_width(const HeadShape& h, int vc) {
   int best = HEAD_BN;
   long long cost = -1;
   for (int bn = HEAD_BN; bn >= 64; bn -= 32) {
-    const long long tiles = static_cast<long long>(h.row_tiles()) * ceil_div(h.V, bn);
+    const long long tiles = static_cast<long long>(h.row_tiles()) * ceil_div(vc, bn);
     const long long c = (tiles + h.slots() - 1) / h.slots() * (bn + 100);
     if (cost < 0 || c < cost) {
       cost = c;
@@ -528,7 +565,7 @@ FwdLayout fwd_layout(const HeadShape& h) {
   FwdLayout L;
   L.r = rows_layout(c, h);
   L.part_ld = (static_cast<long long>(h.M) + 31) / 32 * 32;
-  L.bn = lse_width(h);
+  L.bn = logits_width(h, h.V);
   L.n_tiles = h.gemv() ? HEAD_SMS : ceil_div(h.V, L.bn);
   L.part = c.take(static_cast<size_t>(L.n_tiles) * L.part_ld * sizeof(float2));
   L.part_sum = h.k > 0 ? 0 : c.take(static_cast<size_t>(L.n_tiles) * L.part_ld * sizeof(float));
@@ -540,6 +577,7 @@ FwdLayout fwd_layout(const HeadShape& h) {
 struct BwdLayout {
   RowsLayout r;
   size_t g_max, xs, dl, slab, total;
+  int bn;                      // column-tile width of the logits
   int piece, splits;           // vocabulary rows per piece (a multiple of 256), slabs of dx
 };
 
@@ -596,6 +634,7 @@ BwdLayout bwd_layout(const HeadShape& h) {
     }
   }
   L.splits = dx_splits(h, L.piece);
+  L.bn = logits_width(h, L.piece) / 64 * 64;     // whole staging boxes; past the piece the store is clipped
   const size_t m = static_cast<size_t>(h.M);
   L.g_max = c.take(256);
   L.xs = c.take(m * h.d * 2);
@@ -688,7 +727,7 @@ struct Targets {
 
 cudaError_t launch_lists(const HeadShape& h, const Targets& t, int* idx, float* p, int* cnt, uint32_t* err,
                          cudaStream_t s) {
-  const size_t smem = static_cast<size_t>(h.k) * 12;
+  const size_t smem = static_cast<size_t>((h.k + 3) & ~3) * 12;
   const float inv_t = 1.0f / t.temperature;
   const dim3 grid(h.M), block(LIST_THREADS);
   if (t.top_type == WB_F32)
@@ -913,7 +952,7 @@ wb_status head_backward(const HeadShape& h, const Targets& t, const float* dloss
   std::memset(&gm, 0, sizeof(gm));
   const uint64_t ld = L.piece;
   bool ok = map2(&lm.a0, b.xc, h.d, h.M, h.d, HEAD_BK, 128) &&
-            map2(&lm.b0, w, h.d, h.V, h.d, HEAD_BK, h.pair ? HEAD_BN / 2 : HEAD_BN) &&
+            map2(&lm.b0, w, h.d, h.V, h.d, HEAD_BK, h.pair ? L.bn / 2 : L.bn) &&
             map2(&lm.o0, dl, ld, h.M, ld, 64, 32);
   if (dx) {
     const uint64_t dims[3] = {static_cast<uint64_t>(h.d), static_cast<uint64_t>(h.M), static_cast<uint64_t>(L.splits)};
@@ -930,7 +969,7 @@ wb_status head_backward(const HeadShape& h, const Targets& t, const float* dloss
     p.v0 = v0;
     p.vc = h.V - v0 < L.piece ? h.V - v0 : L.piece;
     p.first_piece = v0 == 0;
-    p.bn = HEAD_BN;
+    p.bn = L.bn;
     {
       Prof pr(PC_HEAD_DLOGITS, s);
       WB_CUDA(launch_head<HEAD_DLOGITS>(h, lm, p, s));

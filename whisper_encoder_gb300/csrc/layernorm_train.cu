@@ -10,6 +10,7 @@
 // Forward: a team of 1, 2, 4 or 8 warps (by the width) holds a row, at most 40 elements a lane; teams of
 // one warp need no barrier.  Backward: see there.
 #include <mutex>
+#include <type_traits>
 
 #include "../../include/wb.h"
 #include "internal.h"
@@ -204,15 +205,17 @@ __device__ __forceinline__ uint64_t pair_of(const Raw& r, int i, T*) {
 
 // Warps of a block, one block an SM.  Measured with 8 / 12 / 16: 48000 x 1280 bf16 with dt (W = 1) 108 / 101 / 98 us;
 // both directions of 3001 x 5120 f16 (W = 4) 74 / 70 / 73 us.
-constexpr int lnb_warps(int W) { return W < 4 ? 16 : W == 4 ? 12 : 8; }
+constexpr int lnb_warps(int W, int es) { return W < 4 && es == 2 ? 16 : W < 8 ? 12 : 8; }
+constexpr int LNB_RING = 200 * 1024;   // bytes of the rings of a block
 
 // Partial rows part[block] = [dg (d) | db (d)]; null where the caller wants dx alone.
 template <typename T, int VEC, int NV, int W>
-__global__ void __launch_bounds__(lnb_warps(W) * 32, 1)
+__global__ void __launch_bounds__(lnb_warps(W, sizeof(T)) * 32, 1)
     ln_train_bwd_kernel(const T* __restrict__ dy, const T* __restrict__ x, const float* __restrict__ g,
                         const float2* __restrict__ stats, const T* __restrict__ dt, int rows, int d,
                         T* __restrict__ dx, float* __restrict__ part, int stages, uint32_t* err) {
-  constexpr int TEAMS = lnb_warps(W) / W, NP = VEC / 2;    // pairs a vector
+  constexpr int TEAMS = lnb_warps(W, sizeof(T)) / W, NP = VEC / 2;    // pairs a vector
+  static_assert(TEAMS * 3 * (W * 32 * NV * VEC) * static_cast<int>(sizeof(T)) <= LNB_RING, "a row of each team");
   using Raw = typename Pack<T, VEC>::Raw;
   extern __shared__ __align__(16) uint8_t ring[];          // [teams][stages][x, dy, dt][row]; at the end [teams][2 d] sums
   __shared__ uint64_t full[TEAMS][LNT_STAGES];
@@ -336,7 +339,7 @@ __global__ void __launch_bounds__(lnb_warps(W) * 32, 1)
     }
   }
   __syncthreads();
-  for (int c = threadIdx.x; c < d; c += lnb_warps(W) * 32) {       // pairs of the 2 d sums, teams in order
+  for (int c = threadIdx.x; c < d; c += lnb_warps(W, sizeof(T)) * 32) {       // pairs of the 2 d sums, teams in order
     uint64_t sum = acc[c];
 #pragma unroll
     for (int t = 1; t < TEAMS; ++t) sum = f32x2_add(sum, acc[t * d + c]);
@@ -409,6 +412,57 @@ __global__ void __launch_bounds__(LNT_WARPS * 32, NV <= 6 ? 3 : NV <= 10 ? 2 : 1
   }
 }
 
+// The forward pass for such widths, a block of up to 8 warps a row (4097 x 1283 f32, both directions: 41 us;
+// with two warps a row forward 54).
+template <typename T, int NV>
+__global__ void __launch_bounds__(LNT_WARPS * 32, NV <= 6 ? 4 : NV <= 10 ? 3 : NV <= 20 ? 2 : 1)
+    ln_train_fwd_any_kernel(const T* __restrict__ x, const T* __restrict__ res, const float* __restrict__ g,
+                            const float* __restrict__ bta, int rows, int d, float eps, T* __restrict__ y,
+                            T* __restrict__ total, float2* __restrict__ stats, uint32_t* err) {
+  __shared__ float2 red[2][LNT_WARPS];
+  const int nt = blockDim.x, tid = threadIdx.x;
+  const float inv_d = 1.0f / static_cast<float>(d);
+  const long long n_el = static_cast<long long>(rows) * d;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
+    const long long base = row * d;
+    T u[NV], r[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = i * nt + tid;
+      u[i] = r[i] = from_f32<T>(0.0f);
+      if (col < d && in_bounds(err, base + col, 1, n_el, SITE_LNT_X)) {
+        u[i] = x[base + col];
+        if (res) r[i] = res[base + col];
+      }
+    }
+    float v[NV], sm = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = i * nt + tid;
+      if (res) {
+        u[i] = from_f32<T>(to_f32<T>(u[i]) + to_f32<T>(r[i]));
+        if (col < d && in_bounds(err, base + col, 1, n_el, SITE_LNT_TOTAL)) total[base + col] = u[i];
+      }
+      v[i] = to_f32<T>(u[i]);
+      sm += v[i];
+    }
+    const float mean = block_sum(sm, 0.0f, red, 0).x * inv_d;
+    float q = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) q += i * nt + tid < d ? (v[i] - mean) * (v[i] - mean) : 0.0f;
+    const float rstd = rsqrtf(block_sum(q, 0.0f, red, 1).x * inv_d + eps);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = i * nt + tid;
+      if (col < d && in_bounds(err, base + col, 1, n_el, SITE_LNT_Y))
+        y[base + col] = from_f32<T>(fmaf((v[i] - mean) * rstd, __ldg(g + col), __ldg(bta + col)));
+    }
+    if (tid == 0 && in_bounds(err, row, 1, rows, SITE_LNT_STATS)) stats[row] = make_float2(mean, rstd);
+  }
+}
+
 // dg and db: sums of the partial rows, 32 columns and COL_SLICES interleaved slices of the rows a block.
 __global__ void __launch_bounds__(32 * COL_SLICES)
     ln_train_colsum_kernel(const float* __restrict__ part, int n_part, int d, float* __restrict__ dg,
@@ -449,13 +503,13 @@ int fwd_blocks(int rows, int d) {
   return static_cast<int>(b < LNT_FWD_BLOCKS ? b : LNT_FWD_BLOCKS);
 }
 
-// How the backward pass spreads its rows, by width, type and the tensors that a row is read from.
+// How rows are spread, by width, type and (backward) the tensors that a row is read from.
 struct Spread {
   bool vec;      // rows start on 16 bytes
   int nv;        // element-wise: loads a lane, the fewest (of those compiled) that leave a row to 8 warps
   int warps;     // per row
-  int stages;    // rows in flight per team: what 200 KB of shared memory hold
-  int blocks;    // what the device holds at the kernels' bound of registers and shared memory, at most one a row
+  int stages;    // backward: rows in flight per team, what 200 KB of shared memory hold
+  int blocks;    // backward: what the device holds at the kernels' bound of registers and shared memory, at most one a row
 };
 
 Spread spread(int rows, int d, int dtype, int tensors) {
@@ -465,7 +519,7 @@ Spread spread(int rows, int d, int dtype, int tensors) {
   int per_sm = 1;
   if (s.vec) {
     s.warps = team_warps(d);
-    const int fit = 200 * 1024 / (lnb_warps(s.warps) / s.warps * d * es * tensors);
+    const int fit = LNB_RING / (lnb_warps(s.warps, es) / s.warps * d * es * tensors);
     s.stages = fit < LNT_STAGES ? fit : LNT_STAGES;
   } else {
     const int need = (d + 32 * LNT_WARPS - 1) / (32 * LNT_WARPS);
@@ -512,7 +566,7 @@ cudaError_t ring_attr(K kern, uint64_t* done) {
   if (dev < 0 || dev > 63) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lk(g_lnt_mu);
   if (*done & (1ull << dev)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, LNB_RING);
   if (e == cudaSuccess) *done |= 1ull << dev;
   return e;
 }
@@ -522,17 +576,34 @@ cudaError_t go(const BwdArgs<T>& a, const Spread& sp, cudaStream_t s) {
   static uint64_t done = 0;
   const cudaError_t e = ring_attr(ln_train_bwd_kernel<T, VEC, NV, W>, &done);
   if (e != cudaSuccess) return e;
-  constexpr size_t TEAMS = lnb_warps(W) / W;
+  constexpr size_t TEAMS = lnb_warps(W, sizeof(T)) / W;
   size_t smem = TEAMS * sp.stages * (a.dt ? 3 : 2) * a.d * sizeof(T);
   const size_t sums = TEAMS * 2 * a.d * sizeof(float);
   if (smem < sums) smem = sums;
-  return launch_pdl(ln_train_bwd_kernel<T, VEC, NV, W>, dim3(sp.blocks), dim3(lnb_warps(W) * 32), smem, s, a.dy, a.x,
+  return launch_pdl(ln_train_bwd_kernel<T, VEC, NV, W>, dim3(sp.blocks), dim3(lnb_warps(W, sizeof(T)) * 32), smem, s, a.dy, a.x,
                     a.g, a.stats, a.dt, a.rows, a.d, a.dx, a.part, sp.stages, a.err);
 }
 template <typename T, int NV>
 cudaError_t go_any(const BwdArgs<T>& a, const Spread& sp, cudaStream_t s) {
   return launch_pdl(ln_train_bwd_any_kernel<T, NV>, dim3(sp.blocks), dim3(32 * sp.warps), 0, s, a.dy, a.x, a.g, a.stats,
                     a.dt, a.rows, a.d, a.dx, a.part, a.err);
+}
+
+// The element-wise kernels, by loads a lane.
+template <typename T, int NV>
+cudaError_t go_any(const FwdArgs<T>& a, const Spread& sp, cudaStream_t s);
+template <typename Args>
+cudaError_t any_by_width(const Args& a, const Spread& sp, cudaStream_t s) {
+  using T = std::remove_const_t<std::remove_pointer_t<decltype(a.x)>>;
+  switch (sp.nv) {
+    case 1: return go_any<T, 1>(a, sp, s);
+    case 2: return go_any<T, 2>(a, sp, s);
+    case 4: return go_any<T, 4>(a, sp, s);
+    case 6: return go_any<T, 6>(a, sp, s);
+    case 10: return go_any<T, 10>(a, sp, s);
+    case 20: return go_any<T, 20>(a, sp, s);
+    default: return go_any<T, 40>(a, sp, s);
+  }
 }
 
 template <typename T>
@@ -548,15 +619,7 @@ cudaError_t bwd_by_width(const BwdArgs<T>& a, const Spread& sp, cudaStream_t s) 
     if (a.d <= 1024) return go<T, VEC, 4 * FULL / 5, 1>(a, sp, s);
     return go<T, VEC, FULL, 1>(a, sp, s);
   }
-  switch (sp.nv) {
-    case 1: return go_any<T, 1>(a, sp, s);
-    case 2: return go_any<T, 2>(a, sp, s);
-    case 4: return go_any<T, 4>(a, sp, s);
-    case 6: return go_any<T, 6>(a, sp, s);
-    case 10: return go_any<T, 10>(a, sp, s);
-    case 20: return go_any<T, 20>(a, sp, s);
-    default: return go_any<T, 40>(a, sp, s);
-  }
+  return any_by_width(a, sp, s);
 }
 
 template <typename T, int VEC, int NV, int W>
@@ -564,15 +627,20 @@ cudaError_t go(const FwdArgs<T>& a, cudaStream_t s) {
   return launch_pdl(ln_train_fwd_kernel<T, VEC, NV, W>, dim3(fwd_blocks(a.rows, a.d)), dim3(lnt_warps(W) * 32), 0, s,
                     a.x, a.res, a.g, a.b, a.rows, a.d, a.eps, a.y, a.total, a.stats, a.err);
 }
+template <typename T, int NV>
+cudaError_t go_any(const FwdArgs<T>& a, const Spread& sp, cudaStream_t s) {
+  return launch_pdl(ln_train_fwd_any_kernel<T, NV>, dim3(a.rows < LNT_FWD_BLOCKS ? a.rows : LNT_FWD_BLOCKS),
+                    dim3(32 * sp.warps), 0, s, a.x, a.res, a.g, a.b, a.rows, a.d, a.eps, a.y, a.total, a.stats, a.err);
+}
 
 // Elements a lane: fifths of 40 for rows of one warp (short rows keep few registers), 40 for the rest.
-template <typename T, int VEC>
-cudaError_t fwd_by_width(const FwdArgs<T>& a, cudaStream_t s) {
-  constexpr int FULL = 40 / VEC;
-  const int w = team_warps(a.d);
-  if (w == 2) return go<T, VEC, FULL, 2>(a, s);
-  if (w == 4) return go<T, VEC, FULL, 4>(a, s);
-  if (w == 8) return go<T, VEC, FULL, 8>(a, s);
+template <typename T>
+cudaError_t fwd_by_width(const FwdArgs<T>& a, const Spread& sp, cudaStream_t s) {
+  constexpr int VEC = 16 / sizeof(T), FULL = 40 / VEC;
+  if (!sp.vec) return any_by_width(a, sp, s);
+  if (sp.warps == 2) return go<T, VEC, FULL, 2>(a, s);
+  if (sp.warps == 4) return go<T, VEC, FULL, 4>(a, s);
+  if (sp.warps == 8) return go<T, VEC, FULL, 8>(a, s);
   if (a.d <= 256) return go<T, VEC, FULL / 5, 1>(a, s);
   if (a.d <= 512) return go<T, VEC, 2 * FULL / 5, 1>(a, s);
   if (a.d <= 768) return go<T, VEC, 3 * FULL / 5, 1>(a, s);
@@ -584,11 +652,10 @@ bool type_ok(int dtype) { return dtype == WB_BF16 || dtype == WB_F16 || dtype ==
 
 template <typename T>
 cudaError_t fwd_t(const void* x, const void* res, const float* g, const float* b, int rows, int d, float eps, void* y,
-                  void* total, float* stats, uint32_t* err, cudaStream_t s) {
+                  void* total, float* stats, const Spread& sp, uint32_t* err, cudaStream_t s) {
   const FwdArgs<T> a{static_cast<const T*>(x), static_cast<const T*>(res), g, b, rows, d, eps, static_cast<T*>(y),
                      static_cast<T*>(total), reinterpret_cast<float2*>(stats), err};
-  constexpr int VEC = 16 / sizeof(T);
-  return d % VEC == 0 ? fwd_by_width<T, VEC>(a, s) : fwd_by_width<T, 1>(a, s);
+  return fwd_by_width<T>(a, sp, s);
 }
 template <typename T>
 cudaError_t bwd_t(const void* dy, const void* x, const float* g, const float* stats, const void* dt, int rows, int d,
@@ -617,10 +684,11 @@ wb_status wb_layernorm_forward(const void* x, const void* residual, const float*
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint32_t* err = tc_err_ptr();
   if (!err) return WB_ECUDA;
+  const Spread sp = spread(rows, d, dtype, 1);
   Prof pr(PC_TRAIN_LN, s);
-  if (dtype == WB_BF16) WB_CUDA(fwd_t<__nv_bfloat16>(x, residual, g, b, rows, d, eps, y, total, stats, err, s));
-  else if (dtype == WB_F16) WB_CUDA(fwd_t<__half>(x, residual, g, b, rows, d, eps, y, total, stats, err, s));
-  else WB_CUDA(fwd_t<float>(x, residual, g, b, rows, d, eps, y, total, stats, err, s));
+  if (dtype == WB_BF16) WB_CUDA(fwd_t<__nv_bfloat16>(x, residual, g, b, rows, d, eps, y, total, stats, sp, err, s));
+  else if (dtype == WB_F16) WB_CUDA(fwd_t<__half>(x, residual, g, b, rows, d, eps, y, total, stats, sp, err, s));
+  else WB_CUDA(fwd_t<float>(x, residual, g, b, rows, d, eps, y, total, stats, sp, err, s));
   return WB_OK;
 }
 
