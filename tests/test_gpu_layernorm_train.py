@@ -121,15 +121,16 @@ def test_no_rows(wb):
     assert dx.shape == (0, 384) and not dg.any() and not db.any()
 
 
-def test_dx_may_overwrite_an_input(wb):
+@pytest.mark.parametrize("d", [1280, 1283, 5120])
+def test_dx_may_overwrite_an_input(wb, d):
     from whisper_encoder_gb300 import _lib
-    x, _, g, b, dy, dt = _inputs(301, 1280, torch.bfloat16, 8, True)
+    x, _, g, b, dy, dt = _inputs(3001, d, torch.bfloat16, 8, True)
     _, total, stats = wb.layernorm_forward(x, g, b)
     want, _, _ = wb.layernorm_backward(dy, total, g, stats, dtotal=dt, need_params=False)
     for which in range(3):
         a = [dy.clone(), total.clone(), dt.clone()]
         p = [t.data_ptr() for t in a]
-        _lib.call("wb_layernorm_backward", p[0], p[1], g.data_ptr(), stats.data_ptr(), p[2], 301, 1280, _lib.WB_BF16,
+        _lib.call("wb_layernorm_backward", p[0], p[1], g.data_ptr(), stats.data_ptr(), p[2], 3001, d, _lib.WB_BF16,
                   p[which], None, None, None, 0, torch.cuda.current_stream().cuda_stream)
         assert torch.equal(a[which], want)
 

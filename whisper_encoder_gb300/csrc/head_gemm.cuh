@@ -84,6 +84,7 @@ struct HeadParams {
   float* part_sum;           // [column tile][part_ld]: plain sum of logits, null without smoothing
   long long part_ld;
   float* tgt_s;              // [row][k]: logits at the targets
+  int dl_cols;               // columns of D's buffer
   // DLOGITS in
   const float* row_lse2;     // by compact row, log2 units
   // dw
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
       };
       for (long long t = t_first; t < total && ok; t += t_step) {
         const Tile tl = tile_at(t);
-        const int row0 = tl.mt * BM + static_cast<int>(rank) * (128);
+        const int row0 = tl.mt * BM + static_cast<int>(rank) * 128;
         const int col0 = tl.nt * bn + static_cast<int>(rank) * half;
         for (int kb = tl.kb0; kb < tl.kb1; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, p.err, abort_flag, 24)) { ok = false; break; }
@@ -303,7 +304,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
       const Tile tl = tile_at(t);
       const int acc = local & 1;
       const uint32_t acc_phase = (local >> 1) & 1;
-      const int m0 = tl.mt * BM + static_cast<int>(rank) * (128) + quarter * 32;   // first row of this warp
+      const int m0 = tl.mt * BM + static_cast<int>(rank) * 128 + quarter * 32;   // first row of this warp
       const int m = m0 + lane;
       const bool row_ok = m < n;
       const int ncol0 = tl.nt * bn + ch0 * 32;         // first column inside the piece / the width
@@ -333,7 +334,11 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
           if (pos < cnt) next = p.tgt_idx[tb + pos];
         }
       }
-      if (!mbar_wait(&tfull[acc], acc_phase, p.err, abort_flag, 27)) { ok = false; break; }
+      // the same answer in all lanes: the loads from TMEM are a whole warp's
+      if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, p.err, abort_flag, 27))) {
+        ok = false;
+        break;
+      }
       tc_fence_after();
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * HEAD_BN;
 
@@ -501,7 +506,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
           fence_proxy_async_smem();
           __syncwarp();
           const int b0 = tl.nt * bn + ch0 * 32;
-          if (lane == 0 && (KIND == HEAD_DLOGITS || b0 < p.d)) {
+          if (lane == 0 && b0 < (KIND == HEAD_DLOGITS ? p.dl_cols : p.d)) {
             if (KIND == HEAD_DLOGITS) tma_store_2d(&maps.o0, box, b0, m0);
             else tma_store_2d(&maps.o1, box, b0, p.v0 + m0);
             bulk_commit();

@@ -942,6 +942,7 @@ wb_status head_backward(const HeadShape& h, const Targets& t, const float* dloss
     WB_CUDA(launch_rows(a, s));
   }
   HeadParams p = head_params(b, t);
+  p.dl_cols = L.piece;
   p.row_lse2 = b.row_lse2;
   p.g_scale = g_max;
   p.out_scale = t.temperature;
