@@ -65,6 +65,8 @@ struct HeadParams {
   int V, d;
   int v0, vc;                // this piece of the vocabulary (LSE: all of it)
   int bn;                    // columns of a tile, a multiple of 32
+  int a_rows;                // rows of a load of x or D: 128, or fewer where the call has fewer (what lies in the
+                             // rest of the tile's rows reaches only rows that are not there)
   int panel;                 // column tiles walked together (LSE, DLOGITS)
   int dx_splits;             // GRADS: slabs, 0 without dx
   int want_dw;
@@ -211,7 +213,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         const int col0 = tl.nt * bn + static_cast<int>(rank) * half;
         for (int kb = tl.kb0; kb < tl.kb1; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, p.err, abort_flag, 24)) { ok = false; break; }
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * (S::A_BYTES + b_bytes));
+          if (rank == 0)
+            mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * ((tl.dw ? S::A_BYTES : p.a_rows * 128) + b_bytes));
           uint8_t* sa = smem + stage * S::STAGE_BYTES;
           uint8_t* sb = sa + S::A_BYTES;
           if (LOGITS) {
@@ -487,7 +490,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
               for (int i = 0; i < 32; ++i)
                 if (!row_ok || p.v0 + n0 + i >= p.V) v[i] = 0.0f;
             }
-            if (m0 >= p.m_cap) continue;
+            if (m0 >= kb_n * HEAD_BK) continue;     // past the rows that dw's sum runs over
           } else {                                        // dw
             if (p.v0 + m0 >= p.V) continue;
 #pragma unroll

@@ -150,6 +150,7 @@ struct RowsArgs {
   const int64_t* labels;     // cross entropy: 0 <= label < V takes part
   const int* cnt;            // distillation: cnt > 0 takes part
   int M, V, d, rows_per_block;
+  int m_pad;                 // rows of xc and xs
   const __nv_bfloat16* x;
   __nv_bfloat16* xc;         // compacted
   int* row_src;
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) rows_kernel(const __grid_constan
   } else if (a.xs) {
     g = *a.g_max;
   }
-  const long long n_el = static_cast<long long>(a.M) * a.d;
+  const long long n_el = static_cast<long long>(a.M) * a.d;   // xc and xs have at least as many
   for (int i = r0 + warp; i < r1; i += ROWS_THREADS / 32) {
     const int dst = at[i - r0];
     if (dst < 0) {
@@ -290,10 +291,11 @@ __global__ void __launch_bounds__(ROWS_THREADS) rows_kernel(const __grid_constan
   }
   // x' up to the next whole block of 64 rows is a factor of the sum over rows: zeros
   if (a.xs && blockIdx.x == gridDim.x - 1) {
-    const int end = min(max((all + 63) / 64 * 64, 64), a.M);
+    const int end = max((all + 63) / 64 * 64, 64);
     for (long long v = static_cast<long long>(all) * nv + threadIdx.x; v < static_cast<long long>(end) * nv;
          v += ROWS_THREADS)
-      if (in_bounds(a.err, v * 8, 8, n_el, SITE_HEAD_X)) reinterpret_cast<uint4*>(a.xs)[v] = make_uint4(0, 0, 0, 0);
+      if (in_bounds(a.err, v * 8, 8, static_cast<long long>(a.m_pad) * a.d, SITE_HEAD_X))
+        reinterpret_cast<uint4*>(a.xs)[v] = make_uint4(0, 0, 0, 0);
   }
 }
 
@@ -424,7 +426,7 @@ __global__ void __launch_bounds__(FIN_ROWS* FIN_SLICES) head_finish_kernel(const
 // dx of the rows that take part: the slabs' sum times T dloss, rounded once.  `lanes` (1 to 8) threads
 // share a vector of 8 columns, each adding every lanes-th slab; their sums are added in order.
 __global__ void __launch_bounds__(256)
-    head_dx_kernel(const int* __restrict__ n_rows, const int* __restrict__ row_src, int M, int d, int splits, int lanes,
+    head_dx_kernel(const int* __restrict__ n_rows, const int* __restrict__ row_src, int M, int m_pad, int d, int splits, int lanes,
                    const float* __restrict__ slab, const float* __restrict__ dloss, float temperature,
                    __nv_bfloat16* __restrict__ dx, uint32_t* err) {
   __shared__ float sm[256][8];
@@ -432,7 +434,7 @@ __global__ void __launch_bounds__(256)
   grid_dependents_launch();
   const int n = min(max(*n_rows, 0), M);
   const int nv = d / 8, per_block = 256 / lanes;
-  const long long per_slab = static_cast<long long>(M) * d;
+  const long long per_slab = static_cast<long long>(m_pad) * d;
   const long long work = static_cast<long long>(n) * nv;
   const int vx = threadIdx.x % per_block, sl = threadIdx.x / per_block;
   for (long long w0 = static_cast<long long>(blockIdx.x) * per_block; w0 < work;
@@ -469,7 +471,7 @@ __global__ void __launch_bounds__(256)
     }
     if (!on) continue;
     const long long o = static_cast<long long>(src) * d + 8 * v;
-    if (in_bounds(err, o, 8, per_slab, SITE_HEAD_DX))
+    if (in_bounds(err, o, 8, static_cast<long long>(M) * d, SITE_HEAD_DX))
       *reinterpret_cast<uint4*>(dx + o) = make_uint4(pack_bf16(s[0] * f, s[1] * f), pack_bf16(s[2] * f, s[3] * f),
                                                      pack_bf16(s[4] * f, s[5] * f), pack_bf16(s[6] * f, s[7] * f));
   }
@@ -485,6 +487,10 @@ struct HeadShape {
   int bm() const { return head_bm(pair); }
   int slots() const { return pair ? HEAD_SMS / 2 : HEAD_SMS; }   // tiles at a time
   int row_tiles() const { return ceil_div(M, bm()); }
+  // rows of the workspace's matrices: whole tiles, so that no load of theirs runs past the end (filling rows
+  // that are not there is slow: 17 rows against 51866 x 1280 took 43 us with boxes of 128 rows, 33 with 24)
+  int m_pad() const { return row_tiles() * bm(); }
+  int a_rows() const { return M < 128 ? (M + 7) / 8 * 8 : 128; }
   // one tile of rows: taking out rows saves no product, so the forward pass reads x as it is
   bool direct() const { return row_tiles() <= 1; }
   // a few rows: w straight to registers (head_gemv.cuh)
@@ -549,7 +555,7 @@ RowsLayout rows_layout(Carver& c, const HeadShape& h) {
   } else {
     L.row_tgt = c.take(m * sizeof(int));
   }
-  L.xc = c.take(m * h.d * 2);
+  L.xc = c.take(static_cast<size_t>(h.m_pad()) * h.d * 2);
   return L;
 }
 
@@ -635,7 +641,7 @@ BwdLayout bwd_layout(const HeadShape& h) {
   }
   L.splits = dx_splits(h, L.piece);
   L.bn = logits_width(h, L.piece) / 64 * 64;     // whole staging boxes; past the piece the store is clipped
-  const size_t m = static_cast<size_t>(h.M);
+  const size_t m = static_cast<size_t>(h.m_pad());
   L.g_max = c.take(256);
   L.xs = c.take(m * h.d * 2);
   L.dl = c.take(m * static_cast<size_t>(most) * 2);
@@ -771,6 +777,7 @@ HeadParams head_params(const HeadBase& b, const Targets& t) {
   p.d = b.h.d;
   p.vc = b.h.V;
   p.bn = HEAD_BN;
+  p.a_rows = b.h.a_rows();
   p.panel = 8;
   p.scale_log2 = 1.4426950408889634f / t.temperature;
   p.row_tgt = b.h.k > 0 ? b.row_src : b.row_tgt;
@@ -809,6 +816,7 @@ RowsArgs rows_args(const HeadBase& b, const Targets& t, const RowsLayout& L, con
   a.V = b.h.V;
   a.d = b.h.d;
   a.rows_per_block = rows_per_block(b.h.M);
+  a.m_pad = b.h.m_pad();
   a.x = static_cast<const __nv_bfloat16*>(x);
   a.xc = b.xc;
   a.row_src = reinterpret_cast<int*>(b.ws + L.row_src);
@@ -881,7 +889,7 @@ wb_status head_forward(const HeadShape& h, const Targets& t, const void* x, cons
     p.bn = L.bn;
     HeadMaps maps;
     std::memset(&maps, 0, sizeof(maps));
-    if (!map2(&maps.a0, direct ? x : b.xc, h.d, h.M, h.d, HEAD_BK, 128) ||
+    if (!map2(&maps.a0, direct ? x : b.xc, h.d, direct ? h.M : h.m_pad(), h.d, HEAD_BK, h.a_rows()) ||
         !map2(&maps.b0, w, h.d, h.V, h.d, HEAD_BK, h.pair ? L.bn / 2 : L.bn))
       return WB_ECUDA;
     {
@@ -951,19 +959,19 @@ wb_status head_backward(const HeadShape& h, const Targets& t, const float* dloss
   HeadMaps lm, gm;
   std::memset(&lm, 0, sizeof(lm));
   std::memset(&gm, 0, sizeof(gm));
-  const uint64_t ld = L.piece;
-  bool ok = map2(&lm.a0, b.xc, h.d, h.M, h.d, HEAD_BK, 128) &&
+  const uint64_t ld = L.piece, mp = h.m_pad();
+  bool ok = map2(&lm.a0, b.xc, h.d, mp, h.d, HEAD_BK, h.a_rows()) &&
             map2(&lm.b0, w, h.d, h.V, h.d, HEAD_BK, h.pair ? L.bn / 2 : L.bn) &&
-            map2(&lm.o0, dl, ld, h.M, ld, 64, 32);
+            map2(&lm.o0, dl, ld, mp, ld, 64, 32);
   if (dx) {
-    const uint64_t dims[3] = {static_cast<uint64_t>(h.d), static_cast<uint64_t>(h.M), static_cast<uint64_t>(L.splits)};
-    const uint64_t str[2] = {static_cast<uint64_t>(h.d) * 4, static_cast<uint64_t>(h.d) * 4 * h.M};
+    const uint64_t dims[3] = {static_cast<uint64_t>(h.d), mp, static_cast<uint64_t>(L.splits)};
+    const uint64_t str[2] = {static_cast<uint64_t>(h.d) * 4, static_cast<uint64_t>(h.d) * 4 * mp};
     const uint32_t box[3] = {32, 32, 1};
-    ok = ok && map2(&gm.a0, dl, ld, h.M, ld, HEAD_BK, 128) && map2(&gm.b0, w, h.d, h.V, h.d, 64, HEAD_BK) &&
+    ok = ok && map2(&gm.a0, dl, ld, mp, ld, HEAD_BK, h.a_rows()) && map2(&gm.b0, w, h.d, h.V, h.d, 64, HEAD_BK) &&
          tma_map_f32(&gm.o0, 3, slab, dims, str, box);
   }
   if (dw)
-    ok = ok && map2(&gm.a1, dl, ld, h.M, ld, 64, HEAD_BK) && map2(&gm.b1, xs, h.d, h.M, h.d, 64, HEAD_BK) &&
+    ok = ok && map2(&gm.a1, dl, ld, mp, ld, 64, HEAD_BK) && map2(&gm.b1, xs, h.d, mp, h.d, 64, HEAD_BK) &&
          map2(&gm.o1, dw, h.d, h.V, h.d, 64, 32);
   if (!ok) return WB_ECUDA;
   for (int v0 = 0; v0 < h.V; v0 += L.piece) {
@@ -985,7 +993,7 @@ wb_status head_backward(const HeadShape& h, const Targets& t, const float* dloss
     const long long work = static_cast<long long>(h.M) * (h.d / 8) * lanes;
     const long long blocks = (work + 255) / 256;
     WB_CUDA(launch_pdl(head_dx_kernel, dim3(static_cast<unsigned>(blocks < 2432 ? blocks : 2432)), dim3(256), 0, s,
-                       b.n_rows, b.row_src, h.M, h.d, L.splits, lanes, static_cast<const float*>(slab), dloss,
+                       b.n_rows, b.row_src, h.M, h.m_pad(), h.d, L.splits, lanes, static_cast<const float*>(slab), dloss,
                        t.temperature, static_cast<__nv_bfloat16*>(dx), err));
   }
   return WB_OK;
