@@ -386,7 +386,7 @@ wb_status wb_dequantize_e5m2(const uint8_t* q, const float* scale, int64_t n, vo
  * (float32 [rows][2]) for the backward pass, and normalises the rounded sum, so that the backward
  * pass can read it back from `total`.  dtype is WB_BF16, WB_F16 or WB_F32 and holds for x,
  * residual, y and total, all [rows, d]; g, b: float32 [d].  residual and total are both given or
- * both NULL.
+ * both NULL.  The outputs overlap neither an input nor each other.
  *
  * wb_layernorm_backward: with h = (x - mean) rstd and u = g dy (x being the forward pass's `total`,
  * or its x without a residual):

@@ -80,6 +80,23 @@ def test_forward_and_backward_match_the_formulas(wb, rows, d, kind, residual):
     _close(db, rdb, 0.0, n_sum * dy.double().abs().sum(0) + 1e-30)
 
 
+# more rows than the device holds at once: every slot is filled several times over
+@pytest.mark.parametrize("rows,d", [(20011, 136), (15001, 1280), (12007, 1928), (7001, 4104), (4003, 10240), (3001, 1283)])
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("residual", [False, True])
+def test_a_row_does_not_depend_on_the_rows_around_it(wb, rows, d, kind, residual):
+    x, res, g, b, dy, dt = _inputs(rows, d, TYPES[kind], d, residual)
+    y, total, stats = wb.layernorm_forward(x, g, b, residual=res)
+    dx, _, _ = wb.layernorm_backward(dy, total, g, stats, dtotal=dt, need_params=False)
+    assert wb.check_device_error() == 0
+    cut = lambda t, a: None if t is None else t[a:a + 100].clone()  # noqa: E731
+    for at in (0, 1187, rows // 2, rows - 100):
+        ys, ts, ss = wb.layernorm_forward(cut(x, at), g, b, residual=cut(res, at))
+        ds, _, _ = wb.layernorm_backward(cut(dy, at), ts, g, ss, dtotal=cut(dt, at), need_params=False)
+        for whole, part in ((y, ys), (total, ts), (stats, ss), (dx, ds)):
+            assert torch.equal(whole[at:at + 100], part)
+
+
 def test_backward_matches_differences_of_the_forward(wb):
     # directional derivative of sum(dy . y) + sum(dt . total) along random directions, f32
     rows, d = 6, 96

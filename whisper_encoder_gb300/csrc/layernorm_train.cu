@@ -8,7 +8,7 @@
 // Both passes are bound by memory: each element is read once and written once.  Statistics, row sums and
 // the sums over rows are fp32, and the row statistics take their two passes over registers.
 // Forward: a team of 1, 2, 4 or 8 warps (by the width) holds a row, at most 40 elements a lane; teams of
-// one warp need no barrier.  Backward: see there.
+// one warp need no barrier.  16-bit rows that need it come through rings of shared memory.  Backward: see there.
 #include <mutex>
 #include <type_traits>
 
@@ -347,6 +347,103 @@ __global__ void __launch_bounds__(lnb_warps(W, sizeof(T)) * 32, 1)
   }
 }
 
+// The forward pass of 16-bit rows through the same rings: the next rows arrive while the team waits at its sums.
+// The host's choice between the two forward kernels has the figures.
+template <typename T, int VEC, int NV, int W>
+__global__ void __launch_bounds__(lnb_warps(W, sizeof(T)) * 32, 1)
+    ln_train_fwd_ring_kernel(const T* __restrict__ x, const T* __restrict__ res, const float* __restrict__ g,
+                             const float* __restrict__ bta, int rows, int d, float eps, T* __restrict__ y,
+                             T* __restrict__ total, float2* __restrict__ stats, int stages, uint32_t* err) {
+  constexpr int TEAMS = lnb_warps(W, sizeof(T)) / W;
+  using Raw = typename Pack<T, VEC>::Raw;
+  extern __shared__ __align__(16) uint8_t ring[];          // [teams][stages][x, res][row]
+  __shared__ uint64_t full[TEAMS][LNT_STAGES];
+  __shared__ int abort_flag;
+  __shared__ float2 red[TEAMS][2][W];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int team = warp / W, wt = warp % W;
+  const float inv_d = 1.0f / static_cast<float>(d);
+  const long long n_el = static_cast<long long>(rows) * d;
+  const uint32_t bytes = static_cast<uint32_t>(d) * sizeof(T);
+  const uint32_t stage_bytes = bytes * (res ? 2 : 1);
+  uint8_t* mine = ring + static_cast<size_t>(team) * stages * stage_bytes;
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < TEAMS; ++t)
+      for (int i = 0; i < LNT_STAGES; ++i) mbar_init(&full[t][i], 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const bool feeder = wt == 0 && lane == 0;
+  auto issue = [&](long long row, int stage) {
+    mbar_arrive_expect_tx(&full[team][stage], stage_bytes);
+    uint8_t* to = mine + static_cast<size_t>(stage) * stage_bytes;
+    bulk_load(to, x + row * d, bytes, &full[team][stage]);
+    if (res) bulk_load(to + bytes, res + row * d, bytes, &full[team][stage]);
+  };
+  const long long first = blockIdx.x + static_cast<long long>(gridDim.x) * team;     // few rows: one a block
+  const long long step = static_cast<long long>(gridDim.x) * TEAMS;
+  if (feeder)
+    for (int s = 0; s < stages && first + s * step < rows; ++s) issue(first + s * step, s);
+  int stage = 0;
+  uint32_t parity = 0;
+  for (long long row = first; row < rows; row += step) {
+    const long long base = row * d;
+    const uint8_t* at = mine + static_cast<size_t>(stage) * stage_bytes;
+    // a wait that runs out marks the error word and goes on: every thread keeps to the same barriers
+    mbar_wait(&full[team][stage], parity, err, &abort_flag, 31);
+    float v[NV * VEC];
+    float sm = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = ((i * W + wt) * 32 + lane) * VEC;
+      const bool on = col < d;
+      Raw u = on ? *reinterpret_cast<const Raw*>(at + col * sizeof(T)) : Raw{};
+      if (on && res) {
+        const Raw r = *reinterpret_cast<const Raw*>(at + bytes + col * sizeof(T));
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) u.e[j] = from_f32<T>(to_f32<T>(u.e[j]) + to_f32<T>(r.e[j]));
+        if (in_bounds(err, base + col, VEC, n_el, SITE_LNT_TOTAL)) *reinterpret_cast<Raw*>(total + base + col) = u;
+      }
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        v[i * VEC + j] = on ? to_f32<T>(u.e[j]) : 0.0f;
+        sm += v[i * VEC + j];
+      }
+    }
+    const float mean = team_sum<W>(sm, 0.0f, red[team], team, wt, lane, 0).x * inv_d;
+    // the team has read the stage: its next row may come
+    if (feeder && row + stages * step < rows) issue(row + stages * step, stage);
+    if (++stage == stages) { stage = 0; parity ^= 1u; }
+    float q = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const bool on = ((i * W + wt) * 32 + lane) * VEC < d;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const float t = v[i * VEC + j] - mean;
+        q += on ? t * t : 0.0f;
+      }
+    }
+    const float rstd = rsqrtf(team_sum<W>(q, 0.0f, red[team], team, wt, lane, 1).x * inv_d + eps);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = ((i * W + wt) * 32 + lane) * VEC;
+      if (col >= d || !in_bounds(err, base + col, VEC, n_el, SITE_LNT_Y)) continue;
+      float gg[VEC], bb[VEC];
+      load_params<VEC>(g + col, gg);
+      load_params<VEC>(bta + col, bb);
+      Raw o;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) o.e[j] = from_f32<T>(fmaf((v[i * VEC + j] - mean) * rstd, gg[j], bb[j]));
+      *reinterpret_cast<Raw*>(y + base + col) = o;
+    }
+    if (feeder && in_bounds(err, row, 1, rows, SITE_LNT_STATS)) stats[row] = make_float2(mean, rstd);
+  }
+}
+
 // The same for widths whose rows do not start on 16 bytes: a block of up to 8 warps a row, single elements,
 // read directly.
 template <typename T, int NV>
@@ -508,7 +605,7 @@ struct Spread {
   bool vec;      // rows start on 16 bytes
   int nv;        // element-wise: loads a lane, the fewest (of those compiled) that leave a row to 8 warps
   int warps;     // per row
-  int stages;    // backward: rows in flight per team, what 200 KB of shared memory hold
+  int stages;    // rings: rows in flight per team, what 200 KB of shared memory hold
   int blocks;    // backward: what the device holds at the kernels' bound of registers and shared memory, at most one a row
 };
 
@@ -633,14 +730,43 @@ cudaError_t go_any(const FwdArgs<T>& a, const Spread& sp, cudaStream_t s) {
                     dim3(32 * sp.warps), 0, s, a.x, a.res, a.g, a.b, a.rows, a.d, a.eps, a.y, a.total, a.stats, a.err);
 }
 
+template <typename T, int VEC, int NV, int W>
+cudaError_t go_ring(const FwdArgs<T>& a, const Spread& sp, cudaStream_t s) {
+  static uint64_t done = 0;
+  const cudaError_t e = ring_attr(ln_train_fwd_ring_kernel<T, VEC, NV, W>, &done);
+  if (e != cudaSuccess) return e;
+  const size_t smem = static_cast<size_t>(lnb_warps(W, sizeof(T)) / W) * sp.stages * (a.res ? 2 : 1) * a.d * sizeof(T);
+  return launch_pdl(ln_train_fwd_ring_kernel<T, VEC, NV, W>, dim3(sp.blocks), dim3(lnb_warps(W, sizeof(T)) * 32), smem, s,
+                    a.x, a.res, a.g, a.b, a.rows, a.d, a.eps, a.y, a.total, a.stats, sp.stages, a.err);
+}
+
 // Elements a lane: fifths of 40 for rows of one warp (short rows keep few registers), 40 for the rest.
 template <typename T>
 cudaError_t fwd_by_width(const FwdArgs<T>& a, const Spread& sp, cudaStream_t s) {
   constexpr int VEC = 16 / sizeof(T), FULL = 40 / VEC;
   if (!sp.vec) return any_by_width(a, sp, s);
-  if (sp.warps == 2) return go<T, VEC, FULL, 2>(a, s);
-  if (sp.warps == 4) return go<T, VEC, FULL, 4>(a, s);
-  if (sp.warps == 8) return go<T, VEC, FULL, 8>(a, s);
+  // 16-bit rows go through the rings where the direct kernel is short of bytes in flight or of overlap: rows of
+  // several warps, whose barriers hold the next row's loads back (with a residual, direct against ring: 12000 x
+  // 5120 bf16 156 / 110 us, 24000 x 2560 150 / 90, 6000 x 10240 207 / 124, 100 x 5120 6.2 both), and one input
+  // (48000 x 1280 bf16 80 / 67, 48000 x 1024 f16 55 / 50, 100000 x 384 75 / 51).  One warp a row with a residual has
+  // the loads of two inputs in flight by itself (48000 x 1280 89 / 90, 48000 x 1024 67 / 72), and so have f32 rows,
+  // twice the bytes an element (24000 x 1280 with a residual 79 / 87, 6000 x 5120 80 / 85; without 45 / 52, 49 / 57).
+  if constexpr (sizeof(T) == 2) {
+    if (sp.warps == 2) return go_ring<T, VEC, FULL, 2>(a, sp, s);
+    if (sp.warps == 4) return go_ring<T, VEC, FULL, 4>(a, sp, s);
+    if (sp.warps == 8) return go_ring<T, VEC, FULL, 8>(a, sp, s);
+    if (!a.res) {
+      if (a.d <= 256) return go_ring<T, VEC, FULL / 5, 1>(a, sp, s);
+      if (a.d <= 512) return go_ring<T, VEC, 2 * FULL / 5, 1>(a, sp, s);
+      if (a.d <= 768) return go_ring<T, VEC, 3 * FULL / 5, 1>(a, sp, s);
+      if (a.d <= 1024) return go_ring<T, VEC, 4 * FULL / 5, 1>(a, sp, s);
+      return go_ring<T, VEC, FULL, 1>(a, sp, s);
+    }
+  } else {
+    if (sp.warps == 2) return go<T, VEC, FULL, 2>(a, s);
+    if (sp.warps == 4) return go<T, VEC, FULL, 4>(a, s);
+    if (sp.warps == 8) return go<T, VEC, FULL, 8>(a, s);
+  }
   if (a.d <= 256) return go<T, VEC, FULL / 5, 1>(a, s);
   if (a.d <= 512) return go<T, VEC, 2 * FULL / 5, 1>(a, s);
   if (a.d <= 768) return go<T, VEC, 3 * FULL / 5, 1>(a, s);
@@ -684,7 +810,7 @@ wb_status wb_layernorm_forward(const void* x, const void* residual, const float*
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint32_t* err = tc_err_ptr();
   if (!err) return WB_ECUDA;
-  const Spread sp = spread(rows, d, dtype, 1);
+  const Spread sp = spread(rows, d, dtype, residual ? 2 : 1);
   Prof pr(PC_TRAIN_LN, s);
   if (dtype == WB_BF16) WB_CUDA(fwd_t<__nv_bfloat16>(x, residual, g, b, rows, d, eps, y, total, stats, sp, err, s));
   else if (dtype == WB_F16) WB_CUDA(fwd_t<__half>(x, residual, g, b, rows, d, eps, y, total, stats, sp, err, s));
