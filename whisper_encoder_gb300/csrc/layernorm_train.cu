@@ -8,7 +8,7 @@
 // Both passes are bound by memory: each element is read once and written once.  Statistics, row sums and
 // the sums over rows are fp32, and the row statistics take their two passes over registers.
 // Forward: a team of 1, 2, 4 or 8 warps (by the width) holds a row, at most 40 elements a lane; teams of
-// one warp need no barrier.  16-bit rows that need it come through rings of shared memory.  Backward: see there.
+// one warp need no barrier.  Backward: see there.
 #include <mutex>
 #include <type_traits>
 
@@ -20,7 +20,7 @@ namespace wb {
 namespace {
 
 constexpr int LNT_MAX_D = 10240;
-constexpr int LNT_FWD_BLOCKS = 152 * 8;   // grid cap
+constexpr int LNT_FWD_BLOCKS = 152 * 32;   // grid cap
 constexpr int COL_SLICES = 32;            // column-sum kernel: slices of the partial rows per block
 
 template <typename T>
@@ -87,6 +87,41 @@ __device__ __forceinline__ float2 team_sum(float a, float b, float2 (*red)[W], i
   return make_float2(a, b);
 }
 
+__device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// Pair i of a loaded vector as two floats, and back: 16-bit pairs as whole words (element by element the compiler
+// takes twice the conversions and puts the halves together with permutes).
+template <typename T, typename Raw>
+__device__ __forceinline__ uint64_t pair_of(const Raw& r, int i) {
+  if constexpr (sizeof(T) == 4) {
+    return f32x2_pack(r.e[2 * i], r.e[2 * i + 1]);
+  } else {
+    const uint32_t w = reinterpret_cast<const uint32_t*>(r.e)[i];
+    if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+      return f32x2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+      return f32x2_pack(f.x, f.y);
+    }
+  }
+}
+template <typename T, typename Raw>
+__device__ __forceinline__ void set_pair(Raw& r, int i, uint64_t v) {
+  float lo, hi;
+  f32x2_unpack(v, lo, hi);
+  if constexpr (sizeof(T) == 4) {
+    r.e[2 * i] = lo;
+    r.e[2 * i + 1] = hi;
+  } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+    reinterpret_cast<__nv_bfloat162*>(r.e)[i] = __floats2bfloat162_rn(lo, hi);
+  } else {
+    reinterpret_cast<__half2*>(r.e)[i] = __floats2half2_rn(lo, hi);
+  }
+}
+
 constexpr int lnt_warps(int W) { return W < 4 ? 4 : W; }   // warps per block: one to four teams
 
 template <typename T, int VEC, int NV, int W>
@@ -94,7 +129,7 @@ __global__ void __launch_bounds__(lnt_warps(W) * 32)
     ln_train_fwd_kernel(const T* __restrict__ x, const T* __restrict__ res, const float* __restrict__ g,
                         const float* __restrict__ bta, int rows, int d, float eps, T* __restrict__ y,
                         T* __restrict__ total, float2* __restrict__ stats, uint32_t* err) {
-  constexpr int TEAMS = lnt_warps(W) / W;
+  constexpr int TEAMS = lnt_warps(W) / W, NP = VEC / 2;
   using Raw = typename Pack<T, VEC>::Raw;
   __shared__ float2 red[TEAMS][2][W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -110,42 +145,46 @@ __global__ void __launch_bounds__(lnt_warps(W) * 32)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = ((i * W + wt) * 32 + lane) * VEC;
+      u[i] = Raw{};
       if (col < d && in_bounds(err, base + col, VEC, n_el, SITE_LNT_X)) {
         u[i] = *reinterpret_cast<const Raw*>(x + base + col);
         if (res) r[i] = *reinterpret_cast<const Raw*>(res + base + col);
       }
     }
-    float v[NV * VEC];
-    float sm = 0.0f;
+    uint64_t v[NV * NP], acc[2] = {0, 0};                  // two chains of adds
+    float lo, hi;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = ((i * W + wt) * 32 + lane) * VEC;
-      const bool on = col < d;
-      if (on && res) {
+      if (col < d && res) {
         // the sum is rounded to the tensor's type first: what is normalised is what is stored
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) u[i].e[j] = from_f32<T>(to_f32<T>(u[i].e[j]) + to_f32<T>(r[i].e[j]));
+        for (int j = 0; j < NP; ++j) set_pair<T>(u[i], j, f32x2_add(pair_of<T>(u[i], j), pair_of<T>(r[i], j)));
         if (in_bounds(err, base + col, VEC, n_el, SITE_LNT_TOTAL))
           *reinterpret_cast<Raw*>(total + base + col) = u[i];
       }
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        v[i * VEC + j] = on ? to_f32<T>(u[i].e[j]) : 0.0f;
-        sm += v[i * VEC + j];
+      for (int j = 0; j < NP; ++j) {
+        v[i * NP + j] = pair_of<T>(u[i], j);
+        acc[j & 1] = f32x2_add(acc[j & 1], v[i * NP + j]);
       }
     }
-    const float mean = team_sum<W>(sm, 0.0f, red[team], team, wt, lane, 0).x * inv_d;
-    float q = 0.0f;
+    f32x2_unpack(f32x2_add(acc[0], acc[1]), lo, hi);
+    const float mean = team_sum<W>(lo + hi, 0.0f, red[team], team, wt, lane, 0).x * inv_d;
+    acc[0] = acc[1] = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const bool on = ((i * W + wt) * 32 + lane) * VEC < d;
+      const float nm = ((i * W + wt) * 32 + lane) * VEC < d ? -mean : 0.0f;      // past the row: stays 0
+      const uint64_t nm2 = f32x2_pack(nm, nm);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float t = v[i * VEC + j] - mean;
-        q += on ? t * t : 0.0f;
+      for (int j = 0; j < NP; ++j) {
+        v[i * NP + j] = f32x2_add(v[i * NP + j], nm2);
+        acc[j & 1] = f32x2_fma(v[i * NP + j], v[i * NP + j], acc[j & 1]);
       }
     }
-    const float rstd = rsqrtf(team_sum<W>(q, 0.0f, red[team], team, wt, lane, 1).x * inv_d + eps);
+    f32x2_unpack(f32x2_add(acc[0], acc[1]), lo, hi);
+    const float rstd = rsqrtf(team_sum<W>(lo + hi, 0.0f, red[team], team, wt, lane, 1).x * inv_d + eps);
+    const uint64_t rs2 = f32x2_pack(rstd, rstd);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = ((i * W + wt) * 32 + lane) * VEC;
@@ -155,7 +194,9 @@ __global__ void __launch_bounds__(lnt_warps(W) * 32)
       load_params<VEC>(bta + col, bb);
       Raw o;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) o.e[j] = from_f32<T>(fmaf((v[i * VEC + j] - mean) * rstd, gg[j], bb[j]));
+      for (int j = 0; j < NP; ++j)
+        set_pair<T>(o, j, f32x2_fma(f32x2_mul(v[i * NP + j], rs2), f32x2_pack(gg[2 * j], gg[2 * j + 1]),
+                                    f32x2_pack(bb[2 * j], bb[2 * j + 1])));
       *reinterpret_cast<Raw*>(y + base + col) = o;
     }
     if (wt == 0 && lane == 0 && in_bounds(err, row, 1, rows, SITE_LNT_STATS)) stats[row] = make_float2(mean, rstd);
@@ -190,17 +231,6 @@ __device__ __forceinline__ float2 block_sum(float a, float b, float2 (*red)[LNT_
     b += red[slot][i].y;
   }
   return make_float2(a, b);
-}
-
-__device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-// Pair i of a loaded vector as two floats.
-template <typename Raw, typename T>
-__device__ __forceinline__ uint64_t pair_of(const Raw& r, int i, T*) {
-  return f32x2_pack(to_f32<T>(r.e[2 * i]), to_f32<T>(r.e[2 * i + 1]));
 }
 
 // Warps of a block, one block an SM.  Measured with 8 / 12 / 16: 48000 x 1280 bf16 with dt (W = 1) 108 / 101 / 98 us;
@@ -278,8 +308,8 @@ __global__ void __launch_bounds__(lnb_warps(W, sizeof(T)) * 32, 1)
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
         const int e = i * NP + j;
-        const uint64_t y2 = pair_of(yv, j, static_cast<T*>(nullptr));
-        const uint64_t h2 = f32x2_mul(f32x2_add(pair_of(xv, j, static_cast<T*>(nullptr)), nm2), rs2);
+        const uint64_t y2 = pair_of<T>(yv, j);
+        const uint64_t h2 = f32x2_mul(f32x2_add(pair_of<T>(xv, j), nm2), rs2);
         const uint64_t u2 = f32x2_mul(f32x2_pack(gg[2 * j], gg[2 * j + 1]), y2);
         ag[e] = f32x2_fma(y2, h2, ag[e]);
         ab[e] = f32x2_add(ab[e], y2);
@@ -308,12 +338,10 @@ __global__ void __launch_bounds__(lnb_warps(W, sizeof(T)) * 32, 1)
       if (dt) tv = *reinterpret_cast<const Raw*>(at + 2 * bytes + col * sizeof(T));
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
-        const uint64_t h2 = f32x2_mul(f32x2_add(pair_of(xv, j, static_cast<T*>(nullptr)), nm2), rs2);
-        const uint64_t u2 = f32x2_fma(f32x2_pack(gg[2 * j], gg[2 * j + 1]), pair_of(yv, j, static_cast<T*>(nullptr)), c12);
+        const uint64_t h2 = f32x2_mul(f32x2_add(pair_of<T>(xv, j), nm2), rs2);
+        const uint64_t u2 = f32x2_fma(f32x2_pack(gg[2 * j], gg[2 * j + 1]), pair_of<T>(yv, j), c12);
         const uint64_t in = f32x2_fma(h2, c22, u2);
-        f32x2_unpack(dt ? f32x2_fma(in, rs2, pair_of(tv, j, static_cast<T*>(nullptr))) : f32x2_mul(in, rs2), lo, hi);
-        o.e[2 * j] = from_f32<T>(lo);
-        o.e[2 * j + 1] = from_f32<T>(hi);
+        set_pair<T>(o, j, dt ? f32x2_fma(in, rs2, pair_of<T>(tv, j)) : f32x2_mul(in, rs2));
       }
       *reinterpret_cast<Raw*>(dx + base + col) = o;
     }
@@ -344,103 +372,6 @@ __global__ void __launch_bounds__(lnb_warps(W, sizeof(T)) * 32, 1)
 #pragma unroll
     for (int t = 1; t < TEAMS; ++t) sum = f32x2_add(sum, acc[t * d + c]);
     if (in_bounds(err, (dst - part) + 2 * c, 2, part_el, SITE_LNT_PART)) reinterpret_cast<uint64_t*>(dst)[c] = sum;
-  }
-}
-
-// The forward pass of 16-bit rows through the same rings: the next rows arrive while the team waits at its sums.
-// The host's choice between the two forward kernels has the figures.
-template <typename T, int VEC, int NV, int W>
-__global__ void __launch_bounds__(lnb_warps(W, sizeof(T)) * 32, 1)
-    ln_train_fwd_ring_kernel(const T* __restrict__ x, const T* __restrict__ res, const float* __restrict__ g,
-                             const float* __restrict__ bta, int rows, int d, float eps, T* __restrict__ y,
-                             T* __restrict__ total, float2* __restrict__ stats, int stages, uint32_t* err) {
-  constexpr int TEAMS = lnb_warps(W, sizeof(T)) / W;
-  using Raw = typename Pack<T, VEC>::Raw;
-  extern __shared__ __align__(16) uint8_t ring[];          // [teams][stages][x, res][row]
-  __shared__ uint64_t full[TEAMS][LNT_STAGES];
-  __shared__ int abort_flag;
-  __shared__ float2 red[TEAMS][2][W];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int team = warp / W, wt = warp % W;
-  const float inv_d = 1.0f / static_cast<float>(d);
-  const long long n_el = static_cast<long long>(rows) * d;
-  const uint32_t bytes = static_cast<uint32_t>(d) * sizeof(T);
-  const uint32_t stage_bytes = bytes * (res ? 2 : 1);
-  uint8_t* mine = ring + static_cast<size_t>(team) * stages * stage_bytes;
-  if (threadIdx.x == 0) {
-    for (int t = 0; t < TEAMS; ++t)
-      for (int i = 0; i < LNT_STAGES; ++i) mbar_init(&full[t][i], 1);
-    abort_flag = 0;
-    fence_mbar_init();
-  }
-  __syncthreads();
-  grid_dependency_wait();
-  grid_dependents_launch();
-  const bool feeder = wt == 0 && lane == 0;
-  auto issue = [&](long long row, int stage) {
-    mbar_arrive_expect_tx(&full[team][stage], stage_bytes);
-    uint8_t* to = mine + static_cast<size_t>(stage) * stage_bytes;
-    bulk_load(to, x + row * d, bytes, &full[team][stage]);
-    if (res) bulk_load(to + bytes, res + row * d, bytes, &full[team][stage]);
-  };
-  const long long first = blockIdx.x + static_cast<long long>(gridDim.x) * team;     // few rows: one a block
-  const long long step = static_cast<long long>(gridDim.x) * TEAMS;
-  if (feeder)
-    for (int s = 0; s < stages && first + s * step < rows; ++s) issue(first + s * step, s);
-  int stage = 0;
-  uint32_t parity = 0;
-  for (long long row = first; row < rows; row += step) {
-    const long long base = row * d;
-    const uint8_t* at = mine + static_cast<size_t>(stage) * stage_bytes;
-    // a wait that runs out marks the error word and goes on: every thread keeps to the same barriers
-    mbar_wait(&full[team][stage], parity, err, &abort_flag, 31);
-    float v[NV * VEC];
-    float sm = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int col = ((i * W + wt) * 32 + lane) * VEC;
-      const bool on = col < d;
-      Raw u = on ? *reinterpret_cast<const Raw*>(at + col * sizeof(T)) : Raw{};
-      if (on && res) {
-        const Raw r = *reinterpret_cast<const Raw*>(at + bytes + col * sizeof(T));
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) u.e[j] = from_f32<T>(to_f32<T>(u.e[j]) + to_f32<T>(r.e[j]));
-        if (in_bounds(err, base + col, VEC, n_el, SITE_LNT_TOTAL)) *reinterpret_cast<Raw*>(total + base + col) = u;
-      }
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        v[i * VEC + j] = on ? to_f32<T>(u.e[j]) : 0.0f;
-        sm += v[i * VEC + j];
-      }
-    }
-    const float mean = team_sum<W>(sm, 0.0f, red[team], team, wt, lane, 0).x * inv_d;
-    // the team has read the stage: its next row may come
-    if (feeder && row + stages * step < rows) issue(row + stages * step, stage);
-    if (++stage == stages) { stage = 0; parity ^= 1u; }
-    float q = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const bool on = ((i * W + wt) * 32 + lane) * VEC < d;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float t = v[i * VEC + j] - mean;
-        q += on ? t * t : 0.0f;
-      }
-    }
-    const float rstd = rsqrtf(team_sum<W>(q, 0.0f, red[team], team, wt, lane, 1).x * inv_d + eps);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int col = ((i * W + wt) * 32 + lane) * VEC;
-      if (col >= d || !in_bounds(err, base + col, VEC, n_el, SITE_LNT_Y)) continue;
-      float gg[VEC], bb[VEC];
-      load_params<VEC>(g + col, gg);
-      load_params<VEC>(bta + col, bb);
-      Raw o;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) o.e[j] = from_f32<T>(fmaf((v[i * VEC + j] - mean) * rstd, gg[j], bb[j]));
-      *reinterpret_cast<Raw*>(y + base + col) = o;
-    }
-    if (feeder && in_bounds(err, row, 1, rows, SITE_LNT_STATS)) stats[row] = make_float2(mean, rstd);
   }
 }
 
@@ -605,7 +536,7 @@ struct Spread {
   bool vec;      // rows start on 16 bytes
   int nv;        // element-wise: loads a lane, the fewest (of those compiled) that leave a row to 8 warps
   int warps;     // per row
-  int stages;    // rings: rows in flight per team, what 200 KB of shared memory hold
+  int stages;    // backward: rows in flight per team, what 200 KB of shared memory hold
   int blocks;    // backward: what the device holds at the kernels' bound of registers and shared memory, at most one a row
 };
 
@@ -730,43 +661,14 @@ cudaError_t go_any(const FwdArgs<T>& a, const Spread& sp, cudaStream_t s) {
                     dim3(32 * sp.warps), 0, s, a.x, a.res, a.g, a.b, a.rows, a.d, a.eps, a.y, a.total, a.stats, a.err);
 }
 
-template <typename T, int VEC, int NV, int W>
-cudaError_t go_ring(const FwdArgs<T>& a, const Spread& sp, cudaStream_t s) {
-  static uint64_t done = 0;
-  const cudaError_t e = ring_attr(ln_train_fwd_ring_kernel<T, VEC, NV, W>, &done);
-  if (e != cudaSuccess) return e;
-  const size_t smem = static_cast<size_t>(lnb_warps(W, sizeof(T)) / W) * sp.stages * (a.res ? 2 : 1) * a.d * sizeof(T);
-  return launch_pdl(ln_train_fwd_ring_kernel<T, VEC, NV, W>, dim3(sp.blocks), dim3(lnb_warps(W, sizeof(T)) * 32), smem, s,
-                    a.x, a.res, a.g, a.b, a.rows, a.d, a.eps, a.y, a.total, a.stats, sp.stages, a.err);
-}
-
 // Elements a lane: fifths of 40 for rows of one warp (short rows keep few registers), 40 for the rest.
 template <typename T>
 cudaError_t fwd_by_width(const FwdArgs<T>& a, const Spread& sp, cudaStream_t s) {
   constexpr int VEC = 16 / sizeof(T), FULL = 40 / VEC;
   if (!sp.vec) return any_by_width(a, sp, s);
-  // 16-bit rows go through the rings where the direct kernel is short of bytes in flight or of overlap: rows of
-  // several warps, whose barriers hold the next row's loads back (with a residual, direct against ring: 12000 x
-  // 5120 bf16 156 / 110 us, 24000 x 2560 150 / 90, 6000 x 10240 207 / 124, 100 x 5120 6.2 both), and one input
-  // (48000 x 1280 bf16 80 / 67, 48000 x 1024 f16 55 / 50, 100000 x 384 75 / 51).  One warp a row with a residual has
-  // the loads of two inputs in flight by itself (48000 x 1280 89 / 90, 48000 x 1024 67 / 72), and so have f32 rows,
-  // twice the bytes an element (24000 x 1280 with a residual 79 / 87, 6000 x 5120 80 / 85; without 45 / 52, 49 / 57).
-  if constexpr (sizeof(T) == 2) {
-    if (sp.warps == 2) return go_ring<T, VEC, FULL, 2>(a, sp, s);
-    if (sp.warps == 4) return go_ring<T, VEC, FULL, 4>(a, sp, s);
-    if (sp.warps == 8) return go_ring<T, VEC, FULL, 8>(a, sp, s);
-    if (!a.res) {
-      if (a.d <= 256) return go_ring<T, VEC, FULL / 5, 1>(a, sp, s);
-      if (a.d <= 512) return go_ring<T, VEC, 2 * FULL / 5, 1>(a, sp, s);
-      if (a.d <= 768) return go_ring<T, VEC, 3 * FULL / 5, 1>(a, sp, s);
-      if (a.d <= 1024) return go_ring<T, VEC, 4 * FULL / 5, 1>(a, sp, s);
-      return go_ring<T, VEC, FULL, 1>(a, sp, s);
-    }
-  } else {
-    if (sp.warps == 2) return go<T, VEC, FULL, 2>(a, s);
-    if (sp.warps == 4) return go<T, VEC, FULL, 4>(a, s);
-    if (sp.warps == 8) return go<T, VEC, FULL, 8>(a, s);
-  }
+  if (sp.warps == 2) return go<T, VEC, FULL, 2>(a, s);
+  if (sp.warps == 4) return go<T, VEC, FULL, 4>(a, s);
+  if (sp.warps == 8) return go<T, VEC, FULL, 8>(a, s);
   if (a.d <= 256) return go<T, VEC, FULL / 5, 1>(a, s);
   if (a.d <= 512) return go<T, VEC, 2 * FULL / 5, 1>(a, s);
   if (a.d <= 768) return go<T, VEC, 3 * FULL / 5, 1>(a, s);
@@ -810,7 +712,7 @@ wb_status wb_layernorm_forward(const void* x, const void* residual, const float*
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint32_t* err = tc_err_ptr();
   if (!err) return WB_ECUDA;
-  const Spread sp = spread(rows, d, dtype, residual ? 2 : 1);
+  const Spread sp = spread(rows, d, dtype, 1);
   Prof pr(PC_TRAIN_LN, s);
   if (dtype == WB_BF16) WB_CUDA(fwd_t<__nv_bfloat16>(x, residual, g, b, rows, d, eps, y, total, stats, sp, err, s));
   else if (dtype == WB_F16) WB_CUDA(fwd_t<__half>(x, residual, g, b, rows, d, eps, y, total, stats, sp, err, s));
