@@ -9,6 +9,7 @@
 // the sums over rows are fp32, and the row statistics take their two passes over registers.
 // Forward: a team of 1, 2, 4 or 8 warps (by the width) holds a row, at most 40 elements a lane; teams of
 // one warp need no barrier.  Backward: see there.
+#include <cstring>
 #include <mutex>
 #include <type_traits>
 
@@ -20,7 +21,8 @@ namespace wb {
 namespace {
 
 constexpr int LNT_MAX_D = 10240;
-constexpr int LNT_FWD_BLOCKS = 152 * 32;   // grid cap
+// Grid cap: well above what is resident, so that the SMs take rows as they get through them (152 * 8: 82 us, this 78).
+constexpr int LNT_FWD_BLOCKS = 152 * 32;
 constexpr int COL_SLICES = 32;            // column-sum kernel: slices of the partial rows per block
 
 template <typename T>
@@ -93,17 +95,21 @@ __device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
   return d;
 }
 // Pair i of a loaded vector as two floats, and back: 16-bit pairs as whole words (element by element the compiler
-// takes twice the conversions and puts the halves together with permutes).
+// takes twice the conversions and puts the halves together with permutes: the forward pass of 48000 x 1280 bf16 with
+// a residual took 86 us that way, 78 so).
 template <typename T, typename Raw>
 __device__ __forceinline__ uint64_t pair_of(const Raw& r, int i) {
   if constexpr (sizeof(T) == 4) {
     return f32x2_pack(r.e[2 * i], r.e[2 * i + 1]);
   } else {
-    const uint32_t w = reinterpret_cast<const uint32_t*>(r.e)[i];
     if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+      uint32_t w;
+      memcpy(&w, r.e + 2 * i, 4);
       return f32x2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     } else {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+      __half2 w;
+      memcpy(&w, r.e + 2 * i, 4);
+      const float2 f = __half22float2(w);
       return f32x2_pack(f.x, f.y);
     }
   }
@@ -116,14 +122,20 @@ __device__ __forceinline__ void set_pair(Raw& r, int i, uint64_t v) {
     r.e[2 * i] = lo;
     r.e[2 * i + 1] = hi;
   } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
-    reinterpret_cast<__nv_bfloat162*>(r.e)[i] = __floats2bfloat162_rn(lo, hi);
+    const __nv_bfloat162 w = __floats2bfloat162_rn(lo, hi);
+    memcpy(r.e + 2 * i, &w, 4);
   } else {
-    reinterpret_cast<__half2*>(r.e)[i] = __floats2half2_rn(lo, hi);
+    const __half2 w = __floats2half2_rn(lo, hi);
+    memcpy(r.e + 2 * i, &w, 4);
   }
 }
 
 constexpr int lnt_warps(int W) { return W < 4 ? 4 : W; }   // warps per block: one to four teams
 
+// Rows are read into registers, all loads of a row before its first sum; columns past the row count as zeros, so that
+// the sums have no branches (with branches the compiler keeps the loads apart: 3000 x 10240 f32 88 us against 78).
+// 48000 x 1280 bf16 with a residual: 78 us, 6.3 TB/s, 24000 x 1280 f32 76.  Rings of shared memory in front of the same
+// arithmetic take 85 to 89 (16 warps an SM, one or two rows at a time).
 template <typename T, int VEC, int NV, int W>
 __global__ void __launch_bounds__(lnt_warps(W) * 32)
     ln_train_fwd_kernel(const T* __restrict__ x, const T* __restrict__ res, const float* __restrict__ g,
@@ -209,8 +221,10 @@ __global__ void __launch_bounds__(lnt_warps(W) * 32)
 // block order: no atomics, the same result every time.  A team's rows come through its own ring of shared
 // memory, filled by one lane with bulk copies, and are read from there twice (for the row's sums, then for
 // dx), so that neither the rows in flight nor the row at hand cost registers.  The arithmetic is on packed
-// pairs.  Measured at 48000 x 1280 bf16 with dt: 98 us (5.0 TB/s); rows held in registers and read directly 274 us
-// (216 registers, 8 warps an SM); four resident blocks a SM instead of one write more partial rows (5120 wide: 77 us against 72 with the forward pass).
+// pairs.  g lies in shared memory too: read from global memory twice a row, 32 bytes apart from lane to lane, it took
+// more of the L1 than the rows themselves (98 us against 86 at 48000 x 1280 bf16 with dt, 6000 x 10240 128 against 86).
+// Measured there: 82 us (6.0 TB/s); rows held in registers and read directly 274 us (216 registers, 8 warps an SM);
+// four resident blocks a SM instead of one write more partial rows.
 // Widths whose rows do not start on 16 bytes are read directly, element by element.
 constexpr int LNT_WARPS = 8;     // per block of the element-wise kernel, at most
 constexpr int LNT_STAGES = 4;    // rows in flight per team, at most
@@ -233,21 +247,29 @@ __device__ __forceinline__ float2 block_sum(float a, float b, float2 (*red)[LNT_
   return make_float2(a, b);
 }
 
-// Warps of a block, one block an SM.  Measured with 8 / 12 / 16: 48000 x 1280 bf16 with dt (W = 1) 108 / 101 / 98 us;
-// both directions of 3001 x 5120 f16 (W = 4) 74 / 70 / 73 us.
-constexpr int lnb_warps(int W, int es) { return W < 4 && es == 2 ? 16 : W < 8 ? 12 : 8; }
-constexpr int LNB_RING = 200 * 1024;   // bytes of the rings of a block
+// Elements a lane: fifths of 40 for rows of one warp (short rows keep few registers), 40 for the rest.
+constexpr int lane_elems(int d) { return d > 1280 ? 40 : (d + 255) / 256 * 8; }
+// Warps of a block, one block an SM.  Rows of many elements a lane take few warps, whose registers hold more loads
+// at once and whose rings then have two rows each; short rows take many, as their chains of sums are long for their
+// bytes.  bf16 with dt, 8 / 12 / 16 warps: 48000 x 1280 82 / 86 / 86 us, 24000 x 2560 82 / 85 / 88, 60000 x 768
+// 65 / 65 / 68, 80000 x 640 80 / 71 / 70, 100000 x 512 79 / 70 / 69, 100000 x 256 61 / 49 / 45; with 6 and 4 warps
+// 48000 x 1280 takes 86 and 102.  f32: 24000 x 1280 82 / 85 / -, 50000 x 384 55 / 54 / -; four warps a row, 6000 x
+// 5120: 89 / 85 / -.
+constexpr int lnb_warps(int W, int es, int elems) {
+  return W == 8 || (W < 4 && elems >= 32) ? 8 : es == 2 && elems <= 16 ? 16 : 12;
+}
+constexpr int LNB_RING = 224 * 1024;   // bytes of g and the rings of a block
 
 // Partial rows part[block] = [dg (d) | db (d)]; null where the caller wants dx alone.
 template <typename T, int VEC, int NV, int W>
-__global__ void __launch_bounds__(lnb_warps(W, sizeof(T)) * 32, 1)
+__global__ void __launch_bounds__(lnb_warps(W, sizeof(T), NV * VEC) * 32, 1)
     ln_train_bwd_kernel(const T* __restrict__ dy, const T* __restrict__ x, const float* __restrict__ g,
                         const float2* __restrict__ stats, const T* __restrict__ dt, int rows, int d,
                         T* __restrict__ dx, float* __restrict__ part, int stages, uint32_t* err) {
-  constexpr int TEAMS = lnb_warps(W, sizeof(T)) / W, NP = VEC / 2;    // pairs a vector
-  static_assert(TEAMS * 3 * (W * 32 * NV * VEC) * static_cast<int>(sizeof(T)) <= LNB_RING, "a row of each team");
+  constexpr int TEAMS = lnb_warps(W, sizeof(T), NV * VEC) / W, NP = VEC / 2;    // pairs a vector
+  static_assert((TEAMS * 3 * static_cast<int>(sizeof(T)) + 4) * (W * 32 * NV * VEC) <= LNB_RING, "g, a row a team");
   using Raw = typename Pack<T, VEC>::Raw;
-  extern __shared__ __align__(16) uint8_t ring[];          // [teams][stages][x, dy, dt][row]; at the end [teams][2 d] sums
+  extern __shared__ __align__(16) uint8_t ring[];     // g, [teams][stages][x, dy, dt][row]; at the end [teams][2 d]
   __shared__ uint64_t full[TEAMS][LNT_STAGES];
   __shared__ int abort_flag;
   __shared__ float2 red[TEAMS][2][W];
@@ -257,18 +279,31 @@ __global__ void __launch_bounds__(lnb_warps(W, sizeof(T)) * 32, 1)
   const long long n_el = static_cast<long long>(rows) * d;
   const uint32_t bytes = static_cast<uint32_t>(d) * sizeof(T);
   const uint32_t stage_bytes = bytes * (dt ? 3 : 2);
-  uint8_t* mine = ring + static_cast<size_t>(team) * stages * stage_bytes;
+  // g, by (vector, quarter of a vector, lane): neighbouring lanes read neighbouring 16 bytes
+  float4* gs = reinterpret_cast<float4*>(ring);
+  constexpr int G4 = VEC / 4;
+  uint8_t* mine = ring + W * NV * 32 * VEC * sizeof(float) + static_cast<size_t>(team) * stages * stage_bytes;
   if (threadIdx.x == 0) {
     for (int t = 0; t < TEAMS; ++t)
       for (int i = 0; i < LNT_STAGES; ++i) mbar_init(&full[t][i], 1);
     abort_flag = 0;
     fence_mbar_init();
   }
+  grid_dependency_wait();
+  if (team == 0) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = ((i * W + wt) * 32 + lane) * VEC;
+#pragma unroll
+      for (int q = 0; q < G4; ++q)
+        gs[((i * W + wt) * G4 + q) * 32 + lane] =
+            col < d ? __ldg(reinterpret_cast<const float4*>(g + col) + q) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+  }
   __syncthreads();
   uint64_t ag[NV * NP], ab[NV * NP];         // this lane's columns of dg and db, in pairs
 #pragma unroll
   for (int i = 0; i < NV * NP; ++i) ag[i] = ab[i] = 0;
-  grid_dependency_wait();
   grid_dependents_launch();
   const bool feeder = wt == 0 && lane == 0;
   auto issue = [&](long long row, int stage) {
@@ -284,6 +319,13 @@ __global__ void __launch_bounds__(lnb_warps(W, sizeof(T)) * 32, 1)
     for (int s = 0; s < stages && first + s * step < rows; ++s) issue(first + s * step, s);
   auto stats_of = [&](long long row) {
     return row < rows && in_bounds(err, row, 1, rows, SITE_LNT_STATS) ? __ldg(stats + row) : make_float2(0.0f, 0.0f);
+  };
+  auto load_gs = [&](int i, float (&o)[VEC]) {
+#pragma unroll
+    for (int q = 0; q < G4; ++q) {
+      const float4 f = gs[((i * W + wt) * G4 + q) * 32 + lane];
+      o[4 * q] = f.x; o[4 * q + 1] = f.y; o[4 * q + 2] = f.z; o[4 * q + 3] = f.w;
+    }
   };
   float2 ahead = stats_of(first);            // statistics of the next row, loaded a row early
   int stage = 0, slot = 0;
@@ -304,7 +346,7 @@ __global__ void __launch_bounds__(lnb_warps(W, sizeof(T)) * 32, 1)
       const Raw xv = *reinterpret_cast<const Raw*>(at + col * sizeof(T));
       const Raw yv = *reinterpret_cast<const Raw*>(at + bytes + col * sizeof(T));
       float gg[VEC];
-      load_params<VEC>(g + col, gg);
+      load_gs(i, gg);
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
         const int e = i * NP + j;
@@ -333,7 +375,7 @@ __global__ void __launch_bounds__(lnb_warps(W, sizeof(T)) * 32, 1)
       const Raw xv = *reinterpret_cast<const Raw*>(at + col * sizeof(T));
       const Raw yv = *reinterpret_cast<const Raw*>(at + bytes + col * sizeof(T));
       float gg[VEC];
-      load_params<VEC>(g + col, gg);
+      load_gs(i, gg);
       Raw tv, o;
       if (dt) tv = *reinterpret_cast<const Raw*>(at + 2 * bytes + col * sizeof(T));
 #pragma unroll
@@ -367,7 +409,7 @@ __global__ void __launch_bounds__(lnb_warps(W, sizeof(T)) * 32, 1)
     }
   }
   __syncthreads();
-  for (int c = threadIdx.x; c < d; c += lnb_warps(W, sizeof(T)) * 32) {       // pairs of the 2 d sums, teams in order
+  for (int c = threadIdx.x; c < d; c += TEAMS * W * 32) {  // pairs of the 2 d sums, teams in order
     uint64_t sum = acc[c];
 #pragma unroll
     for (int t = 1; t < TEAMS; ++t) sum = f32x2_add(sum, acc[t * d + c]);
@@ -536,8 +578,8 @@ struct Spread {
   bool vec;      // rows start on 16 bytes
   int nv;        // element-wise: loads a lane, the fewest (of those compiled) that leave a row to 8 warps
   int warps;     // per row
-  int stages;    // backward: rows in flight per team, what 200 KB of shared memory hold
-  int blocks;    // backward: what the device holds at the kernels' bound of registers and shared memory, at most one a row
+  int stages;    // backward: rows in flight per team, what the shared memory holds
+  int blocks;    // backward: what the device holds at the kernels' bound of registers and memory, at most one a row
 };
 
 Spread spread(int rows, int d, int dtype, int tensors) {
@@ -547,7 +589,8 @@ Spread spread(int rows, int d, int dtype, int tensors) {
   int per_sm = 1;
   if (s.vec) {
     s.warps = team_warps(d);
-    const int fit = LNB_RING / (lnb_warps(s.warps, es) / s.warps * d * es * tensors);
+    const int teams = lnb_warps(s.warps, es, lane_elems(d)) / s.warps;
+    const int fit = (LNB_RING - s.warps * 1280 * 4) / (teams * d * es * tensors);
     s.stages = fit < LNT_STAGES ? fit : LNT_STAGES;
   } else {
     const int need = (d + 32 * LNT_WARPS - 1) / (32 * LNT_WARPS);
@@ -604,12 +647,13 @@ cudaError_t go(const BwdArgs<T>& a, const Spread& sp, cudaStream_t s) {
   static uint64_t done = 0;
   const cudaError_t e = ring_attr(ln_train_bwd_kernel<T, VEC, NV, W>, &done);
   if (e != cudaSuccess) return e;
-  constexpr size_t TEAMS = lnb_warps(W, sizeof(T)) / W;
-  size_t smem = TEAMS * sp.stages * (a.dt ? 3 : 2) * a.d * sizeof(T);
+  constexpr int WARPS = lnb_warps(W, sizeof(T), NV * VEC);
+  constexpr size_t TEAMS = WARPS / W;
+  size_t smem = W * NV * 32 * VEC * sizeof(float) + TEAMS * sp.stages * (a.dt ? 3 : 2) * a.d * sizeof(T);
   const size_t sums = TEAMS * 2 * a.d * sizeof(float);
   if (smem < sums) smem = sums;
-  return launch_pdl(ln_train_bwd_kernel<T, VEC, NV, W>, dim3(sp.blocks), dim3(lnb_warps(W, sizeof(T)) * 32), smem, s, a.dy, a.x,
-                    a.g, a.stats, a.dt, a.rows, a.d, a.dx, a.part, sp.stages, a.err);
+  return launch_pdl(ln_train_bwd_kernel<T, VEC, NV, W>, dim3(sp.blocks), dim3(WARPS * 32), smem, s, a.dy, a.x, a.g,
+                    a.stats, a.dt, a.rows, a.d, a.dx, a.part, sp.stages, a.err);
 }
 template <typename T, int NV>
 cudaError_t go_any(const BwdArgs<T>& a, const Spread& sp, cudaStream_t s) {
@@ -636,7 +680,7 @@ cudaError_t any_by_width(const Args& a, const Spread& sp, cudaStream_t s) {
 
 template <typename T>
 cudaError_t bwd_by_width(const BwdArgs<T>& a, const Spread& sp, cudaStream_t s) {
-  constexpr int VEC = 16 / sizeof(T), FULL = 40 / VEC;     // elements a lane as in fwd_by_width
+  constexpr int VEC = 16 / sizeof(T), FULL = 40 / VEC;     // lane_elems(d) of them
   if (sp.vec) {
     if (sp.warps == 2) return go<T, VEC, FULL, 2>(a, sp, s);
     if (sp.warps == 4) return go<T, VEC, FULL, 4>(a, sp, s);
@@ -661,13 +705,15 @@ cudaError_t go_any(const FwdArgs<T>& a, const Spread& sp, cudaStream_t s) {
                     dim3(32 * sp.warps), 0, s, a.x, a.res, a.g, a.b, a.rows, a.d, a.eps, a.y, a.total, a.stats, a.err);
 }
 
-// Elements a lane: fifths of 40 for rows of one warp (short rows keep few registers), 40 for the rest.
+// Vectors of 8 bytes for 16-bit rows: g and b then are 16 neighbouring bytes a lane.  Against 16 bytes: 48000 x 1280
+// bf16 without a residual 52 / 57 us, with one 77.5 / 77.9, 6000 x 10240 83 / 89; rows of two or four warps gain
+// nothing (24000 x 2560 80 / 80) or lose (3001 x 5120 27.5 / 26.1), and take 16 bytes.
 template <typename T>
 cudaError_t fwd_by_width(const FwdArgs<T>& a, const Spread& sp, cudaStream_t s) {
-  constexpr int VEC = 16 / sizeof(T), FULL = 40 / VEC;
+  constexpr int WIDE = 16 / sizeof(T), VEC = 4, FULL = 40 / VEC;
   if (!sp.vec) return any_by_width(a, sp, s);
-  if (sp.warps == 2) return go<T, VEC, FULL, 2>(a, s);
-  if (sp.warps == 4) return go<T, VEC, FULL, 4>(a, s);
+  if (sp.warps == 2) return go<T, WIDE, 40 / WIDE, 2>(a, s);
+  if (sp.warps == 4) return go<T, WIDE, 40 / WIDE, 4>(a, s);
   if (sp.warps == 8) return go<T, VEC, FULL, 8>(a, s);
   if (a.d <= 256) return go<T, VEC, FULL / 5, 1>(a, s);
   if (a.d <= 512) return go<T, VEC, 2 * FULL / 5, 1>(a, s);
