@@ -81,7 +81,8 @@ def test_forward_and_backward_match_the_formulas(wb, rows, d, kind, residual):
 
 
 # more rows than the device holds at once: every slot is filled several times over
-@pytest.mark.parametrize("rows,d", [(20011, 136), (15001, 1280), (12007, 1928), (7001, 4104), (4003, 10240), (3001, 1283)])
+@pytest.mark.parametrize("rows,d", [(20011, 136), (15001, 1280), (12007, 1928), (7001, 4104), (4003, 10240),
+                                    (3001, 1283), (20011, 387), (9001, 1021), (6001, 5123), (2503, 10239)])
 @pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("residual", [False, True])
 def test_a_row_does_not_depend_on_the_rows_around_it(wb, rows, d, kind, residual):

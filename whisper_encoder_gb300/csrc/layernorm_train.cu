@@ -225,7 +225,9 @@ __global__ void __launch_bounds__(lnt_warps(W) * 32)
 // more of the L1 than the rows themselves (98 us against 86 at 48000 x 1280 bf16 with dt, 6000 x 10240 128 against 86).
 // Measured there: 82 us (6.0 TB/s); rows held in registers and read directly 274 us (216 registers, 8 warps an SM);
 // four resident blocks a SM instead of one write more partial rows.
-// Widths whose rows do not start on 16 bytes are read directly, element by element.
+// Rows that do not start on 16 bytes (ragged) come through the same rings, copied with the elements that share their
+// first and last 16 bytes, and are read element by element, lanes side by side: 10000 x 5123 bf16 with dt 182 us,
+// 40000 x 387 45, 4097 x 1283 f32 27 (a block a row, read directly into registers: 1195, 165 and 27).
 constexpr int LNT_WARPS = 8;     // per block of the element-wise kernel, at most
 constexpr int LNT_STAGES = 4;    // rows in flight per team, at most
 
@@ -254,20 +256,28 @@ constexpr int lane_elems(int d) { return d > 1280 ? 40 : (d + 255) / 256 * 8; }
 // bytes.  bf16 with dt, 8 / 12 / 16 warps: 48000 x 1280 82 / 86 / 86 us, 24000 x 2560 82 / 85 / 88, 60000 x 768
 // 65 / 65 / 68, 80000 x 640 80 / 71 / 70, 100000 x 512 79 / 70 / 69, 100000 x 256 61 / 49 / 45; with 6 and 4 warps
 // 48000 x 1280 takes 86 and 102.  f32: 24000 x 1280 82 / 85 / -, 50000 x 384 55 / 54 / -; four warps a row, 6000 x
-// 5120: 89 / 85 / -.
-constexpr int lnb_warps(int W, int es, int elems) {
-  return W == 8 || (W < 4 && elems >= 32) ? 8 : es == 2 && elems <= 16 ? 16 : 12;
+// 5120: 89 / 85 / -.  Ragged rows are bound by the reads of single elements and want the warps: 40000 x 1283 bf16
+// 191 / 156 / 138, 40000 x 901 101 / 86 / 80, 40000 x 1283 f32 174 / 135 / -.
+constexpr int lnb_warps(int W, int es, int elems, bool ragged) {
+  return W == 8 || (!ragged && W < 4 && elems >= 32) ? 8 : es == 2 && W < 4 && (ragged || elems <= 16) ? 16 : 12;
 }
 constexpr int LNB_RING = 224 * 1024;   // bytes of g and the rings of a block
+// Bytes of a row in a ring: a ragged row does not start on 16 bytes and is copied with what lies around it.
+__host__ __device__ constexpr int lnb_slot(int d, int es, bool ragged) {
+  return ragged ? (d * es + 14 + 15) / 16 * 16 : d * es;
+}
 
 // Partial rows part[block] = [dg (d) | db (d)]; null where the caller wants dx alone.
 template <typename T, int VEC, int NV, int W>
-__global__ void __launch_bounds__(lnb_warps(W, sizeof(T), NV * VEC) * 32, 1)
+__global__ void __launch_bounds__(lnb_warps(W, sizeof(T), NV * VEC, VEC * sizeof(T) < 16) * 32, 1)
     ln_train_bwd_kernel(const T* __restrict__ dy, const T* __restrict__ x, const float* __restrict__ g,
                         const float2* __restrict__ stats, const T* __restrict__ dt, int rows, int d,
                         T* __restrict__ dx, float* __restrict__ part, int stages, uint32_t* err) {
-  constexpr int TEAMS = lnb_warps(W, sizeof(T), NV * VEC) / W, NP = VEC / 2;    // pairs a vector
-  static_assert((TEAMS * 3 * static_cast<int>(sizeof(T)) + 4) * (W * 32 * NV * VEC) <= LNB_RING, "g, a row a team");
+  constexpr int TEAMS = lnb_warps(W, sizeof(T), NV * VEC, VEC * sizeof(T) < 16) / W, NP = VEC / 2;    // pairs a vector
+  constexpr bool RAGGED = VEC * sizeof(T) < 16;
+  static_assert(!RAGGED || VEC == 2, "a pair of elements 32 W columns apart");
+  static_assert((TEAMS * 3 * static_cast<int>(sizeof(T)) + 4) * (W * 32 * NV * VEC) + TEAMS * 3 * 32 <= LNB_RING,
+                "g and a row of each team");
   using Raw = typename Pack<T, VEC>::Raw;
   extern __shared__ __align__(16) uint8_t ring[];     // g, [teams][stages][x, dy, dt][row]; at the end [teams][2 d]
   __shared__ uint64_t full[TEAMS][LNT_STAGES];
@@ -277,10 +287,11 @@ __global__ void __launch_bounds__(lnb_warps(W, sizeof(T), NV * VEC) * 32, 1)
   const int team = warp / W, wt = warp % W;
   const float inv_d = 1.0f / static_cast<float>(d);
   const long long n_el = static_cast<long long>(rows) * d;
-  const uint32_t bytes = static_cast<uint32_t>(d) * sizeof(T);
+  const uint32_t bytes = lnb_slot(d, sizeof(T), RAGGED);
   const uint32_t stage_bytes = bytes * (dt ? 3 : 2);
-  // g, by (vector, quarter of a vector, lane): neighbouring lanes read neighbouring 16 bytes
+  // g, by (vector, quarter of a vector, lane): neighbouring lanes read neighbouring 16 bytes (ragged: by column)
   float4* gs = reinterpret_cast<float4*>(ring);
+  float* gs1 = reinterpret_cast<float*>(ring);
   constexpr int G4 = VEC / 4;
   uint8_t* mine = ring + W * NV * 32 * VEC * sizeof(float) + static_cast<size_t>(team) * stages * stage_bytes;
   if (threadIdx.x == 0) {
@@ -290,7 +301,9 @@ __global__ void __launch_bounds__(lnb_warps(W, sizeof(T), NV * VEC) * 32, 1)
     fence_mbar_init();
   }
   grid_dependency_wait();
-  if (team == 0) {
+  if (RAGGED) {
+    for (int c = threadIdx.x; c < d; c += TEAMS * W * 32) gs1[c] = __ldg(g + c);
+  } else if (team == 0) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = ((i * W + wt) * 32 + lane) * VEC;
@@ -307,11 +320,33 @@ __global__ void __launch_bounds__(lnb_warps(W, sizeof(T), NV * VEC) * 32, 1)
   grid_dependents_launch();
   const bool feeder = wt == 0 && lane == 0;
   auto issue = [&](long long row, int stage) {
-    mbar_arrive_expect_tx(&full[team][stage], stage_bytes);
     uint8_t* to = mine + static_cast<size_t>(stage) * stage_bytes;
-    bulk_load(to, x + row * d, bytes, &full[team][stage]);
-    bulk_load(to + bytes, dy + row * d, bytes, &full[team][stage]);
-    if (dt) bulk_load(to + 2 * bytes, dt + row * d, bytes, &full[team][stage]);
+    if constexpr (!RAGGED) {
+      mbar_arrive_expect_tx(&full[team][stage], stage_bytes);
+      bulk_load(to, x + row * d, bytes, &full[team][stage]);
+      bulk_load(to + bytes, dy + row * d, bytes, &full[team][stage]);
+      if (dt) bulk_load(to + 2 * bytes, dt + row * d, bytes, &full[team][stage]);
+    } else {
+      // the whole 16 bytes that the row lies in, as far as the tensor has them; what is left of the last row by hand.
+      // (dx over an input: the neighbours' elements in them may be old or new, and are not looked at.)
+      constexpr int PER = 16 / sizeof(T);
+      const long long lo = row * d / PER * PER, end = (row + 1) * d, whole = n_el / PER * PER;
+      const long long hi = (end + PER - 1) / PER * PER;
+      const uint32_t n = static_cast<uint32_t>((hi <= n_el ? hi : whole) - lo) * sizeof(T);
+      if (hi > n_el) {
+        for (long long e = whole; e < n_el; ++e) {
+          reinterpret_cast<T*>(to)[e - lo] = x[e];
+          reinterpret_cast<T*>(to + bytes)[e - lo] = dy[e];
+          if (dt) reinterpret_cast<T*>(to + 2 * bytes)[e - lo] = dt[e];
+        }
+      }
+      mbar_arrive_expect_tx(&full[team][stage], n * (dt ? 3 : 2));
+      if (n) {
+        bulk_load(to, x + lo, n, &full[team][stage]);
+        bulk_load(to + bytes, dy + lo, n, &full[team][stage]);
+        if (dt) bulk_load(to + 2 * bytes, dt + lo, n, &full[team][stage]);
+      }
+    }
   };
   const long long first = blockIdx.x + static_cast<long long>(gridDim.x) * team;     // few rows: one a block
   const long long step = static_cast<long long>(gridDim.x) * TEAMS;
@@ -320,11 +355,30 @@ __global__ void __launch_bounds__(lnb_warps(W, sizeof(T), NV * VEC) * 32, 1)
   auto stats_of = [&](long long row) {
     return row < rows && in_bounds(err, row, 1, rows, SITE_LNT_STATS) ? __ldg(stats + row) : make_float2(0.0f, 0.0f);
   };
+  // column of a vector's first element, and of its second where rows are ragged
+  auto col_of = [&](int i) { return RAGGED ? (2 * i * W + wt) * 32 + lane : ((i * W + wt) * 32 + lane) * VEC; };
+  constexpr int NEXT = W * 32;
   auto load_gs = [&](int i, float (&o)[VEC]) {
+    if constexpr (RAGGED) {
+      const int c = col_of(i);
+      o[0] = gs1[c];
+      o[1] = c + NEXT < d ? gs1[c + NEXT] : 0.0f;
+    } else {
 #pragma unroll
-    for (int q = 0; q < G4; ++q) {
-      const float4 f = gs[((i * W + wt) * G4 + q) * 32 + lane];
-      o[4 * q] = f.x; o[4 * q + 1] = f.y; o[4 * q + 2] = f.z; o[4 * q + 3] = f.w;
+      for (int q = 0; q < G4; ++q) {
+        const float4 f = gs[((i * W + wt) * G4 + q) * 32 + lane];
+        o[4 * q] = f.x; o[4 * q + 1] = f.y; o[4 * q + 2] = f.z; o[4 * q + 3] = f.w;
+      }
+    }
+  };
+  auto load_row = [&](const uint8_t* from, int col) -> Raw {
+    if constexpr (RAGGED) {
+      Raw r = {};
+      r.e[0] = reinterpret_cast<const T*>(from)[col];
+      if (col + NEXT < d) r.e[1] = reinterpret_cast<const T*>(from)[col + NEXT];
+      return r;
+    } else {
+      return *reinterpret_cast<const Raw*>(from + col * sizeof(T));
     }
   };
   float2 ahead = stats_of(first);            // statistics of the next row, loaded a row early
@@ -336,15 +390,16 @@ __global__ void __launch_bounds__(lnb_warps(W, sizeof(T), NV * VEC) * 32, 1)
     ahead = stats_of(row + step);
     const uint64_t nm2 = f32x2_pack(-st.x, -st.x), rs2 = f32x2_pack(st.y, st.y);
     const uint8_t* at = mine + static_cast<size_t>(stage) * stage_bytes;
+    if (RAGGED) at += base * sizeof(T) % 16;
     // a wait that runs out marks the error word and goes on: every thread keeps to the same barriers
     mbar_wait(&full[team][stage], parity, err, &abort_flag, 31);
     uint64_t c1p = 0, c2p = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = ((i * W + wt) * 32 + lane) * VEC;
+      const int col = col_of(i);
       if (col >= d) continue;
-      const Raw xv = *reinterpret_cast<const Raw*>(at + col * sizeof(T));
-      const Raw yv = *reinterpret_cast<const Raw*>(at + bytes + col * sizeof(T));
+      const Raw xv = load_row(at, col);
+      const Raw yv = load_row(at + bytes, col);
       float gg[VEC];
       load_gs(i, gg);
 #pragma unroll
@@ -370,14 +425,14 @@ __global__ void __launch_bounds__(lnb_warps(W, sizeof(T), NV * VEC) * 32, 1)
     const uint64_t c12 = f32x2_pack(c1, c1), c22 = f32x2_pack(c2, c2);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = ((i * W + wt) * 32 + lane) * VEC;
-      if (col >= d || !in_bounds(err, base + col, VEC, n_el, SITE_LNT_Y)) continue;
-      const Raw xv = *reinterpret_cast<const Raw*>(at + col * sizeof(T));
-      const Raw yv = *reinterpret_cast<const Raw*>(at + bytes + col * sizeof(T));
+      const int col = col_of(i);
+      if (col >= d || !in_bounds(err, base + col, RAGGED ? 1 : VEC, n_el, SITE_LNT_Y)) continue;
+      const Raw xv = load_row(at, col);
+      const Raw yv = load_row(at + bytes, col);
       float gg[VEC];
       load_gs(i, gg);
       Raw tv, o;
-      if (dt) tv = *reinterpret_cast<const Raw*>(at + 2 * bytes + col * sizeof(T));
+      if (dt) tv = load_row(at + 2 * bytes, col);
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
         const uint64_t h2 = f32x2_mul(f32x2_add(pair_of<T>(xv, j), nm2), rs2);
@@ -385,7 +440,12 @@ __global__ void __launch_bounds__(lnb_warps(W, sizeof(T), NV * VEC) * 32, 1)
         const uint64_t in = f32x2_fma(h2, c22, u2);
         set_pair<T>(o, j, dt ? f32x2_fma(in, rs2, pair_of<T>(tv, j)) : f32x2_mul(in, rs2));
       }
-      *reinterpret_cast<Raw*>(dx + base + col) = o;
+      if constexpr (RAGGED) {
+        dx[base + col] = o.e[0];
+        if (col + NEXT < d) dx[base + col + NEXT] = o.e[1];
+      } else {
+        *reinterpret_cast<Raw*>(dx + base + col) = o;
+      }
     }
     // the team has read the stage for the second time: its next row may come
     if (W == 1) __syncwarp();
@@ -400,12 +460,23 @@ __global__ void __launch_bounds__(lnb_warps(W, sizeof(T), NV * VEC) * 32, 1)
   if (TEAMS > 1) __syncthreads();
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int col = ((i * W + wt) * 32 + lane) * VEC;
+    const int col = col_of(i);
     if (col >= d) continue;
+    if constexpr (RAGGED) {
+      float* to = reinterpret_cast<float*>(ring) + static_cast<size_t>(team) * 2 * d + col;
+      float lo, hi;
+      f32x2_unpack(ag[i], lo, hi);
+      to[0] = lo;
+      if (col + NEXT < d) to[NEXT] = hi;
+      f32x2_unpack(ab[i], lo, hi);
+      to[d] = lo;
+      if (col + NEXT < d) to[d + NEXT] = hi;
+    } else {
 #pragma unroll
-    for (int j = 0; j < NP; ++j) {                         // VEC divides d: pairs start on 8 bytes in both halves
-      acc[(team * 2 * d + col) / 2 + j] = ag[i * NP + j];
-      acc[(team * 2 * d + d + col) / 2 + j] = ab[i * NP + j];
+      for (int j = 0; j < NP; ++j) {                       // VEC divides d: pairs start on 8 bytes in both halves
+        acc[(team * 2 * d + col) / 2 + j] = ag[i * NP + j];
+        acc[(team * 2 * d + d + col) / 2 + j] = ab[i * NP + j];
+      }
     }
   }
   __syncthreads();
@@ -417,75 +488,10 @@ __global__ void __launch_bounds__(lnb_warps(W, sizeof(T), NV * VEC) * 32, 1)
   }
 }
 
-// The same for widths whose rows do not start on 16 bytes: a block of up to 8 warps a row, single elements,
-// read directly.
+// The forward pass of ragged rows: a block of up to 8 warps a row, single elements, read directly (4097 x 1283 f32
+// 18 us, 40000 x 1283 bf16 with a residual 143).
 template <typename T, int NV>
-__global__ void __launch_bounds__(LNT_WARPS * 32, NV <= 6 ? 3 : NV <= 10 ? 2 : 1)
-    ln_train_bwd_any_kernel(const T* __restrict__ dy, const T* __restrict__ x, const float* __restrict__ g,
-                            const float2* __restrict__ stats, const T* __restrict__ dt, int rows, int d,
-                            T* __restrict__ dx, float* __restrict__ part, uint32_t* err) {
-  __shared__ float2 red[2][LNT_WARPS];
-  const int nt = blockDim.x, tid = threadIdx.x;
-  const float inv_d = 1.0f / static_cast<float>(d);
-  const long long n_el = static_cast<long long>(rows) * d;
-  float ag[NV], ab[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) ag[i] = ab[i] = 0.0f;
-  grid_dependency_wait();
-  grid_dependents_launch();
-  int slot = 0;
-  for (long long row = blockIdx.x; row < rows; row += gridDim.x, slot ^= 1) {
-    const long long base = row * d;
-    const float2 st = in_bounds(err, row, 1, rows, SITE_LNT_STATS) ? stats[row] : make_float2(0.0f, 0.0f);
-    T u[NV], w[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int col = i * nt + tid;
-      u[i] = w[i] = from_f32<T>(0.0f);
-      if (col < d && in_bounds(err, base + col, 1, n_el, SITE_LNT_X)) {
-        u[i] = x[base + col];
-        w[i] = dy[base + col];
-      }
-    }
-    float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int col = i * nt + tid;
-      if (col >= d) continue;
-      const float h = (to_f32<T>(u[i]) - st.x) * st.y, y = to_f32<T>(w[i]), gy = __ldg(g + col) * y;
-      ag[i] = fmaf(y, h, ag[i]);
-      ab[i] += y;
-      s1 += gy;
-      s2 = fmaf(gy, h, s2);
-    }
-    const float2 c = block_sum(s1, s2, red, slot);
-    const float c1 = c.x * inv_d, c2 = c.y * inv_d;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int col = i * nt + tid;
-      if (col >= d || !in_bounds(err, base + col, 1, n_el, SITE_LNT_Y)) continue;
-      const float h = (to_f32<T>(u[i]) - st.x) * st.y;
-      float r = st.y * (fmaf(__ldg(g + col), to_f32<T>(w[i]), -c1) - h * c2);
-      if (dt) r += to_f32<T>(dt[base + col]);
-      dx[base + col] = from_f32<T>(r);
-    }
-  }
-  if (!part) return;
-  float* dst = part + static_cast<long long>(blockIdx.x) * 2 * d;
-  const long long part_el = static_cast<long long>(gridDim.x) * 2 * d;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int col = i * nt + tid;
-    if (col >= d || !in_bounds(err, (dst - part) + d + col, 1, part_el, SITE_LNT_PART)) continue;
-    dst[col] = ag[i];
-    dst[d + col] = ab[i];
-  }
-}
-
-// The forward pass for such widths, a block of up to 8 warps a row (4097 x 1283 f32, both directions: 41 us;
-// with two warps a row forward 54).
-template <typename T, int NV>
-__global__ void __launch_bounds__(LNT_WARPS * 32, NV <= 6 ? 4 : NV <= 10 ? 3 : NV <= 20 ? 2 : 1)
+__global__ void __launch_bounds__(LNT_WARPS * 32, NV <= 6 ? 6 : NV <= 10 ? 3 : NV <= 20 ? 2 : 1)
     ln_train_fwd_any_kernel(const T* __restrict__ x, const T* __restrict__ res, const float* __restrict__ g,
                             const float* __restrict__ bta, int rows, int d, float eps, T* __restrict__ y,
                             T* __restrict__ total, float2* __restrict__ stats, uint32_t* err) {
@@ -576,30 +582,25 @@ int fwd_blocks(int rows, int d) {
 // How rows are spread, by width, type and (backward) the tensors that a row is read from.
 struct Spread {
   bool vec;      // rows start on 16 bytes
-  int nv;        // element-wise: loads a lane, the fewest (of those compiled) that leave a row to 8 warps
   int warps;     // per row
   int stages;    // backward: rows in flight per team, what the shared memory holds
-  int blocks;    // backward: what the device holds at the kernels' bound of registers and memory, at most one a row
+  int blocks;    // backward: one an SM, at most one a row
+  int any_nv;    // ragged forward pass: loads a lane, the fewest (of those compiled) that leave a row to 8 warps
+  int any_warps;
 };
 
 Spread spread(int rows, int d, int dtype, int tensors) {
   const int es = dtype == WB_F32 ? 4 : 2;
   Spread s = {};
   s.vec = d % (16 / es) == 0;
-  int per_sm = 1;
-  if (s.vec) {
-    s.warps = team_warps(d);
-    const int teams = lnb_warps(s.warps, es, lane_elems(d)) / s.warps;
-    const int fit = (LNB_RING - s.warps * 1280 * 4) / (teams * d * es * tensors);
-    s.stages = fit < LNT_STAGES ? fit : LNT_STAGES;
-  } else {
-    const int need = (d + 32 * LNT_WARPS - 1) / (32 * LNT_WARPS);
-    s.nv = need <= 2 ? need : need <= 4 ? 4 : need <= 6 ? 6 : need <= 10 ? 10 : need <= 20 ? 20 : 40;
-    s.warps = (d + 32 * s.nv - 1) / (32 * s.nv);
-    per_sm = 8 * (s.nv <= 6 ? 3 : s.nv <= 10 ? 2 : 1) / s.warps;
-    if (per_sm > 16) per_sm = 16;
-  }
-  s.blocks = rows < 152 * per_sm ? rows : 152 * per_sm;
+  s.warps = team_warps(d);
+  const int teams = lnb_warps(s.warps, es, lane_elems(d), !s.vec) / s.warps;
+  const int fit = (LNB_RING - s.warps * 1280 * 4) / (teams * lnb_slot(d, es, !s.vec) * tensors);
+  s.stages = fit < LNT_STAGES ? fit : LNT_STAGES;
+  s.blocks = rows < 152 ? rows : 152;
+  const int need = (d + 32 * LNT_WARPS - 1) / (32 * LNT_WARPS);
+  s.any_nv = need <= 2 ? need : need <= 4 ? 4 : need <= 6 ? 6 : need <= 10 ? 10 : need <= 20 ? 20 : 40;
+  s.any_warps = (d + 32 * s.any_nv - 1) / (32 * s.any_nv);
   return s;
 }
 
@@ -647,51 +648,26 @@ cudaError_t go(const BwdArgs<T>& a, const Spread& sp, cudaStream_t s) {
   static uint64_t done = 0;
   const cudaError_t e = ring_attr(ln_train_bwd_kernel<T, VEC, NV, W>, &done);
   if (e != cudaSuccess) return e;
-  constexpr int WARPS = lnb_warps(W, sizeof(T), NV * VEC);
+  constexpr int WARPS = lnb_warps(W, sizeof(T), NV * VEC, VEC * sizeof(T) < 16);
   constexpr size_t TEAMS = WARPS / W;
-  size_t smem = W * NV * 32 * VEC * sizeof(float) + TEAMS * sp.stages * (a.dt ? 3 : 2) * a.d * sizeof(T);
+  size_t smem = W * NV * 32 * VEC * sizeof(float) +
+                TEAMS * sp.stages * (a.dt ? 3 : 2) * lnb_slot(a.d, sizeof(T), VEC * sizeof(T) < 16);
   const size_t sums = TEAMS * 2 * a.d * sizeof(float);
   if (smem < sums) smem = sums;
   return launch_pdl(ln_train_bwd_kernel<T, VEC, NV, W>, dim3(sp.blocks), dim3(WARPS * 32), smem, s, a.dy, a.x, a.g,
                     a.stats, a.dt, a.rows, a.d, a.dx, a.part, sp.stages, a.err);
 }
-template <typename T, int NV>
-cudaError_t go_any(const BwdArgs<T>& a, const Spread& sp, cudaStream_t s) {
-  return launch_pdl(ln_train_bwd_any_kernel<T, NV>, dim3(sp.blocks), dim3(32 * sp.warps), 0, s, a.dy, a.x, a.g, a.stats,
-                    a.dt, a.rows, a.d, a.dx, a.part, a.err);
-}
-
-// The element-wise kernels, by loads a lane.
-template <typename T, int NV>
-cudaError_t go_any(const FwdArgs<T>& a, const Spread& sp, cudaStream_t s);
-template <typename Args>
-cudaError_t any_by_width(const Args& a, const Spread& sp, cudaStream_t s) {
-  using T = std::remove_const_t<std::remove_pointer_t<decltype(a.x)>>;
-  switch (sp.nv) {
-    case 1: return go_any<T, 1>(a, sp, s);
-    case 2: return go_any<T, 2>(a, sp, s);
-    case 4: return go_any<T, 4>(a, sp, s);
-    case 6: return go_any<T, 6>(a, sp, s);
-    case 10: return go_any<T, 10>(a, sp, s);
-    case 20: return go_any<T, 20>(a, sp, s);
-    default: return go_any<T, 40>(a, sp, s);
-  }
-}
-
-template <typename T>
+template <typename T, int VEC>
 cudaError_t bwd_by_width(const BwdArgs<T>& a, const Spread& sp, cudaStream_t s) {
-  constexpr int VEC = 16 / sizeof(T), FULL = 40 / VEC;     // lane_elems(d) of them
-  if (sp.vec) {
-    if (sp.warps == 2) return go<T, VEC, FULL, 2>(a, sp, s);
-    if (sp.warps == 4) return go<T, VEC, FULL, 4>(a, sp, s);
-    if (sp.warps == 8) return go<T, VEC, FULL, 8>(a, sp, s);
-    if (a.d <= 256) return go<T, VEC, FULL / 5, 1>(a, sp, s);
-    if (a.d <= 512) return go<T, VEC, 2 * FULL / 5, 1>(a, sp, s);
-    if (a.d <= 768) return go<T, VEC, 3 * FULL / 5, 1>(a, sp, s);
-    if (a.d <= 1024) return go<T, VEC, 4 * FULL / 5, 1>(a, sp, s);
-    return go<T, VEC, FULL, 1>(a, sp, s);
-  }
-  return any_by_width(a, sp, s);
+  constexpr int FULL = 40 / VEC;                           // lane_elems(d) of them
+  if (sp.warps == 2) return go<T, VEC, FULL, 2>(a, sp, s);
+  if (sp.warps == 4) return go<T, VEC, FULL, 4>(a, sp, s);
+  if (sp.warps == 8) return go<T, VEC, FULL, 8>(a, sp, s);
+  if (a.d <= 256) return go<T, VEC, FULL / 5, 1>(a, sp, s);
+  if (a.d <= 512) return go<T, VEC, 2 * FULL / 5, 1>(a, sp, s);
+  if (a.d <= 768) return go<T, VEC, 3 * FULL / 5, 1>(a, sp, s);
+  if (a.d <= 1024) return go<T, VEC, 4 * FULL / 5, 1>(a, sp, s);
+  return go<T, VEC, FULL, 1>(a, sp, s);
 }
 
 template <typename T, int VEC, int NV, int W>
@@ -702,7 +678,20 @@ cudaError_t go(const FwdArgs<T>& a, cudaStream_t s) {
 template <typename T, int NV>
 cudaError_t go_any(const FwdArgs<T>& a, const Spread& sp, cudaStream_t s) {
   return launch_pdl(ln_train_fwd_any_kernel<T, NV>, dim3(a.rows < LNT_FWD_BLOCKS ? a.rows : LNT_FWD_BLOCKS),
-                    dim3(32 * sp.warps), 0, s, a.x, a.res, a.g, a.b, a.rows, a.d, a.eps, a.y, a.total, a.stats, a.err);
+                    dim3(32 * sp.any_warps), 0, s, a.x, a.res, a.g, a.b, a.rows, a.d, a.eps, a.y, a.total, a.stats,
+                    a.err);
+}
+template <typename T>
+cudaError_t any_by_width(const FwdArgs<T>& a, const Spread& sp, cudaStream_t s) {
+  switch (sp.any_nv) {
+    case 1: return go_any<T, 1>(a, sp, s);
+    case 2: return go_any<T, 2>(a, sp, s);
+    case 4: return go_any<T, 4>(a, sp, s);
+    case 6: return go_any<T, 6>(a, sp, s);
+    case 10: return go_any<T, 10>(a, sp, s);
+    case 20: return go_any<T, 20>(a, sp, s);
+    default: return go_any<T, 40>(a, sp, s);
+  }
 }
 
 // Vectors of 8 bytes for 16-bit rows: g and b then are 16 neighbouring bytes a lane.  Against 16 bytes: 48000 x 1280
@@ -736,7 +725,7 @@ cudaError_t bwd_t(const void* dy, const void* x, const float* g, const float* st
                   void* dx, float* part, const Spread& sp, uint32_t* err, cudaStream_t s) {
   const BwdArgs<T> a{static_cast<const T*>(dy), static_cast<const T*>(x), g, reinterpret_cast<const float2*>(stats),
                      static_cast<const T*>(dt), rows, d, static_cast<T*>(dx), part, err};
-  return bwd_by_width<T>(a, sp, s);
+  return sp.vec ? bwd_by_width<T, 16 / sizeof(T)>(a, sp, s) : bwd_by_width<T, 2>(a, sp, s);
 }
 
 }  // namespace
