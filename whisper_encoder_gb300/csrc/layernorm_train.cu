@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(lnt_warps(W) * 32)
 // Rows that do not start on 16 bytes (ragged) come through the same rings, copied with the elements that share their
 // first and last 16 bytes, and are read element by element, lanes side by side: 10000 x 5123 bf16 with dt 182 us,
 // 40000 x 387 45, 4097 x 1283 f32 27 (a block a row, read directly into registers: 1195, 165 and 27).
-constexpr int LNT_WARPS = 8;     // per block of the element-wise kernel, at most
+constexpr int LNT_WARPS = 32;    // per block of the ragged forward kernel, at most
 constexpr int LNT_STAGES = 4;    // rows in flight per team, at most
 
 // Sums of (a, b) over the block; `slot` as in team_sum.
@@ -489,9 +489,12 @@ __global__ void __launch_bounds__(lnb_warps(W, sizeof(T), NV * VEC, VEC * sizeof
 }
 
 // The forward pass of ragged rows: a block of up to 8 warps a row, single elements, read directly (4097 x 1283 f32
-// 18 us, 40000 x 1283 bf16 with a residual 143).
-template <typename T, int NV>
-__global__ void __launch_bounds__(LNT_WARPS * 32, NV <= 6 ? 6 : NV <= 10 ? 3 : NV <= 20 ? 2 : 1)
+// 18 us, 40000 x 1283 bf16 with a residual 143; the team kernel above with single elements 29 and 809).  Wide rows
+// take more warps rather than more loads a lane, two blocks an SM while 16 warps hold them (with a residual, 11 loads
+// against 20 or 40 in 8 warps: 10000 x 2561 bf16 88 / 125 us, 10000 x 5001 186 / 201, 10000 x 5123 188 / 467; without
+// one 10000 x 5001 loses, 143 / 128), then 10 loads in up to 32 (5000 x 10239 f16 208 us against 331 with 40 in 8).
+template <typename T, int NV, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, WARPS > 16 ? 1 : WARPS > 8 ? 2 : NV <= 6 ? 6 : 3)
     ln_train_fwd_any_kernel(const T* __restrict__ x, const T* __restrict__ res, const float* __restrict__ g,
                             const float* __restrict__ bta, int rows, int d, float eps, T* __restrict__ y,
                             T* __restrict__ total, float2* __restrict__ stats, uint32_t* err) {
@@ -585,7 +588,7 @@ struct Spread {
   int warps;     // per row
   int stages;    // backward: rows in flight per team, what the shared memory holds
   int blocks;    // backward: one an SM, at most one a row
-  int any_nv;    // ragged forward pass: loads a lane, the fewest (of those compiled) that leave a row to 8 warps
+  int any_nv;    // ragged forward pass: loads a lane, see there
   int any_warps;
 };
 
@@ -598,8 +601,8 @@ Spread spread(int rows, int d, int dtype, int tensors) {
   const int fit = (LNB_RING - s.warps * 1280 * 4) / (teams * lnb_slot(d, es, !s.vec) * tensors);
   s.stages = fit < LNT_STAGES ? fit : LNT_STAGES;
   s.blocks = rows < 152 ? rows : 152;
-  const int need = (d + 32 * LNT_WARPS - 1) / (32 * LNT_WARPS);
-  s.any_nv = need <= 2 ? need : need <= 4 ? 4 : need <= 6 ? 6 : need <= 10 ? 10 : need <= 20 ? 20 : 40;
+  const int need = (d + 32 * 8 - 1) / (32 * 8);
+  s.any_nv = need <= 2 ? need : need <= 4 ? 4 : need <= 6 ? 6 : need <= 10 ? 10 : d <= 11 * 32 * 16 ? 11 : 10;
   s.any_warps = (d + 32 * s.any_nv - 1) / (32 * s.any_nv);
   return s;
 }
@@ -675,9 +678,9 @@ cudaError_t go(const FwdArgs<T>& a, cudaStream_t s) {
   return launch_pdl(ln_train_fwd_kernel<T, VEC, NV, W>, dim3(fwd_blocks(a.rows, a.d)), dim3(lnt_warps(W) * 32), 0, s,
                     a.x, a.res, a.g, a.b, a.rows, a.d, a.eps, a.y, a.total, a.stats, a.err);
 }
-template <typename T, int NV>
+template <typename T, int NV, int WARPS = 8>
 cudaError_t go_any(const FwdArgs<T>& a, const Spread& sp, cudaStream_t s) {
-  return launch_pdl(ln_train_fwd_any_kernel<T, NV>, dim3(a.rows < LNT_FWD_BLOCKS ? a.rows : LNT_FWD_BLOCKS),
+  return launch_pdl(ln_train_fwd_any_kernel<T, NV, WARPS>, dim3(a.rows < LNT_FWD_BLOCKS ? a.rows : LNT_FWD_BLOCKS),
                     dim3(32 * sp.any_warps), 0, s, a.x, a.res, a.g, a.b, a.rows, a.d, a.eps, a.y, a.total, a.stats,
                     a.err);
 }
@@ -688,9 +691,8 @@ cudaError_t any_by_width(const FwdArgs<T>& a, const Spread& sp, cudaStream_t s) 
     case 2: return go_any<T, 2>(a, sp, s);
     case 4: return go_any<T, 4>(a, sp, s);
     case 6: return go_any<T, 6>(a, sp, s);
-    case 10: return go_any<T, 10>(a, sp, s);
-    case 20: return go_any<T, 20>(a, sp, s);
-    default: return go_any<T, 40>(a, sp, s);
+    case 11: return go_any<T, 11, 16>(a, sp, s);
+    default: return sp.any_warps <= 8 ? go_any<T, 10>(a, sp, s) : go_any<T, 10, 32>(a, sp, s);
   }
 }
 
