@@ -116,8 +116,8 @@ __global__ void __launch_bounds__(LIST_THREADS)
           p += pr[q + u];
         }
     }
-    // a weight of zero is no entry
-    lead[j] = first && !(p == 0.0f) ? my : NONE;
+    // a weight of zero is no entry (log 0): the weight as it is stored, which may be zero where exp was not
+    lead[j] = first && !(p / sum == 0.0f) ? my : NONE;
   }
   __syncthreads();
   for (int j = threadIdx.x; j < k; j += LIST_THREADS) {
