@@ -1,4 +1,6 @@
 """The training operators where values are at their edges (GPU), against float64 evaluations."""
+import math
+
 import pytest
 import torch
 
@@ -25,3 +27,32 @@ def test_teacher_logits_far_below_the_top(wb, tops, T, M):
     target, valid = _distill_target(top, index, V, T)
     assert bool(valid.all())
     _check(_distill(wb, x, w, top, index, dloss, T), _reference(x, w, target, valid, dloss, T), ("loss", "lse", "dx", "dw"))
+
+
+@pytest.mark.parametrize("low", [-1e10, -1e30, -1.5e38, torch.finfo(torch.bfloat16).min, -math.inf])
+@pytest.mark.parametrize("M", [4, 60, 300])
+def test_vocabulary_entries_masked_by_a_low_logit(wb, low, M):
+    # one feature lowers 300 entries in a row (whole tiles' shares of columns among them): they take no part at all,
+    # so everything is as over the other entries alone
+    d, V, lo, hi = 64, 1000, 100, 400
+    x, w, dloss, g = _data(M, d, V, 43)
+    x[:, 0] = 1
+    w[:, 0] = 0
+    w[lo:hi, 0] = low
+    keep = torch.ones(V, dtype=torch.bool, device=DEV)
+    keep[lo:hi] = False
+    label = torch.randint(0, V - (hi - lo), (M,), generator=g, device=DEV)
+    target = torch.zeros(M, int(keep.sum()), dtype=torch.float64, device=DEV).scatter_(1, label[:, None], 1.0)
+    labels = torch.where(label < lo, label, label + (hi - lo))
+    ref = _reference(x, w[keep], target, torch.ones(M, dtype=torch.bool, device=DEV), dloss, 1.0)
+    loss, lse = wb.linear_cross_entropy(x, w, labels)
+    _check({"loss": loss, "lse": lse}, ref, ("loss", "lse"))
+    kl, lse2 = wb.linear_distill(x, w, torch.zeros(M, 1, device=DEV), labels[:, None].contiguous())
+    _check({"loss": kl, "lse": lse2}, ref, ("loss", "lse"))
+    dx, dw = wb.linear_cross_entropy_backward(dloss, x, w, labels, lse)
+    assert wb.check_device_error() == 0
+    assert not dw[lo:hi].any()
+    if low == -math.inf:              # 0 * -infinity, in the lowered feature alone
+        assert torch.isnan(dx[:, 0]).all()
+        dx[:, 0] = ref["dx"][0][:, 0].to(torch.bfloat16)
+    _check({"dx": dx, "dw": dw[keep]}, ref, ("dx", "dw"))

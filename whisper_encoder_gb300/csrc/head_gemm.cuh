@@ -2,7 +2,7 @@
 //
 // n rows of hidden states x (bf16 [n, d], compacted: rows that take no part are gone), a projection
 // matrix w (bf16 [V, d]), logits s = x w^T that are never stored:
-//   HEAD_LSE      s tile by tile -> per row and tile (max, sum 2^(s c - max)) and the targets' logits
+//   HEAD_LSE      s tile by tile -> per row and tile (max, sum 2^((s - max) c)) and the targets' logits
 //   HEAD_DLOGITS  s again for a piece of the vocabulary -> D = softmax - target, bf16 [n, piece]
 //   HEAD_GRADS    for the piece, in one launch: D w, added to float32 slabs of dx, and D^T x', the
 //                 piece's rows of dw
@@ -82,7 +82,7 @@ struct HeadParams {
   float label_p;             // cross entropy: weight of the label
   float smooth;              // what every column's target has on top (label smoothing / V)
   // LSE out
-  float2* part;              // [column tile][part_ld]: (max, sum) in log2 units
+  float2* part;              // [column tile][part_ld]: (max logit, sum of 2^((logit - max) scale_log2))
   float* part_sum;           // [column tile][part_ld]: plain sum of logits, null without smoothing
   long long part_ld;
   float* tgt_s;              // [row][k]: logits at the targets
@@ -382,18 +382,20 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             x0 = fmax3(x0, v[i], v[i + 1]);
             x1 = fmax3(x1, v[i + 2], v[i + 3]);
           }
-          const float mn = fmaxf(mx, fmaxf(x0, x1) * c);
+          const float mn = fmaxf(mx, fmaxf(x0, x1));
           const float mo = mn == -INFINITY ? 0.0f : mn;     // columns that are all -inf add nothing
+          // the difference first, then the scale: it is never positive.  (In one operation, v c - round(max c), what the
+          // rounding leaves of large logits is an exponent: 32 entries at -1e30 made a sum of infinity.)
           float s0 = 0.0f, s1 = 0.0f;
           const uint64_t c2 = f32x2_pack(c, c), n2 = f32x2_pack(-mo, -mo);
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
             float a, b;
-            fma_f32x2(a, b, v[i], v[i + 1], c2, n2);
+            f32x2_unpack(f32x2_mul(f32x2_add(f32x2_pack(v[i], v[i + 1]), n2), c2), a, b);
             s0 += ex2_approx(a);
             s1 += ex2_approx(b);
           }
-          l = l * ex2_approx(mx - mo) + (s0 + s1);
+          l = l * ex2_approx((mx - mo) * c) + (s0 + s1);
           mx = mn;
         }
         float* r3 = red + ((acc * 4 + quarter) * 3) * 128;    // [3][4][32]
@@ -416,10 +418,10 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 #pragma unroll
           for (int q = 1; q < 4; ++q) mm = fmaxf(mm, r3[q * 32 + lane]);
           const float mo = mm == -INFINITY ? 0.0f : mm;
-          l *= ex2_approx(mx - mo);
+          l *= ex2_approx((mx - mo) * c);
 #pragma unroll
           for (int q = 1; q < 4; ++q) {
-            l += r3[128 + q * 32 + lane] * ex2_approx(r3[q * 32 + lane] - mo);
+            l += r3[128 + q * 32 + lane] * ex2_approx((r3[q * 32 + lane] - mo) * c);
             sum += r3[256 + q * 32 + lane];
           }
           // the accumulator goes back only now: the tile after next then finds the exchange area read

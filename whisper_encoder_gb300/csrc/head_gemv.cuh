@@ -45,10 +45,10 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// (m, l) joined with (m2, l2), in log2 units.
-__device__ __forceinline__ void lse_join(float& m, float& l, float m2, float l2) {
+// (m, l) joined with (m2, l2): l = sum of 2^((logit - m) c).
+__device__ __forceinline__ void lse_join(float& m, float& l, float m2, float l2, float c) {
   const float mn = fmaxf(m, m2), mo = mn == -INFINITY ? 0.0f : mn;
-  l = l * ex2_approx(m - mo) + l2 * ex2_approx(m2 - mo);
+  l = l * ex2_approx((m - mo) * c) + l2 * ex2_approx((m2 - mo) * c);
   m = mn;
 }
 
@@ -123,9 +123,9 @@ __global__ void __launch_bounds__(GEMV_WARPS * 32, 1) head_gemv_kernel(const __g
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const int i = 2 * mt + t;
-        const float s0 = on0 ? acc[mt][t] * c2 : -INFINITY, s1 = on1 ? acc[mt][2 + t] * c2 : -INFINITY;
+        const float s0 = on0 ? acc[mt][t] : -INFINITY, s1 = on1 ? acc[mt][2 + t] : -INFINITY;
         const float mn = fmaxf(mx[i], fmaxf(s0, s1)), mo = mn == -INFINITY ? 0.0f : mn;
-        l[i] = l[i] * ex2_approx(mx[i] - mo) + ex2_approx(s0 - mo) + ex2_approx(s1 - mo);
+        l[i] = l[i] * ex2_approx((mx[i] - mo) * c2) + ex2_approx((s0 - mo) * c2) + ex2_approx((s1 - mo) * c2);
         mx[i] = mn;
         sum[i] += (on0 ? acc[mt][t] : 0.0f) + (on1 ? acc[mt][2 + t] : 0.0f);
       }
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(GEMV_WARPS * 32, 1) head_gemv_kernel(const __g
   for (int i = 0; i < 2 * MT; ++i) {
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
-      lse_join(mx[i], l[i], __shfl_xor_sync(0xffffffffu, mx[i], o), __shfl_xor_sync(0xffffffffu, l[i], o));
+      lse_join(mx[i], l[i], __shfl_xor_sync(0xffffffffu, mx[i], o), __shfl_xor_sync(0xffffffffu, l[i], o), c2);
       sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
     }
     if (g == 0) {
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(GEMV_WARPS * 32, 1) head_gemv_kernel(const __g
   if (tok < p.M) {
     float m = red[0][0][tok], s = red[1][0][tok], t = red[2][0][tok];
     for (int w = 1; w < GEMV_WARPS; ++w) {
-      lse_join(m, s, red[0][w][tok], red[1][w][tok]);
+      lse_join(m, s, red[0][w][tok], red[1][w][tok], c2);
       t += red[2][w][tok];
     }
     const long long i = blockIdx.x * p.part_ld + tok;

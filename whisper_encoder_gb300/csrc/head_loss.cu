@@ -333,7 +333,7 @@ struct FinishArgs {
   const float* tgt_s;        // by compact row
   const float* tgt_p;        // by source row; null: cross entropy
   const int* tgt_cnt;
-  float inv_t, smoothing;
+  float inv_t, scale_log2, smoothing;
   float* loss;
   float* lse;
   uint32_t* err;
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(FIN_ROWS* FIN_SLICES) head_finish_kernel(const
         if (!in_bounds(a.err, i, 1, static_cast<long long>(a.n_tiles) * a.part_ld, SITE_HEAD_PART)) continue;
         const float2 q = a.part[i];
         const float mn = fmaxf(m, q.x), mo = mn == -INFINITY ? 0.0f : mn;
-        l = l * exp2f(m - mo) + q.y * exp2f(q.x - mo);
+        l = l * exp2f((m - mo) * a.scale_log2) + q.y * exp2f((q.x - mo) * a.scale_log2);
         m = mn;
         if (a.part_sum) s += a.part_sum[i];
       }
@@ -388,10 +388,10 @@ __global__ void __launch_bounds__(FIN_ROWS* FIN_SLICES) head_finish_kernel(const
       s = 0.0f;
 #pragma unroll
       for (int q = 0; q < FIN_SLICES; ++q) {
-        l += sm[1][q][rx] * exp2f(sm[0][q][rx] - mo);
+        l += sm[1][q][rx] * exp2f((sm[0][q][rx] - mo) * a.scale_log2);
         s += sm[2][q][rx];
       }
-      const float lse = fmaf(mo, 0.69314718055994531f, logf(l));
+      const float lse = fmaf(mo, a.inv_t, logf(l));
       row_lse[rx] = lse;
       if (in_bounds(a.err, src, 1, a.M, SITE_HEAD_ROWS)) {
         a.lse[src] = state == 1 ? lse : 0.0f;
@@ -912,6 +912,7 @@ wb_status head_forward(const HeadShape& h, const Targets& t, const void* x, cons
   f.tgt_p = b.tgt_p;
   f.tgt_cnt = b.tgt_cnt;
   f.inv_t = 1.0f / t.temperature;
+  f.scale_log2 = 1.4426950408889634f / t.temperature;
   f.smoothing = t.smoothing;
   f.loss = loss;
   f.lse = lse;

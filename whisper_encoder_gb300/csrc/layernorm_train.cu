@@ -89,11 +89,6 @@ __device__ __forceinline__ float2 team_sum(float a, float b, float2 (*red)[W], i
   return make_float2(a, b);
 }
 
-__device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 // Pair i of a loaded vector as two floats, and back: 16-bit pairs as whole words (element by element the compiler
 // takes twice the conversions and puts the halves together with permutes: the forward pass of 48000 x 1280 bf16 with
 // a residual took 86 us that way, 78 so).
