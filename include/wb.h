@@ -421,7 +421,7 @@ wb_status wb_layernorm_backward(const void* dy, const void* x, const float* g, c
  * are computed again, a piece of the vocabulary at a time.
  *
  * wb_linear_distill: each row has k (1 to 1024) of a teacher's logits, top (float32, bf16 or f16
- * [M, k]) at the vocabulary entries index (int64 [M, k]).  At temperature T, with p the softmax of
+ * [M, k]) at the vocabulary entries index (int64 [M, k]).  At temperature T (2^-126 or more, finite), with p the softmax of
  * top / T over the row's entries and q the softmax of s / T over the whole vocabulary,
  *   loss[i] = T^2 sum_j p_j (log p_j - log q_j),  lse[i] = log sum_v exp(s[i, v] / T).
  * An entry with a negative index or a logit of -infinity is not there; an index that comes twice

@@ -56,3 +56,52 @@ def test_vocabulary_entries_masked_by_a_low_logit(wb, low, M):
         assert torch.isnan(dx[:, 0]).all()
         dx[:, 0] = ref["dx"][0][:, 0].to(torch.bfloat16)
     _check({"dx": dx, "dw": dw[keep]}, ref, ("dx", "dw"))
+
+
+@pytest.mark.parametrize("T", [1e-30, 1e-20, 1e-3, 7.0])
+@pytest.mark.parametrize("M", [5, 70])
+def test_the_loss_at_small_and_large_temperatures(wb, T, M):
+    # one certain entry: the loss is T (T lse - s), its parts far outside of float32's range of squares.  Logits and
+    # lse are off as in test_gpu_head_loss, relative to themselves; the factor T^2 has two roundings more
+    d, V = 64, 300
+    x, w, _, g = _data(M, d, V, 41)
+    label = torch.randint(0, V, (M, 1), generator=g, device=DEV)
+    loss, lse = wb.linear_distill(x, w, torch.full((M, 1), 1e10, device=DEV), label, T)
+    assert wb.check_device_error() == 0
+    f = torch.tensor(T, dtype=torch.float32).double().item()
+    s = x.double() @ w.double().T / f
+    want = torch.logsumexp(s, 1)
+    mag = (x.double().abs() @ w.double().abs().T).amax(1) / f
+    e_lse = 2.0 ** -18 * mag + 2.0 ** -21 * (want.abs() + 1)
+    assert bool(((lse.double() - want).abs() <= e_lse).all())
+    kl = (want - s.gather(1, label)[:, 0])
+    assert bool(((loss.double() - f * f * kl).abs() <= f * f * (2 * e_lse + 2.0 ** -22 * kl.abs())).all())
+
+
+@pytest.mark.parametrize("T", [1e-30, 1e-20, 1e-10])
+@pytest.mark.parametrize("M", [5, 70, 300])
+def test_gradients_at_small_temperatures(wb, T, M):
+    # logits on a grid of 2^-8, exact in every form of the product; over such a T each step of the grid is at least
+    # 2^25, so the softmax is all at the largest logit.  D is then -1, 0 or 1, and only the results are rounded
+    d, V = 64, 300
+    g = torch.Generator(device=DEV).manual_seed(M)
+    x = (torch.randint(-16, 17, (M, d), generator=g, device=DEV) / 16).to(torch.bfloat16)
+    w = (torch.randint(-16, 17, (V, d), generator=g, device=DEV) / 16).to(torch.bfloat16)
+    s = x.double() @ w.double().T
+    most, first = s.max(1)
+    valid = (s == most[:, None]).sum(1) == 1                      # no softmax to compare with where two are the largest
+    label = torch.randint(0, V, (M,), generator=g, device=DEV)
+    label[::3] = first[::3]                                       # rows whose softmax is their target
+    index = torch.where(valid, label, -1)[:, None].contiguous()
+    dloss = torch.full((M,), 0.25, device=DEV)
+    top = torch.zeros(M, 1, device=DEV)
+    _, lse = wb.linear_distill(x, w, top, index, T)
+    dx, dw = wb.linear_distill_backward(dloss, x, w, top, index, lse, T)
+    assert wb.check_device_error() == 0 and int(valid.sum()) > M // 2
+    D = torch.zeros(M, V, dtype=torch.float64, device=DEV)
+    D[torch.arange(M, device=DEV), first] += 1
+    D[torch.arange(M, device=DEV), label] -= 1
+    D *= torch.where(valid, 0.25 * torch.tensor(T, dtype=torch.float32).double().item(), 0.0)[:, None]
+    # sums of such terms are exact in float32; the scale and the result are rounded, 2^-24 each and 2^-8
+    for got, want in ((dx, D @ w.double()), (dw, D.T @ x.double())):
+        assert bool(((got.double() - want).abs() <= (2.0 ** -8 + 2.0 ** -22) * want.abs()).all())

@@ -88,7 +88,8 @@ struct HeadParams {
   float* tgt_s;              // [row][k]: logits at the targets
   int dl_cols;               // columns of D's buffer
   // DLOGITS in
-  const float* row_lse2;     // by compact row, log2 units
+  const float* row_lse;      // by compact row
+  float inv_t;
   // dw
   const float* g_scale;      // device scalar that x' was divided by
   float out_scale;
@@ -315,10 +316,10 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
       const int lo = p.v0 + ncol0;
       int pos = 0, cnt = 0, next = 0x7fffffff;
       long long tb = 0;
-      float lse2 = 0.0f, smooth = 0.0f;
+      float lse = 0.0f, smooth = 0.0f;
       if (LOGITS && row_ok && in_bounds(p.err, m, 1, p.m_cap, SITE_HEAD_ROWS)) {
         if (KIND == HEAD_DLOGITS) {
-          lse2 = p.row_lse2[m];
+          lse = p.row_lse[m];
           smooth = p.smooth;
         }
         const long long tl64 = p.labels ? p.labels[m] : p.row_tgt ? p.row_tgt[m] : m;
@@ -466,13 +467,17 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             continue;
           }
           if constexpr (KIND == HEAD_DLOGITS) {
-            const uint64_t c2 = f32x2_pack(c, c), l2 = f32x2_pack(-lse2, -lse2);
+            // s / T is rounded before the difference: it is then never above the lse that the forward pass rounded from the
+            // same sums (as a packed pair the product was measured to be fused with the difference, hence single ones);
+            // and no softmax is above 1, however far rounding puts a large logit (a NaN stays)
+            constexpr float LOG2E = 1.4426950408889634f;
+            const uint64_t l2 = f32x2_pack(-lse, -lse), e2 = f32x2_pack(LOG2E, LOG2E);
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               float a, b;
-              fma_f32x2(a, b, v[i], v[i + 1], c2, l2);
-              v[i] = ex2_approx(a) - smooth;
-              v[i + 1] = ex2_approx(b) - smooth;
+              f32x2_unpack(f32x2_mul(f32x2_add(f32x2_pack(__fmul_rn(v[i], p.inv_t), __fmul_rn(v[i + 1], p.inv_t)), l2), e2), a, b);
+              v[i] = ex2_approx(min_nan(a, 0.0f)) - smooth;
+              v[i + 1] = ex2_approx(min_nan(b, 0.0f)) - smooth;
             }
             const int end = p.v0 + n0 + 32;
             while (__any_sync(0xffffffffu, next < end)) {

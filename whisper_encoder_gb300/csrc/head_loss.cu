@@ -13,6 +13,7 @@
 // two gradient products; |D| <= 1, and dloss stays outside of it (applied to the float32 sums of dx,
 // and to x' = dloss / max|dloss| x for dw, exactly 1 where all dloss are equal), so that one rounding of
 // dloss is not shared by all of a row's or all of dw's entries.
+#include <cfloat>
 #include <cstring>
 #include <mutex>
 
@@ -84,7 +85,7 @@ __global__ void __launch_bounds__(LIST_THREADS)
     pr[j] = 0.0f;
     if (j >= k || !in_bounds(err, base + j, 1, n_el, SITE_HEAD_LIST)) continue;
     const long long v = index[base + j];
-    const float t = teacher_f32<T>(top[base + j]) * inv_t;
+    const float t = teacher_f32<T>(top[base + j]);
     if (v >= V) atomicAdd(&n_bad, 1);
     const bool on = v >= 0 && v < V && !(t == -INFINITY);
     id[j] = on ? static_cast<int>(v) : -1;
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(LIST_THREADS)
   float sum = 0.0f;
   for (int j = threadIdx.x; j < k; j += LIST_THREADS) {
     if (id[j] < 0) continue;
-    pr[j] = expf(pr[j] - mx);
+    pr[j] = expf((pr[j] - mx) * inv_t);          // a difference that is never positive, whatever the temperature
     sum += pr[j];
   }
   sum = block_reduce(sum, false, sm);
@@ -156,7 +157,7 @@ struct RowsArgs {
   int* row_src;
   int* row_tgt;              // by compact row: its label (cross entropy); distillation reads row_src and row_cnt
   int* row_cnt;
-  float* row_lse2;           // by compact row: lse in log2 units (backward)
+  float* row_lse;            // by compact row (backward)
   int* n_rows;
   // forward: what the rows without a target get
   float* loss;
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) rows_kernel(const __grid_constan
       a.row_src[off] = row;
       if (a.labels) a.row_tgt[off] = static_cast<int>(a.labels[row]);
       else a.row_cnt[off] = a.cnt[row];
-      if (a.lse_in) a.row_lse2[off] = a.lse_in[row] * 1.4426950408889634f;
+      if (a.lse_in) a.row_lse[off] = a.lse_in[row];
     }
     if (st != 1 && a.loss) {
       a.loss[row] = st == 0 ? 0.0f : __int_as_float(0x7fc00000);
@@ -333,7 +334,7 @@ struct FinishArgs {
   const float* tgt_s;        // by compact row
   const float* tgt_p;        // by source row; null: cross entropy
   const int* tgt_cnt;
-  float inv_t, scale_log2, smoothing;
+  float inv_t, scale_log2, temperature, smoothing;
   float* loss;
   float* lse;
   uint32_t* err;
@@ -417,7 +418,7 @@ __global__ void __launch_bounds__(FIN_ROWS* FIN_SLICES) head_finish_kernel(const
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-      if (rx == 0 && t_cnt > 0) a.loss[t_src] = t / (a.inv_t * a.inv_t);
+      if (rx == 0 && t_cnt > 0) a.loss[t_src] = t * a.temperature * a.temperature;   // T^2 alone may be out of range
       __syncthreads();
     }
   }
@@ -537,7 +538,7 @@ int grad_width(int d) {
 
 // Targets and row map, shared by both passes.
 struct RowsLayout {
-  size_t n_rows, row_src, row_tgt, row_cnt, row_lse2, idx, p, cnt, xc;
+  size_t n_rows, row_src, row_tgt, row_cnt, row_lse, idx, p, cnt, xc;
 };
 
 RowsLayout rows_layout(Carver& c, const HeadShape& h) {
@@ -545,7 +546,7 @@ RowsLayout rows_layout(Carver& c, const HeadShape& h) {
   const size_t m = static_cast<size_t>(h.M);
   L.n_rows = c.take(256);
   L.row_src = c.take(m * sizeof(int));
-  L.row_lse2 = c.take(m * sizeof(float));
+  L.row_lse = c.take(m * sizeof(float));
   L.row_tgt = L.row_cnt = L.idx = L.p = L.cnt = 0;
   if (h.k > 0) {
     L.row_cnt = c.take(m * sizeof(int));
@@ -762,7 +763,7 @@ struct HeadBase {
   const int* n_rows;
   int* row_tgt;                // cross entropy
   int* row_cnt;                // distillation, and the lists by source row
-  float* row_lse2;
+  float* row_lse;
   int* tgt_idx;
   float* tgt_p;
   int* tgt_cnt;
@@ -780,6 +781,7 @@ HeadParams head_params(const HeadBase& b, const Targets& t) {
   p.a_rows = b.h.a_rows();
   p.panel = 8;
   p.scale_log2 = 1.4426950408889634f / t.temperature;
+  p.inv_t = 1.0f / t.temperature;
   p.row_tgt = b.h.k > 0 ? b.row_src : b.row_tgt;
   p.row_cnt = b.row_cnt;
   p.tgt_idx = b.tgt_idx;
@@ -800,7 +802,7 @@ HeadBase head_base(const HeadShape& h, uint8_t* ws, const RowsLayout& L, uint32_
   b.n_rows = reinterpret_cast<int*>(ws + L.n_rows);
   b.row_tgt = h.k > 0 ? nullptr : reinterpret_cast<int*>(ws + L.row_tgt);
   b.row_cnt = h.k > 0 ? reinterpret_cast<int*>(ws + L.row_cnt) : nullptr;
-  b.row_lse2 = reinterpret_cast<float*>(ws + L.row_lse2);
+  b.row_lse = reinterpret_cast<float*>(ws + L.row_lse);
   b.tgt_idx = h.k > 0 ? reinterpret_cast<int*>(ws + L.idx) : nullptr;
   b.tgt_p = h.k > 0 ? reinterpret_cast<float*>(ws + L.p) : nullptr;
   b.tgt_cnt = h.k > 0 ? reinterpret_cast<int*>(ws + L.cnt) : nullptr;
@@ -823,7 +825,7 @@ RowsArgs rows_args(const HeadBase& b, const Targets& t, const RowsLayout& L, con
   a.n_rows = reinterpret_cast<int*>(b.ws + L.n_rows);
   a.row_tgt = b.row_tgt;
   a.row_cnt = b.row_cnt;
-  a.row_lse2 = b.row_lse2;
+  a.row_lse = b.row_lse;
   a.err = b.err;
   return a;
 }
@@ -913,6 +915,7 @@ wb_status head_forward(const HeadShape& h, const Targets& t, const void* x, cons
   f.tgt_cnt = b.tgt_cnt;
   f.inv_t = 1.0f / t.temperature;
   f.scale_log2 = 1.4426950408889634f / t.temperature;
+  f.temperature = t.temperature;
   f.smoothing = t.smoothing;
   f.loss = loss;
   f.lse = lse;
@@ -952,7 +955,7 @@ wb_status head_backward(const HeadShape& h, const Targets& t, const float* dloss
   }
   HeadParams p = head_params(b, t);
   p.dl_cols = L.piece;
-  p.row_lse2 = b.row_lse2;
+  p.row_lse = b.row_lse;
   p.g_scale = g_max;
   p.out_scale = t.temperature;
   p.dx_splits = dx ? L.splits : 0;
@@ -1022,7 +1025,8 @@ wb_status check_backward(const HeadShape& h, const float* dloss, const void* x, 
 
 bool top_aligned(const void* p, int type) { return (reinterpret_cast<uintptr_t>(p) & (type == WB_F32 ? 3u : 1u)) == 0; }
 bool top_ok(int type) { return type == WB_BF16 || type == WB_F16 || type == WB_F32; }
-bool positive(float t) { return t > 0.0f && t < INFINITY; }
+// From the smallest normal value on: below, 1 / T is not finite.
+bool temperature_ok(float t) { return t >= FLT_MIN && t < INFINITY; }
 
 }  // namespace
 }  // namespace wb
@@ -1080,7 +1084,7 @@ wb_status wb_linear_distill(const void* x, const void* w, const void* top, int t
                             int d, int V, int k, float temperature, float* loss, float* lse, void* workspace,
                             size_t workspace_bytes, void* stream) {
   if (!top_ok(top_dtype)) return WB_EUNSUPPORTED;
-  if (!shape_ok(M, d, V) || k < 1 || k > HEAD_MAX_K || !positive(temperature)) return WB_EINVAL;
+  if (!shape_ok(M, d, V) || k < 1 || k > HEAD_MAX_K || !temperature_ok(temperature)) return WB_EINVAL;
   if (M == 0) return WB_OK;
   if (!top || !index || !top_aligned(top, top_dtype) || !aligned8(index)) return WB_EINVAL;
   const HeadShape h = fwd_shape(M, d, V, k);
@@ -1095,7 +1099,7 @@ wb_status wb_linear_distill_backward(const float* dloss, const void* x, const vo
                                      float temperature, void* dx, void* dw, void* workspace, size_t workspace_bytes,
                                      void* stream) {
   if (!top_ok(top_dtype)) return WB_EUNSUPPORTED;
-  if (!shape_ok(M, d, V) || k < 1 || k > HEAD_MAX_K || !positive(temperature)) return WB_EINVAL;
+  if (!shape_ok(M, d, V) || k < 1 || k > HEAD_MAX_K || !temperature_ok(temperature)) return WB_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (M == 0) {
     if (dw && !aligned16(dw)) return WB_EINVAL;
