@@ -24,3 +24,13 @@ def test_temperatures_without_a_finite_reciprocal_are_refused(lib, T):
                                           None) == L.WB_EINVAL
     # without rows too
     assert lib.wb_linear_distill(None, FAKE, None, L.WB_F32, None, 0, 64, 100, 4, T, None, None, None, 0, None) == L.WB_EINVAL
+
+
+@pytest.mark.parametrize("M,d,V", [(1, 64, 1 << 24), (17, 64, 1 << 24), (129, 1280, 1_000_000), (257, 384, 1_000_000), (4480, 1280, 1 << 20)])
+def test_a_piece_of_the_gradient_stays_within_its_bound(lib, M, d, V):
+    # the piece of softmax - target takes 2^28 bytes at most, whole tiles of rows included; what else there is: x and
+    # x' in 16 bits, float32 slabs of dx (together at most 152 tiles of 128 x 256 or as many tiles as dx has), row maps
+    rows = -(-M // 256) * 256
+    slabs = max(152 * 128 * 256, rows * (d + 256)) * 4
+    rest = 2 * rows * d * 2 + slabs + 64 * M + 4096
+    assert lib.wb_linear_cross_entropy_backward_workspace_bytes(M, d, V) <= (1 << 28) + rest

@@ -588,7 +588,7 @@ struct BwdLayout {
   int piece, splits;           // vocabulary rows per piece (a multiple of 256), slabs of dx
 };
 
-// A piece's D takes at most about this much memory.
+// A piece's D (whole tiles of rows) takes at most this much memory, or 256 columns: from 2^19 rows on 512 bytes a row.
 constexpr long long PIECE_BYTES = 256ll << 20;
 
 // Slabs of dx: where its tiles are too few for the device, the sum over the piece is split.
@@ -621,7 +621,7 @@ BwdLayout bwd_layout(const HeadShape& h) {
   BwdLayout L;
   L.r = rows_layout(c, h);
   const long long v256 = (static_cast<long long>(h.V) + 255) / 256 * 256;
-  long long most = PIECE_BYTES / (2ll * h.M) / 256 * 256;
+  long long most = PIECE_BYTES / (2ll * h.m_pad()) / 256 * 256;
   if (most < 256) most = 256;
   if (most > v256) most = v256;
   // equal pieces, as many as leave the fewest idle SMs: 14336 rows of 1280, a quarter padding, both
