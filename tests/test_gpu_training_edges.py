@@ -4,7 +4,7 @@ import math
 import pytest
 import torch
 
-from test_gpu_head_loss import _check, _data, _distill, _distill_target, _reference
+from test_gpu_head_loss import _ce, _check, _data, _distill, _distill_target, _reference
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -105,3 +105,13 @@ def test_gradients_at_small_temperatures(wb, T, M):
     # sums of such terms are exact in float32; the scale and the result are rounded, 2^-24 each and 2^-8
     for got, want in ((dx, D @ w.double()), (dw, D.T @ x.double())):
         assert bool(((got.double() - want).abs() <= (2.0 ** -8 + 2.0 ** -22) * want.abs()).all())
+
+
+def test_more_rows_than_a_thousand_blocks_of_the_row_map_take_at_once(wb):
+    M, d, V = 700_003, 8, 5
+    x, w, dloss, g = _data(M, d, V, 44)
+    labels = torch.randint(-1, V, (M,), generator=g, device=DEV)
+    valid = labels >= 0
+    target = torch.zeros(M, V, dtype=torch.float64, device=DEV).scatter_(1, labels.clamp(min=0)[:, None], 1.0)
+    ref = _reference(x, w, target, valid, dloss, 1.0)
+    _check(_ce(wb, x, w, labels, dloss, 0.0), ref, ("loss", "lse", "dx", "dw"))

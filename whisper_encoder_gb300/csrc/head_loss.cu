@@ -214,82 +214,88 @@ __global__ void __launch_bounds__(ROWS_THREADS) rows_kernel(const __grid_constan
 #pragma unroll
   for (int w = 0; w < ROWS_THREADS / 32; ++w) before += warp_sum[w];
   __syncthreads();
-  // the block's own rows, one a thread
-  const int row = r0 + threadIdx.x;
-  const int st = row < r1 ? row_state(a, row) : 0;
-  const unsigned ball = __ballot_sync(0xffffffffu, st == 1);
-  if (lane == 0) warp_sum[warp] = __popc(ball);
-  __syncthreads();
-  int off = before, all = before;
+  int all = before;                          // rows that take part up to the end of the chunk at hand
+  float g = 0.0f;
+  const long long n_el = static_cast<long long>(a.M) * a.d;   // xc and xs have at least as many
+  // the block's own rows, a chunk of one a thread at a time (beyond 311296 rows a block has more than one chunk)
+  for (int c0 = r0; c0 < r1; c0 += ROWS_THREADS) {
+    const int c1 = min(c0 + ROWS_THREADS, r1);
+    if (c0 != r0) __syncthreads();           // at and warp_sum have been read
+    const int row = c0 + threadIdx.x;
+    const int st = row < c1 ? row_state(a, row) : 0;
+    const unsigned ball = __ballot_sync(0xffffffffu, st == 1);
+    if (lane == 0) warp_sum[warp] = __popc(ball);
+    __syncthreads();
+    int off = all;
 #pragma unroll
-  for (int w = 0; w < ROWS_THREADS / 32; ++w) {
-    if (w < warp) off += warp_sum[w];
-    all += warp_sum[w];
-  }
-  off += __popc(ball & ((1u << lane) - 1u));
-  if (row < r1) {
-    at[threadIdx.x] = st == 1 ? off : -1;
-    if (st == 1 && in_bounds(a.err, off, 1, a.M, SITE_HEAD_ROWS)) {
-      a.row_src[off] = row;
-      if (a.labels) a.row_tgt[off] = static_cast<int>(a.labels[row]);
-      else a.row_cnt[off] = a.cnt[row];
-      if (a.lse_in) a.row_lse[off] = a.lse_in[row];
+    for (int w = 0; w < ROWS_THREADS / 32; ++w) {
+      if (w < warp) off += warp_sum[w];
+      all += warp_sum[w];
     }
-    if (st != 1 && a.loss) {
-      a.loss[row] = st == 0 ? 0.0f : __int_as_float(0x7fc00000);
-      a.lse[row] = 0.0f;
+    off += __popc(ball & ((1u << lane) - 1u));
+    if (row < c1) {
+      at[threadIdx.x] = st == 1 ? off : -1;
+      if (st == 1 && in_bounds(a.err, off, 1, a.M, SITE_HEAD_ROWS)) {
+        a.row_src[off] = row;
+        if (a.labels) a.row_tgt[off] = static_cast<int>(a.labels[row]);
+        else a.row_cnt[off] = a.cnt[row];
+        if (a.lse_in) a.row_lse[off] = a.lse_in[row];
+      }
+      if (st != 1 && a.loss) {
+        a.loss[row] = st == 0 ? 0.0f : __int_as_float(0x7fc00000);
+        a.lse[row] = 0.0f;
+      }
+    }
+    const bool find_max = a.xs && a.own_max && c0 == r0;
+    if (find_max) {
+      for (int i = threadIdx.x; i < a.M; i += ROWS_THREADS)
+        if (row_state(a, i) == 1) g = fmaxf(g, fabsf(a.dloss[i]));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+      if (lane == 0) warp_max[warp] = g;
+    }
+    __syncthreads();
+    if (find_max) {
+#pragma unroll
+      for (int w = 0; w < ROWS_THREADS / 32; ++w) g = fmaxf(g, warp_max[w]);
+      if (blockIdx.x == 0 && threadIdx.x == 0) *a.g_max = g;
+    } else if (a.xs && !a.own_max) {
+      g = *a.g_max;
+    }
+    for (int i = c0 + warp; i < c1; i += ROWS_THREADS / 32) {
+      const int dst = at[i - c0];
+      if (dst < 0) {
+        if (a.dx)
+          for (int v = lane; v < nv; v += 32)
+            if (in_bounds(a.err, static_cast<long long>(i) * a.d + 8 * v, 8, n_el, SITE_HEAD_DX))
+              *reinterpret_cast<uint4*>(a.dx + static_cast<long long>(i) * a.d + 8 * v) = make_uint4(0, 0, 0, 0);
+        continue;
+      }
+      const uint4* src = reinterpret_cast<const uint4*>(a.x + static_cast<long long>(i) * a.d);
+      uint4* to = reinterpret_cast<uint4*>(a.xc + static_cast<long long>(dst) * a.d);
+      const float r = a.xs ? (g > 0.0f ? a.dloss[i] / g : a.dloss[i]) : 0.0f;   // g = 0: all zero (or not a number)
+      auto put = [&](int v, uint4 u) {
+        if (!in_bounds(a.err, static_cast<long long>(dst) * a.d + 8 * v, 8, n_el, SITE_HEAD_X)) return;
+        to[v] = u;
+        if (a.xs) {
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+          uint32_t o[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            o[q] = pack_bf16(__uint_as_float(w[q] << 16) * r, __uint_as_float(w[q] & 0xffff0000u) * r);
+          *reinterpret_cast<uint4*>(a.xs + static_cast<long long>(dst) * a.d + 8 * v) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      };
+      int v = lane;
+      if (i == r0 + warp) {
+#pragma unroll
+        for (int q = 0; q < PRE; ++q, v += 32)
+          if (v < nv) put(v, pre[q]);
+      }
+      for (; v < nv; v += 32) put(v, src[v]);
     }
   }
   if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) *a.n_rows = all;
-  float g = 0.0f;
-  if (a.xs && a.own_max) {
-    for (int i = threadIdx.x; i < a.M; i += ROWS_THREADS)
-      if (row_state(a, i) == 1) g = fmaxf(g, fabsf(a.dloss[i]));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
-    if (lane == 0) warp_max[warp] = g;
-  }
-  __syncthreads();
-  if (a.xs && a.own_max) {
-#pragma unroll
-    for (int w = 0; w < ROWS_THREADS / 32; ++w) g = fmaxf(g, warp_max[w]);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.g_max = g;
-  } else if (a.xs) {
-    g = *a.g_max;
-  }
-  const long long n_el = static_cast<long long>(a.M) * a.d;   // xc and xs have at least as many
-  for (int i = r0 + warp; i < r1; i += ROWS_THREADS / 32) {
-    const int dst = at[i - r0];
-    if (dst < 0) {
-      if (a.dx)
-        for (int v = lane; v < nv; v += 32)
-          if (in_bounds(a.err, static_cast<long long>(i) * a.d + 8 * v, 8, n_el, SITE_HEAD_DX))
-            *reinterpret_cast<uint4*>(a.dx + static_cast<long long>(i) * a.d + 8 * v) = make_uint4(0, 0, 0, 0);
-      continue;
-    }
-    const uint4* src = reinterpret_cast<const uint4*>(a.x + static_cast<long long>(i) * a.d);
-    uint4* to = reinterpret_cast<uint4*>(a.xc + static_cast<long long>(dst) * a.d);
-    const float r = a.xs ? (g > 0.0f ? a.dloss[i] / g : a.dloss[i]) : 0.0f;   // g = 0: all zero (or not a number)
-    auto put = [&](int v, uint4 u) {
-      if (!in_bounds(a.err, static_cast<long long>(dst) * a.d + 8 * v, 8, n_el, SITE_HEAD_X)) return;
-      to[v] = u;
-      if (a.xs) {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        uint32_t o[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          o[q] = pack_bf16(__uint_as_float(w[q] << 16) * r, __uint_as_float(w[q] & 0xffff0000u) * r);
-        *reinterpret_cast<uint4*>(a.xs + static_cast<long long>(dst) * a.d + 8 * v) = make_uint4(o[0], o[1], o[2], o[3]);
-      }
-    };
-    int v = lane;
-    if (i == r0 + warp) {
-#pragma unroll
-      for (int q = 0; q < PRE; ++q, v += 32)
-        if (v < nv) put(v, pre[q]);
-    }
-    for (; v < nv; v += 32) put(v, src[v]);
-  }
   // x' up to the next whole block of 64 rows is a factor of the sum over rows: zeros
   if (a.xs && blockIdx.x == gridDim.x - 1) {
     const int end = max((all + 63) / 64 * 64, 64);
@@ -748,10 +754,11 @@ cudaError_t launch_lists(const HeadShape& h, const Targets& t, int* idx, float* 
 }
 
 // Fewer rows a block while there are few (the copy wants many blocks); each block counts the rows
-// before its own, which grows with the square of the blocks, so at most about a thousand of them.
+// before its own, M / 2 labels on average, so at most 1216 of them (blocks of 256 rows, as many as it takes:
+// 2^24 rows of 8 forward 226 ms against 13.4, 2^20 rows 1.17 against 0.69).
 int rows_per_block(int M) {
   int r = 8;
-  while (r < ROWS_THREADS && M > 1216 * r) r *= 2;
+  while (M > 1216 * r) r *= 2;
   return r;
 }
 
