@@ -485,9 +485,11 @@ __global__ void __launch_bounds__(lnb_warps(W, sizeof(T), NV * VEC, VEC * sizeof
 
 // The forward pass of ragged rows: a block of up to 8 warps a row, single elements, read directly (4097 x 1283 f32
 // 18 us, 40000 x 1283 bf16 with a residual 143; the team kernel above with single elements 29 and 809).  Wide rows
-// take more warps rather than more loads a lane, two blocks an SM while 16 warps hold them (with a residual, 11 loads
-// against 20 or 40 in 8 warps: 10000 x 2561 bf16 88 / 125 us, 10000 x 5001 186 / 201, 10000 x 5123 188 / 467; without
-// one 10000 x 5001 loses, 143 / 128), then 10 loads in up to 32 (5000 x 10239 f16 208 us against 331 with 40 in 8).
+// take more warps rather than more loads a lane (with a residual, 11 loads against 20 or 40 in 8 warps: 10000 x 2561
+// bf16 88 / 125 us, 10000 x 5123 188 / 467; 5000 x 10239 f16 10 loads in 32 warps 208, 40 in 8 331): 11 loads while 10
+// warps hold a row, 10 loads while 16 do, 11 loads again while 16 do, then 10 in up to 32.  11 / 10 loads, bf16
+// without a residual: 14692 x 3403 128 / 135, 14200 x 3521 150 / 132, 9998 x 5001 140 / 119, 9759 x 5123 138 / 187; with
+// one 169 / 170, 195 / 169, 182 / 153, 179 / 231; f32 without one, half the rows: 66 / 75, 81 / 72, 75 / 66, 74 / 106.
 template <typename T, int NV, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, WARPS > 16 ? 1 : WARPS > 8 ? 2 : NV <= 6 ? 6 : 3)
     ln_train_fwd_any_kernel(const T* __restrict__ x, const T* __restrict__ res, const float* __restrict__ g,
@@ -597,7 +599,8 @@ Spread spread(int rows, int d, int dtype, int tensors) {
   s.stages = fit < LNT_STAGES ? fit : LNT_STAGES;
   s.blocks = rows < 152 ? rows : 152;
   const int need = (d + 32 * 8 - 1) / (32 * 8);
-  s.any_nv = need <= 2 ? need : need <= 4 ? 4 : need <= 6 ? 6 : need <= 10 ? 10 : d <= 11 * 32 * 16 ? 11 : 10;
+  s.any_nv = need <= 2 ? need : need <= 4 ? 4 : need <= 6 ? 6 : need <= 10 ? 10
+             : d <= 11 * 32 * 10 || (d > 10 * 32 * 16 && d <= 11 * 32 * 16) ? 11 : 10;
   s.any_warps = (d + 32 * s.any_nv - 1) / (32 * s.any_nv);
   return s;
 }
