@@ -396,7 +396,10 @@ wb_status wb_dequantize_e5m2(const uint8_t* q, const float* scale, int64_t n, vo
  * both NULL; NULL leaves them out and needs no workspace.  The sums run in a fixed order: the same
  * call gives the same bits.  dx may be the buffer of dy, x or dtotal.
  * Statistics and sums are float32.  rows = 0 writes zeros to dg and db.
- * WB_EUNSUPPORTED for another dtype, WB_EINVAL for bad sizes, pointers or alignment. */
+ * Every pointer of both calls, the workspace too, is 16-byte aligned, except stats: 8 bytes (so a call
+ * may start at any row of the statistics, but only at a row of the tensors that lies on 16 bytes).
+ * WB_EUNSUPPORTED for another dtype, WB_EINVAL for bad sizes, pointers or alignment, WB_EWORKSPACE for
+ * a missing, small or unaligned workspace. */
 wb_status wb_layernorm_forward(const void* x, const void* residual, const float* g, const float* b, int rows, int d,
                                float eps, int dtype, void* y, void* total, float* stats, void* stream);
 size_t wb_layernorm_backward_workspace_bytes(int rows, int d, int dtype);
@@ -421,19 +424,21 @@ wb_status wb_layernorm_backward(const void* dy, const void* x, const float* g, c
  * are computed again, a piece of the vocabulary at a time.
  *
  * wb_linear_distill: each row has k (1 to 1024) of a teacher's logits, top (float32, bf16 or f16
- * [M, k]) at the vocabulary entries index (int64 [M, k]).  At temperature T (2^-126 or more, finite), with p the softmax of
- * top / T over the row's entries and q the softmax of s / T over the whole vocabulary,
+ * [M, k]) at the vocabulary entries index (int64 [M, k]).  At temperature T (2^-126 or more, finite),
+ * with p the softmax of top / T over the row's entries and q the softmax of s / T over the whole
+ * vocabulary,
  *   loss[i] = T^2 sum_j p_j (log p_j - log q_j),  lse[i] = log sum_v exp(s[i, v] / T).
  * An entry with a negative index or a logit of -infinity is not there; an index that comes twice
  * counts with both entries' p.  A row without entries takes no part, as above; a row with an index
- * >= V is a mistake, as above.
+ * >= V is a mistake, as above, whatever the logit beside it.
  * wb_linear_distill_backward: as wb_linear_cross_entropy_backward.
  *
  * Sums, softmax statistics and losses are float32.  softmax - target is rounded to bf16 once, as a
  * factor of the two gradient products, and so is x dloss / max|dloss| for dw.  All sums run in a
  * fixed order: the same call gives the same bits.  Two calls that may overlap on the GPU need a
- * workspace each.  x, w, dx, dw: 16-byte aligned; the others to their element.  WB_EINVAL for bad sizes, pointers or alignment,
- * WB_EUNSUPPORTED for another top_dtype, WB_EWORKSPACE for a missing or small workspace. */
+ * workspace each.  x, w, dx, dw and the workspace: 16-byte aligned; the others to their element.
+ * WB_EINVAL for bad sizes, pointers or alignment, WB_EUNSUPPORTED for another top_dtype, WB_EWORKSPACE
+ * for a missing, small or unaligned workspace. */
 size_t wb_linear_cross_entropy_workspace_bytes(int M, int d, int V);
 wb_status wb_linear_cross_entropy(const void* x, const void* w, const int64_t* labels, int M, int d, int V,
                                   float label_smoothing, float* loss, float* lse, void* workspace,

@@ -115,3 +115,55 @@ def test_more_rows_than_a_thousand_blocks_of_the_row_map_take_at_once(wb):
     target = torch.zeros(M, V, dtype=torch.float64, device=DEV).scatter_(1, labels.clamp(min=0)[:, None], 1.0)
     ref = _reference(x, w, target, valid, dloss, 1.0)
     _check(_ce(wb, x, w, labels, dloss, 0.0), ref, ("loss", "lse", "dx", "dw"))
+
+
+def test_statistics_on_8_bytes(wb):
+    # a slice of the statistics of a larger batch
+    x = torch.randn(65, 384, device=DEV).to(torch.bfloat16)
+    dy = torch.randn_like(x)
+    gamma = torch.rand(384, device=DEV)
+    _, _, stats = wb.layernorm_forward(x, gamma, gamma)
+    part = wb.layernorm_backward(dy[1:], x[1:], gamma, stats[1:])
+    whole = wb.layernorm_backward(dy[1:], x[1:], gamma, stats[1:].clone())
+    for a, b in zip(part, whole):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("M", [4, 60, 300])
+def test_infinite_logits(wb, M):
+    # w's first column is -infinity for 300 entries (a whole tile of columns and more): where x's first is 1 their
+    # logits are -infinity and take no part; where it is -1 they are +infinity and the row has no softmax
+    d, V = 64, 1000
+    x, w, _, g = _data(M, d, V, 43)
+    x[:, 0] = 1
+    w[:300, 0] = -float("inf")
+    labels = torch.randint(300, V, (M,), generator=g, device=DEV)
+    loss, lse = wb.linear_cross_entropy(x, w, labels)
+    s = x.double() @ w.double().T
+    want = torch.logsumexp(s, 1)
+    tol = 2.0 ** -18 * (x.double().abs() @ w[300:].double().abs().T).amax(1) + 2.0 ** -21 * (want.abs() + 8)
+    assert bool(((lse.double() - want).abs() <= tol).all())
+    assert bool(((loss.double() - (want - s.gather(1, labels[:, None])[:, 0])).abs() <= 2 * tol).all())
+    # a target among them is infinitely unlikely, and so is smoothing over them
+    gone = labels.clone()
+    gone[1] = 7
+    assert wb.linear_cross_entropy(x, w, gone)[0][1] == float("inf")
+    assert torch.isfinite(wb.linear_cross_entropy(x, w, gone)[0]).sum() == M - 1
+    assert bool((wb.linear_cross_entropy(x, w, labels, 0.1)[0] == float("inf")).all())
+    kl, lse_t = wb.linear_distill(x, w, torch.zeros(M, 1, device=DEV), gone[:, None].contiguous())
+    assert kl[1] == float("inf") and torch.isfinite(kl).sum() == M - 1 and torch.equal(lse_t, lse)
+    x[2, 0] = -1
+    bad, _ = wb.linear_cross_entropy(x, w, labels)
+    assert not torch.isfinite(bad[2]) and torch.isfinite(bad).sum() == M - 1
+    assert torch.equal(bad[3:], loss[3:]) and torch.equal(bad[:2], loss[:2])
+    assert wb.check_device_error() == 0
+
+
+def test_an_index_past_the_vocabulary_is_a_mistake_beside_any_logit(wb):
+    x, w, _, _ = _data(20, 64, 50, 45)
+    index = torch.arange(40, device=DEV).view(20, 2) % 50
+    index[3, 1] = 50
+    top = torch.zeros(20, 2, device=DEV)
+    top[:, 1] = -math.inf
+    loss, lse = wb.linear_distill(x, w, top, index)
+    assert torch.isnan(loss[3]) and lse[3] == 0 and int(torch.isnan(loss).sum()) == 1

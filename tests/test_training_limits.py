@@ -34,3 +34,22 @@ def test_a_piece_of_the_gradient_stays_within_its_bound(lib, M, d, V):
     slabs = max(152 * 128 * 256, rows * (d + 256)) * 4
     rest = 2 * rows * d * 2 + slabs + 64 * M + 4096
     assert lib.wb_linear_cross_entropy_backward_workspace_bytes(M, d, V) <= (1 << 28) + rest
+
+
+def test_layernorm_pointers_are_aligned_as_the_header_says(lib):
+    from whisper_encoder_gb300 import _lib as L
+    at = lambda n: ctypes.c_void_p((1 << 20) + n)  # noqa: E731
+
+    def fwd(x=FAKE, res=OTHER, g=FAKE, b=FAKE, y=FAKE, total=FAKE, stats=FAKE, d=7):
+        return lib.wb_layernorm_forward(x, res, g, b, 4, d, 1e-5, L.WB_BF16, y, total, stats, None)
+
+    def bwd(dy=FAKE, x=FAKE, g=FAKE, stats=FAKE, dt=FAKE, dx=FAKE, dg=FAKE, db=FAKE, ws=FAKE, d=7):
+        return lib.wb_layernorm_backward(dy, x, g, stats, dt, 4, d, L.WB_BF16, dx, dg, db, ws, 1 << 30, None)
+
+    for d in (7, 64):
+        for name in ("x", "res", "g", "b", "y", "total"):
+            assert fwd(**{name: at(8)}, d=d) == L.WB_EINVAL, name
+        for name in ("dy", "x", "g", "dt", "dx", "dg", "db"):
+            assert bwd(**{name: at(8)}, d=d) == L.WB_EINVAL, name
+        assert bwd(ws=at(8), d=d) == L.WB_EWORKSPACE
+        assert fwd(stats=at(4), d=d) == L.WB_EINVAL and bwd(stats=at(4), d=d) == L.WB_EINVAL

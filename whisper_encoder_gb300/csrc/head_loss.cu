@@ -1010,7 +1010,6 @@ wb_status head_backward(const HeadShape& h, const Targets& t, const float* dloss
   return WB_OK;
 }
 
-bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 wb_status check_forward(const HeadShape& h, const void* x, const void* w, const float* loss, const float* lse,

@@ -94,6 +94,7 @@ bool tma_map_f32(CUtensorMap* m, int rank, const void* base, const uint64_t* dim
                  const uint32_t* box, CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
 struct Carver {
   size_t off = 0;

@@ -741,7 +741,7 @@ wb_status wb_layernorm_forward(const void* x, const void* residual, const float*
   if (rows < 0 || d < 1 || d > LNT_MAX_D || !(eps > 0.0f)) return WB_EINVAL;
   if (rows == 0) return WB_OK;
   if (!x || !g || !b || !y || !stats || !aligned16(x) || !aligned16(g) || !aligned16(b) || !aligned16(y) ||
-      !aligned16(stats))
+      !aligned8(stats))
     return WB_EINVAL;
   if (residual ? !aligned16(residual) || !total || !aligned16(total) : total != nullptr) return WB_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -775,7 +775,7 @@ wb_status wb_layernorm_backward(const void* dy, const void* x, const float* g, c
     }
     return WB_OK;
   }
-  if (!dy || !x || !g || !stats || !dx || !aligned16(dy) || !aligned16(x) || !aligned16(g) || !aligned16(stats) ||
+  if (!dy || !x || !g || !stats || !dx || !aligned16(dy) || !aligned16(x) || !aligned16(g) || !aligned8(stats) ||
       !aligned16(dx) || (dtotal && !aligned16(dtotal)))
     return WB_EINVAL;
   if (dg && (!workspace || !aligned16(workspace) ||
