@@ -266,6 +266,9 @@ def cross_kv(enc_out: torch.Tensor, dims, layers: list, stream=None) -> torch.Te
 
 
 # --------------------------------- training -----------------------------------
+# Explicit forward and backward calls: nothing here is recorded by autograd, so outputs carry no grad_fn
+# even where an input requires grad.  Pointers need 16 bytes (WbError otherwise): g, b and every [..., d]
+# tensor; a slice x[1:] has them where d is a multiple of 16 bytes.  Statistics need 8.
 _LN_TYPES = {torch.bfloat16: WB_BF16, torch.float16: WB_F16, torch.float32: WB_F32}
 
 
@@ -321,7 +324,8 @@ def layernorm_forward(x, g, b, eps: float = 1e-5, residual=None, stream=None):
     """LayerNorm that keeps what its backward pass needs: (y, total, stats).
 
     x [..., d] of bf16, f16 or f32, 1 <= d <= 10240; total = x + residual rounded to x's type (x itself
-    without a residual); stats f32 [rows, 2] = (mean, rstd) of total's rows."""
+    without a residual); stats f32 [rows, 2] = (mean, rstd) of total's rows.  Not recorded by autograd:
+    gradients come from layernorm_backward."""
     rows, d, ty = _ln_rows(x, "x")
     _need_shape(g, torch.float32, (d,), "g")
     _need_shape(b, torch.float32, (d,), "b")
@@ -388,7 +392,10 @@ def linear_cross_entropy(x, w, labels, label_smoothing: float = 0.0, workspace=N
     """Softmax cross entropy of the logits x w^T against labels, without storing the logits: (loss, lse).
 
     x bf16 [M, d], w bf16 [V, d], labels int64 [M]; loss and lse f32 [M].  Rows with a negative label
-    take no part (loss 0); a label >= V gives a loss of NaN."""
+    take no part (loss 0); a label >= V gives a loss of NaN.  Not recorded by autograd: gradients come from
+    linear_cross_entropy_backward.  workspace, if given: uint8, as many bytes as
+    load().wb_linear_cross_entropy_workspace_bytes(M, d, V) says (the other calls have a query of their
+    name), for one call at a time."""
     M, d, V = _head_shape(x, w)
     _need_shape(labels, torch.int64, (M,), "labels")
     with _place(stream, x, w, labels, workspace):
@@ -422,7 +429,7 @@ def linear_distill(x, w, top, index, temperature: float = 1.0, workspace=None, s
 
     x bf16 [M, d], w bf16 [V, d]; top f32, bf16 or f16 [M, k] are teacher logits of the vocabulary
     entries index int64 [M, k] (negative: not there).  loss and lse f32 [M]; rows without entries take
-    no part (loss 0)."""
+    no part (loss 0).  Not recorded by autograd: gradients come from linear_distill_backward."""
     M, d, V = _head_shape(x, w)
     k, ty = _teacher(top, index, M)
     with _place(stream, x, w, top, index, workspace):

@@ -13,9 +13,8 @@
 // Two forms.  PAIR: two CTAs (a cluster, one SM each) make one tile of 256 rows x up to 256 columns: each
 // loads 128 rows of A and half of B's columns: 32 KB per 64 of k, which an SM's 64 bytes a clock from L2
 // bring in the 512 clocks of its MMAs.  Single: one CTA, 128 rows: 48 KB for the same MMAs.  The tensor pipe
-// was active for 78 % (pair) and 73 % (single) of the SMs' time in HEAD_DLOGITS, 81 % and 72 to 79 % in the
-// gradient products (3000 x 1280 against 20000); with the loads taken out the pair's forward product is 17 %
-// faster, with three of four MMAs taken out 35 %.  The single form has the finer rows, starts sooner and wins
+// was active for 75 to 78 % (pair) and 73 % (single) of the SMs' time in HEAD_DLOGITS, 81 % and 72 to 79 % in
+// the gradient products (3000 x 1280 against 20000).  The single form has the finer rows, starts sooner and wins
 // where a product is short.
 // Per CTA, as in the other GEMMs of this library: warp 0 lane 0 loads a ring of stages with TMA; warp 1
 // lane 0 (of the pair's first CTA) issues the MMAs into one of two 256-column TMEM accumulators; warps 2-17
@@ -469,7 +468,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
           if constexpr (KIND == HEAD_DLOGITS) {
             // s / T is rounded before the difference: it is then never above the lse that the forward pass rounded from the
             // same sums (as a packed pair the product was measured to be fused with the difference, hence single ones);
-            // and no softmax is above 1, however far rounding puts a large logit (a NaN stays)
+            // and no softmax is above 1, however far rounding puts a large logit (a NaN stays).  Against one fused step:
+            // 77 x 384 both ways 61.5 us / 61.1, 14336 x 1280 the same within the noise
             constexpr float LOG2E = 1.4426950408889634f;
             const uint64_t l2 = f32x2_pack(-lse, -lse), e2 = f32x2_pack(LOG2E, LOG2E);
 #pragma unroll

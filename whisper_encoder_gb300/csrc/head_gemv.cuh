@@ -2,11 +2,11 @@
 // logits as HEAD_LSE, for M <= 16.
 //
 // Bound by reading w once: 51866 x 1280 bf16 are 133 MB, 19.5 us at 6.8 TB/s.  The tcgen05 tile carries that
-// through a ring of shared memory and 128 rows of accumulators, and has two or three tiles a CTA; with the
-// launch around it it takes 32.8 us at one row and 32.6 at 16, this form 28.6 and 31.2 (d = 384: 17.2 and 17.3
-// against 14.2 and 15.7).  Here w goes straight from global memory to
-// registers, 16 bytes a lane, as the A operand of m16n8k16 MMAs: a warp takes 16 vocabulary rows, lane
-// (g, q) reads 8 k of rows g and g + 8.  A dot product does not mind the order of its k, so the lane's 8
+// through a ring of shared memory and 128 rows of accumulators, and has two or three tiles a CTA.  Both kernels
+// of the loss, calls back to back in a graph over four matrices in turn: with the tiles 28.1 us at one row and
+// 27.8 at 16, with this form 25.7 and 27.5 (d = 384: 13.7 and 13.7 against 11.5 and 12.9).  Here w goes straight
+// from global memory to registers, 16 bytes a lane, as the A operand of m16n8k16 MMAs: a warp takes 16
+// vocabulary rows, lane (g, q) reads 8 k of rows g and g + 8.  A dot product does not mind the order of its k, so the lane's 8
 // consecutive k fill the fragment slots of two MMAs, and x (shared memory, read the same way) fills B's
 // slots in the same order.  Each lane keeps a running (max, sum) of its rows for its tokens; lanes and
 // warps are joined once at the end, and a block leaves one partial per token.

@@ -42,7 +42,8 @@ __device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bflo
 template <>
 __device__ __forceinline__ __half from_f32(float v) { return __float2half_rn(v); }
 
-// VEC elements of T as one load: 16 bytes, or a single element where no vector divides the width.
+// VEC elements of T.  Where rows start on 16 bytes they are one load, of 16 bytes or (forward, 16-bit types) 8; in the
+// ragged backward pass a pair whose second element lies 32 W columns on.
 template <typename T, int VEC>
 struct Pack {
   struct alignas(VEC * sizeof(T)) Raw {
@@ -89,9 +90,8 @@ __device__ __forceinline__ float2 team_sum(float a, float b, float2 (*red)[W], i
   return make_float2(a, b);
 }
 
-// Pair i of a loaded vector as two floats, and back: 16-bit pairs as whole words (element by element the compiler
-// takes twice the conversions and puts the halves together with permutes: the forward pass of 48000 x 1280 bf16 with
-// a residual took 86 us that way, 78 so).
+// Pair i of a loaded vector as two floats, and back: 16-bit pairs as whole words (the forward pass of 48000 x 1280
+// bf16 with a residual took 86 us converting element by element, 78 so).
 template <typename T, typename Raw>
 __device__ __forceinline__ uint64_t pair_of(const Raw& r, int i) {
   if constexpr (sizeof(T) == 4) {
@@ -128,7 +128,7 @@ __device__ __forceinline__ void set_pair(Raw& r, int i, uint64_t v) {
 constexpr int lnt_warps(int W) { return W < 4 ? 4 : W; }   // warps per block: one to four teams
 
 // Rows are read into registers, all loads of a row before its first sum; columns past the row count as zeros, so that
-// the sums have no branches (with branches the compiler keeps the loads apart: 3000 x 10240 f32 88 us against 78).
+// the sums have no branches (3000 x 10240 f32 88 us with them, 78 without).
 // 48000 x 1280 bf16 with a residual: 78 us, 6.3 TB/s, 24000 x 1280 f32 76.  Rings of shared memory in front of the same
 // arithmetic take 85 to 89 (16 warps an SM, one or two rows at a time).
 template <typename T, int VEC, int NV, int W>
@@ -579,6 +579,8 @@ int fwd_blocks(int rows, int d) {
   return static_cast<int>(b < LNT_FWD_BLOCKS ? b : LNT_FWD_BLOCKS);
 }
 
+int bwd_blocks(int rows) { return rows < 152 ? rows : 152; }   // a partial row each
+
 // How rows are spread, by width, type and (backward) the tensors that a row is read from.
 struct Spread {
   bool vec;      // rows start on 16 bytes
@@ -597,7 +599,7 @@ Spread spread(int rows, int d, int dtype, int tensors) {
   const int teams = lnb_warps(s.warps, es, lane_elems(d), !s.vec) / s.warps;
   const int fit = (LNB_RING - s.warps * 1280 * 4) / (teams * lnb_slot(d, es, !s.vec) * tensors);
   s.stages = fit < LNT_STAGES ? fit : LNT_STAGES;
-  s.blocks = rows < 152 ? rows : 152;
+  s.blocks = bwd_blocks(rows);
   const int need = (d + 32 * 8 - 1) / (32 * 8);
   s.any_nv = need <= 2 ? need : need <= 4 ? 4 : need <= 6 ? 6 : need <= 10 ? 10
              : d <= 11 * 32 * 10 || (d > 10 * 32 * 16 && d <= 11 * 32 * 16) ? 11 : 10;
@@ -757,8 +759,7 @@ wb_status wb_layernorm_forward(const void* x, const void* residual, const float*
 
 size_t wb_layernorm_backward_workspace_bytes(int rows, int d, int dtype) {
   if (rows < 1 || d < 1 || d > LNT_MAX_D || !type_ok(dtype)) return 0;
-  // fewer tensors a row may mean more blocks: the larger of the two
-  return static_cast<size_t>(spread(rows, d, dtype, 2).blocks) * 2 * d * sizeof(float);
+  return static_cast<size_t>(bwd_blocks(rows)) * 2 * d * sizeof(float);
 }
 
 wb_status wb_layernorm_backward(const void* dy, const void* x, const float* g, const float* stats, const void* dtotal,
