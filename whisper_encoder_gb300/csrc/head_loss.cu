@@ -10,7 +10,9 @@
 // and whatever their x holds reaches nothing.  head_gemm.cuh has the products.
 //
 // Precision: s, lse, losses and every sum are float32.  D is rounded to bf16 once, as a factor of the
-// two gradient products; |D| <= 1, and dloss stays outside of it (applied to the float32 sums of dx,
+// two gradient products: w and x are bf16 and an MMA's operands have one type.  That makes dx and dw 1.8e-3 to
+// 2.4e-3 of the 2-norm off 64 bits, their own rounding alone 1.7e-3; D in two parts would be two products more on
+// top of four.  |D| <= 1, and dloss stays outside of it (applied to the float32 sums of dx,
 // and to x' = dloss / max|dloss| x for dw, exactly 1 where all dloss are equal), so that one rounding of
 // dloss is not shared by all of a row's or all of dw's entries.
 #include <cfloat>
