@@ -48,7 +48,7 @@ typedef enum {
 
 /* Element types of one precision site (showcase site, "The Approach": a
  * PrecisionConfig assigns weight and activation precision per layer site).  WB_F16 and WB_F32 are
- * types of the training LayerNorm below only; a precision site is WB_BF16 or WB_E4M3. */
+ * types of training operators below only; a precision site is WB_BF16 or WB_E4M3. */
 typedef enum { WB_BF16 = 0, WB_E4M3 = 1, WB_F16 = 2, WB_F32 = 3 } wb_dtype;
 
 /* The three encoder layer sites of the showcase site's precision table
@@ -456,6 +456,94 @@ wb_status wb_linear_distill_backward(const float* dloss, const void* x, const vo
                                      const int64_t* index, const float* lse, int M, int d, int V, int k,
                                      float temperature, void* dx, void* dw, void* workspace, size_t workspace_bytes,
                                      void* stream);
+
+/* --- a decoder's attention to the encoder's states --------------------------------
+ * The showcase site, "The Solution" (decoder cross-attention is one of the three attention patterns).
+ * What wb_cross_kv prepares, read by the decoder's rows, and the way back.  Head dim 64; H = n_heads
+ * query heads share Hk = n_kv_heads heads of keys and values, H a multiple of Hk (query head h reads
+ * head h / (H / Hk)).  Per item of the batch and head:
+ *   s = scale q k^T,  out = softmax(s) v,  lse = ln sum exp s,
+ * without a mask among the rows: the hypotheses of one state are rows of one item (q [batch, beams, d]
+ * for a step of a beam search).
+ *  - q, dout: bf16 rows of 64 H, [batch, Tq]; k, v: bf16 rows of 64 Hk, [batch, Tk].  *_batch and *_row
+ *    are the strides from item to item and row to row, in elements: multiples of 8, rows not overlapping,
+ *    below 2^38; a batch stride of 0 is one item's rows for all (k and v both or neither).  So k and v can be the halves
+ *    of wb_cross_kv's rows (k_row = v_row = 2d, v = k + d).  The stride of a dimension of 1 is not looked at.
+ *  - q_lens, kv_lens: int32 [batch] on the device or NULL: the first q_lens[i] rows and kv_lens[i] keys take
+ *    part (values outside 0..T count as the nearer of the two).  The others may hold anything.
+ *    A row that takes no part, or has no keys, gives out = 0, lse = -infinity and no gradient; keys that
+ *    take no part get gradients of 0.
+ *  - out, dq: bf16 [batch, Tq, 64 H]; lse: float32 [batch, H, Tq]; dk, dv: bf16 [batch, Tk, 64 Hk], each
+ *    item's own, also where a batch stride of 0 gave all items the same rows.  All contiguous,
+ *    written whole, overlapping neither an input nor each other.
+ *  - dq may be NULL, and dk and dv both: not wanted.
+ * Scores, sums, statistics and accumulators are float32; exp(s - max) and the gradient of s are rounded to
+ * bf16 once each, as operands.  All sums run in a fixed order: the same call gives the same bits (another batch
+ * size may split the keys of few rows differently).
+ * Tq, Tk: 0 to 2^24, H up to 1024; scale from 2^-64 to 2^64.  q, k, v, dout, out, dq, dk, dv and the workspace:
+ * 16-byte aligned; lse and lengths: 4.  WB_EINVAL for bad sizes, strides, pointers or alignment, WB_EWORKSPACE for a
+ * missing, small or unaligned workspace.  Two calls that may overlap on the GPU need a workspace each. */
+wb_status wb_cross_attention(const void* q, int64_t q_batch, int64_t q_row, const void* k, int64_t k_batch, int64_t k_row,
+                             const void* v, int64_t v_batch, int64_t v_row, const int32_t* q_lens, const int32_t* kv_lens,
+                             int batch, int Tq, int Tk, int n_heads, int n_kv_heads, float scale, void* out, float* lse,
+                             void* stream);
+size_t wb_cross_attention_backward_workspace_bytes(int batch, int Tq, int n_heads);
+wb_status wb_cross_attention_backward(const void* dout, int64_t do_batch, int64_t do_row, const void* q, int64_t q_batch,
+                                      int64_t q_row, const void* k, int64_t k_batch, int64_t k_row, const void* v,
+                                      int64_t v_batch, int64_t v_row, const void* out, const float* lse,
+                                      const int32_t* q_lens, const int32_t* kv_lens, int batch, int Tq, int Tk, int n_heads,
+                                      int n_kv_heads, float scale, void* dq, void* dk, void* dv, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/* --- training: the global norm of the gradients, and clipping -----------------------
+ * The source pages have no counterpart.  norm = sqrt(sum over all tensors of g^2); where it is finite and
+ * above max_norm, outs[i] = grads[i] max_norm / norm, else outs[i] = grads[i].  *norm (float32, device)
+ * receives it; a norm that is not finite leaves the values as they are, for the caller to see and skip the step.
+ *  - grads, outs, numel, dtypes, out_dtypes: HOST arrays of n_tensors entries, read before the call returns;
+ *    the pointers in them are device pointers.  dtypes: WB_BF16, WB_F16 or WB_F32, mixed as they come;
+ *    numel 0 is allowed.
+ *  - outs[i] is grads[i] itself (in place; nothing is written where nothing has to be scaled), or a tensor of the same type
+ *    or float32.  outs NULL: only the norm (max_norm and out_dtypes are not looked at).
+ *  - Tensors that are written overlap nothing else of the call; a tensor listed twice is refused with outs, and counts
+ *    twice without.  Pointers are aligned to their element.
+ * Squares are summed in float32 over at most 128 elements, then in float64, in a fixed order, over the whole range of
+ * the types (elements whose squares leave float32's range are scaled first).
+ * WB_EINVAL for bad pointers, sizes, alignment, overlaps or a max_norm that is negative or NaN, WB_EUNSUPPORTED for
+ * other types, WB_EWORKSPACE for a missing, small or unaligned workspace. */
+#define WB_CLIP_MAX_TENSORS 65536
+size_t wb_clip_grad_norm_workspace_bytes(int n_tensors);
+wb_status wb_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numel, const int32_t* dtypes,
+                            const int32_t* out_dtypes, int n_tensors, float max_norm, float* norm, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* --- training: clipped policy loss with a KL term -----------------------------------
+ * The source pages have no counterpart.  For sequence-level rewards (word errors of sampled transcripts): S sequences
+ * of T tokens, nll = -log p of each token, as wb_linear_cross_entropy gives it.  With d = old_nll - nll, x = nll - ref_nll
+ * and the advantage A of the token's sequence,
+ *   l = -min(e^d A, clip(e^d, 1 - clip_low, 1 + clip_high) A) + kl_weight (e^x - x - 1),
+ *   loss = sum of w l over the tokens with labels >= 0,
+ * w = 1 / (number of such tokens), or with per_sequence 1 / (n B): the mean over the B sequences that have such
+ * tokens of the mean over a sequence's n.  Tokens with a negative label take no part: nothing of theirs is used.
+ *  - nll, old_nll, ref_nll (or NULL: no KL term; kl_weight must be 0): float32 [S, T]; labels: int64 [S, T];
+ *    advantage: float32 [S], or [S, T] with advantage_per_token.
+ *  - stats (float32 [3]) = (loss, sum of w (e^x - x - 1), sum of w over the clipped tokens); weight (float32 [S]): w of
+ *    each sequence's tokens, 0 for one without; the backward pass takes it.  Without any token all are 0.
+ *  - backward: dnll (float32 [S, T], 0 for tokens that take no part) = *dloss (float32, device) times d loss / d nll:
+ *    w (e^d A where not clipped + kl_weight (e^x - 1)), the dloss of wb_linear_cross_entropy_backward.  On the clip's border the
+ *    token is not clipped.  dnll may be the buffer of nll, old_nll or ref_nll.
+ * Whether a token is clipped is decided on the exact difference; sums run in float32 within a sequence and in float64 across,
+ * in a fixed order.  0 <= clip_low <= 1, 0 <= clip_high <= 1e30, kl_weight finite; S up to 2^31, T up to 2^30, S T up to 2^40.
+ * Pointers are aligned to their element, the workspace to 16 bytes.
+ * WB_EINVAL for bad sizes, values or pointers, WB_EWORKSPACE for a missing, small or unaligned workspace. */
+size_t wb_policy_loss_workspace_bytes(int64_t S, int64_t T);
+wb_status wb_policy_loss(const float* nll, const float* old_nll, const float* ref_nll, const float* advantage,
+                         int advantage_per_token, const int64_t* labels, int64_t S, int64_t T, double clip_low,
+                         double clip_high, float kl_weight, int per_sequence, float* stats, float* weight, void* workspace,
+                         size_t workspace_bytes, void* stream);
+wb_status wb_policy_loss_backward(const float* dloss, const float* nll, const float* old_nll, const float* ref_nll,
+                                  const float* advantage, int advantage_per_token, const int64_t* labels, const float* weight,
+                                  int64_t S, int64_t T, double clip_low, double clip_high, float kl_weight, float* dnll,
+                                  void* stream);
 
 /* --- kernel timing (benchmarks) -------------------------------------------------
  * Between wb_profile_begin() and wb_profile_end() every kernel that libwb

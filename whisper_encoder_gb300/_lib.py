@@ -15,11 +15,13 @@ LIB_PATH = _build.LIB
 
 WB_OK, WB_EINVAL, WB_ECUDA, WB_EUNSUPPORTED, WB_ETIMEOUT, WB_EWORKSPACE, WB_EBOUNDS = 0, -1, -2, -3, -4, -5, -6
 WB_BF16, WB_E4M3, WB_F16, WB_F32 = 0, 1, 2, 3
+WB_CLIP_MAX_TENSORS = 65536       # include/wb.h
 WB_LOGMEL_STATIC_MAX_CHUNKS = 2   # include/wb.h
 WB_SELFTEST_WAIT_SITE = 0x7F      # include/wb.h
 WB_SELFTEST_BOUNDS_SITE = 0x7E    # include/wb.h
 
-c_int, c_i64, c_size, c_void, c_float = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float
+c_int, c_i64, c_size, c_void, c_float, c_double = (
+    ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float, ctypes.c_double)
 P = ctypes.POINTER
 
 
@@ -108,6 +110,17 @@ SIGNATURES = {
     "wb_linear_distill_backward_workspace_bytes": (c_size, [c_int, c_int, c_int, c_int]),
     "wb_linear_distill_backward": (c_int, [c_void, c_void, c_void, c_void, c_int, c_void, c_void, c_int, c_int, c_int,
                                            c_int, c_float, c_void, c_void, c_void, c_size, c_void]),
+    "wb_cross_attention": (c_int, [c_void, c_i64, c_i64] * 3 + [c_void, c_void] + [c_int] * 5 + [c_float, c_void, c_void, c_void]),
+    "wb_cross_attention_backward_workspace_bytes": (c_size, [c_int, c_int, c_int]),
+    "wb_cross_attention_backward": (c_int, [c_void, c_i64, c_i64] * 4 + [c_void] * 4 + [c_int] * 5 + [c_float] + [c_void] * 4 +
+                                    [c_size, c_void]),
+    "wb_clip_grad_norm_workspace_bytes": (c_size, [c_int]),
+    "wb_clip_grad_norm": (c_int, [c_void, c_void, c_void, c_void, c_void, c_int, c_float, c_void, c_void, c_size, c_void]),
+    "wb_policy_loss_workspace_bytes": (c_size, [c_i64, c_i64]),
+    "wb_policy_loss": (c_int, [c_void, c_void, c_void, c_void, c_int, c_void, c_i64, c_i64, c_double, c_double, c_float, c_int,
+                               c_void, c_void, c_void, c_size, c_void]),
+    "wb_policy_loss_backward": (c_int, [c_void, c_void, c_void, c_void, c_void, c_int, c_void, c_void, c_i64, c_i64, c_double,
+                                        c_double, c_float, c_void, c_void]),
     "wb_profile_begin": (c_int, []),
     "wb_profile_end": (c_int, [c_int, P(ctypes.c_char_p), P(ctypes.c_double), P(ctypes.c_int64)]),
 }

@@ -6,6 +6,7 @@ current torch CUDA stream.  All arithmetic happens in libwb's kernels.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import dataclasses
@@ -456,6 +457,190 @@ def linear_distill_backward(dloss, x, w, top, index, lse, temperature: float = 1
         call("wb_linear_distill_backward", _a(dloss), _a(x), _a(w), _a(top), ty, _a(index), _a(lse), M, d, V, k,
              temperature, _a(dx), _a(dw), _a(ws), ws.numel(), _raw_stream(x))
     return dx, dw
+
+
+def _attn_rows(t, name, like=None):
+    """A bf16 [batch, T, heads * 64] tensor whose rows are contiguous: (batch, T, heads)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 3:
+        raise ValueError(f"{name}: expected a CUDA bfloat16 tensor [batch, T, heads * 64]")
+    batch, T, d = t.shape
+    if d == 0 or d % 64 or t.stride(2) != 1:
+        raise ValueError(f"{name}: expected rows of whole heads (64 elements each, contiguous), got {tuple(t.shape)}, strides {t.stride()}")
+    if like is not None and t.shape != like.shape:
+        raise ValueError(f"{name}: expected shape {tuple(like.shape)}, got {tuple(t.shape)}")
+    return batch, T, d // 64
+
+
+def _attn_shape(q, k, v, q_lens, kv_lens):
+    batch, Tq, H = _attn_rows(q, "q")
+    kv_batch, Tk, Hk = _attn_rows(k, "k")
+    _attn_rows(v, "v", k)
+    if kv_batch != batch or H % Hk:
+        raise ValueError(f"q and k: expected the same batch and whole groups of heads, got {tuple(q.shape)} and {tuple(k.shape)}")
+    if max(Tq, Tk) > 1 << 24 or H > 1024:
+        raise ValueError("q and k: at most 2^24 rows of 1024 heads")
+    for t, name in ((q_lens, "q_lens"), (kv_lens, "kv_lens")):
+        if t is not None:
+            _need_shape(t, torch.int32, (batch,), name)
+    return batch, Tq, Tk, H, Hk
+
+
+def cross_attention(q, k, v, scale: float = 0.125, q_lens=None, kv_lens=None, stream=None):
+    """Attention of a decoder's rows to the encoder's states: (out bf16 [batch, Tq, 64 H], lse f32 [batch, H, Tq]).
+
+    q bf16 [batch, Tq, 64 H], k and v bf16 [batch, Tk, 64 Hk] with H a multiple of Hk; rows contiguous, other strides free
+    (k and v can be the halves of cross_kv's rows, or expanded over the batch).  The hypotheses of a beam are rows of one
+    item.  q_lens, kv_lens: int32 [batch] on the device, how many rows and keys of an item take part (default: all);
+    a row without keys or past q_lens gives out 0 and lse -inf.  Not recorded by autograd: gradients come from
+    cross_attention_backward."""
+    batch, Tq, Tk, H, Hk = _attn_shape(q, k, v, q_lens, kv_lens)
+    with _place(stream, q, k, v, q_lens, kv_lens):
+        out = torch.empty((batch, Tq, 64 * H), dtype=torch.bfloat16, device=q.device)
+        lse = torch.empty((batch, H, Tq), dtype=torch.float32, device=q.device)
+        call("wb_cross_attention", _a(q), q.stride(0), q.stride(1), _a(k), k.stride(0), k.stride(1), _a(v), v.stride(0), v.stride(1),
+             _a(q_lens), _a(kv_lens), batch, Tq, Tk, H, Hk, scale, _a(out), _a(lse), _raw_stream(q))
+    return out, lse
+
+
+def cross_attention_backward(dout, q, k, v, out, lse, scale: float = 0.125, q_lens=None, kv_lens=None, need_dq: bool = True,
+                             need_dkv: bool = True, workspace=None, stream=None):
+    """Gradients (dq, dk, dv) of cross_attention from dout, its inputs and its results; None for those not needed.
+
+    dout as q (strides free).  dq like q, dk and dv like k, contiguous; the rows of all heads that share a key head are summed.
+    workspace, if given: uint8, as many bytes as load().wb_cross_attention_backward_workspace_bytes(batch, Tq, H) says, for
+    one call at a time."""
+    batch, Tq, Tk, H, Hk = _attn_shape(q, k, v, q_lens, kv_lens)
+    _attn_rows(dout, "dout", q)
+    _need_shape(out, torch.bfloat16, q.shape, "out")
+    _need_shape(lse, torch.float32, (batch, H, Tq), "lse")
+    with _place(stream, q, k, v, dout, out, lse, q_lens, kv_lens, workspace):
+        dq = torch.empty((batch, Tq, 64 * H), dtype=torch.bfloat16, device=q.device) if need_dq else None
+        dk = torch.empty((batch, Tk, 64 * Hk), dtype=torch.bfloat16, device=q.device) if need_dkv else None
+        dv = torch.empty_like(dk) if need_dkv else None
+        ws = _head_workspace(workspace, "wb_cross_attention_backward_workspace_bytes", q.device, batch, Tq, H)
+        call("wb_cross_attention_backward", _a(dout), dout.stride(0), dout.stride(1), _a(q), q.stride(0), q.stride(1), _a(k), k.stride(0),
+             k.stride(1), _a(v), v.stride(0), v.stride(1), _a(out), _a(lse), _a(q_lens), _a(kv_lens), batch, Tq, Tk, H, Hk, scale,
+             _a(dq), _a(dk), _a(dv), _a(ws), ws.numel(), _raw_stream(q))
+    return dq, dk, dv
+
+
+def _dense(t):
+    """Whether t's elements fill one piece of memory, in any order of its dimensions."""
+    if t.is_contiguous():
+        return True
+    n = 1
+    for stride, size in sorted((st, sz) for st, sz in zip(t.stride(), t.shape) if sz > 1):
+        if stride != n:
+            return False
+        n *= size
+    return True
+
+
+def _i64(values):
+    return (ctypes.c_int64 * len(values)).from_buffer(array.array("q", values))
+
+
+def _i32(values):
+    return (ctypes.c_int32 * len(values)).from_buffer(array.array("i", values))
+
+
+def _grad_list(tensors, name):
+    """Pointers, sizes and types of a list of tensors of one device."""
+    for t in tensors:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _LN_TYPES or not _dense(t):
+            raise ValueError(f"{name}: expected CUDA tensors of bf16, f16 or f32 without gaps")
+    return [t.data_ptr() for t in tensors], [t.numel() for t in tensors], [_LN_TYPES[t.dtype] for t in tensors]
+
+
+def _grad_norm(grads, max_norm, out, workspace, stream):
+    grads = list(grads)
+    if not grads:
+        raise ValueError("grads: expected at least one tensor")
+    if len(grads) > _lib.WB_CLIP_MAX_TENSORS:
+        raise ValueError(f"grads: at most {_lib.WB_CLIP_MAX_TENSORS} tensors")
+    at, numel, types = _grad_list(grads, "grads")
+    outs = out_types = None
+    if out is not None:
+        out = list(out)
+        if out is not grads:
+            if len(out) != len(grads) or any(o.shape != g.shape or o.stride() != g.stride() for o, g in zip(out, grads)):
+                raise ValueError("out: expected one tensor for each gradient, of its shape and strides")
+        outs, _, out_types = _grad_list(out, "out")
+        if any(o != t and o != WB_F32 for o, t in zip(out_types, types)):
+            raise ValueError("out: expected each gradient's type or float32")
+        outs, out_types = _i64(outs), _i32(out_types)
+    with _place(stream, *grads, *(out or ()), workspace):
+        norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
+        ws = _head_workspace(workspace, "wb_clip_grad_norm_workspace_bytes", norm.device, len(grads))
+        call("wb_clip_grad_norm", _i64(at), outs, _i64(numel), _i32(types), out_types, len(grads), max_norm, _a(norm), _a(ws),
+             ws.numel(), _raw_stream(norm))
+    return norm
+
+
+def grad_norm(grads, workspace=None, stream=None):
+    """2-norm over all elements of a list of gradients (bf16, f16 or f32, mixed), as a float32 scalar on the device.
+
+    Tensors may be of any shape and order of dimensions that leaves no gaps; an empty one counts nothing."""
+    return _grad_norm(grads, 0.0, None, workspace, stream)
+
+
+def clip_grad_norm(grads, max_norm: float, out=None, workspace=None, stream=None):
+    """Scale gradients by max_norm / norm where their global norm is above max_norm; returns the norm (f32 scalar, device).
+
+    In place, or into ``out``: a tensor for each gradient, of its shape and strides, of its type or float32 (written
+    whether or not anything has to be scaled).  A norm that is not finite leaves the values as they are.  No tensor
+    may share memory with another one of the call."""
+    grads = list(grads)
+    return _grad_norm(grads, max_norm, grads if out is None else out, workspace, stream)
+
+
+def _policy_shape(nll, old_nll, advantage, labels, ref_nll, kl_weight):
+    if not isinstance(nll, torch.Tensor) or nll.dim() != 2:
+        raise ValueError("nll: expected a f32 tensor [S, T]")
+    _need(nll, torch.float32, "nll")
+    _need_shape(old_nll, torch.float32, nll.shape, "old_nll")
+    _need_shape(labels, torch.int64, nll.shape, "labels")
+    if ref_nll is not None:
+        _need_shape(ref_nll, torch.float32, nll.shape, "ref_nll")
+    elif kl_weight:
+        raise ValueError("kl_weight: needs ref_nll")
+    per_token = isinstance(advantage, torch.Tensor) and advantage.dim() == 2
+    _need_shape(advantage, torch.float32, nll.shape if per_token else nll.shape[:1], "advantage")
+    return nll.shape[0], nll.shape[1], int(per_token)
+
+
+def policy_loss(nll, old_nll, advantage, labels, ref_nll=None, clip_low: float = 0.2, clip_high: float = 0.2, kl_weight: float = 0.0,
+                per_sequence: bool = False, workspace=None, stream=None):
+    """Clipped policy loss of sampled sequences with a KL term: (stats f32 [3], weight f32 [S]).
+
+    nll, old_nll, ref_nll (optional): f32 [S, T], -log p of each token now, when it was sampled and by the reference
+    (linear_cross_entropy's loss rows); labels int64 [S, T], negative: the token takes no part; advantage f32 [S] or
+    [S, T].  stats = (loss, mean KL, share of clipped tokens), means over the tokens that take part or, with per_sequence,
+    over the sequences' means; weight is what policy_loss_backward takes.  Not recorded by autograd."""
+    S, T, per_token = _policy_shape(nll, old_nll, advantage, labels, ref_nll, kl_weight)
+    with _place(stream, nll, old_nll, advantage, labels, ref_nll, workspace):
+        stats = torch.empty(3, dtype=torch.float32, device=nll.device)
+        weight = torch.empty(S, dtype=torch.float32, device=nll.device)
+        ws = _head_workspace(workspace, "wb_policy_loss_workspace_bytes", nll.device, S, T)
+        call("wb_policy_loss", _a(nll), _a(old_nll), _a(ref_nll), _a(advantage), per_token, _a(labels), S, T, clip_low, clip_high,
+             kl_weight, 1 if per_sequence else 0, _a(stats), _a(weight), _a(ws), ws.numel(), _raw_stream(nll))
+    return stats, weight
+
+
+def policy_loss_backward(dloss, nll, old_nll, advantage, labels, weight, ref_nll=None, clip_low: float = 0.2, clip_high: float = 0.2,
+                         kl_weight: float = 0.0, stream=None):
+    """Gradient of nll (f32 [S, T], 0 for tokens that take no part) of policy_loss from dloss (f32 scalar, on the device) and its
+    weight: what linear_cross_entropy_backward takes as dloss."""
+    S, T, per_token = _policy_shape(nll, old_nll, advantage, labels, ref_nll, kl_weight)
+    if not isinstance(dloss, torch.Tensor) or dloss.numel() != 1:
+        raise ValueError("dloss: expected a f32 scalar on the device")
+    _need(dloss, torch.float32, "dloss")
+    _need_shape(weight, torch.float32, (S,), "weight")
+    with _place(stream, nll, old_nll, advantage, labels, ref_nll, weight, dloss):
+        dnll = torch.empty_like(nll)
+        call("wb_policy_loss_backward", _a(dloss), _a(nll), _a(old_nll), _a(ref_nll), _a(advantage), per_token, _a(labels), _a(weight),
+             S, T, clip_low, clip_high, kl_weight, _a(dnll), _raw_stream(nll))
+    return dnll
 
 
 def profile_begin() -> None:

@@ -21,7 +21,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libwb.so")
 BUILD_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_DEBUG = os.path.join(BUILD_DEBUG, "libwb_debug.so")
-SOURCES = ["api.cu", "kernels.cu", "tc_kernels.cu", "static_scratch.cu", "host_pipeline.cu", "layernorm_train.cu", "head_loss.cu"]
+SOURCES = ["api.cu", "kernels.cu", "tc_kernels.cu", "static_scratch.cu", "host_pipeline.cu", "layernorm_train.cu", "head_loss.cu",
+           "cross_attention.cu", "grad_clip.cu", "policy_loss.cu"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

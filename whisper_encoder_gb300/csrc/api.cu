@@ -110,7 +110,7 @@ const char* const kProfNames[PC_COUNT] = {
     "logmel.prep", "logmel.dft", "logmel.mel", "logmel.post", "stem.prep", "stem.conv1", "stem.conv2",
     "enc.layernorm", "enc.quantize", "enc.qkv", "enc.attention", "enc.out_proj", "enc.fc1", "enc.fc2", "other",
     "train.layernorm", "train.head_rows", "train.head_lse", "train.head_finish", "train.head_dlogits",
-    "train.head_grads"};
+    "train.head_grads", "cross.attention", "cross.backward", "train.clip", "train.policy"};
 
 struct ProfRec {
   int cls, kernels;

@@ -114,7 +114,8 @@ struct Carver {
 enum ProfClass {
   PC_LOGMEL_PREP, PC_LOGMEL_DFT, PC_LOGMEL_MEL, PC_LOGMEL_POST, PC_STEM_PREP, PC_STEM_CONV1, PC_STEM_CONV2,
   PC_ENC_LN, PC_ENC_QUANT, PC_ENC_QKV, PC_ENC_ATTN, PC_ENC_OUT, PC_ENC_FC1, PC_ENC_FC2, PC_OTHER,
-  PC_TRAIN_LN, PC_HEAD_ROWS, PC_HEAD_LSE, PC_HEAD_FINISH, PC_HEAD_DLOGITS, PC_HEAD_GRADS, PC_COUNT
+  PC_TRAIN_LN, PC_HEAD_ROWS, PC_HEAD_LSE, PC_HEAD_FINISH, PC_HEAD_DLOGITS, PC_HEAD_GRADS,
+  PC_CROSS_FWD, PC_CROSS_BWD, PC_CLIP, PC_POLICY, PC_COUNT
 };
 struct Prof {
   int cls, kernels;

@@ -1,0 +1,402 @@
+// Clipped policy loss on per-token log-probabilities, with a KL term against a reference, and its gradient.
+//
+// With nll = -log p of a sampled token (what the vocabulary losses give as a row's loss), d = old_nll - nll
+// and x = nll - ref_nll, a token of a sequence with advantage A has
+//   l = -min(e^d A, clip(e^d, 1 - lo, 1 + hi) A) + beta (e^x - x - 1),
+//   dl/dnll = (clipped ? 0 : e^d A) + beta (e^x - 1),
+// and the loss is sum w l with w = 1 / N over the N tokens that take part, or 1 / (B n_b): the mean over the B
+// sequences that have tokens of the means over their n_b tokens.
+//
+// Bound by memory (20 bytes a token forward, 24 backward), below a million tokens by the two launches' latency.
+// Forward: a team of 1 to 8 warps of a block takes a sequence; a block leaves one partial row, and a second kernel joins those
+// in order, in every one of its blocks, and turns counts into weights.  No atomics: the same call gives the same bits.
+//
+// Numbers.  Whether a token is clipped is decided on d against log1p(hi) and log1p(-lo), both as unevaluated sums of
+// two float32 (the rounding of a difference is exact in float32): one rounding near the border would turn a
+// whole gradient on or off.  e^x - x - 1 is x^2 / 2 for small x: below 1/2 its series, above it the
+// difference of expm1, which loses two bits at most.  An advantage of zero gives zero, whatever e^d is.
+#include <cmath>
+
+#include "../../include/wb.h"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace wb {
+namespace {
+
+constexpr int POL_THREADS = 256, POL_WARPS = POL_THREADS / 32;
+constexpr int POL_MAX_BLOCKS = 1216;      // 8 on each SM
+constexpr int POL_TILE = 4;               // tokens of a thread and step
+
+struct PolicyArgs {
+  const float* nll;
+  const float* old_nll;
+  const float* ref_nll;      // or null
+  const float* adv;
+  const int64_t* labels;
+  long long S, T;
+  int adv_tok;               // one for each token, else one for each sequence
+  float hi0, hi1, lo0, lo1;  // log1p(hi), log1p(-lo): value and what its rounding left
+  float hold_hi, hold_lo;    // 1 + hi, 1 - lo
+  float beta;
+  int per_sequence;
+  uint32_t* err;
+};
+
+struct Token {
+  float loss, kl, grad;
+  bool clipped;
+};
+
+// x^2/2 + x^3/6 + ... for |x| < 1/2: the first term left out, x^10 / 10! relative to x^2 / 2, is below 2^-28.
+__device__ __forceinline__ float exp_minus_x_minus_1(float x, float em1) {
+  float p = fmaf(x, 1.0f / 9.0f, 1.0f);
+  p = fmaf(x * (1.0f / 8.0f), p, 1.0f);
+  p = fmaf(x * (1.0f / 7.0f), p, 1.0f);
+  p = fmaf(x * (1.0f / 6.0f), p, 1.0f);
+  p = fmaf(x * (1.0f / 5.0f), p, 1.0f);
+  p = fmaf(x * (1.0f / 4.0f), p, 1.0f);
+  p = fmaf(x * (1.0f / 3.0f), p, 1.0f);
+  return fabsf(x) < 0.5f ? 0.5f * x * x * p : em1 - x;
+}
+
+__device__ __forceinline__ Token policy_token(const PolicyArgs& a, float nll, float old_nll, float ref, float adv) {
+  Token t;
+  const float d = old_nll - nll;
+  const float bb = d - old_nll;
+  const float e = (old_nll - (d - bb)) - (nll + bb);     // d + e is the difference itself
+  const bool above = d > a.hi0 || (d == a.hi0 && e > a.hi1);
+  const bool below = d < a.lo0 || (d == a.lo0 && e < a.lo1);
+  t.clipped = (adv > 0.0f && above) || (adv < 0.0f && below);
+  const float ra = adv == 0.0f ? 0.0f : expf(d) * adv;
+  t.loss = t.clipped ? -(adv > 0.0f ? a.hold_hi : a.hold_lo) * adv : -ra;
+  t.grad = t.clipped ? 0.0f : ra;
+  t.kl = 0.0f;
+  if (a.ref_nll) {
+    const float x = nll - ref;
+    const float em1 = expm1f(x);
+    t.kl = exp_minus_x_minus_1(x, em1);
+    if (a.beta != 0.0f) {
+      t.loss += a.beta * t.kl;
+      t.grad += a.beta * em1;
+    }
+  }
+  return t;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Partial row of a block: sums of loss, KL and clipped tokens (each divided by its sequence's tokens where sequences
+// count the same), tokens, and sequences with tokens.
+struct PolicyPart {
+  double loss, kl, clipped;
+  long long tokens, seqs;
+};
+
+// W warps a sequence.
+template <int W>
+__global__ void __launch_bounds__(POL_THREADS) policy_sum_kernel(const __grid_constant__ PolicyArgs a, int* counts,
+                                                                 PolicyPart* part, int parts) {
+  constexpr int TEAMS = POL_WARPS / W;
+  __shared__ float red[POL_WARPS][4];
+  __shared__ PolicyPart join[TEAMS];
+  const int lane = lane_id(), warp = warp_id(), team = warp / W, in_team = warp % W;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  PolicyPart sum = {0.0, 0.0, 0.0, 0, 0};
+  const long long n_el = a.S * a.T;
+  // all teams of a block make the same number of rounds: there are barriers inside
+  for (long long s0 = static_cast<long long>(blockIdx.x) * TEAMS; s0 < a.S; s0 += static_cast<long long>(gridDim.x) * TEAMS) {
+    const long long s = s0 + team;
+    float loss = 0.0f, kl = 0.0f;
+    int clipped = 0, count = 0;
+    if (s < a.S) {
+      const long long base = s * a.T;
+      const float adv_s = a.adv_tok == 0 && in_bounds(a.err, s, 1, a.S, SITE_POLICY_IN) ? a.adv[s] : 0.0f;
+      for (long long t0 = in_team * 32 + lane; t0 < a.T; t0 += W * 32 * POL_TILE) {
+        int64_t lab[POL_TILE];
+        float nll[POL_TILE], old[POL_TILE], ref[POL_TILE], adv[POL_TILE];
+#pragma unroll
+        for (int i = 0; i < POL_TILE; ++i) {
+          const long long t = t0 + i * W * 32;
+          lab[i] = -1;
+          nll[i] = old[i] = ref[i] = 0.0f;
+          adv[i] = adv_s;
+          if (t < a.T && in_bounds(a.err, base + t, 1, n_el, SITE_POLICY_IN)) {
+            lab[i] = a.labels[base + t];
+            nll[i] = a.nll[base + t];
+            old[i] = a.old_nll[base + t];
+            if (a.ref_nll) ref[i] = a.ref_nll[base + t];
+            if (a.adv_tok) adv[i] = a.adv[base + t];
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < POL_TILE; ++i) {
+          if (lab[i] < 0) continue;
+          const Token k = policy_token(a, nll[i], old[i], ref[i], adv[i]);
+          loss += k.loss;
+          kl += k.kl;
+          clipped += k.clipped;
+          ++count;
+        }
+      }
+    }
+    loss = warp_sum(loss);
+    kl = warp_sum(kl);
+    clipped = __reduce_add_sync(0xffffffffu, clipped);
+    count = __reduce_add_sync(0xffffffffu, count);
+    if (W > 1) {
+      if (lane == 0) {
+        red[warp][0] = loss;
+        red[warp][1] = kl;
+        red[warp][2] = __int_as_float(clipped);
+        red[warp][3] = __int_as_float(count);
+      }
+      __syncthreads();
+      loss = kl = 0.0f;
+      clipped = count = 0;
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        loss += red[team * W + i][0];
+        kl += red[team * W + i][1];
+        clipped += __float_as_int(red[team * W + i][2]);
+        count += __float_as_int(red[team * W + i][3]);
+      }
+      __syncthreads();
+    }
+    if (in_team == 0 && lane == 0 && s < a.S) {
+      if (in_bounds(a.err, s, 1, a.S, SITE_POLICY_OUT)) counts[s] = count;
+      if (count > 0) {
+        const double f = a.per_sequence ? 1.0 / count : 1.0;
+        sum.loss += loss * f;
+        sum.kl += kl * f;
+        sum.clipped += clipped * f;
+        sum.tokens += count;
+        sum.seqs += 1;
+      }
+    }
+  }
+  if (in_team == 0 && lane == 0) join[team] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0 && in_bounds(a.err, blockIdx.x, 1, parts, SITE_POLICY_OUT)) {
+    for (int i = 1; i < TEAMS; ++i) {
+      sum.loss += join[i].loss;
+      sum.kl += join[i].kl;
+      sum.clipped += join[i].clipped;
+      sum.tokens += join[i].tokens;
+      sum.seqs += join[i].seqs;
+    }
+    part[blockIdx.x] = sum;
+  }
+}
+
+template <typename V>
+__device__ __forceinline__ V pol_block_sum(V v) {
+  __shared__ V red[POL_WARPS];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if (lane_id() == 0) red[warp_id()] = v;
+  __syncthreads();
+  v = 0;
+#pragma unroll
+  for (int i = 0; i < POL_WARPS; ++i) v += red[i];
+  return v;
+}
+
+// stats = (loss, mean KL, share of clipped tokens); weight of each sequence's tokens.
+__global__ void __launch_bounds__(POL_THREADS) policy_join_kernel(const PolicyPart* part, int parts, const int* counts, long long S,
+                                                                  int per_sequence, float* stats, float* weight, uint32_t* err) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  PolicyPart sum = {0.0, 0.0, 0.0, 0, 0};
+  for (int i = threadIdx.x; i < parts; i += POL_THREADS) {
+    const PolicyPart p = part[i];
+    sum.loss += p.loss;
+    sum.kl += p.kl;
+    sum.clipped += p.clipped;
+    sum.tokens += p.tokens;
+    sum.seqs += p.seqs;
+  }
+  const long long n = pol_block_sum(per_sequence ? sum.seqs : sum.tokens);
+  const double f = n > 0 ? 1.0 / static_cast<double>(n) : 0.0;
+  if (blockIdx.x == 0) {
+    const double loss = pol_block_sum(sum.loss), kl = pol_block_sum(sum.kl), clipped = pol_block_sum(sum.clipped);
+    if (threadIdx.x == 0) {
+      stats[0] = static_cast<float>(loss * f);
+      stats[1] = static_cast<float>(kl * f);
+      stats[2] = static_cast<float>(clipped * f);
+    }
+  }
+  const long long s = static_cast<long long>(blockIdx.x) * POL_THREADS + threadIdx.x;
+  if (s < S && in_bounds(err, s, 1, S, SITE_POLICY_OUT)) {
+    const int c = counts[s];
+    weight[s] = c == 0 ? 0.0f : static_cast<float>(per_sequence ? f / c : f);
+  }
+}
+
+__global__ void __launch_bounds__(POL_THREADS) policy_grad_kernel(const __grid_constant__ PolicyArgs a, const float* dloss,
+                                                                  const float* weight, float* dnll) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const long long n_el = a.S * a.T;
+  const float dl = *dloss;
+  const long long span = static_cast<long long>(POL_THREADS) * POL_TILE;
+  for (long long i0 = blockIdx.x * span + threadIdx.x; i0 < n_el; i0 += gridDim.x * span) {
+    int64_t lab[POL_TILE];
+    float nll[POL_TILE], old[POL_TILE], ref[POL_TILE], adv[POL_TILE], w[POL_TILE];
+#pragma unroll
+    for (int i = 0; i < POL_TILE; ++i) {
+      const long long t = i0 + i * POL_THREADS;
+      lab[i] = -1;
+      nll[i] = old[i] = ref[i] = adv[i] = w[i] = 0.0f;
+      if (t < n_el && in_bounds(a.err, t, 1, n_el, SITE_POLICY_IN)) {
+        // 64-bit division only where 32 bits do not hold the index
+        const long long s = n_el <= 0x7fffffff ? static_cast<uint32_t>(t) / static_cast<uint32_t>(a.T) : t / a.T;
+        lab[i] = a.labels[t];
+        nll[i] = a.nll[t];
+        old[i] = a.old_nll[t];
+        if (a.ref_nll) ref[i] = a.ref_nll[t];
+        adv[i] = a.adv[a.adv_tok ? t : s];
+        w[i] = weight[s];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < POL_TILE; ++i) {
+      const long long t = i0 + i * POL_THREADS;
+      if (t >= n_el || !in_bounds(a.err, t, 1, n_el, SITE_POLICY_OUT)) continue;
+      dnll[t] = lab[i] < 0 ? 0.0f : policy_token(a, nll[i], old[i], ref[i], adv[i]).grad * (w[i] * dl);
+    }
+  }
+}
+
+int policy_blocks(long long units) {
+  return static_cast<int>(units < 1 ? 1 : units < POL_MAX_BLOCKS ? units : POL_MAX_BLOCKS);
+}
+
+// Warps a sequence: as many as leave each lane at most 16 tokens, up to a whole block.
+int policy_warps(long long T) {
+  int w = 1;
+  while (w < POL_WARPS && T > 512LL * w) w *= 2;
+  return w;
+}
+
+bool aligned_to(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Arguments that both directions share.
+wb_status policy_args(PolicyArgs& a, const float* nll, const float* old_nll, const float* ref_nll, const float* advantage,
+                      int advantage_per_token, const int64_t* labels, int64_t S, int64_t T, double clip_low, double clip_high,
+                      float kl_weight, bool& empty) {
+  if (S < 0 || T < 0 || S > (1LL << 31) || T > (1LL << 30) || (T > 0 && S > (1LL << 40) / T)) return WB_EINVAL;
+  if (!(clip_low >= 0.0 && clip_low <= 1.0) || !(clip_high >= 0.0 && clip_high <= 1e30)) return WB_EINVAL;
+  if (!std::isfinite(kl_weight) || (kl_weight != 0.0f && !ref_nll && S > 0 && T > 0)) return WB_EINVAL;
+  empty = S == 0 || T == 0;
+  if (empty) return WB_OK;
+  if (!nll || !old_nll || !advantage || !labels || !aligned_to(nll, 4) || !aligned_to(old_nll, 4) || !aligned_to(ref_nll, 4) ||
+      !aligned_to(advantage, 4) || !aligned_to(labels, 8))
+    return WB_EINVAL;
+  const double hi = std::log1p(clip_high), lo = std::log1p(-clip_low);
+  a.nll = nll;
+  a.old_nll = old_nll;
+  a.ref_nll = ref_nll;
+  a.adv = advantage;
+  a.labels = labels;
+  a.S = S;
+  a.T = T;
+  a.adv_tok = advantage_per_token ? 1 : 0;
+  a.hi0 = static_cast<float>(hi);
+  a.hi1 = static_cast<float>(hi - a.hi0);
+  a.lo0 = static_cast<float>(lo);
+  a.lo1 = std::isfinite(lo) ? static_cast<float>(lo - a.lo0) : 0.0f;
+  a.hold_hi = static_cast<float>(1.0 + clip_high);
+  a.hold_lo = static_cast<float>(1.0 - clip_low);
+  a.beta = kl_weight;
+  a.per_sequence = 0;
+  a.err = nullptr;
+  return WB_OK;
+}
+
+struct PolicyWs {
+  size_t part, counts, total;
+};
+PolicyWs policy_ws(int64_t S) {
+  Carver c;
+  PolicyWs w;
+  w.part = c.take(sizeof(PolicyPart) * POL_MAX_BLOCKS);
+  w.counts = c.take(sizeof(int) * static_cast<size_t>(S));
+  w.total = c.off;
+  return w;
+}
+
+}  // namespace
+}  // namespace wb
+
+using namespace wb;
+
+extern "C" {
+
+size_t wb_policy_loss_workspace_bytes(int64_t S, int64_t T) {
+  if (S < 1 || T < 1 || S > (1LL << 31) || T > (1LL << 30) || S > (1LL << 40) / T) return 0;
+  return policy_ws(S).total;
+}
+
+wb_status wb_policy_loss(const float* nll, const float* old_nll, const float* ref_nll, const float* advantage,
+                         int advantage_per_token, const int64_t* labels, int64_t S, int64_t T, double clip_low,
+                         double clip_high, float kl_weight, int per_sequence, float* stats, float* weight, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  PolicyArgs a;
+  bool empty = false;
+  const wb_status st = policy_args(a, nll, old_nll, ref_nll, advantage, advantage_per_token, labels, S, T, clip_low, clip_high,
+                                   kl_weight, empty);
+  if (st != WB_OK) return st;
+  if (!stats || !aligned_to(stats, 4) || (S > 0 && (!weight || !aligned_to(weight, 4)))) return WB_EINVAL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (empty) {
+    WB_CUDA(cudaMemsetAsync(stats, 0, 3 * sizeof(float), s));
+    if (S > 0) WB_CUDA(cudaMemsetAsync(weight, 0, sizeof(float) * static_cast<size_t>(S), s));
+    return WB_OK;
+  }
+  if (!workspace || !aligned16(workspace) || workspace_bytes < policy_ws(S).total) return WB_EWORKSPACE;
+  a.per_sequence = per_sequence != 0;
+  a.err = tc_err_ptr();
+  if (!a.err) return WB_ECUDA;
+  const PolicyWs w = policy_ws(S);
+  auto* part = reinterpret_cast<PolicyPart*>(static_cast<char*>(workspace) + w.part);
+  int* counts = reinterpret_cast<int*>(static_cast<char*>(workspace) + w.counts);
+  const int warps = policy_warps(T);
+  const int teams = POL_WARPS / warps;
+  const int blocks = policy_blocks((S + teams - 1) / teams);
+  Prof pr(PC_POLICY, s, 2);
+  auto kern = warps == 1 ? policy_sum_kernel<1> : warps == 2 ? policy_sum_kernel<2> : warps == 4 ? policy_sum_kernel<4> : policy_sum_kernel<8>;
+  WB_CUDA(launch_pdl(kern, dim3(blocks), dim3(POL_THREADS), 0, s, a, counts, part, blocks));
+  WB_CUDA(launch_pdl(policy_join_kernel, dim3(static_cast<unsigned>((S + POL_THREADS - 1) / POL_THREADS)), dim3(POL_THREADS), 0, s,
+                     static_cast<const PolicyPart*>(part), blocks, static_cast<const int*>(counts), static_cast<long long>(S),
+                     a.per_sequence, stats, weight, a.err));
+  return WB_OK;
+}
+
+wb_status wb_policy_loss_backward(const float* dloss, const float* nll, const float* old_nll, const float* ref_nll,
+                                  const float* advantage, int advantage_per_token, const int64_t* labels, const float* weight,
+                                  int64_t S, int64_t T, double clip_low, double clip_high, float kl_weight, float* dnll,
+                                  void* stream) {
+  PolicyArgs a;
+  bool empty = false;
+  const wb_status st = policy_args(a, nll, old_nll, ref_nll, advantage, advantage_per_token, labels, S, T, clip_low, clip_high,
+                                   kl_weight, empty);
+  if (st != WB_OK) return st;
+  if (empty) return WB_OK;
+  if (!dloss || !weight || !dnll || !aligned_to(dloss, 4) || !aligned_to(weight, 4) || !aligned_to(dnll, 4)) return WB_EINVAL;
+  a.err = tc_err_ptr();
+  if (!a.err) return WB_ECUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Prof pr(PC_POLICY, s);
+  const long long span = static_cast<long long>(POL_THREADS) * POL_TILE;
+  WB_CUDA(launch_pdl(policy_grad_kernel, dim3(policy_blocks((a.S * a.T + span - 1) / span)), dim3(POL_THREADS), 0, s, a, dloss, weight, dnll));
+  return WB_OK;
+}
+
+}  // extern "C"

@@ -116,7 +116,7 @@ struct AttnParams {
 
 // Sites (bits 8..15 of the error word) of the debug bounds checks: 0x20-0x3F the SIMT kernels,
 // 0x40-0x4F the GEMM epilogues, 0x50-0x5F the attention epilogue, 0x60-0x67 the LayerNorm of training,
-// 0x68-0x6F the vocabulary losses.
+// 0x68-0x6F the vocabulary losses, 0x70-0x74 gradient clipping and the policy loss, 0x75-0x7A cross attention.
 enum : uint32_t {
   SITE_PAD_SPLIT = 0x20, SITE_DFT_BASIS, SITE_MEL_FB, SITE_LOGMEL_POST, SITE_STEM_T_IN, SITE_STEM_T_OUT,
   SITE_ZERO_ROWS, SITE_PACK_CONV, SITE_LN_X, SITE_LN_Y, SITE_LN_GB, SITE_STATS_X, SITE_STATS_OUT,
@@ -127,7 +127,9 @@ enum : uint32_t {
   SITE_GEMM_MEL, SITE_GEMM_AMAX, SITE_GEMM_LNPART,
   SITE_ATT_OUT = 0x50, SITE_ATT_AMAX,
   SITE_LNT_X = 0x60, SITE_LNT_Y, SITE_LNT_TOTAL, SITE_LNT_STATS, SITE_LNT_PART, SITE_LNT_GRAD,
-  SITE_HEAD_ROWS = 0x68, SITE_HEAD_TARGET, SITE_HEAD_PART, SITE_HEAD_X, SITE_HEAD_LIST, SITE_HEAD_SLAB, SITE_HEAD_DX
+  SITE_HEAD_ROWS = 0x68, SITE_HEAD_TARGET, SITE_HEAD_PART, SITE_HEAD_X, SITE_HEAD_LIST, SITE_HEAD_SLAB, SITE_HEAD_DX,
+  SITE_CLIP_IN = 0x70, SITE_CLIP_OUT, SITE_CLIP_PART, SITE_POLICY_IN, SITE_POLICY_OUT,
+  SITE_CROSS_Q = 0x75, SITE_CROSS_KV, SITE_CROSS_OUT, SITE_CROSS_LSE, SITE_CROSS_STATS, SITE_CROSS_LENS
 };
 
 }  // namespace wb
