@@ -545,35 +545,41 @@ def _i32(values):
 
 
 def _grad_list(tensors, name):
-    """Pointers, sizes and types of a list of tensors of one device."""
-    for t in tensors:
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _LN_TYPES or not _dense(t):
-            raise ValueError(f"{name}: expected CUDA tensors of bf16, f16 or f32 without gaps")
-    return [t.data_ptr() for t in tensors], [t.numel() for t in tensors], [_LN_TYPES[t.dtype] for t in tensors]
+    """Pointers, sizes and types of a list of tensors.  One attribute at a time: the list can be hundreds long, and the host's
+    time a tensor is what a small model's call takes."""
+    try:
+        types = [_LN_TYPES[t.dtype] for t in tensors]
+        dense = all([t.is_contiguous() for t in tensors]) or all([_dense(t) for t in tensors])
+        if dense and min([t.get_device() for t in tensors]) >= 0:
+            return [t.data_ptr() for t in tensors], [t.numel() for t in tensors], types
+    except (KeyError, AttributeError):
+        pass
+    raise ValueError(f"{name}: expected CUDA tensors of bf16, f16 or f32 without gaps")
 
 
 def _grad_norm(grads, max_norm, out, workspace, stream):
-    grads = list(grads)
     if not grads:
         raise ValueError("grads: expected at least one tensor")
     if len(grads) > _lib.WB_CLIP_MAX_TENSORS:
         raise ValueError(f"grads: at most {_lib.WB_CLIP_MAX_TENSORS} tensors")
     at, numel, types = _grad_list(grads, "grads")
+    at, n32 = _i64(at), _i32(types)
     outs = out_types = None
-    if out is not None:
-        out = list(out)
-        if out is not grads:
-            if len(out) != len(grads) or any(o.shape != g.shape or o.stride() != g.stride() for o, g in zip(out, grads)):
-                raise ValueError("out: expected one tensor for each gradient, of its shape and strides")
+    if out is grads:
+        outs, out_types = at, n32
+    elif out is not None:
         outs, _, out_types = _grad_list(out, "out")
-        if any(o != t and o != WB_F32 for o, t in zip(out_types, types)):
+        if [o.shape for o in out] != [g.shape for g in grads] or not (
+                all([t.is_contiguous() for t in grads + out]) or all([o.stride() == g.stride() for o, g in zip(out, grads)])):
+            raise ValueError("out: expected one tensor for each gradient, of its shape and strides")
+        if any([o != t and o != WB_F32 for o, t in zip(out_types, types)]):
             raise ValueError("out: expected each gradient's type or float32")
         outs, out_types = _i64(outs), _i32(out_types)
-    with _place(stream, *grads, *(out or ()), workspace):
+    with _place(stream, *grads, *(() if out is None or out is grads else out), workspace):
         norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
         ws = _head_workspace(workspace, "wb_clip_grad_norm_workspace_bytes", norm.device, len(grads))
-        call("wb_clip_grad_norm", _i64(at), outs, _i64(numel), _i32(types), out_types, len(grads), max_norm, _a(norm), _a(ws),
-             ws.numel(), _raw_stream(norm))
+        call("wb_clip_grad_norm", at, outs, _i64(numel), n32, out_types, len(grads), max_norm, _a(norm), _a(ws), ws.numel(),
+             _raw_stream(norm))
     return norm
 
 
@@ -581,7 +587,7 @@ def grad_norm(grads, workspace=None, stream=None):
     """2-norm over all elements of a list of gradients (bf16, f16 or f32, mixed), as a float32 scalar on the device.
 
     Tensors may be of any shape and order of dimensions that leaves no gaps; an empty one counts nothing."""
-    return _grad_norm(grads, 0.0, None, workspace, stream)
+    return _grad_norm(list(grads), 0.0, None, workspace, stream)
 
 
 def clip_grad_norm(grads, max_norm: float, out=None, workspace=None, stream=None):
@@ -591,7 +597,7 @@ def clip_grad_norm(grads, max_norm: float, out=None, workspace=None, stream=None
     whether or not anything has to be scaled).  A norm that is not finite leaves the values as they are.  No tensor
     may share memory with another one of the call."""
     grads = list(grads)
-    return _grad_norm(grads, max_norm, grads if out is None else out, workspace, stream)
+    return _grad_norm(grads, max_norm, grads if out is None else list(out), workspace, stream)
 
 
 def _policy_shape(nll, old_nll, advantage, labels, ref_nll, kl_weight):

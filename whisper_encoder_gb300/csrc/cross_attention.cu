@@ -84,10 +84,9 @@ void base(CrossParams& x, int batch, int Tq, int Tk, int H, int Hk, float scale,
   x.err = tc_err_ptr();
 }
 
-template <int MT>
 cudaError_t launch_few(const FewParams& p, cudaStream_t s) {
   static uint64_t done = 0;
-  cudaError_t e = allow_smem(cross_few_kernel<MT>, few_smem(MT), &done);
+  cudaError_t e = allow_smem(cross_few_kernel, FewSmem::TOTAL, &done);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -98,17 +97,17 @@ cudaError_t launch_few(const FewParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.x.batch) * p.x.Hk * p.splits);
   cfg.blockDim = dim3(FEW_THREADS);
-  cfg.dynamicSmemBytes = few_smem(MT);
+  cfg.dynamicSmemBytes = FewSmem::TOTAL;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, cross_few_kernel<MT>, p);
+  cfg.numAttrs = p.splits > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, cross_few_kernel, p);
 }
 
-// Splits of the keys: 1, 2, 4 or 8, as long as the (item, head) pairs leave SMs idle and every warp of a split has 16 keys.
+// Splits of the keys: 1, 2, 4 or 8, while the (item, head) pairs leave places for CTAs empty and a split has 64 keys.
 int few_splits(long long pairs, int Tk) {
   int n = 1;
-  while (n < 8 && pairs * n < 2LL * sm_count() && Tk > 2 * n * FEW_WARPS * 16) n *= 2;
+  while (n < FEW_MAX_SPLITS && pairs * n < 2LL * sm_count() && Tk >= 2 * n * 64) n *= 2;
   return n;
 }
 
@@ -139,7 +138,7 @@ wb_status wb_cross_attention(const void* q, int64_t q_batch, int64_t q_row, cons
   p.x.lse = lse;
   Prof pr(PC_CROSS_FWD, s);
   const long long rows = static_cast<long long>(p.x.group) * Tq;
-  if (rows <= FEW_MAX_ROWS) {
+  if (rows <= FEW_ROWS) {
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.k = static_cast<const __nv_bfloat16*>(k);
     p.v = static_cast<const __nv_bfloat16*>(v);
@@ -150,7 +149,7 @@ wb_status wb_cross_attention(const void* q, int64_t q_batch, int64_t q_row, cons
     p.v_batch = rv.batch;
     p.v_row = rv.row;
     p.splits = few_splits(static_cast<long long>(batch) * n_kv_heads, Tk);
-    WB_CUDA(rows <= 16 ? launch_few<1>(p, s) : launch_few<2>(p, s));
+    WB_CUDA(launch_few(p, s));
     return WB_OK;
   }
   CUtensorMap qm, km, vm;
