@@ -165,7 +165,7 @@ wb_status wb_cross_attention(const void* q, int64_t q_batch, int64_t q_row, cons
 
 size_t wb_cross_attention_backward_workspace_bytes(int batch, int Tq, int n_heads) {
   if (batch < 1 || Tq < 1 || n_heads < 1 || Tq > MAX_T || n_heads > 1024) return 0;
-  return static_cast<size_t>(batch) * n_heads * ((Tq + 127) / 128 * 128) * sizeof(float2);
+  return static_cast<size_t>(batch) * n_heads * ((Tq + 127) / 128 * 128) * 2 * sizeof(float);
 }
 
 wb_status wb_cross_attention_backward(const void* dout, int64_t do_batch, int64_t do_row, const void* q, int64_t q_batch,
@@ -203,7 +203,7 @@ wb_status wb_cross_attention_backward(const void* dout, int64_t do_batch, int64_
   sp.dout = static_cast<const __nv_bfloat16*>(dout);
   sp.do_batch = ro.batch;
   sp.do_row = ro.row;
-  sp.stats = static_cast<float2*>(workspace);
+  sp.stats = static_cast<float*>(workspace);
   sp.stats_ld = (Tq + 127) / 128 * 128;
   CrossBwdParams p;
   p.x = sp.x;
@@ -213,29 +213,26 @@ wb_status wb_cross_attention_backward(const void* dout, int64_t do_batch, int64_
   p.dq = static_cast<__nv_bfloat16*>(dq);
   p.dk = static_cast<__nv_bfloat16*>(dk);
   p.dv = static_cast<__nv_bfloat16*>(dv);
-  Prof pr(PC_CROSS_BWD, s, 1 + (dq ? 1 : 0) + (dk ? 1 : 0));
+  p.want_dq = dq != nullptr;
+  Prof pr(PC_CROSS_BWD, s, dk ? 3 : 2);
   const long long blocks = (static_cast<long long>(batch) * n_heads * sp.stats_ld + 31) / 32;
-  const int most = sm_count() * 8;
-  WB_CUDA(launch_pdl(cross_stats_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, s, sp));
+  const int sms = sm_count();
+  WB_CUDA(launch_pdl(cross_stats_kernel, dim3(static_cast<unsigned>(blocks < sms * 8 ? blocks : sms * 8)), dim3(256), 0, s, sp));
   CUtensorMap qm, dm, km, vm;
-  if (dk) {
-    if (!rows_map(&qm, rq, batch, Tq, n_heads, CRB_STEP) || !rows_map(&dm, ro, batch, Tq, n_heads, CRB_STEP) ||
-        !rows_map(&km, rk, batch, Tk, n_kv_heads, CRB_M) || !rows_map(&vm, rv, batch, Tk, n_kv_heads, CRB_M))
-      return WB_ECUDA;
-    static uint64_t done = 0;
-    WB_CUDA(allow_smem(cross_dkv_kernel, CrossBwdSmem::TOTAL, &done));
-    const unsigned grid = static_cast<unsigned>(batch) * n_kv_heads * ((Tk + CRB_M - 1) / CRB_M);
-    WB_CUDA(launch_pdl(cross_dkv_kernel, dim3(grid), dim3(CRA_THREADS), CrossBwdSmem::TOTAL, s, qm, dm, km, vm, p));
-  }
-  if (dq) {
-    if (!rows_map(&qm, rq, batch, Tq, n_heads, CRB_M) || !rows_map(&dm, ro, batch, Tq, n_heads, CRB_M) ||
-        !rows_map(&km, rk, batch, Tk, n_kv_heads, CRB_STEP) || !rows_map(&vm, rv, batch, Tk, n_kv_heads, CRB_STEP))
-      return WB_ECUDA;
-    static uint64_t done = 0;
-    WB_CUDA(allow_smem(cross_dq_kernel, CrossBwdSmem::TOTAL, &done));
-    const unsigned grid = static_cast<unsigned>(batch) * n_heads * ((Tq + CRB_M - 1) / CRB_M);
-    WB_CUDA(launch_pdl(cross_dq_kernel, dim3(grid), dim3(CRA_THREADS), CrossBwdSmem::TOTAL, s, qm, dm, km, vm, p));
-  }
+  if (!rows_map(&qm, rq, batch, Tq, n_heads, CRB_M) || !rows_map(&dm, ro, batch, Tq, n_heads, CRB_M) ||
+      !rows_map(&km, rk, batch, Tk, n_kv_heads, CRB_M) || !rows_map(&vm, rv, batch, Tk, n_kv_heads, CRB_M))
+    return WB_ECUDA;
+  static uint64_t dq_done = 0, dkv_done = 0;
+  constexpr int SMEM = CrossBwdSmem::TOTAL;
+  WB_CUDA(allow_smem(cross_bwd_kernel<false>, SMEM, &dq_done));
+  WB_CUDA(allow_smem(cross_bwd_kernel<true>, SMEM, &dkv_done));
+  const long long q_items = static_cast<long long>(batch) * n_heads * ((Tq + CRB_M - 1) / CRB_M);
+  const long long k_items = static_cast<long long>(batch) * n_kv_heads * ((Tk + CRB_M - 1) / CRB_M);
+  WB_CUDA(launch_pdl(cross_bwd_kernel<false>, dim3(static_cast<unsigned>(q_items < sms ? q_items : sms)), dim3(CRB_THREADS), SMEM, s, qm, dm,
+                     km, vm, p));
+  if (dk)
+    WB_CUDA(launch_pdl(cross_bwd_kernel<true>, dim3(static_cast<unsigned>(k_items < sms ? k_items : sms)), dim3(CRB_THREADS), SMEM, s, km, vm,
+                       qm, dm, p));
   return WB_OK;
 }
 

@@ -1,46 +1,59 @@
 // Backward pass of cross_fwd_kernel on tcgen05 (head dim 64).
 //
-// With P = exp(s - lse), dP = dout v^T, delta = sum_e dout out and dS = P (dP - delta):
+// With P = exp(s - lse), dP = dout v^T, delta = sum_k P dP and dS = P (dP - delta):
 //   dv = P^T dout,  dk = scale dS^T q   (over the rows of all heads of a group),   dq = scale dS k
 // No scores are stored: two kernels form P and dP again, each from the side whose sums it keeps, so that every sum runs inside one
 // CTA in a fixed order and nothing is added through memory (one kernel for all three would save two of seven products
 // and add dq of every key tile to float32 memory, in an order that changes).
-//   cross_dkv_kernel  128 keys a CTA, 64 query rows a step: S^T = K Q^T and dP^T = V dO^T (lane = key) -> P^T and dS^T as
-//                     packed bf16 over the columns they came from -> dV += P^T dO, dK += dS^T Q
-//   cross_dq_kernel   128 query rows a CTA, 64 keys a step: S = Q K^T, dP = dO V^T -> dS -> dQ += dS K
-// P^T and dS^T are A operands read from TMEM; Q, dO and K are read both as K-major and as MN-major B tiles of the
-// same shared memory, so nothing is transposed.  256 TMEM columns a CTA, two CTAs an SM: one's softmax under the other's products.
-// cross_stats_kernel prepares (lse / scale, delta) of every row, (infinity, 0) for rows that take no part: their P is 0.
+//   cross_stats_kernel        -lse / scale and -sum_e dout out of every row, -infinity and 0 for rows that take no part: their P is 0
+//   cross_bwd_kernel<false>   128 query rows an item, 128 keys a step: S = Q K^T, dP = dO V^T -> dQ += dS K, M += P K
+//   cross_bwd_kernel<true>    128 keys an item, 128 query rows a step: S^T = K Q^T, dP^T = V dO^T (lane = key) ->
+//                             dV += P^T dO, dK += dS^T Q
+// P and dS go as packed bf16 over the TMEM columns S came from and are read there as A operands; the step's tiles are read both as
+// K-major and as MN-major B tiles of the same shared memory, so nothing is transposed.
 //
-// Numbers.  Sums are float32; P and dS are rounded to bf16 once each, as operands beside bf16 q, k and dout.
-// Rows past their item's lengths may hold anything: they are cleared in shared memory where a zero would multiply them.
+// Persistent, one CTA an SM over its items in turn.  Bound by the tensor pipe: 16 products of 128 x 128 x 16 and 128 x 64 x 16 a
+// step, 64 and 45 cycles each alone.  What keeps it fed: S is double, dP is given back as soon as the softmax holds it in registers, so
+// the scores of step n + 1 are formed under the softmax of step n, and its sums under the softmax of step n + 1; an item's
+// sums are stored after the next item's first softmax.  128 columns a step: with 64, two buffers of both and a group of
+// warps for each, a product took 48 cycles for half the work and a step 2000 (dk and dv of 32 x 448 x 1500 x 20 heads 526 us; one
+// item a CTA, two CTAs an SM, 419).
+// Warp 0 lane 0 loads, warp 1 issues, warps 2-17 run the softmax: 16 rows of half of the columns each.
+//
+// Numbers.  Sums are float32; P and dS are rounded to bf16 once each, as operands beside bf16 q, k and dout.  delta is sum_e dout out as well,
+// but out is rounded to bf16, and what that leaves is the same for all keys of a row: it does not average out (dq and dk were 3.3e-3 of
+// their norm from 64 bits, 2.4e-3 without it).  With d' that delta, b = sum_k P (dP - d') is what it lacks, since sum_k P = 1: the dq
+// kernel subtracts b M, M = sum_k P k, and hands delta = d' + b to the dkv kernel.
+// Rows past their item's lengths may hold anything: a step's are cleared in shared memory before its products, an item's own reach only
+// results that are not stored.
 #pragma once
 #include "cross_attention.cuh"
 
 namespace wb {
 
-constexpr int CRB_M = 128, CRB_STEP = 64;      // accumulator rows of a CTA, rows of the other side a step
-constexpr int CRB_STAGES = 3;
-constexpr uint32_t CRB_TM_S = 0, CRB_TM_D = 64, CRB_TM_ACC0 = 128, CRB_TM_ACC1 = 192, CRB_TM_COLS = 256;
+constexpr int CRB_M = 128, CRB_STEP = 128;     // own rows of an item, rows of the other side a step
+constexpr int CRB_STAGES = 4;
+constexpr int CRB_GROUP_WARPS = 8, CRB_WARPS = 2 * CRB_GROUP_WARPS, CRB_THREADS = 64 + 32 * CRB_WARPS;
+// TMEM: S of even and odd steps (P and dS over it: 64 columns each), dP, the two accumulators
+constexpr uint32_t CRB_TM_S = 128, CRB_TM_D = 256, CRB_TM_ACC = 384, CRB_TM_COLS = 512;
 
 struct CrossBwdSmem {
-  static constexpr int M_BYTES = CRB_M * 128;               // K and V (dkv) or Q and dO (dq)
-  static constexpr int STEP_BYTES = CRB_STEP * 128;         // Q and dO (dkv) or K and V (dq)
-  static constexpr int STATS_BYTES = CRB_STEP * 8;          // dkv: (lse / scale, delta) of the step's rows
-  static constexpr int OFF_M0 = 0;
-  static constexpr int OFF_M1 = OFF_M0 + M_BYTES;
-  static constexpr int OFF_STEP = OFF_M1 + M_BYTES;
-  static constexpr int OFF_STATS = OFF_STEP + CRB_STAGES * 2 * STEP_BYTES;
-  static constexpr int OFF_BAR = OFF_STATS + CRB_STAGES * STATS_BYTES;
-  static constexpr int TOTAL = 1024 + OFF_BAR + 256;
+  static constexpr int TILE = CRB_M * 128;                  // 128 rows of 64 elements
+  static constexpr int STATS_BYTES = 2 * CRB_STEP * 4;      // dkv: -lse / scale, then -delta, of the step's rows
+  static constexpr int OFF_STEP = 4 * TILE;                 // the own tiles have two slots
+  static constexpr int OFF_STATS = OFF_STEP + CRB_STAGES * 2 * TILE;
+  static constexpr int OFF_B = OFF_STATS + CRB_STAGES * STATS_BYTES;    // dq: b by [item parity][column half][row]
+  static constexpr int OFF_BAR = OFF_B + 2 * 2 * CRB_M * 4;
+  static constexpr int TOTAL = 1024 + OFF_BAR + 512;
 };
-static_assert(2 * CrossBwdSmem::TOTAL <= 227 * 1024, "two CTAs an SM");
+static_assert(CrossBwdSmem::TOTAL <= 227 * 1024, "one CTA an SM");
 
 struct CrossBwdParams {
   CrossParams x;             // out and lse unused here
   int do_items;              // as q_items, for dout
-  const float2* stats;       // [batch][H][stats_ld]
+  float* stats;              // [batch][H][2][stats_ld]: -lse / scale, -delta
   int stats_ld;              // Tq rounded up to 128
+  int want_dq;               // cross_bwd_kernel<false>: 0: delta alone
   __nv_bfloat16* dq;         // [batch][Tq][H 64]
   __nv_bfloat16* dk;         // [batch][Tk][Hk 64]
   __nv_bfloat16* dv;
@@ -50,7 +63,7 @@ struct CrossStatsParams {
   CrossParams x;             // lse, out: the forward pass's
   const __nv_bfloat16* dout;
   long long do_batch, do_row;
-  float2* stats;
+  float* stats;
   int stats_ld;
 };
 
@@ -89,416 +102,446 @@ __global__ void __launch_bounds__(256) cross_stats_kernel(const __grid_constant_
     d += __shfl_xor_sync(0xffffffffu, d, 2);
     d += __shfl_xor_sync(0xffffffffu, d, 4);
     if (in && e == 0) {
-      const long long si = (static_cast<long long>(b) * x.H + h) * p.stats_ld + t;
+      const long long si = (static_cast<long long>(b) * x.H + h) * 2 * p.stats_ld + t;
       const long long li = (static_cast<long long>(b) * x.H + h) * x.Tq + t;
-      float2 v = make_float2(INFINITY, 0.0f);
+      float l = INFINITY;
       if (there && in_bounds(x.err, li, 1, static_cast<long long>(x.batch) * x.H * x.Tq, SITE_CROSS_LSE))
-        v = make_float2(x.lse[li] * inv_scale, d);
-      if (in_bounds(x.err, si, 1, rows, SITE_CROSS_STATS)) p.stats[si] = v;
+        l = x.lse[li] * inv_scale;
+      if (in_bounds(x.err, si, 1 + p.stats_ld, 2 * rows, SITE_CROSS_STATS)) {
+        p.stats[si] = -l;
+        p.stats[si + p.stats_ld] = -d;
+      }
     }
   }
 }
 
-// What both kernels share: barriers, TMEM, and the 64-column exchange between products and softmax warps.
-struct CrossBwdBars {
-  uint64_t* m_full;
-  uint64_t* full;            // [CRB_STAGES]
-  uint64_t* empty;           // [CRB_STAGES]
-  uint64_t* s_full;          // S and dP hold a step
-  uint64_t* p_full;          // P and dS written over them
-  uint64_t* fixed;           // dkv: the step's rows that take no part are cleared
-  uint64_t* acc_done;
-  uint32_t* tmem_slot;
-  volatile int* abort_flag;
-};
-__device__ __forceinline__ CrossBwdBars cross_bwd_bars(uint8_t* smem) {
-  CrossBwdBars b;
-  b.m_full = reinterpret_cast<uint64_t*>(smem + CrossBwdSmem::OFF_BAR);
-  b.full = b.m_full + 1;
-  b.empty = b.full + CRB_STAGES;
-  b.s_full = b.empty + CRB_STAGES;
-  b.p_full = b.s_full + 1;
-  b.fixed = b.p_full + 1;
-  b.acc_done = b.fixed + 1;
-  b.tmem_slot = reinterpret_cast<uint32_t*>(b.acc_done + 1);
-  b.abort_flag = reinterpret_cast<volatile int*>(b.tmem_slot + 1);
-  return b;
-}
-__device__ __forceinline__ void cross_bwd_init(const CrossBwdBars& b) {
-  mbar_init(b.m_full, 1);
-  for (int s = 0; s < CRB_STAGES; ++s) {
-    mbar_init(&b.full[s], 1);
-    mbar_init(&b.empty[s], 1);
-  }
-  mbar_init(b.s_full, 1);
-  mbar_init(b.p_full, CRA_SOFTMAX_WARPS);
-  mbar_init(b.fixed, CRA_SOFTMAX_WARPS);
-  mbar_init(b.acc_done, 1);
-  *b.abort_flag = 0;
-  fence_mbar_init();
+// Four lanes t hold words (columns 8k + 2t and + 1) of k = 0..3; lane t gets all four words of k = t: 16 bytes in a row.
+__device__ __forceinline__ uint4 quad_transpose(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, int t) {
+  const bool odd = t & 1, high = t & 2;
+  uint32_t a = __shfl_xor_sync(0xffffffffu, odd ? w0 : w1, 1), b = __shfl_xor_sync(0xffffffffu, odd ? w2 : w3, 1);
+  if (odd) { w0 = a; w2 = b; } else { w1 = a; w3 = b; }
+  a = __shfl_xor_sync(0xffffffffu, high ? w0 : w2, 2);
+  b = __shfl_xor_sync(0xffffffffu, high ? w1 : w3, 2);
+  if (high) { w0 = a; w1 = b; } else { w2 = a; w3 = b; }
+  return make_uint4(w0, w1, w2, w3);
 }
 
-// Rows [valid, CRB_STEP) of a step's tile become zeros: the softmax warps' 256 threads, a row being 128 bytes.
-__device__ __forceinline__ void cross_clear_rows(uint8_t* tile, int valid) {
-  uint4* rows = reinterpret_cast<uint4*>(tile);
-  for (int i = valid * 8 + static_cast<int>(threadIdx.x) - 64; i < CRB_STEP * 8; i += 32 * CRA_SOFTMAX_WARPS)
-    rows[i] = make_uint4(0, 0, 0, 0);
-}
-
-// An accumulator's rows lane_base + lane / 4 and + 8, scaled, as bf16; zeros for rows at or past `there`.
-__device__ __forceinline__ void cross_store_acc(uint32_t tm, float scale, __nv_bfloat16* dst, long long at, long long row_ld,
-                                                long long extent, int row, int there, int rows, int cq, bool any, uint32_t* err) {
-  uint32_t v[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = 0;
-  if (any) {
-    tmem_ld_16x256b_x8(tm, v);
-    tmem_ld_wait();
-  }
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int r = row + 8 * half;
-    if (r >= rows) continue;
-#pragma unroll
-    for (int kk = 0; kk < 8; ++kk) {
-      const long long o = at + 8 * half * row_ld + 8 * kk + cq;
-      const float x0 = __uint_as_float(v[4 * kk + 2 * half]) * scale, x1 = __uint_as_float(v[4 * kk + 2 * half + 1]) * scale;
-      if (in_bounds(err, o, 2, extent, SITE_CROSS_OUT))
-        *reinterpret_cast<uint32_t*>(dst + o) = any && r < there ? pack_bf16(x0, x1) : 0u;
-    }
-  }
-}
-
-// q, do maps: boxes of 64 x 64 rows; k, v maps: boxes of 64 x 128 rows.
-__global__ void __launch_bounds__(CRA_THREADS, 2)
-    cross_dkv_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap do_map,
-                     const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+// own0, own1: K and V (DKV) or Q and dO; step0, step1: Q and dO (DKV) or K and V.  Boxes of 64 x 128 rows.
+template <bool DKV>
+__global__ void __launch_bounds__(CRB_THREADS, 1)
+    cross_bwd_kernel(const __grid_constant__ CUtensorMap own0, const __grid_constant__ CUtensorMap own1,
+                     const __grid_constant__ CUtensorMap step0, const __grid_constant__ CUtensorMap step1,
                      const __grid_constant__ CrossBwdParams p) {
   using S = CrossBwdSmem;
-  constexpr uint32_t IDESC_S = make_idesc(128, CRB_STEP, 1u);
-  constexpr uint32_t IDESC_ACC = make_idesc(128, CRA_HD, 1u) | IDESC_B_MN;
   const CrossParams& x = p.x;
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base_u32 = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base_u32 - smem_u32(smem_raw));
-  const CrossBwdBars bar = cross_bwd_bars(smem);
+  uint64_t* m_full = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);   // [2] an item's own tiles
+  uint64_t* m_empty = m_full + 2;                                      // [2]
+  uint64_t* full = m_empty + 2;                                        // [CRB_STAGES] a step's tiles
+  uint64_t* empty = full + CRB_STAGES;                                 // [CRB_STAGES]
+  uint64_t* s_full = empty + CRB_STAGES;                               // S and dP of a step
+  uint64_t* d_free = s_full + 1;                                       // dP is in registers
+  uint64_t* p_full = d_free + 1;                                       // [2] P and dS written, by parity of the step
+  uint64_t* fixed = p_full + 2;                                        // a ragged step's tiles are cleared
+  uint64_t* acc_full = fixed + 1;                                      // an item's sums
+  uint64_t* acc_empty = acc_full + 1;
+  uint64_t* b_full = acc_empty + 1;                                    // every warp's share of b is written
+  uint64_t* mma_done = b_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = warp_id();
   const int lane = lane_id();
-  const int n_kt = (x.Tk + CRB_M - 1) / CRB_M;
-  const int kt = blockIdx.x % n_kt;
-  const int bh = blockIdx.x / n_kt;
-  const int b = bh / x.Hk, hk = bh % x.Hk;
-  const int k0 = kt * CRB_M;
 
-  if (threadIdx.x == 0) cross_bwd_init(bar);
-  if (warp == 1) tmem_alloc(bar.tmem_slot, CRB_TM_COLS);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&m_full[i], 1);
+      mbar_init(&m_empty[i], 1);
+      mbar_init(&p_full[i], CRB_WARPS);
+    }
+    for (int s = 0; s < CRB_STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(d_free, CRB_WARPS);
+    mbar_init(fixed, CRB_WARPS);
+    mbar_init(acc_full, 1);
+    mbar_init(acc_empty, CRB_WARPS);
+    mbar_init(b_full, CRB_WARPS);
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, CRB_TM_COLS);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *bar.tmem_slot;
+  const uint32_t tmem = *tmem_slot;
   grid_dependency_wait();
   grid_dependents_launch();
 
-  const int q_len = cross_len(x.q_lens, b, x.batch, x.Tq, x.err);
-  const int kv_len = cross_len(x.kv_lens, b, x.batch, x.Tk, x.err);
-  const int per_head = (q_len + CRB_STEP - 1) / CRB_STEP;
-  const int steps = k0 < kv_len ? per_head * x.group : 0;      // the rows of the group's heads, one head after another
+  const int own_T = DKV ? x.Tk : x.Tq, step_T = DKV ? x.Tq : x.Tk, heads = DKV ? x.Hk : x.H;
+  const int n_tiles = (own_T + CRB_M - 1) / CRB_M;
+  const int n_items = x.batch * heads * n_tiles;
+  // every role walks the same items and steps
+  struct Item {
+    int b, h, r0;              // h: head of the own rows; r0: the first of them
+    int own_len, step_len, per_head, steps;
+  };
+  auto item_at = [&](int it) -> Item {
+    Item r;
+    const int bh = it / n_tiles;
+    r.r0 = it % n_tiles * CRB_M;
+    r.b = bh / heads;
+    r.h = bh % heads;
+    const int q_len = cross_len(x.q_lens, r.b, x.batch, x.Tq, x.err), kv_len = cross_len(x.kv_lens, r.b, x.batch, x.Tk, x.err);
+    r.own_len = DKV ? kv_len : q_len;
+    r.step_len = DKV ? q_len : kv_len;
+    r.per_head = (r.step_len + CRB_STEP - 1) / CRB_STEP;
+    r.steps = r.r0 < r.own_len ? r.per_head * (DKV ? x.group : 1) : 0;     // DKV: the group's heads one after another
+    return r;
+  };
+  // rows of a step that starts at t0, and whether its tail holds rows that take no part (behind the last row TMA fills in zeros)
+  auto next_t0 = [](const Item& i, int t0) { return t0 + CRB_STEP >= i.step_len ? 0 : t0 + CRB_STEP; };
+  auto ragged = [&](const Item& i, int t0) { return t0 + CRB_STEP > i.step_len && i.step_len < step_T; };
 
   if (warp == 0) {
-    if (lane == 0 && steps > 0) {
-      const int qb = b * x.q_items, db = b * p.do_items, kb = b * x.kv_items;
-      mbar_arrive_expect_tx(bar.m_full, 2 * S::M_BYTES);
-      tma_load_3d(smem + S::OFF_M0, &k_map, bar.m_full, hk * CRA_HD, k0, kb);
-      tma_load_3d(smem + S::OFF_M1, &v_map, bar.m_full, hk * CRA_HD, k0, kb);
-      uint32_t issued = 0, par = 0;
+    if (lane == 0) {
+      int n = 0, c = 0;                      // steps, and items with steps, so far
       bool ok = true;
-      for (int j = 0; j < steps; ++j) {
-        const int st = j % CRB_STAGES;
-        const uint32_t ph = (j / CRB_STAGES) & 1;
-        if (!mbar_wait(&bar.empty[st], ph ^ 1u, x.err, bar.abort_flag, 43)) { ok = false; break; }
-        mbar_arrive_expect_tx(&bar.full[st], 2 * S::STEP_BYTES + S::STATS_BYTES);
-        const int h = hk * x.group + j / per_head, t0 = (j % per_head) * CRB_STEP;
-        uint8_t* dst = smem + S::OFF_STEP + st * 2 * S::STEP_BYTES;
-        tma_load_3d(dst, &q_map, &bar.full[st], h * CRA_HD, t0, qb);
-        tma_load_3d(dst + S::STEP_BYTES, &do_map, &bar.full[st], h * CRA_HD, t0, db);
-        bulk_load(smem + S::OFF_STATS + st * S::STATS_BYTES, p.stats + (static_cast<long long>(b) * x.H + h) * p.stats_ld + t0,
-                  S::STATS_BYTES, &bar.full[st]);
-        issued |= 1u << st;
-        par = (par & ~(1u << st)) | (ph << st);
+      for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
+        const Item i = item_at(it);
+        if (i.steps == 0) continue;
+        const int slot = c & 1;
+        const int q_at = i.b * x.q_items, do_at = i.b * p.do_items, kv_at = i.b * x.kv_items;
+        if (!mbar_wait(&m_empty[slot], ((c >> 1) & 1) ^ 1u, x.err, abort_flag, 43)) { ok = false; break; }
+        mbar_arrive_expect_tx(&m_full[slot], 2 * S::TILE);
+        tma_load_3d(smem + 2 * slot * S::TILE, &own0, &m_full[slot], i.h * CRA_HD, i.r0, DKV ? kv_at : q_at);
+        tma_load_3d(smem + (2 * slot + 1) * S::TILE, &own1, &m_full[slot], i.h * CRA_HD, i.r0, DKV ? kv_at : do_at);
+        ++c;
+        int h = DKV ? i.h * x.group : i.h / x.group, t0 = 0;
+        for (int j = 0; j < i.steps; ++j, ++n) {
+          const int st = n % CRB_STAGES;
+          if (!mbar_wait(&empty[st], ((n / CRB_STAGES) & 1) ^ 1u, x.err, abort_flag, 44)) { ok = false; break; }
+          mbar_arrive_expect_tx(&full[st], 2 * S::TILE + (DKV ? S::STATS_BYTES : 0));
+          uint8_t* dst = smem + S::OFF_STEP + st * 2 * S::TILE;
+          tma_load_3d(dst, &step0, &full[st], h * CRA_HD, t0, DKV ? q_at : kv_at);
+          tma_load_3d(dst + S::TILE, &step1, &full[st], h * CRA_HD, t0, DKV ? do_at : kv_at);
+          if (DKV) {
+            const float* src = p.stats + (static_cast<long long>(i.b) * x.H + h) * 2 * p.stats_ld + t0;
+            uint8_t* sd = smem + S::OFF_STATS + st * S::STATS_BYTES;
+            bulk_load(sd, src, CRB_STEP * 4, &full[st]);
+            bulk_load(sd + CRB_STEP * 4, src + p.stats_ld, CRB_STEP * 4, &full[st]);
+          }
+          t0 = next_t0(i, t0);
+          if (DKV && t0 == 0) ++h;
+        }
       }
-      if (!ok) {
-        mbar_drain(bar.m_full, 0);
-        for (int s = 0; s < CRB_STAGES; ++s)
-          if (issued & (1u << s)) mbar_drain(&bar.full[s], (par >> s) & 1u);
+      if (!ok) {   // copies already in flight land long before this (their barriers may never be counted out)
+        const uint64_t w0 = globaltimer();
+        while (globaltimer() - w0 < 10000000ull) {
+        }
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && steps > 0) {
-      const uint64_t k_desc = sw128_desc(smem_u32(smem + S::OFF_M0)), v_desc = sw128_desc(smem_u32(smem + S::OFF_M1));
-      const uint32_t step0 = smem_u32(smem + S::OFF_STEP);
-      bool ok = mbar_wait(bar.m_full, 0, x.err, bar.abort_flag, 44);
-      int fixes = 0;
-      for (int j = 0; j < steps && ok; ++j) {
-        const int st = j % CRB_STAGES;
-        ok = mbar_wait(&bar.full[st], (j / CRB_STAGES) & 1, x.err, bar.abort_flag, 45);
-        const int t0 = (j % per_head) * CRB_STEP;
-        if (ok && t0 + CRB_STEP > q_len && q_len < x.Tq) ok = mbar_wait(bar.fixed, fixes++ & 1, x.err, bar.abort_flag, 46);
+    // the whole warp walks and waits; one lane issues
+    const uint32_t step_at = smem_u32(smem + S::OFF_STEP), own_at = smem_u32(smem);
+    constexpr uint32_t IDESC_ACC = make_idesc(128, CRA_HD, 1u) | IDESC_B_MN;
+    auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, x.err, abort_flag, site));
+    };
+    bool ok = true;
+    int n = 0, c = 0, fixes = 0;
+    // the step before, whose sums are issued behind the scores of this one
+    int pn = -1, pc = 0, p_halves = 0;
+    bool p_first = false, p_last = false;
+    auto sums = [&]() -> bool {
+      if (pn < 0) return true;
+      const int st = pn % CRB_STAGES;
+      if (!wait(&p_full[pn & 1], (pn >> 1) & 1, 45)) return false;
+      if (p_first && !wait(acc_empty, (pc & 1) ^ 1u, 46)) return false;
+      tc_fence_after();
+      const uint32_t t_at = step_at + st * 2 * S::TILE;
+      const uint64_t n0 = sw128_mn_desc(t_at, S::TILE), n1 = DKV ? sw128_mn_desc(t_at + S::TILE, S::TILE) : n0;
+      const uint32_t src = tmem + (pn & 1) * CRB_TM_S, acc = tmem + CRB_TM_ACC;
+      const bool want = DKV || p.want_dq;
+      if (elect_one()) {
+        if (want) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            if (k >= 4 && p_halves < 2) break;
+            mma_f16_tmem_a(acc, src + k * 8, n1 + k * (2048 >> 4), IDESC_ACC, !p_first || k != 0);
+            mma_f16_tmem_a(acc + CRA_HD, src + 64 + k * 8, n0 + k * (2048 >> 4), IDESC_ACC, !p_first || k != 0);
+          }
+        }
+        mma_commit(&empty[st]);
+        if (p_last) mma_commit(acc_full);
+      }
+      __syncwarp();
+      pn = -1;
+      return true;
+    };
+    for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
+      const Item i = item_at(it);
+      if (i.steps == 0) continue;
+      const int slot = c & 1;
+      const uint64_t a0 = sw128_desc(own_at + 2 * slot * S::TILE), a1 = sw128_desc(own_at + (2 * slot + 1) * S::TILE);
+      ok = wait(&m_full[slot], (c >> 1) & 1, 47);
+      int t0 = 0;
+      for (int j = 0; j < i.steps && ok; ++j, ++n) {
+        const int st = n % CRB_STAGES;
+        const int halves = i.step_len - t0 > 64 ? 2 : 1;
+        ok = wait(&full[st], (n / CRB_STAGES) & 1, 48);
+        if (ok && ragged(i, t0)) ok = sums() && wait(fixed, fixes++ & 1, 49);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t q_at = step0 + st * 2 * S::STEP_BYTES, do_at = q_at + S::STEP_BYTES;
-        const uint64_t qd = sw128_desc(q_at), dd = sw128_desc(do_at);
-        // the step before is read: its products were issued before these and run before them
+        const uint32_t t_at = step_at + st * 2 * S::TILE;
+        const uint64_t b0 = sw128_desc(t_at), b1 = sw128_desc(t_at + S::TILE);
+        const uint32_t idesc = halves == 2 ? make_idesc(128, 128, 1u) : make_idesc(128, 64, 1u);
+        // the sums that read this S buffer were issued before, and run before
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mma_bf16(tmem + CRB_TM_S, k_desc + 2 * k, qd + 2 * k, IDESC_S, k != 0);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mma_bf16(tmem + CRB_TM_D, v_desc + 2 * k, dd + 2 * k, IDESC_S, k != 0);
-        mma_commit(bar.s_full);
-        if (!mbar_wait(bar.p_full, j & 1, x.err, bar.abort_flag, 47)) { ok = false; break; }
-        tc_fence_after();
-        const uint64_t qn = sw128_mn_desc(q_at, S::STEP_BYTES), dn = sw128_mn_desc(do_at, S::STEP_BYTES);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_f16_tmem_a(tmem + CRB_TM_ACC0, tmem + CRB_TM_S + k * 8, dn + k * (2048 >> 4), IDESC_ACC, (j > 0 || k != 0) ? 1u : 0u);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_f16_tmem_a(tmem + CRB_TM_ACC1, tmem + CRB_TM_D + k * 8, qn + k * (2048 >> 4), IDESC_ACC, (j > 0 || k != 0) ? 1u : 0u);
-        mma_commit(&bar.empty[st]);
-      }
-      mma_commit(bar.acc_done);
-      mbar_drain(bar.acc_done, 0);
-    }
-  } else {
-    const int quarter = warp & 3;
-    const int sub = ((warp - 2) >> 2) & 1;
-    const int lane_base = quarter * 32 + sub * 16;
-    const uint32_t lane_off = static_cast<uint32_t>(lane_base) << 16;
-    const uint32_t s_tm = tmem + lane_off + CRB_TM_S, d_tm = tmem + lane_off + CRB_TM_D;
-    const int cq = 2 * (lane & 3);
-    const uint64_t c2 = f32x2_pack(x.c, x.c);
-    bool ok = true;
-    for (int j = 0; j < steps && ok; ++j) {
-      const int st = j % CRB_STAGES;
-      const int t0 = (j % per_head) * CRB_STEP;
-      if (t0 + CRB_STEP > q_len && q_len < x.Tq) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&bar.full[st], (j / CRB_STAGES) & 1, x.err, bar.abort_flag, 48))) { ok = false; break; }
-        uint8_t* tile = smem + S::OFF_STEP + st * 2 * S::STEP_BYTES;
-        cross_clear_rows(tile, q_len - t0);
-        cross_clear_rows(tile + S::STEP_BYTES, q_len - t0);
-        fence_proxy_async_smem();
+          for (int k = 0; k < 4; ++k) mma_bf16(tmem + (n & 1) * CRB_TM_S, a0 + 2 * k, b0 + 2 * k, idesc, k != 0);
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar.fixed);
-      }
-      // the statistics came with the step's tiles; the products that follow need them too
-      if (!__all_sync(0xffffffffu, mbar_wait(&bar.full[st], (j / CRB_STAGES) & 1, x.err, bar.abort_flag, 48) &&
-                                       mbar_wait(bar.s_full, j & 1, x.err, bar.abort_flag, 49))) { ok = false; break; }
-      tc_fence_after();
-      // s[4k], s[4k+1]: key ra, rows 8k + cq, + 1; s[4k+2], s[4k+3]: key ra + 8, the same rows
-      uint32_t s[32], d[32];
-      tmem_ld_16x256b_x8(s_tm, s);
-      tmem_ld_16x256b_x8(d_tm, d);
-      tmem_ld_wait();
-      const float4* stats = reinterpret_cast<const float4*>(smem + S::OFF_STATS + st * S::STATS_BYTES);
-      uint32_t pw[16], dw[16];
+        if (n > 0) ok = wait(d_free, (n - 1) & 1, 50);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        const float4 z = stats[4 * kk + (lane & 3)];       // (lse, delta) of rows 8k + cq and + 1
-        const uint64_t nl = f32x2_pack(-z.x, -z.z), nd = f32x2_pack(-z.y, -z.w);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint64_t sv = f32x2_pack(__uint_as_float(s[4 * kk + 2 * half]), __uint_as_float(s[4 * kk + 2 * half + 1]));
-          const uint64_t dv = f32x2_pack(__uint_as_float(d[4 * kk + 2 * half]), __uint_as_float(d[4 * kk + 2 * half + 1]));
-          float a, e;
-          f32x2_unpack(f32x2_mul(f32x2_add(sv, nl), c2), a, e);
-          a = ex2_approx(a);
-          e = ex2_approx(e);
-          pw[2 * kk + half] = pack_bf16(a, e);
-          f32x2_unpack(f32x2_mul(f32x2_add(dv, nd), f32x2_pack(a, e)), a, e);
-          dw[2 * kk + half] = pack_bf16(a, e);
+          for (int k = 0; k < 4; ++k) mma_bf16(tmem + CRB_TM_D, a1 + 2 * k, b1 + 2 * k, idesc, k != 0);
+          mma_commit(s_full);
+          if (j + 1 == i.steps) mma_commit(&m_empty[slot]);
         }
+        __syncwarp();
+        ok = sums();
+        pn = n;
+        pc = c;
+        p_halves = halves;
+        p_first = j == 0;
+        p_last = j + 1 == i.steps;
+        t0 = next_t0(i, t0);
       }
-      tmem_st_16x128b_x8(s_tm, pw);
-      tmem_st_16x128b_x8(d_tm, dw);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar.p_full);
+      ++c;
     }
-    if (ok && steps > 0) {
-      ok = __all_sync(0xffffffffu, mbar_wait(bar.acc_done, 0, x.err, bar.abort_flag, 50));
-      tc_fence_after();
+    if (ok) sums();
+    if (elect_one()) {
+      mma_commit(mma_done);
+      mbar_drain(mma_done, 0);
     }
-    if (ok) {
-      const int row = k0 + lane_base + (lane >> 2);
-      const long long ld = static_cast<long long>(x.Hk) * CRA_HD;
-      const long long at = (static_cast<long long>(b) * x.Tk + row) * ld + hk * CRA_HD;
-      const long long extent = static_cast<long long>(x.batch) * x.Tk * ld;
-      cross_store_acc(tmem + lane_off + CRB_TM_ACC0, 1.0f, p.dv, at, ld, extent, row, kv_len, x.Tk, cq, steps > 0, x.err);
-      cross_store_acc(tmem + lane_off + CRB_TM_ACC1, x.scale, p.dk, at, ld, extent, row, kv_len, x.Tk, cq, steps > 0, x.err);
-    }
-  }
-
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, CRB_TM_COLS);
-}
-
-// q, do maps: boxes of 64 x 128 rows; k, v maps: boxes of 64 x 64 rows.
-__global__ void __launch_bounds__(CRA_THREADS, 2)
-    cross_dq_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap do_map,
-                    const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
-                    const __grid_constant__ CrossBwdParams p) {
-  using S = CrossBwdSmem;
-  constexpr uint32_t IDESC_S = make_idesc(128, CRB_STEP, 1u);
-  constexpr uint32_t IDESC_ACC = make_idesc(128, CRA_HD, 1u) | IDESC_B_MN;
-  const CrossParams& x = p.x;
-
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t base_u32 = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  uint8_t* smem = smem_raw + (base_u32 - smem_u32(smem_raw));
-  const CrossBwdBars bar = cross_bwd_bars(smem);
-  const int warp = warp_id();
-  const int lane = lane_id();
-  const int n_qt = (x.Tq + CRB_M - 1) / CRB_M;
-  const int qt = blockIdx.x % n_qt;
-  const int bh = blockIdx.x / n_qt;
-  const int b = bh / x.H, h = bh % x.H;
-  const int q0 = qt * CRB_M;
-
-  if (threadIdx.x == 0) cross_bwd_init(bar);
-  if (warp == 1) tmem_alloc(bar.tmem_slot, CRB_TM_COLS);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *bar.tmem_slot;
-  grid_dependency_wait();
-  grid_dependents_launch();
-
-  const int q_len = cross_len(x.q_lens, b, x.batch, x.Tq, x.err);
-  const int kv_len = cross_len(x.kv_lens, b, x.batch, x.Tk, x.err);
-  const int steps = q0 < q_len ? (kv_len + CRB_STEP - 1) / CRB_STEP : 0;
-
-  if (warp == 0) {
-    if (lane == 0 && steps > 0) {
-      const int hk = h / x.group, qb = b * x.q_items, db = b * p.do_items, kb = b * x.kv_items;
-      mbar_arrive_expect_tx(bar.m_full, 2 * S::M_BYTES);
-      tma_load_3d(smem + S::OFF_M0, &q_map, bar.m_full, h * CRA_HD, q0, qb);
-      tma_load_3d(smem + S::OFF_M1, &do_map, bar.m_full, h * CRA_HD, q0, db);
-      uint32_t issued = 0, par = 0;
-      bool ok = true;
-      for (int j = 0; j < steps; ++j) {
-        const int st = j % CRB_STAGES;
-        const uint32_t ph = (j / CRB_STAGES) & 1;
-        if (!mbar_wait(&bar.empty[st], ph ^ 1u, x.err, bar.abort_flag, 51)) { ok = false; break; }
-        mbar_arrive_expect_tx(&bar.full[st], 2 * S::STEP_BYTES);
-        uint8_t* dst = smem + S::OFF_STEP + st * 2 * S::STEP_BYTES;
-        tma_load_3d(dst, &k_map, &bar.full[st], hk * CRA_HD, j * CRB_STEP, kb);
-        tma_load_3d(dst + S::STEP_BYTES, &v_map, &bar.full[st], hk * CRA_HD, j * CRB_STEP, kb);
-        issued |= 1u << st;
-        par = (par & ~(1u << st)) | (ph << st);
-      }
-      if (!ok) {
-        mbar_drain(bar.m_full, 0);
-        for (int s = 0; s < CRB_STAGES; ++s)
-          if (issued & (1u << s)) mbar_drain(&bar.full[s], (par >> s) & 1u);
-      }
-    }
-  } else if (warp == 1) {
-    if (lane == 0 && steps > 0) {
-      const uint64_t q_desc = sw128_desc(smem_u32(smem + S::OFF_M0)), do_desc = sw128_desc(smem_u32(smem + S::OFF_M1));
-      const uint32_t step0 = smem_u32(smem + S::OFF_STEP);
-      bool ok = mbar_wait(bar.m_full, 0, x.err, bar.abort_flag, 52);
-      for (int j = 0; j < steps && ok; ++j) {
-        const int st = j % CRB_STAGES;
-        if (!mbar_wait(&bar.full[st], (j / CRB_STAGES) & 1, x.err, bar.abort_flag, 53)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t k_at = step0 + st * 2 * S::STEP_BYTES;
-        const uint64_t kd = sw128_desc(k_at), vd = sw128_desc(k_at + S::STEP_BYTES), kn = sw128_mn_desc(k_at, S::STEP_BYTES);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mma_bf16(tmem + CRB_TM_S, q_desc + 2 * k, kd + 2 * k, IDESC_S, k != 0);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mma_bf16(tmem + CRB_TM_D, do_desc + 2 * k, vd + 2 * k, IDESC_S, k != 0);
-        mma_commit(bar.s_full);
-        if (!mbar_wait(bar.p_full, j & 1, x.err, bar.abort_flag, 54)) { ok = false; break; }
-        tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_f16_tmem_a(tmem + CRB_TM_ACC0, tmem + CRB_TM_D + k * 8, kn + k * (2048 >> 4), IDESC_ACC, (j > 0 || k != 0) ? 1u : 0u);
-        mma_commit(&bar.empty[st]);
-      }
-      mma_commit(bar.acc_done);
-      mbar_drain(bar.acc_done, 0);
-    }
+    __syncwarp();
   } else {
+    const int half = (warp - 2) >> 3;                // this warp's 64 columns of a step
     const int quarter = warp & 3;
     const int sub = ((warp - 2) >> 2) & 1;
     const int lane_base = quarter * 32 + sub * 16;
     const uint32_t lane_off = static_cast<uint32_t>(lane_base) << 16;
-    const uint32_t s_tm = tmem + lane_off + CRB_TM_S, d_tm = tmem + lane_off + CRB_TM_D;
-    const int cq = 2 * (lane & 3);
-    const int row = q0 + lane_base + (lane >> 2);
+    const int t = lane & 3, cq = 2 * t;
+    const int ra = lane_base + (lane >> 2);          // this thread's own rows: ra and ra + 8
+    float* const b_part = reinterpret_cast<float*>(smem + S::OFF_B);
     const uint64_t c2 = f32x2_pack(x.c, x.c);
-    const long long si = (static_cast<long long>(b) * x.H + h) * p.stats_ld + row;   // rows up to the next 128 have an entry
-    float2 za = make_float2(INFINITY, 0.0f), zb = za;
-    if (steps > 0 && in_bounds(x.err, si, 9, static_cast<long long>(x.batch) * x.H * p.stats_ld, SITE_CROSS_STATS)) {
-      za = p.stats[si];
-      zb = p.stats[si + 8];
-    }
+    auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, x.err, abort_flag, site));
+    };
     bool ok = true;
-    for (int j = 0; j < steps && ok; ++j) {
-      const int st = j % CRB_STAGES;
-      if (!__all_sync(0xffffffffu, mbar_wait(bar.s_full, j & 1, x.err, bar.abort_flag, 55))) { ok = false; break; }
-      tc_fence_after();
-      uint32_t s[32], d[32];
-      tmem_ld_16x256b_x8(s_tm, s);
-      tmem_ld_16x256b_x8(d_tm, d);
-      tmem_ld_wait();
-      uint32_t dw[16];
+    int n = 0, c = 0;
+
+    // results of an item: DKV: the first half's warps store dv, the second's dk; else 32 columns of dq - b M each
+    auto finish = [&](const Item& i, int ci, float za, float zb) -> bool {
+      const bool any = i.steps > 0;
+      uint32_t v[32];
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
+      for (int k = 0; k < 32; ++k) v[k] = 0;
+      float ba = 0.0f, bb = 0.0f;
+      if (any) {
+        if (!DKV) {
+          if (!wait(b_full, ci & 1, 51)) return false;
+          const float* b_of = b_part + (ci & 1) * 2 * CRB_M;
+          ba = b_of[ra] + b_of[CRB_M + ra];
+          bb = b_of[ra + 8] + b_of[CRB_M + ra + 8];
+          const long long si = (static_cast<long long>(i.b) * x.H + i.h) * 2 * p.stats_ld + p.stats_ld + i.r0 + ra;
+          if (half == 0 && t < 2 && i.r0 + ra + 8 * t < i.own_len &&
+              in_bounds(x.err, si, 9, static_cast<long long>(x.batch) * x.H * 2 * p.stats_ld, SITE_CROSS_STATS))
+            p.stats[si + 8 * t] = t ? zb - bb : za - ba;         // -delta
+        }
+        if (!wait(acc_full, ci & 1, 52)) return false;
+        tc_fence_after();
+        const uint32_t acc = tmem + lane_off + CRB_TM_ACC;
+        if (DKV) {
+          tmem_ld_16x256b_x8(acc + half * CRA_HD, v);
+        } else if (p.want_dq) {
+          uint32_t m[16], d[16];
+          tmem_ld_16x256b_x4(acc + half * 32, m);
+          tmem_ld_16x256b_x4(acc + CRA_HD + half * 32, d);
+          tmem_ld_wait();
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const float2 z = half ? zb : za;
-          const uint64_t sv = f32x2_pack(__uint_as_float(s[4 * kk + 2 * half]), __uint_as_float(s[4 * kk + 2 * half + 1]));
-          const uint64_t dv = f32x2_pack(__uint_as_float(d[4 * kk + 2 * half]), __uint_as_float(d[4 * kk + 2 * half + 1]));
-          float a, e;
-          f32x2_unpack(f32x2_mul(f32x2_add(sv, f32x2_pack(-z.x, -z.x)), c2), a, e);
-          a = ex2_approx(a);
-          e = ex2_approx(e);
-          f32x2_unpack(f32x2_mul(f32x2_add(dv, f32x2_pack(-z.y, -z.y)), f32x2_pack(a, e)), a, e);
-          dw[2 * kk + half] = pack_bf16(a, e);
+          for (int k = 0; k < 16; ++k)
+            v[k] = __float_as_uint(fmaf(-(k & 2 ? bb : ba), __uint_as_float(m[k]), __uint_as_float(d[k])));
+        }
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty);
+      }
+      if (!DKV && !p.want_dq) return true;
+      __nv_bfloat16* const dst = !DKV ? p.dq : half ? p.dk : p.dv;
+      const float k = DKV && half == 0 ? 1.0f : x.scale;
+      const long long ld = static_cast<long long>(heads) * CRA_HD;
+      const long long extent = static_cast<long long>(x.batch) * own_T * ld;
+#pragma unroll
+      for (int e8 = 0; e8 < 2; ++e8) {
+        const int r = i.r0 + ra + 8 * e8;
+        const bool there = any && r < i.own_len;
+#pragma unroll
+        for (int q = 0; q < (DKV ? 2 : 1); ++q) {
+          uint32_t w[4];
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const int e = 16 * q + 4 * kk + 2 * e8;
+            w[kk] = there ? pack_bf16(k * __uint_as_float(v[e]), k * __uint_as_float(v[e + 1])) : 0u;
+          }
+          const uint4 u = quad_transpose(w[0], w[1], w[2], w[3], t);
+          const long long o = (static_cast<long long>(i.b) * own_T + r) * ld + i.h * CRA_HD + 32 * (DKV ? q : half) + 8 * t;
+          if (r < own_T && in_bounds(x.err, o, 8, extent, SITE_CROSS_OUT)) *reinterpret_cast<uint4*>(dst + o) = u;
         }
       }
-      const int valid = kv_len - j * CRB_STEP;
-      if (valid < CRB_STEP) {
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t keep = (8 * kk + cq < valid ? 0xffffu : 0u) | (8 * kk + cq + 1 < valid ? 0xffff0000u : 0u);
-          dw[2 * kk] &= keep;
-          dw[2 * kk + 1] &= keep;
+      return true;
+    };
+
+    Item last;                                       // the item whose results are still to be stored
+    int last_c = -1;
+    float last_za = 0.0f, last_zb = 0.0f;
+    for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
+      const Item i = item_at(it);
+      if (i.steps == 0) {
+        ok = finish(i, 0, 0.0f, 0.0f);
+        continue;
+      }
+      float la = 0.0f, lb = 0.0f, za = 0.0f, zb = 0.0f;      // rows' -lse / scale and -delta
+      if (!DKV) {
+        const long long si = (static_cast<long long>(i.b) * x.H + i.h) * 2 * p.stats_ld + i.r0 + ra;   // every row of a tile has an entry
+        if (in_bounds(x.err, si, p.stats_ld + 9, static_cast<long long>(x.batch) * x.H * 2 * p.stats_ld, SITE_CROSS_STATS)) {
+          la = p.stats[si];
+          lb = p.stats[si + 8];
+          za = p.stats[si + p.stats_ld];
+          zb = p.stats[si + p.stats_ld + 8];
         }
-        if (j * CRB_STEP + valid < x.Tk) {       // K's rows behind the length: factors of those zeros
-          cross_clear_rows(smem + S::OFF_STEP + st * 2 * S::STEP_BYTES, valid);
+      }
+      uint64_t ba2 = 0, bb2 = 0;                     // this thread's share of b of the two rows
+      int t0 = 0;
+      for (int j = 0; j < i.steps; ++j, ++n) {
+        const int st = n % CRB_STAGES;
+        const int rows = i.step_len - t0;            // that take part, in this step
+        if (DKV || ragged(i, t0)) {                  // the statistics come with the step's tiles
+          if (!wait(&full[st], (n / CRB_STAGES) & 1, 53)) { ok = false; break; }
+        }
+        if (ragged(i, t0)) {
+          uint4* tile = reinterpret_cast<uint4*>(smem + S::OFF_STEP + st * 2 * S::TILE);
+          for (int k = rows * 8 + static_cast<int>(threadIdx.x) - 64; k < CRB_STEP * 8; k += 32 * CRB_WARPS)
+            tile[k] = tile[k + S::TILE / 16] = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(fixed);
         }
+        if (!wait(s_full, n & 1, 54)) { ok = false; break; }
+        tc_fence_after();
+        if (rows > 64 * half) {
+          // s[4k], s[4k+1]: own row ra, columns 8k + cq, + 1; s[4k+2], s[4k+3]: row ra + 8
+          const uint32_t s_tm = tmem + lane_off + (n & 1) * CRB_TM_S;
+          uint32_t s[32], d[32];
+          tmem_ld_16x256b_x8(s_tm + 64 * half, s);
+          tmem_ld_16x256b_x8(tmem + lane_off + CRB_TM_D + 64 * half, d);
+          tmem_ld_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(d_free);
+          if (!DKV && rows < 64 * half + 64) {
+            // keys that take no part: P = 0 from a score of -infinity, and dS = 0
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (64 * half + 8 * kk + cq + (e & 1) >= rows) s[4 * kk + e] = 0xff800000u;
+          }
+          const float2* stats = reinterpret_cast<const float2*>(smem + S::OFF_STATS + st * S::STATS_BYTES) + 32 * half + t;
+          uint32_t pw[16], dw[16];
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            uint64_t nl = 0, nd = 0;
+            if (DKV) {                               // of the step's rows 8k + cq and + 1
+              nl = *reinterpret_cast<const uint64_t*>(stats + 4 * kk);
+              nd = *reinterpret_cast<const uint64_t*>(stats + CRB_STEP / 2 + 4 * kk);
+            }
+#pragma unroll
+            for (int e8 = 0; e8 < 2; ++e8) {
+              if (!DKV) {
+                nl = e8 ? f32x2_pack(lb, lb) : f32x2_pack(la, la);
+                nd = e8 ? f32x2_pack(zb, zb) : f32x2_pack(za, za);
+              }
+              const uint64_t sv = f32x2_pack(__uint_as_float(s[4 * kk + 2 * e8]), __uint_as_float(s[4 * kk + 2 * e8 + 1]));
+              const uint64_t dv = f32x2_pack(__uint_as_float(d[4 * kk + 2 * e8]), __uint_as_float(d[4 * kk + 2 * e8 + 1]));
+              float a, e;
+              f32x2_unpack(f32x2_mul(f32x2_add(sv, nl), c2), a, e);
+              a = ex2_approx(a);
+              e = ex2_approx(e);
+              pw[2 * kk + e8] = pack_bf16(a, e);
+              const uint64_t ds = f32x2_mul(f32x2_add(dv, nd), f32x2_pack(a, e));
+              if (!DKV) {
+                if (e8) bb2 = f32x2_add(bb2, ds);
+                else ba2 = f32x2_add(ba2, ds);
+              }
+              f32x2_unpack(ds, a, e);
+              dw[2 * kk + e8] = pack_bf16(a, e);
+            }
+          }
+          // S of both halves is in registers once every warp has given dP back: P and dS go over it
+          if (!wait(d_free, n & 1, 55)) { ok = false; break; }
+          tc_fence_after();
+          tmem_st_16x128b_x8(s_tm + 32 * half, pw);
+          tmem_st_16x128b_x8(s_tm + 64 + 32 * half, dw);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+        } else {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(d_free);
+        }
+        if (lane == 0) mbar_arrive(&p_full[n & 1]);
+        if (last_c >= 0) {
+          if (!finish(last, last_c, last_za, last_zb)) { ok = false; break; }
+          last_c = -1;
+        }
+        t0 = next_t0(i, t0);
       }
-      tmem_st_16x128b_x8(d_tm, dw);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar.p_full);
+      if (!ok) break;
+      if (!DKV) {
+        // b of a row: four threads of this warp and four of the other half's
+        float ba, bb, y;
+        f32x2_unpack(ba2, ba, y);
+        ba += y;
+        f32x2_unpack(bb2, bb, y);
+        bb += y;
+        ba += __shfl_xor_sync(0xffffffffu, ba, 1);
+        bb += __shfl_xor_sync(0xffffffffu, bb, 1);
+        ba += __shfl_xor_sync(0xffffffffu, ba, 2);
+        bb += __shfl_xor_sync(0xffffffffu, bb, 2);
+        float* b_of = b_part + (c & 1) * 2 * CRB_M + half * CRB_M;
+        if (t == 0) {
+          b_of[ra] = ba;
+          b_of[ra + 8] = bb;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_full);
+      }
+      last = i;
+      last_c = c++;
+      last_za = za;
+      last_zb = zb;
     }
-    if (ok && steps > 0) {
-      ok = __all_sync(0xffffffffu, mbar_wait(bar.acc_done, 0, x.err, bar.abort_flag, 56));
-      tc_fence_after();
-    }
-    if (ok) {
-      const long long ld = static_cast<long long>(x.H) * CRA_HD;
-      const long long at = (static_cast<long long>(b) * x.Tq + row) * ld + h * CRA_HD;
-      cross_store_acc(tmem + lane_off + CRB_TM_ACC0, x.scale, p.dq, at, ld, static_cast<long long>(x.batch) * x.Tq * ld, row, q_len,
-                      x.Tq, cq, steps > 0, x.err);
-    }
+    if (ok && last_c >= 0) finish(last, last_c, last_za, last_zb);
   }
 
   tc_fence_before();
