@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(CRA_THREADS, 2)
   const int nkv = q0 < q_len ? (kv_len + CRA_BK - 1) / CRA_BK : 0;
 
   if (warp == 0) {
-    if (lane == 0 && nkv > 0) {
+    if (nkv > 0 && elect_one()) {
       tma_prefetch_desc(&q_map);
       tma_prefetch_desc(&k_map);
       tma_prefetch_desc(&v_map);
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(CRA_THREADS, 2)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && nkv > 0) {
+    if (nkv > 0 && elect_one()) {
       const uint64_t q_desc = sw128_desc(smem_u32(smem + S::OFF_Q));
       const uint64_t k_desc0 = sw128_desc(smem_u32(smem + S::OFF_K));
       const uint64_t v_desc0 = sw128_mn_desc(smem_u32(smem + S::OFF_V), S::KV_BYTES);

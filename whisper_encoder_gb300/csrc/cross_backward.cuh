@@ -34,7 +34,7 @@ namespace wb {
 constexpr int CRB_M = 128, CRB_STEP = 128;     // own rows of an item, rows of the other side a step
 constexpr int CRB_STAGES = 4;
 constexpr int CRB_GROUP_WARPS = 8, CRB_WARPS = 2 * CRB_GROUP_WARPS, CRB_THREADS = 64 + 32 * CRB_WARPS;
-// TMEM: S of even and odd steps (P and dS over it: 64 columns each), dP, the two accumulators
+// TMEM: S of even and odd steps (over each half of it that half's P and dS, 32 columns each), dP, the two accumulators
 constexpr uint32_t CRB_TM_S = 128, CRB_TM_D = 256, CRB_TM_ACC = 384, CRB_TM_COLS = 512;
 
 struct CrossBwdSmem {
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
   auto ragged = [&](const Item& i, int t0) { return t0 + CRB_STEP > i.step_len && i.step_len < step_T; };
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       int n = 0, c = 0;                      // steps, and items with steps, so far
       bool ok = true;
       for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
@@ -247,92 +247,81 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
       }
     }
   } else if (warp == 1) {
-    // the whole warp walks and waits; one lane issues
-    const uint32_t step_at = smem_u32(smem + S::OFF_STEP), own_at = smem_u32(smem);
-    constexpr uint32_t IDESC_ACC = make_idesc(128, CRA_HD, 1u) | IDESC_B_MN;
-    auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, x.err, abort_flag, site));
-    };
-    bool ok = true;
-    int n = 0, c = 0, fixes = 0;
-    // the step before, whose sums are issued behind the scores of this one
-    int pn = -1, pc = 0, p_halves = 0;
-    bool p_first = false, p_last = false;
-    auto sums = [&]() -> bool {
-      if (pn < 0) return true;
-      const int st = pn % CRB_STAGES;
-      if (!wait(&p_full[pn & 1], (pn >> 1) & 1, 45)) return false;
-      if (p_first && !wait(acc_empty, (pc & 1) ^ 1u, 46)) return false;
-      tc_fence_after();
-      const uint32_t t_at = step_at + st * 2 * S::TILE;
-      const uint64_t n0 = sw128_mn_desc(t_at, S::TILE), n1 = DKV ? sw128_mn_desc(t_at + S::TILE, S::TILE) : n0;
-      const uint32_t src = tmem + (pn & 1) * CRB_TM_S, acc = tmem + CRB_TM_ACC;
-      const bool want = DKV || p.want_dq;
-      if (elect_one()) {
-        if (want) {
+    if (elect_one()) {
+      const uint32_t step_at = smem_u32(smem + S::OFF_STEP), own_at = smem_u32(smem);
+      constexpr uint32_t IDESC_ACC = make_idesc(128, CRA_HD, 1u) | IDESC_B_MN;
+      auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) { return mbar_wait(bar, parity, x.err, abort_flag, site); };
+      bool ok = true;
+      int n = 0, c = 0, fixes = 0;
+      // the step before, whose sums are issued behind the scores of this one
+      int pn = -1, pc = 0, p_halves = 0;
+      bool p_first = false, p_last = false;
+      auto sums = [&]() -> bool {
+        if (pn < 0) return true;
+        const int st = pn % CRB_STAGES;
+        if (!wait(&p_full[pn & 1], (pn >> 1) & 1, 45)) return false;
+        if (p_first && !wait(acc_empty, (pc & 1) ^ 1u, 46)) return false;
+        tc_fence_after();
+        const uint32_t n0 = sw128_mn_desc_lo(step_at + st * 2 * S::TILE, S::TILE), n1 = DKV ? n0 + (S::TILE >> 4) : n0;
+        const uint32_t src = tmem + (pn & 1) * CRB_TM_S, acc = tmem + CRB_TM_ACC;
+        if (DKV || p.want_dq) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             if (k >= 4 && p_halves < 2) break;
-            mma_f16_tmem_a(acc, src + k * 8, n1 + k * (2048 >> 4), IDESC_ACC, !p_first || k != 0);
-            mma_f16_tmem_a(acc + CRA_HD, src + 64 + k * 8, n0 + k * (2048 >> 4), IDESC_ACC, !p_first || k != 0);
+            const uint32_t a = src + k / 4 * 64 + k % 4 * 8;
+            mma_f16_tmem_a_lo<IDESC_ACC>(acc, a, n1 + k * (2048 >> 4), !p_first || k != 0);
+            mma_f16_tmem_a_lo<IDESC_ACC>(acc + CRA_HD, a + 32, n0 + k * (2048 >> 4), !p_first || k != 0);
           }
         }
         mma_commit(&empty[st]);
         if (p_last) mma_commit(acc_full);
-      }
-      __syncwarp();
-      pn = -1;
-      return true;
-    };
-    for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
-      const Item i = item_at(it);
-      if (i.steps == 0) continue;
-      const int slot = c & 1;
-      const uint64_t a0 = sw128_desc(own_at + 2 * slot * S::TILE), a1 = sw128_desc(own_at + (2 * slot + 1) * S::TILE);
-      ok = wait(&m_full[slot], (c >> 1) & 1, 47);
-      int t0 = 0;
-      for (int j = 0; j < i.steps && ok; ++j, ++n) {
-        const int st = n % CRB_STAGES;
-        const int halves = i.step_len - t0 > 64 ? 2 : 1;
-        ok = wait(&full[st], (n / CRB_STAGES) & 1, 48);
-        if (ok && ragged(i, t0)) ok = sums() && wait(fixed, fixes++ & 1, 49);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t t_at = step_at + st * 2 * S::TILE;
-        const uint64_t b0 = sw128_desc(t_at), b1 = sw128_desc(t_at + S::TILE);
-        const uint32_t idesc = halves == 2 ? make_idesc(128, 128, 1u) : make_idesc(128, 64, 1u);
-        // the sums that read this S buffer were issued before, and run before
-        if (elect_one()) {
+        pn = -1;
+        return true;
+      };
+      for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
+        const Item i = item_at(it);
+        if (i.steps == 0) continue;
+        const int slot = c & 1;
+        const uint32_t a0 = sw128_desc_lo(own_at + 2 * slot * S::TILE), a1 = a0 + (S::TILE >> 4);
+        ok = wait(&m_full[slot], (c >> 1) & 1, 47);
+        int t0 = 0;
+        for (int j = 0; j < i.steps && ok; ++j, ++n) {
+          const int st = n % CRB_STAGES;
+          const int halves = i.step_len - t0 > 64 ? 2 : 1;
+          ok = wait(&full[st], (n / CRB_STAGES) & 1, 48);
+          // the sums before a ragged step go first: its tiles are cleared when the softmax comes to it
+          if (ok && ragged(i, t0)) ok = sums() && wait(fixed, fixes++ & 1, 49);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t b0 = sw128_desc_lo(step_at + st * 2 * S::TILE), b1 = b0 + (S::TILE >> 4);
+          auto scores = [&](uint32_t d, uint32_t a, uint32_t b) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_bf16(tmem + (n & 1) * CRB_TM_S, a0 + 2 * k, b0 + 2 * k, idesc, k != 0);
-        }
-        __syncwarp();
-        if (n > 0) ok = wait(d_free, (n - 1) & 1, 50);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mma_bf16(tmem + CRB_TM_D, a1 + 2 * k, b1 + 2 * k, idesc, k != 0);
+            for (int k = 0; k < 4; ++k)
+              if (halves == 2) mma_bf16_lo<make_idesc(128, 128, 1u)>(d, a + 2 * k, b + 2 * k, k != 0);
+              else mma_bf16_lo<make_idesc(128, 64, 1u)>(d, a + 2 * k, b + 2 * k, k != 0);
+          };
+          // the sums that read this S buffer were issued before, and run before
+          scores(tmem + (n & 1) * CRB_TM_S, a0, b0);
+          if (n > 0) ok = wait(d_free, (n - 1) & 1, 50);
+          if (!ok) break;
+          tc_fence_after();
+          scores(tmem + CRB_TM_D, a1, b1);
           mma_commit(s_full);
           if (j + 1 == i.steps) mma_commit(&m_empty[slot]);
+          ok = sums();
+          pn = n;
+          pc = c;
+          p_halves = halves;
+          p_first = j == 0;
+          p_last = j + 1 == i.steps;
+          t0 = next_t0(i, t0);
         }
-        __syncwarp();
-        ok = sums();
-        pn = n;
-        pc = c;
-        p_halves = halves;
-        p_first = j == 0;
-        p_last = j + 1 == i.steps;
-        t0 = next_t0(i, t0);
+        ++c;
       }
-      ++c;
-    }
-    if (ok) sums();
-    if (elect_one()) {
+      if (ok) sums();
       mma_commit(mma_done);
       mbar_drain(mma_done, 0);
     }
-    __syncwarp();
   } else {
     const int half = (warp - 2) >> 3;                // this warp's 64 columns of a step
     const int quarter = warp & 3;
@@ -497,11 +486,9 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
               dw[2 * kk + e8] = pack_bf16(a, e);
             }
           }
-          // S of both halves is in registers once every warp has given dP back: P and dS go over it
-          if (!wait(d_free, n & 1, 55)) { ok = false; break; }
-          tc_fence_after();
-          tmem_st_16x128b_x8(s_tm + 32 * half, pw);
-          tmem_st_16x128b_x8(s_tm + 64 + 32 * half, dw);
+          // over the 64 columns of S that this warp has read
+          tmem_st_16x128b_x8(s_tm + 64 * half, pw);
+          tmem_st_16x128b_x8(s_tm + 64 * half + 32, dw);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
