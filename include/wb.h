@@ -534,7 +534,8 @@ wb_status wb_clip_grad_norm(const void* const* grads, void* const* outs, const i
  * Whether a token is clipped is decided on the exact difference; sums run in float32 within a sequence and in float64 across,
  * in a fixed order.  0 <= clip_low <= 1, 0 <= clip_high <= 1e30, kl_weight finite; S up to 2^31, T up to 2^30, S T up to 2^40.
  * Pointers are aligned to their element, the workspace to 16 bytes.
- * WB_EINVAL for bad sizes, values or pointers, WB_EWORKSPACE for a missing, small or unaligned workspace. */
+ * WB_EINVAL for bad sizes, values or pointers, WB_EWORKSPACE for a missing, small or unaligned workspace (NULL where the
+ * query says 0: up to 128 sequences of 512 tokens). */
 size_t wb_policy_loss_workspace_bytes(int64_t S, int64_t T);
 wb_status wb_policy_loss(const float* nll, const float* old_nll, const float* ref_nll, const float* advantage,
                          int advantage_per_token, const int64_t* labels, int64_t S, int64_t T, double clip_low,

@@ -114,9 +114,12 @@ def test_policy_refusals(lib):
             assert f(**{name: value}) == L.WB_EINVAL, (f, name, value)
         assert f(S=1 << 31, T=1 << 30) == L.WB_EINVAL
     assert fwd(stats=None) == L.WB_EINVAL and fwd(stats=ODD) == L.WB_EINVAL
-    assert fwd(ws=None) == L.WB_EWORKSPACE and fwd(ws=ODD) == L.WB_EWORKSPACE
-    need = lib.wb_policy_loss_workspace_bytes(4, 8)
-    assert need > 0 and fwd(n=need - 1) == L.WB_EWORKSPACE
+    # one block's sizes need no workspace
+    assert lib.wb_policy_loss_workspace_bytes(128, 512) == 0
+    for S, T in ((129, 1), (1, 513), (4096, 448)):
+        need = lib.wb_policy_loss_workspace_bytes(S, T)
+        assert need > 0 and fwd(S=S, T=T, n=need - 1) == L.WB_EWORKSPACE
+        assert fwd(S=S, T=T, ws=None) == L.WB_EWORKSPACE and fwd(S=S, T=T, ws=ODD) == L.WB_EWORKSPACE
     assert lib.wb_policy_loss_workspace_bytes(0, 8) == 0 and lib.wb_policy_loss_workspace_bytes(4, 0) == 0
     for name in ("dloss", "dnll"):
         assert bwd(**{name: None}) == L.WB_EINVAL and bwd(**{name: ODD}) == L.WB_EINVAL

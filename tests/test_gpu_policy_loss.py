@@ -75,7 +75,8 @@ def _check(got, ref, labels, dl=1.5):
     assert float(over.max()) <= 0, float(over.max())
 
 
-SHAPES = [(1, 1), (1, 5), (3, 33), (8, 77), (5, 512), (5, 513), (9, 1025), (3, 2049), (2, 5000), (100, 448), (1300, 31), (10000, 7)]
+# up to 128 sequences of 512 tokens are one block's; a sequence has one to eight warps
+SHAPES = [(1, 1), (1, 5), (3, 33), (128, 512), (128, 300), (129, 512), (40, 9), (8, 77), (5, 512), (5, 513), (9, 1025), (3, 2049), (2, 5000), (100, 448), (1300, 31), (10000, 7)]
 
 
 @pytest.mark.parametrize("S,T", SHAPES)

@@ -459,30 +459,33 @@ def linear_distill_backward(dloss, x, w, top, index, lse, temperature: float = 1
     return dx, dw
 
 
-def _attn_rows(t, name, like=None):
-    """A bf16 [batch, T, heads * 64] tensor whose rows are contiguous: (batch, T, heads)."""
+def _attn_rows(t, name):
+    """A bf16 [batch, T, heads * 64] tensor whose rows are contiguous: its shape and strides."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 3:
         raise ValueError(f"{name}: expected a CUDA bfloat16 tensor [batch, T, heads * 64]")
-    batch, T, d = t.shape
-    if d == 0 or d % 64 or t.stride(2) != 1:
-        raise ValueError(f"{name}: expected rows of whole heads (64 elements each, contiguous), got {tuple(t.shape)}, strides {t.stride()}")
-    if like is not None and t.shape != like.shape:
-        raise ValueError(f"{name}: expected shape {tuple(like.shape)}, got {tuple(t.shape)}")
-    return batch, T, d // 64
+    shape, stride = t.shape, t.stride()
+    if shape[2] == 0 or shape[2] % 64 or stride[2] != 1:
+        raise ValueError(f"{name}: expected rows of whole heads (64 elements each, contiguous), got {tuple(shape)}, strides {stride}")
+    return shape, stride
 
 
 def _attn_shape(q, k, v, q_lens, kv_lens):
-    batch, Tq, H = _attn_rows(q, "q")
-    kv_batch, Tk, Hk = _attn_rows(k, "k")
-    _attn_rows(v, "v", k)
-    if kv_batch != batch or H % Hk:
-        raise ValueError(f"q and k: expected the same batch and whole groups of heads, got {tuple(q.shape)} and {tuple(k.shape)}")
-    if max(Tq, Tk) > 1 << 24 or H > 1024:
+    """(batch, Tq, Tk, H, Hk) and the strides that the C calls take for q, k and v."""
+    (batch, Tq, d), qs = _attn_rows(q, "q")
+    k_shape, ks = _attn_rows(k, "k")
+    v_shape, vs = _attn_rows(v, "v")
+    kv_batch, Tk, dk = k_shape
+    if v_shape != k_shape:
+        raise ValueError(f"v: expected shape {tuple(k_shape)}, got {tuple(v_shape)}")
+    if kv_batch != batch or d % dk:
+        raise ValueError(f"q and k: expected the same batch and whole groups of heads, got {tuple(q.shape)} and {tuple(k_shape)}")
+    if Tq > 1 << 24 or Tk > 1 << 24 or d > 65536:
         raise ValueError("q and k: at most 2^24 rows of 1024 heads")
-    for t, name in ((q_lens, "q_lens"), (kv_lens, "kv_lens")):
-        if t is not None:
-            _need_shape(t, torch.int32, (batch,), name)
-    return batch, Tq, Tk, H, Hk
+    if q_lens is not None:
+        _need_shape(q_lens, torch.int32, (batch,), "q_lens")
+    if kv_lens is not None:
+        _need_shape(kv_lens, torch.int32, (batch,), "kv_lens")
+    return batch, Tq, Tk, d // 64, dk // 64, qs, ks, vs
 
 
 def cross_attention(q, k, v, scale: float = 0.125, q_lens=None, kv_lens=None, stream=None):
@@ -493,12 +496,13 @@ def cross_attention(q, k, v, scale: float = 0.125, q_lens=None, kv_lens=None, st
     item.  q_lens, kv_lens: int32 [batch] on the device, how many rows and keys of an item take part (default: all);
     a row without keys or past q_lens gives out 0 and lse -inf.  Not recorded by autograd: gradients come from
     cross_attention_backward."""
-    batch, Tq, Tk, H, Hk = _attn_shape(q, k, v, q_lens, kv_lens)
+    batch, Tq, Tk, H, Hk, qs, ks, vs = _attn_shape(q, k, v, q_lens, kv_lens)
     with _place(stream, q, k, v, q_lens, kv_lens):
-        out = torch.empty((batch, Tq, 64 * H), dtype=torch.bfloat16, device=q.device)
-        lse = torch.empty((batch, H, Tq), dtype=torch.float32, device=q.device)
-        call("wb_cross_attention", _a(q), q.stride(0), q.stride(1), _a(k), k.stride(0), k.stride(1), _a(v), v.stride(0), v.stride(1),
-             _a(q_lens), _a(kv_lens), batch, Tq, Tk, H, Hk, scale, _a(out), _a(lse), _raw_stream(q))
+        device = q.device
+        out = torch.empty((batch, Tq, 64 * H), dtype=torch.bfloat16, device=device)
+        lse = torch.empty((batch, H, Tq), dtype=torch.float32, device=device)
+        call("wb_cross_attention", q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], _a(q_lens),
+             _a(kv_lens), batch, Tq, Tk, H, Hk, scale, out.data_ptr(), lse.data_ptr(), _raw_stream(q))
     return out, lse
 
 
@@ -509,8 +513,10 @@ def cross_attention_backward(dout, q, k, v, out, lse, scale: float = 0.125, q_le
     dout as q (strides free).  dq like q, dk and dv like k, contiguous; the rows of all heads that share a key head are summed.
     workspace, if given: uint8, as many bytes as load().wb_cross_attention_backward_workspace_bytes(batch, Tq, H) says, for
     one call at a time."""
-    batch, Tq, Tk, H, Hk = _attn_shape(q, k, v, q_lens, kv_lens)
-    _attn_rows(dout, "dout", q)
+    batch, Tq, Tk, H, Hk, qs, ks, vs = _attn_shape(q, k, v, q_lens, kv_lens)
+    do_shape, ds = _attn_rows(dout, "dout")
+    if do_shape != q.shape:
+        raise ValueError(f"dout: expected shape {tuple(q.shape)}, got {tuple(do_shape)}")
     _need_shape(out, torch.bfloat16, q.shape, "out")
     _need_shape(lse, torch.float32, (batch, H, Tq), "lse")
     with _place(stream, q, k, v, dout, out, lse, q_lens, kv_lens, workspace):
@@ -518,9 +524,9 @@ def cross_attention_backward(dout, q, k, v, out, lse, scale: float = 0.125, q_le
         dk = torch.empty((batch, Tk, 64 * Hk), dtype=torch.bfloat16, device=q.device) if need_dkv else None
         dv = torch.empty_like(dk) if need_dkv else None
         ws = _head_workspace(workspace, "wb_cross_attention_backward_workspace_bytes", q.device, batch, Tq, H)
-        call("wb_cross_attention_backward", _a(dout), dout.stride(0), dout.stride(1), _a(q), q.stride(0), q.stride(1), _a(k), k.stride(0),
-             k.stride(1), _a(v), v.stride(0), v.stride(1), _a(out), _a(lse), _a(q_lens), _a(kv_lens), batch, Tq, Tk, H, Hk, scale,
-             _a(dq), _a(dk), _a(dv), _a(ws), ws.numel(), _raw_stream(q))
+        call("wb_cross_attention_backward", dout.data_ptr(), ds[0], ds[1], q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1],
+             v.data_ptr(), vs[0], vs[1], out.data_ptr(), lse.data_ptr(), _a(q_lens), _a(kv_lens), batch, Tq, Tk, H, Hk, scale, _a(dq),
+             _a(dk), _a(dv), ws.data_ptr(), ws.numel(), _raw_stream(q))
     return dq, dk, dv
 
 
@@ -627,9 +633,13 @@ def policy_loss(nll, old_nll, advantage, labels, ref_nll=None, clip_low: float =
     with _place(stream, nll, old_nll, advantage, labels, ref_nll, workspace):
         stats = torch.empty(3, dtype=torch.float32, device=nll.device)
         weight = torch.empty(S, dtype=torch.float32, device=nll.device)
-        ws = _head_workspace(workspace, "wb_policy_loss_workspace_bytes", nll.device, S, T)
+        n = load().wb_policy_loss_workspace_bytes(S, T)
+        ws = None
+        if n:
+            ws = _workspace(n, nll.device) if workspace is None else workspace
+            _need(ws, torch.uint8, "workspace")
         call("wb_policy_loss", _a(nll), _a(old_nll), _a(ref_nll), _a(advantage), per_token, _a(labels), S, T, clip_low, clip_high,
-             kl_weight, 1 if per_sequence else 0, _a(stats), _a(weight), _a(ws), ws.numel(), _raw_stream(nll))
+             kl_weight, 1 if per_sequence else 0, _a(stats), _a(weight), _a(ws), ws.numel() if n else 0, _raw_stream(nll))
     return stats, weight
 
 

@@ -7,15 +7,19 @@
 // and the loss is sum w l with w = 1 / N over the N tokens that take part, or 1 / (B n_b): the mean over the B
 // sequences that have tokens of the means over their n_b tokens.
 //
-// Bound by memory (20 bytes a token forward, 24 backward), below a million tokens by the two launches' latency.
+// Bound by memory (16 bytes a token forward, 20 backward, 4 more with a reference), below a million tokens by the launches.
 // Forward: a team of 1 to 8 warps of a block takes a sequence; a block leaves one partial row, and a second kernel joins those
-// in order, in every one of its blocks, and turns counts into weights.  No atomics: the same call gives the same bits.
+// in order, in every one of its blocks, and turns counts into weights.  Up to 128 sequences of 512 tokens are one block's, in
+// one launch (8 x 77 tokens: 5.8 us against 8.2 with two).  No atomics: the same call gives the same bits.
+// 16001 x 448 tokens forward 34 us, 3.4 TB/s: the loads of a warp's next sequence wait for the sums of the last, and with 4 blocks an SM
+// (64 registers; 3 blocks 43 us, 6 with half the loads each 36) there are not enough others.  Backward, without sums, 23 us, 6.2 TB/s.
 //
 // Numbers.  Whether a token is clipped is decided on d against log1p(hi) and log1p(-lo), both as unevaluated sums of
 // two float32 (the rounding of a difference is exact in float32): one rounding near the border would turn a
 // whole gradient on or off.  e^x - x - 1 is x^2 / 2 for small x: below 1/2 its series, above it the
 // difference of expm1, which loses two bits at most.  An advantage of zero gives zero, whatever e^d is.
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/wb.h"
 #include "internal.h"
@@ -25,8 +29,10 @@ namespace wb {
 namespace {
 
 constexpr int POL_THREADS = 256, POL_WARPS = POL_THREADS / 32;
-constexpr int POL_MAX_BLOCKS = 1216;      // 8 on each SM
-constexpr int POL_TILE = 4;               // tokens of a thread and step
+constexpr int POL_MAX_BLOCKS = 608;       // 4 on each SM
+constexpr int POL_TILE = 4;               // tokens of a thread and step, backward
+constexpr int POL_SUM_TILE = 8;           // forward: its loads in flight
+constexpr int POL_SMALL_S = 128, POL_SMALL_T = 512, POL_SMALL_THREADS = 1024;
 
 struct PolicyArgs {
   const float* nll;
@@ -60,25 +66,26 @@ __device__ __forceinline__ float exp_minus_x_minus_1(float x, float em1) {
   return fabsf(x) < 0.5f ? 0.5f * x * x * p : em1 - x;
 }
 
+template <bool REF>
 __device__ __forceinline__ Token policy_token(const PolicyArgs& a, float nll, float old_nll, float ref, float adv) {
   Token t;
   const float d = old_nll - nll;
   const float bb = d - old_nll;
   const float e = (old_nll - (d - bb)) - (nll + bb);     // d + e is the difference itself
-  const bool above = d > a.hi0 || (d == a.hi0 && e > a.hi1);
-  const bool below = d < a.lo0 || (d == a.lo0 && e < a.lo1);
-  t.clipped = (adv > 0.0f && above) || (adv < 0.0f && below);
+  const bool above = (d > a.hi0) | ((d == a.hi0) & (e > a.hi1));
+  const bool below = (d < a.lo0) | ((d == a.lo0) & (e < a.lo1));
+  t.clipped = ((adv > 0.0f) & above) | ((adv < 0.0f) & below);
   const float ra = adv == 0.0f ? 0.0f : expf(d) * adv;
   t.loss = t.clipped ? -(adv > 0.0f ? a.hold_hi : a.hold_lo) * adv : -ra;
   t.grad = t.clipped ? 0.0f : ra;
   t.kl = 0.0f;
-  if (a.ref_nll) {
+  if (REF) {
     const float x = nll - ref;
     const float em1 = expm1f(x);
     t.kl = exp_minus_x_minus_1(x, em1);
-    if (a.beta != 0.0f) {
-      t.loss += a.beta * t.kl;
-      t.grad += a.beta * em1;
+    if (a.beta != 0.0f) {                                // a weight of zero leaves a KL of infinity out
+      t.loss = fmaf(a.beta, t.kl, t.loss);
+      t.grad = fmaf(a.beta, em1, t.grad);
     }
   }
   return t;
@@ -97,148 +104,231 @@ struct PolicyPart {
   long long tokens, seqs;
 };
 
+struct SeqSum {
+  float loss, kl;
+  int clipped, count;
+};
+
+// This warp's share of a sequence, in every lane: warp `part` of W.  No branches among the tokens of a step: they overlap.
+template <int W, bool REF>
+__device__ __forceinline__ SeqSum policy_sequence(const PolicyArgs& a, long long s, int part) {
+  SeqSum r = {0.0f, 0.0f, 0, 0};
+  const long long base = s * a.T, n_el = a.S * a.T;
+  const float adv_s = a.adv_tok == 0 && in_bounds(a.err, s, 1, a.S, SITE_POLICY_IN) ? a.adv[s] : 0.0f;
+  const int T = static_cast<int>(a.T);
+  for (int t0 = part * 32 + static_cast<int>(lane_id()); t0 < T; t0 += W * 32 * POL_SUM_TILE) {
+    const long long at = base + t0;
+    bool on[POL_SUM_TILE];
+    float nll[POL_SUM_TILE], old[POL_SUM_TILE], ref[POL_SUM_TILE], adv[POL_SUM_TILE];
+#pragma unroll
+    for (int i = 0; i < POL_SUM_TILE; ++i) {
+      on[i] = false;
+      nll[i] = old[i] = ref[i] = 0.0f;
+      adv[i] = adv_s;
+      if (i * W * 32 < T - t0 && in_bounds(a.err, at + i * W * 32, 1, n_el, SITE_POLICY_IN)) {
+        on[i] = a.labels[at + i * W * 32] >= 0;
+        nll[i] = a.nll[at + i * W * 32];
+        old[i] = a.old_nll[at + i * W * 32];
+        if (REF) ref[i] = a.ref_nll[at + i * W * 32];
+        if (a.adv_tok) adv[i] = a.adv[at + i * W * 32];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < POL_SUM_TILE; ++i) {
+      const Token k = policy_token<REF>(a, nll[i], old[i], ref[i], adv[i]);
+      r.loss += on[i] ? k.loss : 0.0f;
+      if (REF) r.kl += on[i] ? k.kl : 0.0f;
+      r.clipped += on[i] & k.clipped;
+      r.count += on[i];
+    }
+  }
+  r.loss = warp_sum(r.loss);
+  if (REF) r.kl = warp_sum(r.kl);
+  r.clipped = __reduce_add_sync(0xffffffffu, r.clipped);
+  r.count = __reduce_add_sync(0xffffffffu, r.count);
+  return r;
+}
+
+// A running sum and what its roundings left: float64 units are so few that a sequence's nine operations in one lane, 16 cycles each,
+// were half of the forward pass over 16001 sequences.
+struct Sum2 {
+  float s = 0.0f, c = 0.0f;
+  __device__ __forceinline__ void add(float v) {
+    const float t = s + v, b = t - s;
+    c += (s - (t - b)) + (v - b);
+    s = t;
+  }
+  __device__ __forceinline__ double value() const { return static_cast<double>(s) + static_cast<double>(c); }
+};
+// Sequences of one warp: sums of loss, KL and clipped tokens, weighted for per_sequence.
+struct PolicySum {
+  Sum2 loss, kl, clipped;
+  long long tokens = 0, seqs = 0;
+  __device__ __forceinline__ void add(const SeqSum& r, int per_sequence) {
+    if (r.count == 0) return;
+    const float n = static_cast<float>(r.count);
+    loss.add(per_sequence ? r.loss / n : r.loss);
+    kl.add(per_sequence ? r.kl / n : r.kl);
+    clipped.add(per_sequence ? static_cast<float>(r.clipped) / n : static_cast<float>(r.clipped));
+    tokens += r.count;
+    seqs += 1;
+  }
+  __device__ __forceinline__ PolicyPart part() const { return PolicyPart{loss.value(), kl.value(), clipped.value(), tokens, seqs}; }
+};
+__device__ __forceinline__ void policy_join(PolicyPart& sum, const PolicyPart& p) {
+  sum.loss += p.loss;
+  sum.kl += p.kl;
+  sum.clipped += p.clipped;
+  sum.tokens += p.tokens;
+  sum.seqs += p.seqs;
+}
+// The 32 lanes' rows, in every lane.
+__device__ __forceinline__ PolicyPart policy_warp_join(PolicyPart p) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    PolicyPart q;
+    q.loss = __shfl_xor_sync(0xffffffffu, p.loss, o);
+    q.kl = __shfl_xor_sync(0xffffffffu, p.kl, o);
+    q.clipped = __shfl_xor_sync(0xffffffffu, p.clipped, o);
+    q.tokens = __shfl_xor_sync(0xffffffffu, p.tokens, o);
+    q.seqs = __shfl_xor_sync(0xffffffffu, p.seqs, o);
+    policy_join(p, q);
+  }
+  return p;
+}
+__device__ __forceinline__ float policy_weight(int count, int per_sequence, double f) {
+  return count == 0 ? 0.0f : static_cast<float>(per_sequence ? f / count : f);
+}
+
 // W warps a sequence.
-template <int W>
-__global__ void __launch_bounds__(POL_THREADS) policy_sum_kernel(const __grid_constant__ PolicyArgs a, int* counts,
+template <int W, bool REF>
+__global__ void __launch_bounds__(POL_THREADS, 4) policy_sum_kernel(const __grid_constant__ PolicyArgs a, int* counts,
                                                                  PolicyPart* part, int parts) {
   constexpr int TEAMS = POL_WARPS / W;
-  __shared__ float red[POL_WARPS][4];
+  __shared__ SeqSum red[POL_WARPS];
   __shared__ PolicyPart join[TEAMS];
   const int lane = lane_id(), warp = warp_id(), team = warp / W, in_team = warp % W;
   grid_dependency_wait();
   grid_dependents_launch();
-  PolicyPart sum = {0.0, 0.0, 0.0, 0, 0};
-  const long long n_el = a.S * a.T;
+  PolicySum sum;
   // all teams of a block make the same number of rounds: there are barriers inside
   for (long long s0 = static_cast<long long>(blockIdx.x) * TEAMS; s0 < a.S; s0 += static_cast<long long>(gridDim.x) * TEAMS) {
     const long long s = s0 + team;
-    float loss = 0.0f, kl = 0.0f;
-    int clipped = 0, count = 0;
-    if (s < a.S) {
-      const long long base = s * a.T;
-      const float adv_s = a.adv_tok == 0 && in_bounds(a.err, s, 1, a.S, SITE_POLICY_IN) ? a.adv[s] : 0.0f;
-      for (long long t0 = in_team * 32 + lane; t0 < a.T; t0 += W * 32 * POL_TILE) {
-        int64_t lab[POL_TILE];
-        float nll[POL_TILE], old[POL_TILE], ref[POL_TILE], adv[POL_TILE];
-#pragma unroll
-        for (int i = 0; i < POL_TILE; ++i) {
-          const long long t = t0 + i * W * 32;
-          lab[i] = -1;
-          nll[i] = old[i] = ref[i] = 0.0f;
-          adv[i] = adv_s;
-          if (t < a.T && in_bounds(a.err, base + t, 1, n_el, SITE_POLICY_IN)) {
-            lab[i] = a.labels[base + t];
-            nll[i] = a.nll[base + t];
-            old[i] = a.old_nll[base + t];
-            if (a.ref_nll) ref[i] = a.ref_nll[base + t];
-            if (a.adv_tok) adv[i] = a.adv[base + t];
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < POL_TILE; ++i) {
-          if (lab[i] < 0) continue;
-          const Token k = policy_token(a, nll[i], old[i], ref[i], adv[i]);
-          loss += k.loss;
-          kl += k.kl;
-          clipped += k.clipped;
-          ++count;
-        }
-      }
-    }
-    loss = warp_sum(loss);
-    kl = warp_sum(kl);
-    clipped = __reduce_add_sync(0xffffffffu, clipped);
-    count = __reduce_add_sync(0xffffffffu, count);
+    SeqSum r = {0.0f, 0.0f, 0, 0};
+    if (s < a.S) r = policy_sequence<W, REF>(a, s, in_team);
     if (W > 1) {
-      if (lane == 0) {
-        red[warp][0] = loss;
-        red[warp][1] = kl;
-        red[warp][2] = __int_as_float(clipped);
-        red[warp][3] = __int_as_float(count);
-      }
+      if (lane == 0) red[warp] = r;
       __syncthreads();
-      loss = kl = 0.0f;
-      clipped = count = 0;
+      r = red[team * W];
 #pragma unroll
-      for (int i = 0; i < W; ++i) {
-        loss += red[team * W + i][0];
-        kl += red[team * W + i][1];
-        clipped += __float_as_int(red[team * W + i][2]);
-        count += __float_as_int(red[team * W + i][3]);
+      for (int i = 1; i < W; ++i) {
+        r.loss += red[team * W + i].loss;
+        r.kl += red[team * W + i].kl;
+        r.clipped += red[team * W + i].clipped;
+        r.count += red[team * W + i].count;
       }
       __syncthreads();
     }
     if (in_team == 0 && lane == 0 && s < a.S) {
-      if (in_bounds(a.err, s, 1, a.S, SITE_POLICY_OUT)) counts[s] = count;
-      if (count > 0) {
-        const double f = a.per_sequence ? 1.0 / count : 1.0;
-        sum.loss += loss * f;
-        sum.kl += kl * f;
-        sum.clipped += clipped * f;
-        sum.tokens += count;
-        sum.seqs += 1;
-      }
+      if (in_bounds(a.err, s, 1, a.S, SITE_POLICY_OUT)) counts[s] = r.count;
+      sum.add(r, a.per_sequence);
     }
   }
-  if (in_team == 0 && lane == 0) join[team] = sum;
+  if (in_team == 0 && lane == 0) join[team] = sum.part();
   __syncthreads();
   if (threadIdx.x == 0 && in_bounds(a.err, blockIdx.x, 1, parts, SITE_POLICY_OUT)) {
-    for (int i = 1; i < TEAMS; ++i) {
-      sum.loss += join[i].loss;
-      sum.kl += join[i].kl;
-      sum.clipped += join[i].clipped;
-      sum.tokens += join[i].tokens;
-      sum.seqs += join[i].seqs;
-    }
-    part[blockIdx.x] = sum;
+    PolicyPart all = join[0];
+    for (int i = 1; i < TEAMS; ++i) policy_join(all, join[i]);
+    part[blockIdx.x] = all;
   }
 }
 
-template <typename V>
-__device__ __forceinline__ V pol_block_sum(V v) {
-  __shared__ V red[POL_WARPS];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+// All of it in one block: a warp takes every 32nd sequence.
+template <bool REF>
+__global__ void __launch_bounds__(POL_SMALL_THREADS) policy_small_kernel(const __grid_constant__ PolicyArgs a, float* stats,
+                                                                         float* weight) {
+  constexpr int WARPS = POL_SMALL_THREADS / 32;
+  __shared__ PolicyPart join[WARPS];
+  __shared__ int counts[POL_SMALL_S];
+  __shared__ double factor;
+  const int lane = lane_id(), warp = warp_id();
+  grid_dependency_wait();
+  grid_dependents_launch();
+  PolicySum sum;
+  for (int s = warp; s < a.S; s += WARPS) {
+    const SeqSum r = policy_sequence<1, REF>(a, s, 0);
+    if (lane == 0) {
+      counts[s] = r.count;
+      sum.add(r, a.per_sequence);
+    }
+  }
+  if (lane == 0) join[warp] = sum.part();
   __syncthreads();
-  if (lane_id() == 0) red[warp_id()] = v;
+  if (warp == 0) {
+    static_assert(WARPS == 32, "a row for each lane");
+    const PolicyPart all = policy_warp_join(join[lane]);
+    const long long n = a.per_sequence ? all.seqs : all.tokens;
+    const double f = n > 0 ? 1.0 / static_cast<double>(n) : 0.0;
+    if (lane == 0) {
+      factor = f;
+      stats[0] = static_cast<float>(all.loss * f);
+      stats[1] = static_cast<float>(all.kl * f);
+      stats[2] = static_cast<float>(all.clipped * f);
+    }
+  }
   __syncthreads();
-  v = 0;
-#pragma unroll
-  for (int i = 0; i < POL_WARPS; ++i) v += red[i];
-  return v;
+  const int s = threadIdx.x;
+  if (s < a.S && in_bounds(a.err, s, 1, a.S, SITE_POLICY_OUT)) weight[s] = policy_weight(counts[s], a.per_sequence, factor);
 }
 
-// stats = (loss, mean KL, share of clipped tokens); weight of each sequence's tokens.
+// stats = (loss, mean KL, share of clipped tokens); weight of each sequence's tokens.  The weights need the counts alone: only the first
+// block adds the float64 sums.
 __global__ void __launch_bounds__(POL_THREADS) policy_join_kernel(const PolicyPart* part, int parts, const int* counts, long long S,
                                                                   int per_sequence, float* stats, float* weight, uint32_t* err) {
+  __shared__ PolicyPart join[POL_WARPS];
   grid_dependency_wait();
   grid_dependents_launch();
   PolicyPart sum = {0.0, 0.0, 0.0, 0, 0};
-  for (int i = threadIdx.x; i < parts; i += POL_THREADS) {
-    const PolicyPart p = part[i];
-    sum.loss += p.loss;
-    sum.kl += p.kl;
-    sum.clipped += p.clipped;
-    sum.tokens += p.tokens;
-    sum.seqs += p.seqs;
-  }
-  const long long n = pol_block_sum(per_sequence ? sum.seqs : sum.tokens);
-  const double f = n > 0 ? 1.0 / static_cast<double>(n) : 0.0;
-  if (blockIdx.x == 0) {
-    const double loss = pol_block_sum(sum.loss), kl = pol_block_sum(sum.kl), clipped = pol_block_sum(sum.clipped);
-    if (threadIdx.x == 0) {
-      stats[0] = static_cast<float>(loss * f);
-      stats[1] = static_cast<float>(kl * f);
-      stats[2] = static_cast<float>(clipped * f);
+#pragma unroll
+  for (int k = 0; k < (POL_MAX_BLOCKS + POL_THREADS - 1) / POL_THREADS; ++k) {
+    const int i = threadIdx.x + k * POL_THREADS;
+    if (i >= parts) break;
+    if (blockIdx.x == 0) {
+      policy_join(sum, part[i]);
+    } else {
+      sum.tokens += part[i].tokens;
+      sum.seqs += part[i].seqs;
     }
+  }
+  if (blockIdx.x == 0) {
+    sum = policy_warp_join(sum);
+  } else {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      sum.tokens += __shfl_xor_sync(0xffffffffu, sum.tokens, o);
+      sum.seqs += __shfl_xor_sync(0xffffffffu, sum.seqs, o);
+    }
+  }
+  if (lane_id() == 0) join[warp_id()] = sum;
+  __syncthreads();
+  long long n = 0;
+#pragma unroll
+  for (int i = 0; i < POL_WARPS; ++i) n += per_sequence ? join[i].seqs : join[i].tokens;
+  const double f = n > 0 ? 1.0 / static_cast<double>(n) : 0.0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    sum = join[0];
+    for (int i = 1; i < POL_WARPS; ++i) policy_join(sum, join[i]);
+    stats[0] = static_cast<float>(sum.loss * f);
+    stats[1] = static_cast<float>(sum.kl * f);
+    stats[2] = static_cast<float>(sum.clipped * f);
   }
   const long long s = static_cast<long long>(blockIdx.x) * POL_THREADS + threadIdx.x;
   if (s < S && in_bounds(err, s, 1, S, SITE_POLICY_OUT)) {
-    const int c = counts[s];
-    weight[s] = c == 0 ? 0.0f : static_cast<float>(per_sequence ? f / c : f);
+    weight[s] = policy_weight(counts[s], per_sequence, f);
   }
 }
 
+template <bool REF>
 __global__ void __launch_bounds__(POL_THREADS) policy_grad_kernel(const __grid_constant__ PolicyArgs a, const float* dloss,
                                                                   const float* weight, float* dnll) {
   grid_dependency_wait();
@@ -260,7 +350,7 @@ __global__ void __launch_bounds__(POL_THREADS) policy_grad_kernel(const __grid_c
         lab[i] = a.labels[t];
         nll[i] = a.nll[t];
         old[i] = a.old_nll[t];
-        if (a.ref_nll) ref[i] = a.ref_nll[t];
+        if (REF) ref[i] = a.ref_nll[t];
         adv[i] = a.adv[a.adv_tok ? t : s];
         w[i] = weight[s];
       }
@@ -269,7 +359,7 @@ __global__ void __launch_bounds__(POL_THREADS) policy_grad_kernel(const __grid_c
     for (int i = 0; i < POL_TILE; ++i) {
       const long long t = i0 + i * POL_THREADS;
       if (t >= n_el || !in_bounds(a.err, t, 1, n_el, SITE_POLICY_OUT)) continue;
-      dnll[t] = lab[i] < 0 ? 0.0f : policy_token(a, nll[i], old[i], ref[i], adv[i]).grad * (w[i] * dl);
+      dnll[t] = lab[i] < 0 ? 0.0f : policy_token<REF>(a, nll[i], old[i], ref[i], adv[i]).grad * (w[i] * dl);
     }
   }
 }
@@ -320,6 +410,8 @@ wb_status policy_args(PolicyArgs& a, const float* nll, const float* old_nll, con
   return WB_OK;
 }
 
+bool policy_small(int64_t S, int64_t T) { return S <= POL_SMALL_S && T <= POL_SMALL_T; }
+
 struct PolicyWs {
   size_t part, counts, total;
 };
@@ -341,7 +433,7 @@ extern "C" {
 
 size_t wb_policy_loss_workspace_bytes(int64_t S, int64_t T) {
   if (S < 1 || T < 1 || S > (1LL << 31) || T > (1LL << 30) || S > (1LL << 40) / T) return 0;
-  return policy_ws(S).total;
+  return policy_small(S, T) ? 0 : policy_ws(S).total;
 }
 
 wb_status wb_policy_loss(const float* nll, const float* old_nll, const float* ref_nll, const float* advantage,
@@ -360,10 +452,16 @@ wb_status wb_policy_loss(const float* nll, const float* old_nll, const float* re
     if (S > 0) WB_CUDA(cudaMemsetAsync(weight, 0, sizeof(float) * static_cast<size_t>(S), s));
     return WB_OK;
   }
-  if (!workspace || !aligned16(workspace) || workspace_bytes < policy_ws(S).total) return WB_EWORKSPACE;
+  const bool small = policy_small(S, T);
+  if (!small && (!workspace || !aligned16(workspace) || workspace_bytes < policy_ws(S).total)) return WB_EWORKSPACE;
   a.per_sequence = per_sequence != 0;
   a.err = tc_err_ptr();
   if (!a.err) return WB_ECUDA;
+  if (small) {
+    Prof pr(PC_POLICY, s);
+    WB_CUDA(launch_pdl(ref_nll ? policy_small_kernel<true> : policy_small_kernel<false>, dim3(1), dim3(POL_SMALL_THREADS), 0, s, a, stats, weight));
+    return WB_OK;
+  }
   const PolicyWs w = policy_ws(S);
   auto* part = reinterpret_cast<PolicyPart*>(static_cast<char*>(workspace) + w.part);
   int* counts = reinterpret_cast<int*>(static_cast<char*>(workspace) + w.counts);
@@ -371,7 +469,11 @@ wb_status wb_policy_loss(const float* nll, const float* old_nll, const float* re
   const int teams = POL_WARPS / warps;
   const int blocks = policy_blocks((S + teams - 1) / teams);
   Prof pr(PC_POLICY, s, 2);
-  auto kern = warps == 1 ? policy_sum_kernel<1> : warps == 2 ? policy_sum_kernel<2> : warps == 4 ? policy_sum_kernel<4> : policy_sum_kernel<8>;
+  auto pick = [&](auto ref) {
+    constexpr bool REF = decltype(ref)::value;
+    return warps == 1 ? policy_sum_kernel<1, REF> : warps == 2 ? policy_sum_kernel<2, REF> : warps == 4 ? policy_sum_kernel<4, REF> : policy_sum_kernel<8, REF>;
+  };
+  const auto kern = ref_nll ? pick(std::true_type()) : pick(std::false_type());
   WB_CUDA(launch_pdl(kern, dim3(blocks), dim3(POL_THREADS), 0, s, a, counts, part, blocks));
   WB_CUDA(launch_pdl(policy_join_kernel, dim3(static_cast<unsigned>((S + POL_THREADS - 1) / POL_THREADS)), dim3(POL_THREADS), 0, s,
                      static_cast<const PolicyPart*>(part), blocks, static_cast<const int*>(counts), static_cast<long long>(S),
@@ -395,7 +497,9 @@ wb_status wb_policy_loss_backward(const float* dloss, const float* nll, const fl
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   Prof pr(PC_POLICY, s);
   const long long span = static_cast<long long>(POL_THREADS) * POL_TILE;
-  WB_CUDA(launch_pdl(policy_grad_kernel, dim3(policy_blocks((a.S * a.T + span - 1) / span)), dim3(POL_THREADS), 0, s, a, dloss, weight, dnll));
+  const long long units = (a.S * a.T + span - 1) / span;
+  const int blocks = static_cast<int>(units < 8LL * POL_MAX_BLOCKS ? units : 8LL * POL_MAX_BLOCKS);
+  WB_CUDA(launch_pdl(ref_nll ? policy_grad_kernel<true> : policy_grad_kernel<false>, dim3(blocks), dim3(POL_THREADS), 0, s, a, dloss, weight, dnll));
   return WB_OK;
 }
 
