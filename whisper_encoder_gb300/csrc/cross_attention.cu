@@ -72,6 +72,7 @@ void base(CrossParams& x, int batch, int Tq, int Tk, int H, int Hk, float scale,
   x.H = H;
   x.Hk = Hk;
   x.group = H / Hk;
+  x.splits = 1;
   x.q_items = q.items;
   x.kv_items = k.items;
   x.scale = scale;
@@ -84,30 +85,37 @@ void base(CrossParams& x, int batch, int Tq, int Tk, int H, int Hk, float scale,
   x.err = tc_err_ptr();
 }
 
-cudaError_t launch_few(const FewParams& p, cudaStream_t s) {
-  static uint64_t done = 0;
-  cudaError_t e = allow_smem(cross_few_kernel, FewSmem::TOTAL, &done);
-  if (e != cudaSuccess) return e;
+// As launch_pdl, in clusters of `splits` CTAs.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_split(void (*kern)(KArgs...), unsigned grid, unsigned block, size_t smem, unsigned splits, cudaStream_t s,
+                         Args... args) {
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = p.splits;
+  attr[1].val.clusterDim.x = splits;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.x.batch) * p.x.Hk * p.splits);
-  cfg.blockDim = dim3(FEW_THREADS);
-  cfg.dynamicSmemBytes = FewSmem::TOTAL;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = p.splits > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, cross_few_kernel, p);
+  cfg.numAttrs = splits > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 // Splits of the keys: 1, 2, 4 or 8, while the (item, head) pairs leave places for CTAs empty and a split has 64 keys.
 int few_splits(long long pairs, int Tk) {
   int n = 1;
   while (n < FEW_MAX_SPLITS && pairs * n < 2LL * sm_count() && Tk >= 2 * n * 64) n *= 2;
+  return n;
+}
+
+// Splits of the keys of a tile of rows: 1, 2, 4 or 8, while `places` for CTAs stay empty and a split has two tiles of keys.
+int tile_splits(long long tiles, int Tk, int places) {
+  int n = 1;
+  while (n < CRA_MAX_SPLITS && 2 * tiles * n <= places && Tk > 2 * n * 2 * CRA_BK - CRA_BK) n *= 2;
   return n;
 }
 
@@ -149,7 +157,9 @@ wb_status wb_cross_attention(const void* q, int64_t q_batch, int64_t q_row, cons
     p.v_batch = rv.batch;
     p.v_row = rv.row;
     p.splits = few_splits(static_cast<long long>(batch) * n_kv_heads, Tk);
-    WB_CUDA(launch_few(p, s));
+    static uint64_t few_done = 0;
+    WB_CUDA(allow_smem(cross_few_kernel, FewSmem::TOTAL, &few_done));
+    WB_CUDA(launch_split(cross_few_kernel, static_cast<unsigned>(batch) * n_kv_heads * p.splits, FEW_THREADS, FewSmem::TOTAL, p.splits, s, p));
     return WB_OK;
   }
   CUtensorMap qm, km, vm;
@@ -158,8 +168,9 @@ wb_status wb_cross_attention(const void* q, int64_t q_batch, int64_t q_row, cons
   if (Tk > 0 && (!rows_map(&km, rk, batch, Tk, n_kv_heads, CRA_BK) || !rows_map(&vm, rv, batch, Tk, n_kv_heads, CRA_BK))) return WB_ECUDA;
   static uint64_t done = 0;
   WB_CUDA(allow_smem(cross_fwd_kernel, CrossSmem::TOTAL, &done));
-  const unsigned grid = static_cast<unsigned>(batch) * n_heads * ((Tq + CRA_BQ - 1) / CRA_BQ);
-  WB_CUDA(launch_pdl(cross_fwd_kernel, dim3(grid), dim3(CRA_THREADS), CrossSmem::TOTAL, s, qm, km, vm, p.x));
+  const unsigned tiles = static_cast<unsigned>(batch) * n_heads * ((Tq + CRA_BQ - 1) / CRA_BQ);
+  p.x.splits = tile_splits(tiles, Tk, 2 * sm_count());
+  WB_CUDA(launch_split(cross_fwd_kernel, tiles * p.x.splits, CRA_THREADS, CrossSmem::TOTAL, p.x.splits, s, qm, km, vm, p.x));
   return WB_OK;
 }
 

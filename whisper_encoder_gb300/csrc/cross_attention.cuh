@@ -7,7 +7,10 @@
 //   P = 2^((S - m) c)     -> bf16 in TMEM, 64 columns; the PV product reads its A operand from there
 //   l += row sums of the unrounded P, float32
 //   O += P V_j            -> TMEM, fp32, 64 columns; V is read where it lies, as an MN-major B tile
-// Two CTAs share an SM (256 TMEM columns each), so that one's softmax runs under the other's products.
+// Two CTAs share an SM (256 TMEM columns each), so that one's softmax runs under the other's products.  Where there are too few
+// tiles of rows for the SMs, a cluster of up to 8 CTAs splits a tile's keys; each leaves its O, maxima and sums in
+// shared memory and joins a share of the rows of all of them, in order (224 rows of 16 heads over 13501 keys: 92 us in
+// 32 CTAs, 24 in 256).
 // Warp 0 lane 0 loads with TMA, warp 1 lane 0 issues the MMAs, warps 2-9 run the softmax: each owns 16 query
 // rows through the 16-lane TMEM shapes, four threads a row.
 //
@@ -37,12 +40,17 @@ struct CrossSmem {
   static constexpr int OFF_V = OFF_K + CRA_KSTAGES * KV_BYTES;
   static constexpr int OFF_BAR = OFF_V + CRA_VSTAGES * KV_BYTES;
   static constexpr int TOTAL = 1024 + OFF_BAR + 256;
+  // a split's share, over the rings when they are done: rows of 64 floats of O, its maximum and its sum
+  static constexpr int SHARE_LD = CRA_HD + 4;
 };
 static_assert(2 * CrossSmem::TOTAL <= 227 * 1024, "two CTAs an SM");
+static_assert(CRA_BQ * CrossSmem::SHARE_LD * 4 <= CrossSmem::OFF_BAR, "a share fits the rings");
+constexpr int CRA_MAX_SPLITS = 8;
 
 struct CrossParams {
   int batch, Tq, Tk, H, Hk;
   int group;                 // H / Hk
+  int splits;                // cross_fwd_kernel: CTAs of a cluster, for the keys of a tile
   int q_items, kv_items;     // 0: every item reads the first one's rows (a batch stride of 0), else 1
   float scale;
   float c;                   // scale log2(e)
@@ -57,6 +65,17 @@ struct CrossParams {
 __device__ __forceinline__ int cross_len(const int* lens, int i, int batch, int most, uint32_t* err) {
   if (!lens || !in_bounds(err, i, 1, batch, SITE_CROSS_LENS)) return most;
   return min(max(lens[i], 0), most);
+}
+
+// Four lanes t hold words (columns 8k + 2t and + 1) of k = 0..3; lane t gets all four words of k = t: 16 bytes in a row.
+__device__ __forceinline__ uint4 quad_transpose(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, int t) {
+  const bool odd = t & 1, high = t & 2;
+  uint32_t a = __shfl_xor_sync(0xffffffffu, odd ? w0 : w1, 1), b = __shfl_xor_sync(0xffffffffu, odd ? w2 : w3, 1);
+  if (odd) { w0 = a; w2 = b; } else { w1 = a; w3 = b; }
+  a = __shfl_xor_sync(0xffffffffu, high ? w0 : w2, 2);
+  b = __shfl_xor_sync(0xffffffffu, high ? w1 : w3, 2);
+  if (high) { w0 = a; w1 = b; } else { w2 = a; w3 = b; }
+  return make_uint4(w0, w1, w2, w3);
 }
 
 // q, k, v maps: (64 heads, T, items) of bf16 rows, boxes of 64 x 128 x 1.
@@ -87,8 +106,9 @@ __global__ void __launch_bounds__(CRA_THREADS, 2)
   const int warp = warp_id();
   const int lane = lane_id();
   const int n_qt = (p.Tq + CRA_BQ - 1) / CRA_BQ;
-  const int qt = blockIdx.x % n_qt;
-  const int bh = blockIdx.x / n_qt;
+  const int splits = p.splits, rank = blockIdx.x % splits;
+  const int qt = blockIdx.x / splits % n_qt;
+  const int bh = blockIdx.x / splits / n_qt;
   const int b = bh / p.H, h = bh % p.H;
   const int q0 = qt * CRA_BQ;
 
@@ -110,6 +130,8 @@ __global__ void __launch_bounds__(CRA_THREADS, 2)
     *abort_flag = 0;
     fence_mbar_init();
   }
+  const long long out_el = static_cast<long long>(p.batch) * p.Tq * p.H * CRA_HD;
+  const long long lse_el = static_cast<long long>(p.batch) * p.H * p.Tq;
   if (warp == 1) tmem_alloc(tmem_slot, CRA_TM_COLS);
   tc_fence_before();
   __syncthreads();
@@ -120,8 +142,10 @@ __global__ void __launch_bounds__(CRA_THREADS, 2)
 
   const int q_len = cross_len(p.q_lens, b, p.batch, p.Tq, p.err);
   const int kv_len = cross_len(p.kv_lens, b, p.batch, p.Tk, p.err);
-  // rows that take part, and the tiles of their keys; without any, zeros are written below
-  const int nkv = q0 < q_len ? (kv_len + CRA_BK - 1) / CRA_BK : 0;
+  // rows that take part, and the tiles of their keys, of which this CTA has [j0, j0 + nkv); without any, zeros are written below
+  const int all_kv = q0 < q_len ? (kv_len + CRA_BK - 1) / CRA_BK : 0;
+  const int j0 = static_cast<int>(static_cast<long long>(all_kv) * rank / splits);
+  const int nkv = static_cast<int>(static_cast<long long>(all_kv) * (rank + 1) / splits) - j0;
 
   if (warp == 0) {
     if (nkv > 0 && elect_one()) {
@@ -137,7 +161,7 @@ __global__ void __launch_bounds__(CRA_THREADS, 2)
         const uint32_t ph = (jj / CRA_KSTAGES) & 1;
         if (!mbar_wait(&k_empty[st], ph ^ 1u, p.err, abort_flag, 32)) return false;
         mbar_arrive_expect_tx(&k_full[st], S::KV_BYTES);
-        tma_load_3d(smem + S::OFF_K + st * S::KV_BYTES, &k_map, &k_full[st], hk * CRA_HD, jj * CRA_BK, kb);
+        tma_load_3d(smem + S::OFF_K + st * S::KV_BYTES, &k_map, &k_full[st], hk * CRA_HD, (j0 + jj) * CRA_BK, kb);
         k_issued |= 1u << st;
         k_par = (k_par & ~(1u << st)) | (ph << st);
         return true;
@@ -147,7 +171,7 @@ __global__ void __launch_bounds__(CRA_THREADS, 2)
         const uint32_t ph = (jj / CRA_VSTAGES) & 1;
         if (!mbar_wait(&v_empty[st], ph ^ 1u, p.err, abort_flag, 33)) return false;
         mbar_arrive_expect_tx(&v_full[st], S::KV_BYTES);
-        tma_load_3d(smem + S::OFF_V + st * S::KV_BYTES, &v_map, &v_full[st], hk * CRA_HD, jj * CRA_BK, kb);
+        tma_load_3d(smem + S::OFF_V + st * S::KV_BYTES, &v_map, &v_full[st], hk * CRA_HD, (j0 + jj) * CRA_BK, kb);
         v_issued |= 1u << st;
         v_par = (v_par & ~(1u << st)) | (ph << st);
         return true;
@@ -238,7 +262,7 @@ __global__ void __launch_bounds__(CRA_THREADS, 2)
       tc_fence_before();           // S is in registers: QK of the next key tile may overwrite it
       __syncwarp();
       if (lane == 0) mbar_arrive(s_free);
-      const int valid = kv_len - j * CRA_BK;       // keys of this tile that take part
+      const int valid = kv_len - (j0 + j) * CRA_BK;   // keys of this tile that take part
       if (valid < CRA_BK) {
 #pragma unroll
         for (int kk = 0; kk < 16; ++kk) {
@@ -247,7 +271,7 @@ __global__ void __launch_bounds__(CRA_THREADS, 2)
           if (col + 1 >= valid) s[4 * kk + 1] = s[4 * kk + 3] = -INFINITY;
         }
         // past the last row TMA has filled in zeros; before it V's rows may hold anything
-        if (j * CRA_BK + valid < p.Tk) {
+        if (kv_len < p.Tk) {
           const int st = j % CRA_VSTAGES;
           if (!__all_sync(0xffffffffu, mbar_wait(&v_full[st], (j / CRA_VSTAGES) & 1, p.err, abort_flag, 40))) { ok = false; break; }
           uint4* rows = reinterpret_cast<uint4*>(smem + S::OFF_V + st * S::KV_BYTES);
@@ -356,24 +380,39 @@ __global__ void __launch_bounds__(CRA_THREADS, 2)
         tmem_ld_16x256b_x8(o_tm, v);
         tmem_ld_wait();
       }
-      const long long out_el = static_cast<long long>(p.batch) * p.Tq * p.H * CRA_HD;
-      const long long lse_el = static_cast<long long>(p.batch) * p.H * p.Tq;
+      if (splits > 1 && all_kv > 0) {
+        float* share = reinterpret_cast<float*>(smem);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int q = q0 + ra + 8 * half;
-        if (q >= p.Tq) continue;
-        const bool there = nkv > 0 && q < q_len;
-        const float l = half ? l_b : l_a, inv = 1.0f / l;
-        const long long o = (static_cast<long long>(b) * p.Tq + q) * p.H * CRA_HD + h * CRA_HD + cq;
+        for (int half = 0; half < 2; ++half) {
+          float* row = share + (ra + 8 * half) * S::SHARE_LD;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const float x0 = __uint_as_float(v[4 * kk + 2 * half]), x1 = __uint_as_float(v[4 * kk + 2 * half + 1]);
-          if (in_bounds(p.err, o + 8 * kk, 2, out_el, SITE_CROSS_OUT))
-            *reinterpret_cast<uint32_t*>(p.out + o + 8 * kk) = there ? pack_bf16(x0 * inv, x1 * inv) : 0u;
+          for (int kk = 0; kk < 8; ++kk)
+            *reinterpret_cast<float2*>(row + 8 * kk + cq) =
+                make_float2(__uint_as_float(v[4 * kk + 2 * half]), __uint_as_float(v[4 * kk + 2 * half + 1]));
+          if ((lane & 3) == 0) *reinterpret_cast<float2*>(row + CRA_HD) = half ? make_float2(m_b, l_b) : make_float2(m_a, l_a);
         }
-        const long long li = (static_cast<long long>(b) * p.H + h) * p.Tq + q;
-        if ((lane & 3) == 0 && in_bounds(p.err, li, 1, lse_el, SITE_CROSS_LSE))
-          p.lse[li] = there ? (half ? m_b : m_a) * p.scale + logf(l) : -INFINITY;
+      } else if (rank == 0) {
+        const int t = lane & 3;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int q = q0 + ra + 8 * half;
+          const bool there = nkv > 0 && q < q_len;
+          const float l = half ? l_b : l_a, inv = 1.0f / l;
+          uint32_t w[8];
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            w[kk] = there ? pack_bf16(__uint_as_float(v[4 * kk + 2 * half]) * inv, __uint_as_float(v[4 * kk + 2 * half + 1]) * inv) : 0u;
+          const uint4 u0 = quad_transpose(w[0], w[1], w[2], w[3], t), u1 = quad_transpose(w[4], w[5], w[6], w[7], t);
+          if (q >= p.Tq) continue;
+          const long long o = (static_cast<long long>(b) * p.Tq + q) * p.H * CRA_HD + h * CRA_HD + 8 * t;
+          if (in_bounds(p.err, o, 40, out_el, SITE_CROSS_OUT)) {
+            *reinterpret_cast<uint4*>(p.out + o) = u0;
+            *reinterpret_cast<uint4*>(p.out + o + 32) = u1;
+          }
+          const long long li = (static_cast<long long>(b) * p.H + h) * p.Tq + q;
+          if (t == 0 && in_bounds(p.err, li, 1, lse_el, SITE_CROSS_LSE))
+            p.lse[li] = there ? (half ? m_b : m_a) * p.scale + logf(l) : -INFINITY;
+        }
       }
     }
   }
@@ -382,6 +421,46 @@ __global__ void __launch_bounds__(CRA_THREADS, 2)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, CRA_TM_COLS);
+  if (splits == 1 || all_kv == 0) return;          // the same in all CTAs of a cluster
+  cluster_sync();                                  // everyone's share is written
+  const int r0 = CRA_BQ * rank / splits, r1 = CRA_BQ * (rank + 1) / splits;
+  for (int i = threadIdx.x; i < (r1 - r0) * (CRA_HD / 4); i += CRA_THREADS) {
+    const int r = r0 + i / (CRA_HD / 4), e = i % (CRA_HD / 4) * 4, q = q0 + r;
+    if (q >= p.Tq) break;
+    const uint32_t at = smem_u32(smem) + r * S::SHARE_LD * 4;
+    float4 o[CRA_MAX_SPLITS], ml[CRA_MAX_SPLITS];
+    float top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < CRA_MAX_SPLITS; ++k) {
+      if (k >= splits) continue;
+      const uint32_t from = cluster_map(at, k);
+      o[k] = ld_cluster_f32x4(from + e * 4);
+      ml[k] = ld_cluster_f32x4(from + CRA_HD * 4);
+      top = fmaxf(top, ml[k].x);
+    }
+    const float mo = top == -INFINITY ? 0.0f : top;
+    float l = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < CRA_MAX_SPLITS; ++k) {
+      if (k >= splits) continue;
+      const float f = ex2_approx((ml[k].x - mo) * p.c);
+      l = fmaf(f, ml[k].y, l);
+      acc.x = fmaf(f, o[k].x, acc.x);
+      acc.y = fmaf(f, o[k].y, acc.y);
+      acc.z = fmaf(f, o[k].z, acc.z);
+      acc.w = fmaf(f, o[k].w, acc.w);
+    }
+    const bool there = q < q_len;
+    const float inv = 1.0f / l;
+    const long long at_o = (static_cast<long long>(b) * p.Tq + q) * p.H * CRA_HD + h * CRA_HD + e;
+    if (in_bounds(p.err, at_o, 4, out_el, SITE_CROSS_OUT))
+      *reinterpret_cast<uint2*>(p.out + at_o) =
+          there ? make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv)) : make_uint2(0u, 0u);
+    const long long li = (static_cast<long long>(b) * p.H + h) * p.Tq + q;
+    if (e == 0 && in_bounds(p.err, li, 1, lse_el, SITE_CROSS_LSE)) p.lse[li] = there ? top * p.scale + logf(l) : -INFINITY;
+  }
+  cluster_sync();                                  // the others have read this CTA's share
 }
 
 }  // namespace wb

@@ -115,17 +115,6 @@ __global__ void __launch_bounds__(256) cross_stats_kernel(const __grid_constant_
   }
 }
 
-// Four lanes t hold words (columns 8k + 2t and + 1) of k = 0..3; lane t gets all four words of k = t: 16 bytes in a row.
-__device__ __forceinline__ uint4 quad_transpose(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, int t) {
-  const bool odd = t & 1, high = t & 2;
-  uint32_t a = __shfl_xor_sync(0xffffffffu, odd ? w0 : w1, 1), b = __shfl_xor_sync(0xffffffffu, odd ? w2 : w3, 1);
-  if (odd) { w0 = a; w2 = b; } else { w1 = a; w3 = b; }
-  a = __shfl_xor_sync(0xffffffffu, high ? w0 : w2, 2);
-  b = __shfl_xor_sync(0xffffffffu, high ? w1 : w3, 2);
-  if (high) { w0 = a; w1 = b; } else { w2 = a; w3 = b; }
-  return make_uint4(w0, w1, w2, w3);
-}
-
 // own0, own1: K and V (DKV) or Q and dO; step0, step1: Q and dO (DKV) or K and V.  Boxes of 64 x 128 rows.
 template <bool DKV>
 __global__ void __launch_bounds__(CRB_THREADS, 1)
