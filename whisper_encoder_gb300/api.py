@@ -551,16 +551,18 @@ def _i32(values):
 
 
 def _grad_list(tensors, name):
-    """Pointers, sizes and types of a list of tensors.  One attribute at a time: the list can be hundreds long, and the host's
-    time a tensor is what a small model's call takes."""
+    """Pointers and types of a list of tensors of one device, the device, and whether all are contiguous.  One attribute at a time:
+    the list can be hundreds long, and the host's time a tensor is what a small model's call takes."""
     try:
         types = [_LN_TYPES[t.dtype] for t in tensors]
-        dense = all([t.is_contiguous() for t in tensors]) or all([_dense(t) for t in tensors])
-        if dense and min([t.get_device() for t in tensors]) >= 0:
-            return [t.data_ptr() for t in tensors], [t.numel() for t in tensors], types
+        contiguous = all([t.is_contiguous() for t in tensors])
+        if contiguous or all([_dense(t) for t in tensors]):
+            devices = {t.get_device() for t in tensors}
+            if len(devices) == 1 and min(devices) >= 0:
+                return [t.data_ptr() for t in tensors], types, devices.pop(), contiguous
     except (KeyError, AttributeError):
         pass
-    raise ValueError(f"{name}: expected CUDA tensors of bf16, f16 or f32 without gaps")
+    raise ValueError(f"{name}: expected tensors of bf16, f16 or f32 without gaps, on one CUDA device")
 
 
 def _grad_norm(grads, max_norm, out, workspace, stream):
@@ -568,23 +570,28 @@ def _grad_norm(grads, max_norm, out, workspace, stream):
         raise ValueError("grads: expected at least one tensor")
     if len(grads) > _lib.WB_CLIP_MAX_TENSORS:
         raise ValueError(f"grads: at most {_lib.WB_CLIP_MAX_TENSORS} tensors")
-    at, numel, types = _grad_list(grads, "grads")
-    at, n32 = _i64(at), _i32(types)
+    at, types, device, contiguous = _grad_list(grads, "grads")
+    at, c_types = _i64(at), _i32(types)
     outs = out_types = None
     if out is grads:
-        outs, out_types = at, n32
+        outs, out_types = at, c_types
     elif out is not None:
-        outs, _, out_types = _grad_list(out, "out")
+        outs, out_types, out_device, out_contiguous = _grad_list(out, "out") if out else ([], [], device, True)
+        if out_device != device:
+            raise ValueError(f"tensors on devices {device} and {out_device}: one device expected")
         if [o.shape for o in out] != [g.shape for g in grads] or not (
-                all([t.is_contiguous() for t in grads + out]) or all([o.stride() == g.stride() for o, g in zip(out, grads)])):
+                (contiguous and out_contiguous) or all([o.stride() == g.stride() for o, g in zip(out, grads)])):
             raise ValueError("out: expected one tensor for each gradient, of its shape and strides")
-        if any([o != t and o != WB_F32 for o, t in zip(out_types, types)]):
+        if out_types != types and any([o != t and o != WB_F32 for o, t in zip(out_types, types)]):
             raise ValueError("out: expected each gradient's type or float32")
         outs, out_types = _i64(outs), _i32(out_types)
-    with _place(stream, *grads, *(() if out is None or out is grads else out), workspace):
+    numel = _i64([t.numel() for t in grads])
+    # all tensors of the call are on one device: on its current stream the first one stands for them
+    others = () if stream is None else (*grads[1:], *(() if out is None or out is grads else out))
+    with _place(stream, grads[0], *others, workspace):
         norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
         ws = _head_workspace(workspace, "wb_clip_grad_norm_workspace_bytes", norm.device, len(grads))
-        call("wb_clip_grad_norm", at, outs, _i64(numel), n32, out_types, len(grads), max_norm, _a(norm), _a(ws), ws.numel(),
+        call("wb_clip_grad_norm", at, outs, numel, c_types, out_types, len(grads), max_norm, norm.data_ptr(), ws.data_ptr(), ws.numel(),
              _raw_stream(norm))
     return norm
 
