@@ -7,6 +7,7 @@ library has not been built, every call raises: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 from . import build as _build
@@ -154,6 +155,27 @@ def load(path: str | None = None) -> ctypes.CDLL:
         return _LIB
     _LIB = open_library(path or LIB_PATH)
     return _LIB
+
+
+_HOST = None
+
+
+def host_calls():
+    """The C++ marshalling of the plain calls (wb_host.so), bound to the loaded libwb; False where it is not built."""
+    global _HOST
+    if _HOST is None:
+        lib = load()
+        try:
+            spec = importlib.util.spec_from_file_location("wb_host", _build.LIB_HOST)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            module.bind(*[ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+                "wb_cross_attention", "wb_cross_attention_backward", "wb_cross_attention_backward_workspace_bytes", "wb_clip_grad_norm",
+                "wb_clip_grad_norm_workspace_bytes", "wb_policy_loss", "wb_policy_loss_workspace_bytes", "wb_policy_loss_backward")])
+            _HOST = module
+        except (ImportError, OSError):
+            _HOST = False
+    return _HOST
 
 
 def status_string(status: int) -> str:

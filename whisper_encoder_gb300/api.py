@@ -459,6 +459,12 @@ def linear_distill_backward(dloss, x, w, top, index, lse, temperature: float = 1
     return dx, dw
 
 
+def _plain():
+    """wb_host's functions take the plain case of a call (no stream, everything as documented, on the current device) and return None
+    for any other, which then goes through the checks below."""
+    return _lib._HOST if _lib._HOST is not None else _lib.host_calls()
+
+
 def _attn_rows(t, name):
     """A bf16 [batch, T, heads * 64] tensor whose rows are contiguous: its shape and strides."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 3:
@@ -496,6 +502,10 @@ def cross_attention(q, k, v, scale: float = 0.125, q_lens=None, kv_lens=None, st
     item.  q_lens, kv_lens: int32 [batch] on the device, how many rows and keys of an item take part (default: all);
     a row without keys or past q_lens gives out 0 and lse -inf.  Not recorded by autograd: gradients come from
     cross_attention_backward."""
+    if stream is None and (fast := _plain()):
+        r = fast.cross_attention(q, k, v, scale, q_lens, kv_lens)
+        if r is not None:
+            return r
     batch, Tq, Tk, H, Hk, qs, ks, vs = _attn_shape(q, k, v, q_lens, kv_lens)
     with _place(stream, q, k, v, q_lens, kv_lens):
         device = q.device
@@ -513,6 +523,10 @@ def cross_attention_backward(dout, q, k, v, out, lse, scale: float = 0.125, q_le
     dout as q (strides free).  dq like q, dk and dv like k, contiguous; the rows of all heads that share a key head are summed.
     workspace, if given: uint8, as many bytes as load().wb_cross_attention_backward_workspace_bytes(batch, Tq, H) says, for
     one call at a time."""
+    if stream is None and workspace is None and (fast := _plain()):
+        r = fast.cross_attention_backward(dout, q, k, v, out, lse, scale, q_lens, kv_lens, need_dq, need_dkv)
+        if r is not None:
+            return r
     batch, Tq, Tk, H, Hk, qs, ks, vs = _attn_shape(q, k, v, q_lens, kv_lens)
     do_shape, ds = _attn_rows(dout, "dout")
     if do_shape != q.shape:
@@ -566,6 +580,10 @@ def _grad_list(tensors, name):
 
 
 def _grad_norm(grads, max_norm, out, workspace, stream):
+    if stream is None and workspace is None and (fast := _plain()):
+        r = fast.clip_grad_norm(grads, max_norm, out)
+        if r is not None:
+            return r
     if not grads:
         raise ValueError("grads: expected at least one tensor")
     if len(grads) > _lib.WB_CLIP_MAX_TENSORS:
@@ -636,6 +654,10 @@ def policy_loss(nll, old_nll, advantage, labels, ref_nll=None, clip_low: float =
     (linear_cross_entropy's loss rows); labels int64 [S, T], negative: the token takes no part; advantage f32 [S] or
     [S, T].  stats = (loss, mean KL, share of clipped tokens), means over the tokens that take part or, with per_sequence,
     over the sequences' means; weight is what policy_loss_backward takes.  Not recorded by autograd."""
+    if stream is None and workspace is None and (fast := _plain()):
+        r = fast.policy_loss(nll, old_nll, advantage, labels, ref_nll, clip_low, clip_high, kl_weight, per_sequence)
+        if r is not None:
+            return r
     S, T, per_token = _policy_shape(nll, old_nll, advantage, labels, ref_nll, kl_weight)
     with _place(stream, nll, old_nll, advantage, labels, ref_nll, workspace):
         stats = torch.empty(3, dtype=torch.float32, device=nll.device)
@@ -654,6 +676,10 @@ def policy_loss_backward(dloss, nll, old_nll, advantage, labels, weight, ref_nll
                          kl_weight: float = 0.0, stream=None):
     """Gradient of nll (f32 [S, T], 0 for tokens that take no part) of policy_loss from dloss (f32 scalar, on the device) and its
     weight: what linear_cross_entropy_backward takes as dloss."""
+    if stream is None and (fast := _plain()):
+        r = fast.policy_loss_backward(dloss, nll, old_nll, advantage, labels, weight, ref_nll, clip_low, clip_high, kl_weight)
+        if r is not None:
+            return r
     S, T, per_token = _policy_shape(nll, old_nll, advantage, labels, ref_nll, kl_weight)
     if not isinstance(dloss, torch.Tensor) or dloss.numel() != 1:
         raise ValueError("dloss: expected a f32 scalar on the device")

@@ -2,27 +2,34 @@
 
 Each CUDA translation unit is compiled in parallel, then linked into
 ``whisper_encoder_gb300/_build/libwb.so`` (git-ignored); ``--debug`` builds the
-bounds-checked variant into ``_build_debug/libwb_debug.so``.  Usage:
+bounds-checked variant into ``_build_debug/libwb_debug.so``.  ``wb_host.so``, the C++
+marshalling of a few calls, is built beside it with g++ against the installed torch; it only
+saves host time, so a machine that cannot build it goes without.  Usage:
     python -m whisper_encoder_gb300.build [--force] [--verbose-ptxas] [--debug]
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import hashlib
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libwb.so")
+LIB_HOST = os.path.join(BUILD, "wb_host.so")
 BUILD_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_DEBUG = os.path.join(BUILD_DEBUG, "libwb_debug.so")
 SOURCES = ["api.cu", "kernels.cu", "tc_kernels.cu", "static_scratch.cu", "host_pipeline.cu", "layernorm_train.cu", "head_loss.cu",
            "cross_attention.cu", "grad_clip.cu", "policy_loss.cu"]
+HOST_SOURCE = "host_calls.cpp"
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -46,12 +53,50 @@ def _flags(ptxas_verbose: bool = False, debug: bool = False):
 def _digest(debug: bool = False) -> str:
     h = hashlib.sha256()
     for name in sorted(os.listdir(CSRC)):
+        if name == HOST_SOURCE:
+            continue
         with open(os.path.join(CSRC, name), "rb") as fh:
             h.update(name.encode() + fh.read())
     with open(os.path.join(ROOT, "include", "wb.h"), "rb") as fh:
         h.update(fh.read())
     h.update(" ".join(_flags(debug=debug)).encode())
     return h.hexdigest()
+
+
+def _host_command(out: str) -> list:
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    nvcc = os.path.realpath(_nvcc())
+    include = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include")]
+    libs = os.path.join(torch_dir, "lib")
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", *["-I" + d for d in include], os.path.join(CSRC, HOST_SOURCE),
+            "-o", out, "-L" + libs, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath," + libs]
+
+
+def build_host(force: bool = False) -> str | None:
+    """Compile wb_host.so against the installed torch (if its source, wb.h or torch changed); None where that fails."""
+    try:
+        cmd = _host_command(LIB_HOST + ".tmp")
+        h = hashlib.sha256(" ".join(cmd).encode() + importlib.metadata.version("torch").encode() + sys.version.encode())
+        for path in (os.path.join(CSRC, HOST_SOURCE), os.path.join(ROOT, "include", "wb.h")):
+            with open(path, "rb") as fh:
+                h.update(fh.read())
+        stamp = os.path.join(BUILD, "host_digest.txt")
+        if not force and os.path.exists(LIB_HOST) and os.path.exists(stamp) and open(stamp).read() == h.hexdigest():
+            return LIB_HOST
+        os.makedirs(BUILD, exist_ok=True)
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(r.stderr[-2000:])
+        os.replace(LIB_HOST + ".tmp", LIB_HOST)
+        with open(stamp, "w") as fh:
+            fh.write(h.hexdigest())
+        return LIB_HOST
+    except Exception as e:  # noqa: BLE001 - the package works without it, with more host time a call
+        if os.path.exists(LIB_HOST):
+            os.remove(LIB_HOST)          # of another torch or another wb.h
+        sys.stderr.write(f"wb_host.so is not built: {e}\n")
+        return None
 
 
 def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True, debug: bool = False) -> str:
@@ -64,6 +109,8 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True, 
     stamp = os.path.join(out_dir, "digest.txt")
     dg = _digest(debug)
     if not force and os.path.exists(lib_path) and os.path.exists(stamp) and open(stamp).read() == dg:
+        if not debug:
+            build_host()
         return lib_path
     nvcc = _nvcc()
     objs = []
@@ -76,11 +123,14 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True, 
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        host = None if debug else ex.submit(build_host, force)
         for obj, log in ex.map(compile_one, SOURCES):
             objs.append(obj)
             if log and (ptxas_verbose or not quiet):
                 sys.stderr.write(log)
+        if host:
+            host.result()
     tmp = lib_path + ".tmp"
     cmd = [nvcc, ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
