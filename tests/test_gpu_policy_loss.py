@@ -116,6 +116,22 @@ def test_values_that_take_no_part_reach_nothing(wb):
         assert not x.any()
 
 
+@pytest.mark.parametrize("S", [3, 400])
+def test_losses_without_a_bound(wb, S):
+    # a ratio beyond float32 under a negative advantage is not clipped: the loss is infinite, and so is that token's gradient, alone
+    nll, old, ref, adv, labels = _data(S, 20, 2)
+    labels[1, 3] = 7
+    adv[:] = -1
+    old[1, 3] = nll[1, 3] + 120
+    stats, weight, dnll = _run(wb, (nll, old, None, adv, labels), False, beta=0.0, dl=1.0)
+    assert float(stats[0]) == math.inf and math.isfinite(float(stats[2]))
+    rest = dnll.clone()
+    rest[1, 3] = 0
+    assert float(dnll[1, 3]) == -math.inf and bool(torch.isfinite(rest).all())
+    nll[1, 3] = math.nan
+    assert math.isnan(float(_run(wb, (nll, old, None, adv, labels), True, beta=0.0)[0][0]))
+
+
 def test_the_border_of_the_clip_is_decided_on_the_exact_difference(wb):
     # old - nll lies next to log1p(0.28) by less than a rounding of the difference
     t = math.log1p(0.28)

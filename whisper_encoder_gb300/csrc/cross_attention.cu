@@ -240,8 +240,9 @@ wb_status wb_cross_attention_backward(const void* dout, int64_t do_batch, int64_
   WB_CUDA(allow_smem(cross_bwd_kernel<true>, SMEM, &dkv_done));
   const long long q_items = static_cast<long long>(batch) * n_heads * ((Tq + CRB_M - 1) / CRB_M);
   const long long k_items = static_cast<long long>(batch) * n_kv_heads * ((Tk + CRB_M - 1) / CRB_M);
-  WB_CUDA(launch_pdl(cross_bwd_kernel<false>, dim3(static_cast<unsigned>(q_items < sms ? q_items : sms)), dim3(CRB_THREADS), SMEM, s, qm, dm,
-                     km, vm, p));
+  p.x.splits = tile_splits(q_items, Tk, sms);
+  const unsigned q_grid = p.x.splits > 1 ? static_cast<unsigned>(q_items) * p.x.splits : static_cast<unsigned>(q_items < sms ? q_items : sms);
+  WB_CUDA(launch_split(cross_bwd_kernel<false>, q_grid, CRB_THREADS, SMEM, p.x.splits, s, qm, dm, km, vm, p));
   if (dk)
     WB_CUDA(launch_pdl(cross_bwd_kernel<true>, dim3(static_cast<unsigned>(k_items < sms ? k_items : sms)), dim3(CRB_THREADS), SMEM, s, km, vm,
                        qm, dm, p));

@@ -15,7 +15,8 @@
 // Persistent, one CTA an SM over its items in turn.  Bound by the tensor pipe: 16 products of 128 x 128 x 16 and 128 x 64 x 16 a
 // step, 64 and 45 cycles each alone.  What keeps it fed: S is double, dP is given back as soon as the softmax holds it in registers, so
 // the scores of step n + 1 are formed under the softmax of step n, and its sums under the softmax of step n + 1; an item's
-// sums are stored after the next item's first softmax.  128 columns a step: with 64, two buffers of both and a group of
+// sums are stored after the next item's first softmax.  Where there are fewer tiles of query rows than SMs, clusters of up to 8 CTAs split their
+// keys and join dQ, M and b through distributed shared memory (dq of 224 rows of 16 heads over 13501 keys 106 -> 37 us).  128 columns a step: with 64, two buffers of both and a group of
 // warps for each, a product took 48 cycles for half the work and a step 2000 (dk and dv of 32 x 448 x 1500 x 20 heads 526 us; one
 // item a CTA, two CTAs an SM, 419).
 // Warp 0 lane 0 loads, warp 1 issues, warps 2-17 run the softmax: 16 rows of half of the columns each.
@@ -45,8 +46,11 @@ struct CrossBwdSmem {
   static constexpr int OFF_B = OFF_STATS + CRB_STAGES * STATS_BYTES;    // dq: b by [item parity][column half][row]
   static constexpr int OFF_BAR = OFF_B + 2 * 2 * CRB_M * 4;
   static constexpr int TOTAL = 1024 + OFF_BAR + 512;
+  // dq: a split's share, over the rings when they are done: rows of 64 floats of M, 64 of dQ, and b
+  static constexpr int SHARE_LD = 2 * CRA_HD + 4;
 };
 static_assert(CrossBwdSmem::TOTAL <= 227 * 1024, "one CTA an SM");
+static_assert(CRB_M * CrossBwdSmem::SHARE_LD * 4 <= CrossBwdSmem::OFF_STATS - CrossBwdSmem::OFF_STEP, "a share fits the ring");
 
 struct CrossBwdParams {
   CrossParams x;             // out and lse unused here
@@ -175,10 +179,14 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
   const int own_T = DKV ? x.Tk : x.Tq, step_T = DKV ? x.Tq : x.Tk, heads = DKV ? x.Hk : x.H;
   const int n_tiles = (own_T + CRB_M - 1) / CRB_M;
   const int n_items = x.batch * heads * n_tiles;
+  // CTAs of a cluster share an item's steps; such a grid has one item a cluster
+  const int splits = DKV ? 1 : x.splits, rank = blockIdx.x % splits;
+  const int it_first = blockIdx.x / splits, it_step = gridDim.x / splits;
   // every role walks the same items and steps
   struct Item {
     int b, h, r0;              // h: head of the own rows; r0: the first of them
     int own_len, step_len, per_head, steps;
+    int t_first;               // first row of this CTA's steps
   };
   auto item_at = [&](int it) -> Item {
     Item r;
@@ -191,6 +199,12 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
     r.step_len = DKV ? q_len : kv_len;
     r.per_head = (r.step_len + CRB_STEP - 1) / CRB_STEP;
     r.steps = r.r0 < r.own_len ? r.per_head * (DKV ? x.group : 1) : 0;     // DKV: the group's heads one after another
+    r.t_first = 0;
+    if (!DKV && splits > 1) {
+      const int j0 = r.steps * rank / splits;
+      r.t_first = j0 * CRB_STEP;
+      r.steps = r.steps * (rank + 1) / splits - j0;
+    }
     return r;
   };
   // rows of a step that starts at t0, and whether its tail holds rows that take no part (behind the last row TMA fills in zeros)
@@ -201,7 +215,7 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
     if (elect_one()) {
       int n = 0, c = 0;                      // steps, and items with steps, so far
       bool ok = true;
-      for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
+      for (int it = it_first; it < n_items && ok; it += it_step) {
         const Item i = item_at(it);
         if (i.steps == 0) continue;
         const int slot = c & 1;
@@ -211,7 +225,7 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
         tma_load_3d(smem + 2 * slot * S::TILE, &own0, &m_full[slot], i.h * CRA_HD, i.r0, DKV ? kv_at : q_at);
         tma_load_3d(smem + (2 * slot + 1) * S::TILE, &own1, &m_full[slot], i.h * CRA_HD, i.r0, DKV ? kv_at : do_at);
         ++c;
-        int h = DKV ? i.h * x.group : i.h / x.group, t0 = 0;
+        int h = DKV ? i.h * x.group : i.h / x.group, t0 = i.t_first;
         for (int j = 0; j < i.steps; ++j, ++n) {
           const int st = n % CRB_STAGES;
           if (!mbar_wait(&empty[st], ((n / CRB_STAGES) & 1) ^ 1u, x.err, abort_flag, 44)) { ok = false; break; }
@@ -267,13 +281,13 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
         pn = -1;
         return true;
       };
-      for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
+      for (int it = it_first; it < n_items && ok; it += it_step) {
         const Item i = item_at(it);
         if (i.steps == 0) continue;
         const int slot = c & 1;
         const uint32_t a0 = sw128_desc_lo(own_at + 2 * slot * S::TILE), a1 = a0 + (S::TILE >> 4);
         ok = wait(&m_full[slot], (c >> 1) & 1, 47);
-        int t0 = 0;
+        int t0 = i.t_first;
         for (int j = 0; j < i.steps && ok; ++j, ++n) {
           const int st = n % CRB_STAGES;
           const int halves = i.step_len - t0 > 64 ? 2 : 1;
@@ -334,12 +348,24 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
 #pragma unroll
       for (int k = 0; k < 32; ++k) v[k] = 0;
       float ba = 0.0f, bb = 0.0f;
+      // a split's 32 columns of M and dQ, for the join behind the roles
+      auto share = [&](const uint32_t (&m)[16], const uint32_t (&d)[16]) {
+        float* at = reinterpret_cast<float*>(smem + S::OFF_STEP) + ra * S::SHARE_LD + half * 32 + cq;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float* w = at + (k & 1) * 8 * S::SHARE_LD + k / 2 * 8;
+          *reinterpret_cast<float2*>(w) = make_float2(__uint_as_float(m[2 * k]), __uint_as_float(m[2 * k + 1]));
+          *reinterpret_cast<float2*>(w + CRA_HD) = make_float2(__uint_as_float(d[2 * k]), __uint_as_float(d[2 * k + 1]));
+        }
+      };
       if (any) {
         if (!DKV) {
           if (!wait(b_full, ci & 1, 51)) return false;
           const float* b_of = b_part + (ci & 1) * 2 * CRB_M;
           ba = b_of[ra] + b_of[CRB_M + ra];
           bb = b_of[ra + 8] + b_of[CRB_M + ra + 8];
+        }
+        if (!DKV && splits == 1) {
           const long long si = (static_cast<long long>(i.b) * x.H + i.h) * 2 * p.stats_ld + p.stats_ld + i.r0 + ra;
           if (half == 0 && t < 2 && i.r0 + ra + 8 * t < i.own_len &&
               in_bounds(x.err, si, 9, static_cast<long long>(x.batch) * x.H * 2 * p.stats_ld, SITE_CROSS_STATS))
@@ -355,6 +381,7 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
           tmem_ld_16x256b_x4(acc + half * 32, m);
           tmem_ld_16x256b_x4(acc + CRA_HD + half * 32, d);
           tmem_ld_wait();
+          if (splits > 1) share(m, d);
 #pragma unroll
           for (int k = 0; k < 16; ++k)
             v[k] = __float_as_uint(fmaf(-(k & 2 ? bb : ba), __uint_as_float(m[k]), __uint_as_float(d[k])));
@@ -363,6 +390,18 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_empty);
+      }
+      if (!DKV && splits > 1) {
+        if (!any) {
+          const uint32_t zeros[16] = {};
+          share(zeros, zeros);
+        }
+        if (half == 0 && t == 0) {
+          float* b_at = reinterpret_cast<float*>(smem + S::OFF_STEP) + ra * S::SHARE_LD + 2 * CRA_HD;
+          b_at[0] = ba;
+          b_at[8 * S::SHARE_LD] = bb;
+        }
+        return true;
       }
       if (!DKV && !p.want_dq) return true;
       __nv_bfloat16* const dst = !DKV ? p.dq : half ? p.dk : p.dv;
@@ -392,7 +431,7 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
     Item last;                                       // the item whose results are still to be stored
     int last_c = -1;
     float last_za = 0.0f, last_zb = 0.0f;
-    for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
+    for (int it = it_first; it < n_items && ok; it += it_step) {
       const Item i = item_at(it);
       if (i.steps == 0) {
         ok = finish(i, 0, 0.0f, 0.0f);
@@ -409,7 +448,7 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
         }
       }
       uint64_t ba2 = 0, bb2 = 0;                     // this thread's share of b of the two rows
-      int t0 = 0;
+      int t0 = i.t_first;
       for (int j = 0; j < i.steps; ++j, ++n) {
         const int st = n % CRB_STAGES;
         const int rows = i.step_len - t0;            // that take part, in this step
@@ -524,6 +563,45 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, CRB_TM_COLS);
+  if (DKV || splits == 1) return;
+  // the shares of an item's splits, a part of the rows each: dq = scale (sum dQ - (sum b) (sum M)), -delta less b
+  cluster_sync();
+  const Item i = item_at(it_first);
+  const int r0 = CRB_M * rank / splits, r1 = CRB_M * (rank + 1) / splits;
+  const long long ld = static_cast<long long>(heads) * CRA_HD;
+  for (int k = threadIdx.x; k < (r1 - r0) * (CRA_HD / 4); k += CRB_THREADS) {
+    const int r = r0 + k / (CRA_HD / 4), e = k % (CRA_HD / 4) * 4, row = i.r0 + r;
+    if (row >= own_T) break;
+    const uint32_t at = smem_u32(smem + S::OFF_STEP) + r * S::SHARE_LD * 4;
+    float4 m[CRA_MAX_SPLITS], d[CRA_MAX_SPLITS], b[CRA_MAX_SPLITS];
+#pragma unroll
+    for (int q = 0; q < CRA_MAX_SPLITS; ++q) {
+      if (q >= splits) continue;
+      const uint32_t from = cluster_map(at, q);
+      m[q] = ld_cluster_f32x4(from + e * 4);
+      d[q] = ld_cluster_f32x4(from + (CRA_HD + e) * 4);
+      b[q] = ld_cluster_f32x4(from + 2 * CRA_HD * 4);
+    }
+#pragma unroll
+    for (int q = 1; q < CRA_MAX_SPLITS; ++q) {
+      if (q >= splits) continue;
+      m[0] = make_float4(m[0].x + m[q].x, m[0].y + m[q].y, m[0].z + m[q].z, m[0].w + m[q].w);
+      d[0] = make_float4(d[0].x + d[q].x, d[0].y + d[q].y, d[0].z + d[q].z, d[0].w + d[q].w);
+      b[0].x += b[q].x;
+    }
+    const bool there = row < i.own_len;
+    const long long si = (static_cast<long long>(i.b) * x.H + i.h) * 2 * p.stats_ld + p.stats_ld + row;
+    if (e == 0 && there && in_bounds(x.err, si, 1, static_cast<long long>(x.batch) * x.H * 2 * p.stats_ld, SITE_CROSS_STATS))
+      p.stats[si] -= b[0].x;
+    if (!p.want_dq) continue;
+    const float f = -b[0].x;
+    const uint32_t w0 = pack_bf16(x.scale * fmaf(f, m[0].x, d[0].x), x.scale * fmaf(f, m[0].y, d[0].y));
+    const uint32_t w1 = pack_bf16(x.scale * fmaf(f, m[0].z, d[0].z), x.scale * fmaf(f, m[0].w, d[0].w));
+    const long long o = (static_cast<long long>(i.b) * own_T + row) * ld + i.h * CRA_HD + e;
+    if (in_bounds(x.err, o, 4, static_cast<long long>(x.batch) * own_T * ld, SITE_CROSS_OUT))
+      *reinterpret_cast<uint2*>(p.dq + o) = there ? make_uint2(w0, w1) : make_uint2(0u, 0u);
+  }
+  cluster_sync();                                  // the others have read this CTA's share
 }
 
 }  // namespace wb

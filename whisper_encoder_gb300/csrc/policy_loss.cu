@@ -10,9 +10,9 @@
 // Bound by memory (16 bytes a token forward, 20 backward, 4 more with a reference), below a million tokens by the launches.
 // Forward: a team of 1 to 8 warps of a block takes a sequence; a block leaves one partial row, and a second kernel joins those
 // in order, in every one of its blocks, and turns counts into weights.  Up to 128 sequences of 512 tokens are one block's, in
-// one launch (8 x 77 tokens: 5.8 us against 8.2 with two).  No atomics: the same call gives the same bits.
-// 16001 x 448 tokens forward 34 us, 3.4 TB/s: the loads of a warp's next sequence wait for the sums of the last, and with 4 blocks an SM
-// (64 registers; 3 blocks 43 us, 6 with half the loads each 36) there are not enough others.  Backward, without sums, 23 us, 6.2 TB/s.
+// one launch (8 x 77 tokens: 5.5 us against 8.2 with two).  No atomics: the same call gives the same bits.
+// 16001 x 448 tokens forward 30 us, 3.8 TB/s: the loads of a warp's next sequence wait for the sums of the last, and with 4 blocks an SM
+// (64 registers; 3 blocks a quarter more time, 6 with half the loads each 5 % more) there are not enough others.  Backward, without sums, 23 us, 6.2 TB/s.
 //
 // Numbers.  Whether a token is clipped is decided on d against log1p(hi) and log1p(-lo), both as unevaluated sums of
 // two float32 (the rounding of a difference is exact in float32): one rounding near the border would turn a
@@ -97,10 +97,27 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Partial row of a block: sums of loss, KL and clipped tokens (each divided by its sequence's tokens where sequences
-// count the same), tokens, and sequences with tokens.
+// A running sum and what its roundings left.  Units for float64 are so few (16 cycles a warp's addition) that a sequence's nine
+// operations in one lane were half of the forward pass over 16001 sequences, and the join of 608 rows a microsecond.
+struct Sum2 {
+  float s, c;
+  __device__ __forceinline__ void add(float v) {
+    const float t = s + v, b = t - s;
+    c += (s - (t - b)) + (v - b);
+    s = t;
+  }
+  __device__ __forceinline__ void add(const Sum2& v) {
+    add(v.s);
+    c += v.c;
+  }
+  // (what an infinite sum's roundings left is no number)
+  __device__ __forceinline__ double value() const { return isfinite(s) ? static_cast<double>(s) + static_cast<double>(c) : static_cast<double>(s); }
+};
+
+// Sums of loss, KL and clipped tokens over sequences (each divided by its sequence's tokens where sequences count the same), tokens,
+// and sequences with tokens.
 struct PolicyPart {
-  double loss, kl, clipped;
+  Sum2 loss, kl, clipped;
   long long tokens, seqs;
 };
 
@@ -149,49 +166,31 @@ __device__ __forceinline__ SeqSum policy_sequence(const PolicyArgs& a, long long
   return r;
 }
 
-// A running sum and what its roundings left: float64 units are so few that a sequence's nine operations in one lane, 16 cycles each,
-// were half of the forward pass over 16001 sequences.
-struct Sum2 {
-  float s = 0.0f, c = 0.0f;
-  __device__ __forceinline__ void add(float v) {
-    const float t = s + v, b = t - s;
-    c += (s - (t - b)) + (v - b);
-    s = t;
-  }
-  __device__ __forceinline__ double value() const { return static_cast<double>(s) + static_cast<double>(c); }
-};
-// Sequences of one warp: sums of loss, KL and clipped tokens, weighted for per_sequence.
-struct PolicySum {
-  Sum2 loss, kl, clipped;
-  long long tokens = 0, seqs = 0;
-  __device__ __forceinline__ void add(const SeqSum& r, int per_sequence) {
-    if (r.count == 0) return;
-    const float n = static_cast<float>(r.count);
-    loss.add(per_sequence ? r.loss / n : r.loss);
-    kl.add(per_sequence ? r.kl / n : r.kl);
-    clipped.add(per_sequence ? static_cast<float>(r.clipped) / n : static_cast<float>(r.clipped));
-    tokens += r.count;
-    seqs += 1;
-  }
-  __device__ __forceinline__ PolicyPart part() const { return PolicyPart{loss.value(), kl.value(), clipped.value(), tokens, seqs}; }
-};
+__device__ __forceinline__ void policy_add(PolicyPart& sum, const SeqSum& r, int per_sequence) {
+  if (r.count == 0) return;
+  const float n = static_cast<float>(r.count);
+  sum.loss.add(per_sequence ? r.loss / n : r.loss);
+  sum.kl.add(per_sequence ? r.kl / n : r.kl);
+  sum.clipped.add(per_sequence ? static_cast<float>(r.clipped) / n : static_cast<float>(r.clipped));
+  sum.tokens += r.count;
+  sum.seqs += 1;
+}
 __device__ __forceinline__ void policy_join(PolicyPart& sum, const PolicyPart& p) {
-  sum.loss += p.loss;
-  sum.kl += p.kl;
-  sum.clipped += p.clipped;
+  sum.loss.add(p.loss);
+  sum.kl.add(p.kl);
+  sum.clipped.add(p.clipped);
   sum.tokens += p.tokens;
   sum.seqs += p.seqs;
+}
+__device__ __forceinline__ Sum2 shfl_xor(const Sum2& v, int o) {
+  return Sum2{__shfl_xor_sync(0xffffffffu, v.s, o), __shfl_xor_sync(0xffffffffu, v.c, o)};
 }
 // The 32 lanes' rows, in every lane.
 __device__ __forceinline__ PolicyPart policy_warp_join(PolicyPart p) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    PolicyPart q;
-    q.loss = __shfl_xor_sync(0xffffffffu, p.loss, o);
-    q.kl = __shfl_xor_sync(0xffffffffu, p.kl, o);
-    q.clipped = __shfl_xor_sync(0xffffffffu, p.clipped, o);
-    q.tokens = __shfl_xor_sync(0xffffffffu, p.tokens, o);
-    q.seqs = __shfl_xor_sync(0xffffffffu, p.seqs, o);
+    const PolicyPart q = {shfl_xor(p.loss, o), shfl_xor(p.kl, o), shfl_xor(p.clipped, o), __shfl_xor_sync(0xffffffffu, p.tokens, o),
+                          __shfl_xor_sync(0xffffffffu, p.seqs, o)};
     policy_join(p, q);
   }
   return p;
@@ -210,7 +209,7 @@ __global__ void __launch_bounds__(POL_THREADS, 4) policy_sum_kernel(const __grid
   const int lane = lane_id(), warp = warp_id(), team = warp / W, in_team = warp % W;
   grid_dependency_wait();
   grid_dependents_launch();
-  PolicySum sum;
+  PolicyPart sum = {};
   // all teams of a block make the same number of rounds: there are barriers inside
   for (long long s0 = static_cast<long long>(blockIdx.x) * TEAMS; s0 < a.S; s0 += static_cast<long long>(gridDim.x) * TEAMS) {
     const long long s = s0 + team;
@@ -231,10 +230,10 @@ __global__ void __launch_bounds__(POL_THREADS, 4) policy_sum_kernel(const __grid
     }
     if (in_team == 0 && lane == 0 && s < a.S) {
       if (in_bounds(a.err, s, 1, a.S, SITE_POLICY_OUT)) counts[s] = r.count;
-      sum.add(r, a.per_sequence);
+      policy_add(sum, r, a.per_sequence);
     }
   }
-  if (in_team == 0 && lane == 0) join[team] = sum.part();
+  if (in_team == 0 && lane == 0) join[team] = sum;
   __syncthreads();
   if (threadIdx.x == 0 && in_bounds(a.err, blockIdx.x, 1, parts, SITE_POLICY_OUT)) {
     PolicyPart all = join[0];
@@ -254,15 +253,15 @@ __global__ void __launch_bounds__(POL_SMALL_THREADS) policy_small_kernel(const _
   const int lane = lane_id(), warp = warp_id();
   grid_dependency_wait();
   grid_dependents_launch();
-  PolicySum sum;
+  PolicyPart sum = {};
   for (int s = warp; s < a.S; s += WARPS) {
     const SeqSum r = policy_sequence<1, REF>(a, s, 0);
     if (lane == 0) {
       counts[s] = r.count;
-      sum.add(r, a.per_sequence);
+      policy_add(sum, r, a.per_sequence);
     }
   }
-  if (lane == 0) join[warp] = sum.part();
+  if (lane == 0) join[warp] = sum;
   __syncthreads();
   if (warp == 0) {
     static_assert(WARPS == 32, "a row for each lane");
@@ -271,9 +270,9 @@ __global__ void __launch_bounds__(POL_SMALL_THREADS) policy_small_kernel(const _
     const double f = n > 0 ? 1.0 / static_cast<double>(n) : 0.0;
     if (lane == 0) {
       factor = f;
-      stats[0] = static_cast<float>(all.loss * f);
-      stats[1] = static_cast<float>(all.kl * f);
-      stats[2] = static_cast<float>(all.clipped * f);
+      stats[0] = static_cast<float>(all.loss.value() * f);
+      stats[1] = static_cast<float>(all.kl.value() * f);
+      stats[2] = static_cast<float>(all.clipped.value() * f);
     }
   }
   __syncthreads();
@@ -282,22 +281,28 @@ __global__ void __launch_bounds__(POL_SMALL_THREADS) policy_small_kernel(const _
 }
 
 // stats = (loss, mean KL, share of clipped tokens); weight of each sequence's tokens.  The weights need the counts alone: only the first
-// block adds the float64 sums.
+// block adds the sums.
 __global__ void __launch_bounds__(POL_THREADS) policy_join_kernel(const PolicyPart* part, int parts, const int* counts, long long S,
                                                                   int per_sequence, float* stats, float* weight, uint32_t* err) {
   __shared__ PolicyPart join[POL_WARPS];
   grid_dependency_wait();
   grid_dependents_launch();
-  PolicyPart sum = {0.0, 0.0, 0.0, 0, 0};
+  PolicyPart sum = {};
+  constexpr int LOADS = (POL_MAX_BLOCKS + POL_THREADS - 1) / POL_THREADS;
+  PolicyPart p[LOADS];
 #pragma unroll
-  for (int k = 0; k < (POL_MAX_BLOCKS + POL_THREADS - 1) / POL_THREADS; ++k) {
+  for (int k = 0; k < LOADS; ++k) {
     const int i = threadIdx.x + k * POL_THREADS;
-    if (i >= parts) break;
+    p[k] = {};
+    if (i < parts) p[k] = part[i];
+  }
+#pragma unroll
+  for (int k = 0; k < LOADS; ++k) {
     if (blockIdx.x == 0) {
-      policy_join(sum, part[i]);
+      policy_join(sum, p[k]);
     } else {
-      sum.tokens += part[i].tokens;
-      sum.seqs += part[i].seqs;
+      sum.tokens += p[k].tokens;
+      sum.seqs += p[k].seqs;
     }
   }
   if (blockIdx.x == 0) {
@@ -318,9 +323,9 @@ __global__ void __launch_bounds__(POL_THREADS) policy_join_kernel(const PolicyPa
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     sum = join[0];
     for (int i = 1; i < POL_WARPS; ++i) policy_join(sum, join[i]);
-    stats[0] = static_cast<float>(sum.loss * f);
-    stats[1] = static_cast<float>(sum.kl * f);
-    stats[2] = static_cast<float>(sum.clipped * f);
+    stats[0] = static_cast<float>(sum.loss.value() * f);
+    stats[1] = static_cast<float>(sum.kl.value() * f);
+    stats[2] = static_cast<float>(sum.clipped.value() * f);
   }
   const long long s = static_cast<long long>(blockIdx.x) * POL_THREADS + threadIdx.x;
   if (s < S && in_bounds(err, s, 1, S, SITE_POLICY_OUT)) {
@@ -368,7 +373,8 @@ int policy_blocks(long long units) {
   return static_cast<int>(units < 1 ? 1 : units < POL_MAX_BLOCKS ? units : POL_MAX_BLOCKS);
 }
 
-// Warps a sequence: as many as leave each lane at most 16 tokens, up to a whole block.
+// Warps a sequence: as many as leave each lane at most 16 tokens, up to a whole block.  More of them for few sequences make more partial rows:
+// 1024 x 448 tokens forward 11.9 us with one warp, 13.2 with four.
 int policy_warps(long long T) {
   int w = 1;
   while (w < POL_WARPS && T > 512LL * w) w *= 2;
