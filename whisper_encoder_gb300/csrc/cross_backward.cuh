@@ -213,7 +213,8 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
 
   if (warp == 0) {
     if (elect_one()) {
-      int n = 0, c = 0;                      // steps, and items with steps, so far
+      uint32_t n = 0;                        // steps so far; may pass 32 bits, where its low ones go on as they should
+      int c = 0;                             // items with steps so far
       bool ok = true;
       for (int it = it_first; it < n_items && ok; it += it_step) {
         const Item i = item_at(it);
@@ -255,12 +256,14 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
       constexpr uint32_t IDESC_ACC = make_idesc(128, CRA_HD, 1u) | IDESC_B_MN;
       auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) { return mbar_wait(bar, parity, x.err, abort_flag, site); };
       bool ok = true;
-      int n = 0, c = 0, fixes = 0;
+      uint32_t n = 0;
+      int c = 0, fixes = 0;
       // the step before, whose sums are issued behind the scores of this one
-      int pn = -1, pc = 0, p_halves = 0;
-      bool p_first = false, p_last = false;
+      uint32_t pn = 0;
+      int pc = 0, p_halves = 0;
+      bool p_any = false, p_first = false, p_last = false;
       auto sums = [&]() -> bool {
-        if (pn < 0) return true;
+        if (!p_any) return true;
         const int st = pn % CRB_STAGES;
         if (!wait(&p_full[pn & 1], (pn >> 1) & 1, 45)) return false;
         if (p_first && !wait(acc_empty, (pc & 1) ^ 1u, 46)) return false;
@@ -278,7 +281,7 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
         }
         mma_commit(&empty[st]);
         if (p_last) mma_commit(acc_full);
-        pn = -1;
+        p_any = false;
         return true;
       };
       for (int it = it_first; it < n_items && ok; it += it_step) {
@@ -312,6 +315,7 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
           mma_commit(s_full);
           if (j + 1 == i.steps) mma_commit(&m_empty[slot]);
           ok = sums();
+          p_any = true;
           pn = n;
           pc = c;
           p_halves = halves;
@@ -339,7 +343,8 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, x.err, abort_flag, site));
     };
     bool ok = true;
-    int n = 0, c = 0;
+    uint32_t n = 0;
+    int c = 0;
 
     // results of an item: DKV: the first half's warps store dv, the second's dk; else 32 columns of dq - b M each
     auto finish = [&](const Item& i, int ci, float za, float zb) -> bool {
