@@ -210,6 +210,18 @@ def test_scores_of_minus_infinity(wb, Tq):
     assert bool(torch.isnan(out).all()) and bool((lse == -math.inf).all())
 
 
+@pytest.mark.parametrize("batch,Tq,Tk,H,Hk", [(4, 1, 1500, 8, 8), (3, 9, 700, 8, 2), (2, 64, 900, 4, 4), (2, 33, 500, 4, 1)])
+def test_gradients_of_few_rows_are_rounded_once(wb, batch, Tq, Tk, H, Hk):
+    # Half a step is 2^-8 of a value at most, so one rounding that spreads evenly is off by no more than 2^-8 / sqrt(3) of the values' norm
+    # (near 1.6 of 2.26 thousandths, since most values lie above a power of two).  P and dS rounded to bf16 too would add as much again
+    # in squares: 2.3 to 2.6 thousandths.
+    q, k, v, dout, _ = _data(batch, Tq, Tk, H, Hk, 31 + Tq)
+    got, ref = _both(wb, q, k, v, dout), _reference(q, k, v, dout)
+    for name in ("dk", "dv"):
+        off = float((got[name].double() - ref[name][0]).norm() / ref[name][0].norm())
+        assert off < 2.0 ** -8 / math.sqrt(3), (name, off)
+
+
 @pytest.mark.parametrize("scale", [1.0, 2.0 ** -20, 0.07])
 @pytest.mark.parametrize("Tq", [6, 100])
 def test_scales(wb, scale, Tq):
@@ -285,6 +297,7 @@ def test_same_call_same_bits_and_captured(wb, batch, Tq, Tk, H, Hk):
 
 
 def test_results_do_not_depend_on_the_rest_of_a_batch_of_many_rows(wb):
+    # too few keys for the rule that splits them where a batch has few tiles
     q, k, v, dout, _ = _data(3, 150, 300, 2, 2, 13)
     whole = _both(wb, q, k, v, dout)
     part = _both(wb, q[1:2], k[1:2], v[1:2], dout[1:2])

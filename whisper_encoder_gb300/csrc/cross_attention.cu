@@ -234,18 +234,20 @@ wb_status wb_cross_attention_backward(const void* dout, int64_t do_batch, int64_
   if (!rows_map(&qm, rq, batch, Tq, n_heads, CRB_M) || !rows_map(&dm, ro, batch, Tq, n_heads, CRB_M) ||
       !rows_map(&km, rk, batch, Tk, n_kv_heads, CRB_M) || !rows_map(&vm, rv, batch, Tk, n_kv_heads, CRB_M))
     return WB_ECUDA;
-  static uint64_t dq_done = 0, dkv_done = 0;
+  static uint64_t dq_done[2] = {}, dkv_done[2] = {};
   constexpr int SMEM = CrossBwdSmem::TOTAL;
-  WB_CUDA(allow_smem(cross_bwd_kernel<false>, SMEM, &dq_done));
-  WB_CUDA(allow_smem(cross_bwd_kernel<true>, SMEM, &dkv_done));
+  const bool few_keys = Tk <= CRB_STEP / 2, few_rows = Tq <= CRB_STEP / 2;
+  auto dq_kernel = few_keys ? cross_bwd_kernel<false, true> : cross_bwd_kernel<false, false>;
+  auto dkv_kernel = few_rows ? cross_bwd_kernel<true, true> : cross_bwd_kernel<true, false>;
+  WB_CUDA(allow_smem(dq_kernel, SMEM, &dq_done[few_keys]));
+  if (dk) WB_CUDA(allow_smem(dkv_kernel, SMEM, &dkv_done[few_rows]));
   const long long q_items = static_cast<long long>(batch) * n_heads * ((Tq + CRB_M - 1) / CRB_M);
   const long long k_items = static_cast<long long>(batch) * n_kv_heads * ((Tk + CRB_M - 1) / CRB_M);
   p.x.splits = tile_splits(q_items, Tk, sms);
   const unsigned q_grid = p.x.splits > 1 ? static_cast<unsigned>(q_items) * p.x.splits : static_cast<unsigned>(q_items < sms ? q_items : sms);
-  WB_CUDA(launch_split(cross_bwd_kernel<false>, q_grid, CRB_THREADS, SMEM, p.x.splits, s, qm, dm, km, vm, p));
+  WB_CUDA(launch_split(dq_kernel, q_grid, CRB_THREADS, SMEM, p.x.splits, s, qm, dm, km, vm, p));
   if (dk)
-    WB_CUDA(launch_pdl(cross_bwd_kernel<true>, dim3(static_cast<unsigned>(k_items < sms ? k_items : sms)), dim3(CRB_THREADS), SMEM, s, km, vm,
-                       qm, dm, p));
+    WB_CUDA(launch_pdl(dkv_kernel, dim3(static_cast<unsigned>(k_items < sms ? k_items : sms)), dim3(CRB_THREADS), SMEM, s, km, vm, qm, dm, p));
   return WB_OK;
 }
 

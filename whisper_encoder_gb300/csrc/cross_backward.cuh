@@ -6,8 +6,8 @@
 // CTA in a fixed order and nothing is added through memory (one kernel for all three would save two of seven products
 // and add dq of every key tile to float32 memory, in an order that changes).
 //   cross_stats_kernel        -lse / scale and -sum_e dout out of every row, -infinity and 0 for rows that take no part: their P is 0
-//   cross_bwd_kernel<false>   128 query rows an item, 128 keys a step: S = Q K^T, dP = dO V^T -> dQ += dS K, M += P K
-//   cross_bwd_kernel<true>    128 keys an item, 128 query rows a step: S^T = K Q^T, dP^T = V dO^T (lane = key) ->
+//   cross_bwd_kernel<false,.> 128 query rows an item, 128 keys a step: S = Q K^T, dP = dO V^T -> dQ += dS K, M += P K
+//   cross_bwd_kernel<true,.>  128 keys an item, 128 query rows a step: S^T = K Q^T, dP^T = V dO^T (lane = key) ->
 //                             dV += P^T dO, dK += dS^T Q
 // P and dS go as packed bf16 over the TMEM columns S came from and are read there as A operands; the step's tiles are read both as
 // K-major and as MN-major B tiles of the same shared memory, so nothing is transposed.
@@ -21,7 +21,9 @@
 // item a CTA, two CTAs an SM, 419).
 // Warp 0 lane 0 loads, warp 1 issues, warps 2-17 run the softmax: 16 rows of half of the columns each.
 //
-// Numbers.  Sums are float32; P and dS are rounded to bf16 once each, as operands beside bf16 q, k and dout.  delta is sum_e dout out as well,
+// Numbers.  Sums are float32; P and dS are rounded to bf16 once each, as operands beside bf16 q, k and dout (with 64 rows or keys
+// or fewer that side's free half of S takes what that leaves as a second operand: dk and dv of few rows 2.4e-3 -> 1.7e-3 from 64 bits; as a branch in the
+// one kernel it cost 25 % of every size).  delta is sum_e dout out as well,
 // but out is rounded to bf16, and what that leaves is the same for all keys of a row: it does not average out (dq and dk were 3.3e-3 of
 // their norm from 64 bits, 2.4e-3 without it).  With d' that delta, b = sum_k P (dP - d') is what it lacks, since sum_k P = 1: the dq
 // kernel subtracts b M, M = sum_k P k, and hands delta = d' + b to the dkv kernel.
@@ -57,7 +59,7 @@ struct CrossBwdParams {
   int do_items;              // as q_items, for dout
   float* stats;              // [batch][H][2][stats_ld]: -lse / scale, -delta
   int stats_ld;              // Tq rounded up to 128
-  int want_dq;               // cross_bwd_kernel<false>: 0: delta alone
+  int want_dq;               // cross_bwd_kernel<false,.>: 0: delta alone
   __nv_bfloat16* dq;         // [batch][Tq][H 64]
   __nv_bfloat16* dk;         // [batch][Tk][Hk 64]
   __nv_bfloat16* dv;
@@ -120,7 +122,8 @@ __global__ void __launch_bounds__(256) cross_stats_kernel(const __grid_constant_
 }
 
 // own0, own1: K and V (DKV) or Q and dO; step0, step1: Q and dO (DKV) or K and V.  Boxes of 64 x 128 rows.
-template <bool DKV>
+// TWICE: the step side has 64 rows or fewer in all.
+template <bool DKV, bool TWICE>
 __global__ void __launch_bounds__(CRB_THREADS, 1)
     cross_bwd_kernel(const __grid_constant__ CUtensorMap own0, const __grid_constant__ CUtensorMap own1,
                      const __grid_constant__ CUtensorMap step0, const __grid_constant__ CUtensorMap step1,
@@ -273,10 +276,10 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
         if (DKV || p.want_dq) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            if (k >= 4 && p_halves < 2) break;
-            const uint32_t a = src + k / 4 * 64 + k % 4 * 8;
-            mma_f16_tmem_a_lo<IDESC_ACC>(acc, a, n1 + k * (2048 >> 4), !p_first || k != 0);
-            mma_f16_tmem_a_lo<IDESC_ACC>(acc + CRA_HD, a + 32, n0 + k * (2048 >> 4), !p_first || k != 0);
+            if (!TWICE && k >= 4 && p_halves < 2) break;
+            const uint32_t a = src + k / 4 * 64 + k % 4 * 8, b = (TWICE ? k % 4 : k) * (2048 >> 4);
+            mma_f16_tmem_a_lo<IDESC_ACC>(acc, a, n1 + b, !p_first || k != 0);
+            mma_f16_tmem_a_lo<IDESC_ACC>(acc + CRA_HD, a + 32, n0 + b, !p_first || k != 0);
           }
         }
         mma_commit(&empty[st]);
@@ -470,25 +473,28 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
         }
         if (!wait(s_full, n & 1, 54)) { ok = false; break; }
         tc_fence_after();
-        if (rows > 64 * half) {
+        // TWICE: the second half's warps form the same P and dS, and store what rounding them left
+        const int cols = TWICE ? 0 : 64 * half;      // this warp's first column
+        if (rows > cols) {
           // s[4k], s[4k+1]: own row ra, columns 8k + cq, + 1; s[4k+2], s[4k+3]: row ra + 8
           const uint32_t s_tm = tmem + lane_off + (n & 1) * CRB_TM_S;
           uint32_t s[32], d[32];
-          tmem_ld_16x256b_x8(s_tm + 64 * half, s);
-          tmem_ld_16x256b_x8(tmem + lane_off + CRB_TM_D + 64 * half, d);
+          tmem_ld_16x256b_x8(s_tm + cols, s);
+          tmem_ld_16x256b_x8(tmem + lane_off + CRB_TM_D + cols, d);
           tmem_ld_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(d_free);
-          if (!DKV && rows < 64 * half + 64) {
+          if (!DKV && rows < cols + 64) {
             // keys that take no part: P = 0 from a score of -infinity, and dS = 0
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                if (64 * half + 8 * kk + cq + (e & 1) >= rows) s[4 * kk + e] = 0xff800000u;
+                if (cols + 8 * kk + cq + (e & 1) >= rows) s[4 * kk + e] = 0xff800000u;
           }
-          const float2* stats = reinterpret_cast<const float2*>(smem + S::OFF_STATS + st * S::STATS_BYTES) + 32 * half + t;
+          const float2* stats = reinterpret_cast<const float2*>(smem + S::OFF_STATS + st * S::STATS_BYTES) + cols / 2 + t;
+          const bool rest = TWICE && half;
           uint32_t pw[16], dw[16];
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
@@ -509,17 +515,23 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
               f32x2_unpack(f32x2_mul(f32x2_add(sv, nl), c2), a, e);
               a = ex2_approx(a);
               e = ex2_approx(e);
-              pw[2 * kk + e8] = pack_bf16(a, e);
+              uint32_t w = pack_bf16(a, e);
+              pw[2 * kk + e8] = rest ? pack_bf16_rest(a, e, w) : w;
               const uint64_t ds = f32x2_mul(f32x2_add(dv, nd), f32x2_pack(a, e));
-              if (!DKV) {
+              if (!DKV && !rest) {
                 if (e8) bb2 = f32x2_add(bb2, ds);
                 else ba2 = f32x2_add(ba2, ds);
               }
               f32x2_unpack(ds, a, e);
-              dw[2 * kk + e8] = pack_bf16(a, e);
+              w = pack_bf16(a, e);
+              dw[2 * kk + e8] = rest ? pack_bf16_rest(a, e, w) : w;
             }
           }
-          // over the 64 columns of S that this warp has read
+          // over the 64 columns of S that this warp has read (or that are free); shared columns once all warps have read them
+          if (TWICE && !half) {
+            if (!wait(d_free, n & 1, 55)) { ok = false; break; }
+            tc_fence_after();
+          }
           tmem_st_16x128b_x8(s_tm + 64 * half, pw);
           tmem_st_16x128b_x8(s_tm + 64 * half + 32, dw);
           tmem_st_wait();

@@ -671,6 +671,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// What rounding (lo, hi) to bf16, packed in w, has left, as bf16.
+__device__ __forceinline__ uint32_t pack_bf16_rest(float lo, float hi, uint32_t w) {
+  return pack_bf16(lo - __uint_as_float(w << 16), hi - __uint_as_float(w & 0xffff0000u));
+}
+
 // Two floats -> two E4M3 codes (round to nearest even, saturate to +-448), packed in 16 bits.
 __device__ __forceinline__ uint16_t cvt_e4m3x2(float lo, float hi) {
   uint16_t r;
