@@ -222,6 +222,46 @@ def test_gradients_of_few_rows_are_rounded_once(wb, batch, Tq, Tk, H, Hk):
         assert off < 2.0 ** -8 / math.sqrt(3), (name, off)
 
 
+@pytest.mark.parametrize("Tq,Tk", [(150, 300), (40, 2500), (200, 60)])
+def test_keys_with_a_large_common_part(wb, Tq, Tk):
+    # dq = scale sum_k dS k, and sum_k dS = 0: what all keys share takes no part.  The kernel subtracts (sum_k dS) M, M = sum_k P k, from what it
+    # sums, dS rounded in both, so whatever dS is off by adds up along k - M: half a step, P's relative error and the errors of dP and
+    # delta.  Along k itself: the sums in fp32, and M's P being rounded, times the sum of dS.
+    q, k, v, dout, _ = _data(2, Tq, Tk, 2, 2, 7 + Tk)
+    k = k.clone()
+    k.view(2, Tk, 2, 64)[..., :8] += 48
+    got = _both(wb, q, k, v, dout)
+    heads = lambda x: x.double().view(2, -1, 2, 64).transpose(1, 2)  # noqa: E731
+    qh, kh, vh, do = heads(q), heads(k), heads(v), heads(dout)
+    s = 0.125 * (qh @ kh.mT)
+    es = 2 * SUM * 0.125 * (qh.abs() @ kh.abs().mT).amax(-1, keepdim=True)
+    p = torch.softmax(s, -1)
+    rel = torch.expm1(2 * es + 2.0 ** -20 * (2 * s.abs().amax(-1, keepdim=True) + 10))
+    out = p @ vh
+    e_delta = (do.abs() * (2 * HALF + 3 * rel) * (p @ vh.abs())).sum(-1, keepdim=True)
+    ds = p * (do @ vh.mT - (do * out).sum(-1, keepdim=True))
+    e_ds = (HALF + rel) * ds.abs() + (1 + rel) * p * (SUM * (do.abs() @ vh.abs().mT) + e_delta)
+    m = p @ kh
+    dq = 0.125 * (ds @ kh)
+    sum_ds = e_ds.sum(-1, keepdim=True)
+    away = torch.cat([(e_ds[:, :, t:t + 50, :, None] * (kh[:, :, None] - m[:, :, t:t + 50, None]).abs()).sum(-2) for t in range(0, Tq, 50)], 2)
+    off = 0.125 * (away + SUM * (ds.abs() @ kh.abs()) + sum_ds * (HALF + 2 * SUM) * (p @ kh.abs())) + HALF * dq.abs()
+    over = (heads(got["dq"]) - dq).abs() / off
+    assert float(over.max()) <= 1, float(over.max())
+
+
+@pytest.mark.parametrize("Tq,Tk", [(1, 1), (5, 1), (150, 1), (70, 64), (150, 1500)])
+def test_one_key(wb, Tq, Tk):
+    # its weight is 1 whatever q and k are: no gradient reaches them, and out is its v
+    q, k, v, dout, _ = _data(3, Tq, Tk, 4, 2, Tq, 4.0)
+    lens = torch.tensor([1, Tk, 1], dtype=torch.int32, device=DEV)
+    got = _both(wb, q, k, v, dout, kv_lens=lens)
+    _check(got, _reference(q, k, v, dout, kv_lens=lens))
+    for i in (0, 2):
+        assert not got["dq"][i].any() and not got["dk"][i].any()
+        assert torch.equal(got["out"][i].view(Tq, 2, 2, 64), v[i, :1].reshape(1, 2, 1, 64).expand(Tq, 2, 2, 64))
+
+
 @pytest.mark.parametrize("scale", [1.0, 2.0 ** -20, 0.07])
 @pytest.mark.parametrize("Tq", [6, 100])
 def test_scales(wb, scale, Tq):

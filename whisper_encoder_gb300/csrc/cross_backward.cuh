@@ -26,7 +26,9 @@
 // one kernel it cost 25 % of every size).  delta is sum_e dout out as well,
 // but out is rounded to bf16, and what that leaves is the same for all keys of a row: it does not average out (dq and dk were 3.3e-3 of
 // their norm from 64 bits, 2.4e-3 without it).  With d' that delta, b = sum_k P (dP - d') is what it lacks, since sum_k P = 1: the dq
-// kernel subtracts b M, M = sum_k P k, and hands delta = d' + b to the dkv kernel.
+// kernel hands delta = d' + b to the dkv kernel, and subtracts b' M from dq, M = sum_k P k and b' the sum of dS as it was rounded: what rounding
+// leaves then adds up along k - M alone, which is small where a row's weight lies on one key (dq of sharp rows 2.6e-3 -> 2.1e-3).
+// Rows of one key have P = 1 whatever q and k are: their dq and that key's dk are 0, not what rounding leaves.
 // Rows past their item's lengths may hold anything: a step's are cleared in shared memory before its products, an item's own reach only
 // results that are not stored.
 #pragma once
@@ -45,10 +47,10 @@ struct CrossBwdSmem {
   static constexpr int STATS_BYTES = 2 * CRB_STEP * 4;      // dkv: -lse / scale, then -delta, of the step's rows
   static constexpr int OFF_STEP = 4 * TILE;                 // the own tiles have two slots
   static constexpr int OFF_STATS = OFF_STEP + CRB_STAGES * 2 * TILE;
-  static constexpr int OFF_B = OFF_STATS + CRB_STAGES * STATS_BYTES;    // dq: b by [item parity][column half][row]
-  static constexpr int OFF_BAR = OFF_B + 2 * 2 * CRB_M * 4;
+  static constexpr int OFF_B = OFF_STATS + CRB_STAGES * STATS_BYTES;    // dq: b and b' by [item parity][column half][row]
+  static constexpr int OFF_BAR = OFF_B + 2 * 2 * CRB_M * 8;
   static constexpr int TOTAL = 1024 + OFF_BAR + 512;
-  // dq: a split's share, over the rings when they are done: rows of 64 floats of M, 64 of dQ, and b
+  // dq: a split's share, over the rings when they are done: rows of 64 floats of M, 64 of dQ, b and b'
   static constexpr int SHARE_LD = 2 * CRA_HD + 4;
 };
 static_assert(CrossBwdSmem::TOTAL <= 227 * 1024, "one CTA an SM");
@@ -340,7 +342,7 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
     const uint32_t lane_off = static_cast<uint32_t>(lane_base) << 16;
     const int t = lane & 3, cq = 2 * t;
     const int ra = lane_base + (lane >> 2);          // this thread's own rows: ra and ra + 8
-    float* const b_part = reinterpret_cast<float*>(smem + S::OFF_B);
+    float2* const b_part = reinterpret_cast<float2*>(smem + S::OFF_B);
     const uint64_t c2 = f32x2_pack(x.c, x.c);
     auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, x.err, abort_flag, site));
@@ -349,13 +351,13 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
     uint32_t n = 0;
     int c = 0;
 
-    // results of an item: DKV: the first half's warps store dv, the second's dk; else 32 columns of dq - b M each
+    // results of an item: DKV: the first half's warps store dv, the second's dk; else 32 columns of dq - b' M each
     auto finish = [&](const Item& i, int ci, float za, float zb) -> bool {
       const bool any = i.steps > 0;
       uint32_t v[32];
 #pragma unroll
       for (int k = 0; k < 32; ++k) v[k] = 0;
-      float ba = 0.0f, bb = 0.0f;
+      float2 ba = {}, bb = {};
       // a split's 32 columns of M and dQ, for the join behind the roles
       auto share = [&](const uint32_t (&m)[16], const uint32_t (&d)[16]) {
         float* at = reinterpret_cast<float*>(smem + S::OFF_STEP) + ra * S::SHARE_LD + half * 32 + cq;
@@ -369,15 +371,15 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
       if (any) {
         if (!DKV) {
           if (!wait(b_full, ci & 1, 51)) return false;
-          const float* b_of = b_part + (ci & 1) * 2 * CRB_M;
-          ba = b_of[ra] + b_of[CRB_M + ra];
-          bb = b_of[ra + 8] + b_of[CRB_M + ra + 8];
+          const float2* b_of = b_part + (ci & 1) * 2 * CRB_M + ra;
+          ba = make_float2(b_of[0].x + b_of[CRB_M].x, b_of[0].y + b_of[CRB_M].y);
+          bb = make_float2(b_of[8].x + b_of[CRB_M + 8].x, b_of[8].y + b_of[CRB_M + 8].y);
         }
         if (!DKV && splits == 1) {
           const long long si = (static_cast<long long>(i.b) * x.H + i.h) * 2 * p.stats_ld + p.stats_ld + i.r0 + ra;
           if (half == 0 && t < 2 && i.r0 + ra + 8 * t < i.own_len &&
               in_bounds(x.err, si, 9, static_cast<long long>(x.batch) * x.H * 2 * p.stats_ld, SITE_CROSS_STATS))
-            p.stats[si + 8 * t] = t ? zb - bb : za - ba;         // -delta
+            p.stats[si + 8 * t] = t ? zb - bb.x : za - ba.x;         // -delta
         }
         if (!wait(acc_full, ci & 1, 52)) return false;
         tc_fence_after();
@@ -392,7 +394,7 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
           if (splits > 1) share(m, d);
 #pragma unroll
           for (int k = 0; k < 16; ++k)
-            v[k] = __float_as_uint(fmaf(-(k & 2 ? bb : ba), __uint_as_float(m[k]), __uint_as_float(d[k])));
+            v[k] = __float_as_uint(fmaf(-(k & 2 ? bb.y : ba.y), __uint_as_float(m[k]), __uint_as_float(d[k])));
         }
         tmem_ld_wait();
         tc_fence_before();
@@ -406,14 +408,14 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
         }
         if (half == 0 && t == 0) {
           float* b_at = reinterpret_cast<float*>(smem + S::OFF_STEP) + ra * S::SHARE_LD + 2 * CRA_HD;
-          b_at[0] = ba;
-          b_at[8 * S::SHARE_LD] = bb;
+          *reinterpret_cast<float2*>(b_at) = ba;
+          *reinterpret_cast<float2*>(b_at + 8 * S::SHARE_LD) = bb;
         }
         return true;
       }
       if (!DKV && !p.want_dq) return true;
       __nv_bfloat16* const dst = !DKV ? p.dq : half ? p.dk : p.dv;
-      const float k = DKV && half == 0 ? 1.0f : x.scale;
+      const float k = DKV && half == 0 ? 1.0f : (DKV ? i.own_len : i.step_len) == 1 ? 0.0f : x.scale;
       const long long ld = static_cast<long long>(heads) * CRA_HD;
       const long long extent = static_cast<long long>(x.batch) * own_T * ld;
 #pragma unroll
@@ -456,6 +458,7 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
         }
       }
       uint64_t ba2 = 0, bb2 = 0;                     // this thread's share of b of the two rows
+      float bra = 0.0f, brb = 0.0f;                  // this thread's share of b'
       int t0 = i.t_first;
       for (int j = 0; j < i.steps; ++j, ++n) {
         const int st = n % CRB_STAGES;
@@ -537,11 +540,27 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[n & 1]);
+          if (!DKV) {                                // b', while the products run: 3 % of the backward pass; with mma.sync and ones 11 %
+            uint64_t u0 = 0, u1 = 0;
+#pragma unroll
+            for (int m = 0; m < 16; m += 2) {
+              u0 = f32x2_add(u0, f32x2_pack(__uint_as_float(dw[m] << 16), __uint_as_float(dw[m] & 0xffff0000u)));
+              u1 = f32x2_add(u1, f32x2_pack(__uint_as_float(dw[m + 1] << 16), __uint_as_float(dw[m + 1] & 0xffff0000u)));
+            }
+            float y0, y1, y2, y3;
+            f32x2_unpack(u0, y0, y1);
+            f32x2_unpack(u1, y2, y3);
+            bra += y0 + y1;
+            brb += y2 + y3;
+          }
         } else {
           __syncwarp();
-          if (lane == 0) mbar_arrive(d_free);
+          if (lane == 0) {
+            mbar_arrive(d_free);
+            mbar_arrive(&p_full[n & 1]);
+          }
         }
-        if (lane == 0) mbar_arrive(&p_full[n & 1]);
         if (last_c >= 0) {
           if (!finish(last, last_c, last_za, last_zb)) { ok = false; break; }
           last_c = -1;
@@ -560,10 +579,14 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
         bb += __shfl_xor_sync(0xffffffffu, bb, 1);
         ba += __shfl_xor_sync(0xffffffffu, ba, 2);
         bb += __shfl_xor_sync(0xffffffffu, bb, 2);
-        float* b_of = b_part + (c & 1) * 2 * CRB_M + half * CRB_M;
+        bra += __shfl_xor_sync(0xffffffffu, bra, 1);
+        brb += __shfl_xor_sync(0xffffffffu, brb, 1);
+        bra += __shfl_xor_sync(0xffffffffu, bra, 2);
+        brb += __shfl_xor_sync(0xffffffffu, brb, 2);
+        float2* b_of = b_part + (c & 1) * 2 * CRB_M + half * CRB_M + ra;
         if (t == 0) {
-          b_of[ra] = ba;
-          b_of[ra + 8] = bb;
+          b_of[0] = make_float2(ba, bra);
+          b_of[8] = make_float2(bb, brb);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(b_full);
@@ -581,7 +604,7 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, CRB_TM_COLS);
   if (DKV || splits == 1) return;
-  // the shares of an item's splits, a part of the rows each: dq = scale (sum dQ - (sum b) (sum M)), -delta less b
+  // the shares of an item's splits, a part of the rows each: dq = scale (sum dQ - (sum b') (sum M)), -delta less b
   cluster_sync();
   const Item i = item_at(it_first);
   const int r0 = CRB_M * rank / splits, r1 = CRB_M * (rank + 1) / splits;
@@ -605,15 +628,16 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
       m[0] = make_float4(m[0].x + m[q].x, m[0].y + m[q].y, m[0].z + m[q].z, m[0].w + m[q].w);
       d[0] = make_float4(d[0].x + d[q].x, d[0].y + d[q].y, d[0].z + d[q].z, d[0].w + d[q].w);
       b[0].x += b[q].x;
+      b[0].y += b[q].y;
     }
     const bool there = row < i.own_len;
     const long long si = (static_cast<long long>(i.b) * x.H + i.h) * 2 * p.stats_ld + p.stats_ld + row;
     if (e == 0 && there && in_bounds(x.err, si, 1, static_cast<long long>(x.batch) * x.H * 2 * p.stats_ld, SITE_CROSS_STATS))
       p.stats[si] -= b[0].x;
     if (!p.want_dq) continue;
-    const float f = -b[0].x;
-    const uint32_t w0 = pack_bf16(x.scale * fmaf(f, m[0].x, d[0].x), x.scale * fmaf(f, m[0].y, d[0].y));
-    const uint32_t w1 = pack_bf16(x.scale * fmaf(f, m[0].z, d[0].z), x.scale * fmaf(f, m[0].w, d[0].w));
+    const float f = -b[0].y, c = i.step_len == 1 ? 0.0f : x.scale;
+    const uint32_t w0 = pack_bf16(c * fmaf(f, m[0].x, d[0].x), c * fmaf(f, m[0].y, d[0].y));
+    const uint32_t w1 = pack_bf16(c * fmaf(f, m[0].z, d[0].z), c * fmaf(f, m[0].w, d[0].w));
     const long long o = (static_cast<long long>(i.b) * own_T + row) * ld + i.h * CRA_HD + e;
     if (in_bounds(x.err, o, 4, static_cast<long long>(x.batch) * own_T * ld, SITE_CROSS_OUT))
       *reinterpret_cast<uint2*>(p.dq + o) = there ? make_uint2(w0, w1) : make_uint2(0u, 0u);
