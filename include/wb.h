@@ -477,9 +477,10 @@ wb_status wb_linear_distill_backward(const float* dloss, const void* x, const vo
  *    item's own, also where a batch stride of 0 gave all items the same rows.  All contiguous,
  *    written whole, overlapping neither an input nor each other.
  *  - dq may be NULL, and dk and dv both: not wanted.
+ *  - A row of one key has p = 1 whatever q and k are: its dq, and dk of an item of one key, are 0.
  * Scores, sums, statistics and accumulators are float32; exp(s - max) and the gradient of s are rounded to
- * bf16 once each, as operands.  All sums run in a fixed order: the same call gives the same bits (another batch
- * size may split the keys of few rows differently).
+ * bf16 once each, as operands (the backward pass of 64 rows or keys or fewer keeps what that leaves).  All sums run in a
+ * fixed order: the same call gives the same bits (another batch size may split the keys of a row differently).
  * Tq, Tk: 0 to 2^24, H up to 1024; scale from 2^-64 to 2^64.  q, k, v, dout, out, dq, dk, dv and the workspace:
  * 16-byte aligned; lse and lengths: 4.  WB_EINVAL for bad sizes, strides, pointers or alignment, WB_EWORKSPACE for a
  * missing, small or unaligned workspace.  Two calls that may overlap on the GPU need a workspace each. */

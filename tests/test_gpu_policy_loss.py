@@ -87,6 +87,34 @@ def test_against_float64(wb, S, T, per_sequence, per_token):
     _check(_run(wb, data, per_sequence), _reference(*data, 0.2, 0.28, 0.1, per_sequence), data[-1])
 
 
+def _moved(t, elements):
+    flat = torch.empty(t.numel() + elements, dtype=t.dtype, device=DEV)[elements:]
+    return flat.copy_(t.reshape(-1)).view(t.shape)
+
+
+# four tokens side by side where T is a multiple of 4 and every tensor lies on 16 bytes; one by one else
+@pytest.mark.parametrize("S,T", [(200, 448), (131, 4), (300, 36), (7, 1028), (3, 4100), (2, 20000)])
+@pytest.mark.parametrize("per_token,with_ref", [(False, True), (True, True), (False, False), (True, False)])
+def test_tokens_on_and_off_16_bytes(wb, S, T, per_token, with_ref):
+    data = _data(S, T, 2 * S + T, per_token)
+    beta = 0.1 if with_ref else 0.0
+    if not with_ref:
+        data = data[:2] + (None,) + data[3:]
+    want = _reference(*data, 0.2, 0.28, beta, False)
+    first = _run(wb, data, False, beta=beta)
+    _check(first, want, data[-1])
+    for moved in range(5):
+        off = tuple(_moved(t, 1) if i == moved and t is not None else t for i, t in enumerate(data))
+        got = _run(wb, off, False, beta=beta)
+        _check(got, want, data[-1])
+        assert torch.equal(got[2], first[2])                    # a token's gradient does not depend on the path
+    nll, old, ref, adv, labels = (None if t is None else t.clone() for t in data)
+    for t in (nll, old) + ((ref,) if with_ref else ()) + ((adv,) if per_token else ()):
+        t[labels < 0] = math.nan
+    for a, b in zip(first, _run(wb, (nll, old, ref, adv, labels), False, beta=beta)):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("lo,hi,beta,with_ref", [(0.0, 0.0, 0.0, False), (1.0, 0.2, 0.0, True), (0.2, 1e30, 1.0, True), (0.1, 0.1, -0.3, True)])
 def test_options(wb, lo, hi, beta, with_ref):
     nll, old, ref, adv, labels = _data(20, 100, 3)

@@ -66,17 +66,25 @@ __device__ __forceinline__ float exp_minus_x_minus_1(float x, float em1) {
   return fabsf(x) < 0.5f ? 0.5f * x * x * p : em1 - x;
 }
 
+// What the sign of an advantage decides, once a sequence where it is the sequence's: clipped is sign d above border.
+struct Side {
+  float adv, sign, b0, b1;   // border: value and what its rounding left
+  float held;                // a clipped token's loss
+};
+__device__ __forceinline__ Side policy_side(const PolicyArgs& a, float adv) {
+  const bool up = adv > 0.0f;
+  return Side{adv, up ? 1.0f : adv < 0.0f ? -1.0f : 0.0f, up ? a.hi0 : -a.lo0, up ? a.hi1 : -a.lo1, -(up ? a.hold_hi : a.hold_lo) * adv};
+}
+
 template <bool REF>
-__device__ __forceinline__ Token policy_token(const PolicyArgs& a, float nll, float old_nll, float ref, float adv) {
+__device__ __forceinline__ Token policy_token(const PolicyArgs& a, const Side& k, float nll, float old_nll, float ref) {
   Token t;
-  const float d = old_nll - nll;
+  const float d = old_nll - nll, ds = d * k.sign;
   const float bb = d - old_nll;
-  const float e = (old_nll - (d - bb)) - (nll + bb);     // d + e is the difference itself
-  const bool above = (d > a.hi0) | ((d == a.hi0) & (e > a.hi1));
-  const bool below = (d < a.lo0) | ((d == a.lo0) & (e < a.lo1));
-  t.clipped = ((adv > 0.0f) & above) | ((adv < 0.0f) & below);
-  const float ra = adv == 0.0f ? 0.0f : expf(d) * adv;
-  t.loss = t.clipped ? -(adv > 0.0f ? a.hold_hi : a.hold_lo) * adv : -ra;
+  const float e = (old_nll - (d - bb)) - (nll + bb);       // d + e is the difference itself
+  t.clipped = (ds > k.b0) | ((ds == k.b0) & (e * k.sign > k.b1));
+  const float ra = k.adv == 0.0f ? 0.0f : expf(d) * k.adv;
+  t.loss = t.clipped ? k.held : -ra;
   t.grad = t.clipped ? 0.0f : ra;
   t.kl = 0.0f;
   if (REF) {
@@ -89,6 +97,49 @@ __device__ __forceinline__ Token policy_token(const PolicyArgs& a, float nll, fl
     }
   }
   return t;
+}
+
+// Tokens at..at + 3 * step, as many as `there` says; VEC: side by side, on 16 bytes.  A label counts by its sign, which is in its upper word.
+template <bool REF, bool VEC, bool TOK>
+__device__ __forceinline__ void load4(const PolicyArgs& a, long long at, int step, const bool (&there)[4], int (&lab)[4], float (&nll)[4],
+                                      float (&old)[4], float (&ref)[4], float (&adv)[4]) {
+  const int* hi = reinterpret_cast<const int*>(a.labels) + 1;
+  if (VEC) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lab[i] = -1;
+      nll[i] = old[i] = ref[i] = 0.0f;
+      if (TOK) adv[i] = 0.0f;
+    }
+    if (!there[0] || !in_bounds(a.err, at, 4, a.S * a.T, SITE_POLICY_IN)) return;
+    const int4 l0 = *reinterpret_cast<const int4*>(a.labels + at), l1 = *reinterpret_cast<const int4*>(a.labels + at + 2);
+    const float4 n = *reinterpret_cast<const float4*>(a.nll + at), o = *reinterpret_cast<const float4*>(a.old_nll + at);
+    lab[0] = l0.y; lab[1] = l0.w; lab[2] = l1.y; lab[3] = l1.w;
+    nll[0] = n.x; nll[1] = n.y; nll[2] = n.z; nll[3] = n.w;
+    old[0] = o.x; old[1] = o.y; old[2] = o.z; old[3] = o.w;
+    if (REF) {
+      const float4 r = *reinterpret_cast<const float4*>(a.ref_nll + at);
+      ref[0] = r.x; ref[1] = r.y; ref[2] = r.z; ref[3] = r.w;
+    }
+    if (TOK) {
+      const float4 v = *reinterpret_cast<const float4*>(a.adv + at);
+      adv[0] = v.x; adv[1] = v.y; adv[2] = v.z; adv[3] = v.w;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const long long t = at + static_cast<long long>(i) * step;
+    lab[i] = -1;
+    nll[i] = old[i] = ref[i] = 0.0f;
+    if (TOK) adv[i] = 0.0f;
+    if (!there[i] || !in_bounds(a.err, t, 1, a.S * a.T, SITE_POLICY_IN)) continue;
+    lab[i] = hi[2 * t];
+    nll[i] = a.nll[t];
+    old[i] = a.old_nll[t];
+    if (REF) ref[i] = a.ref_nll[t];
+    if (TOK) adv[i] = a.adv[t];
+  }
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -127,36 +178,35 @@ struct SeqSum {
 };
 
 // This warp's share of a sequence, in every lane: warp `part` of W.  No branches among the tokens of a step: they overlap.
-template <int W, bool REF>
-__device__ __forceinline__ SeqSum policy_sequence(const PolicyArgs& a, long long s, int part) {
+template <bool REF, bool VEC, bool TOK>
+__device__ __forceinline__ SeqSum policy_sequence(const PolicyArgs& a, long long s, int part, int W) {
   SeqSum r = {0.0f, 0.0f, 0, 0};
-  const long long base = s * a.T, n_el = a.S * a.T;
-  const float adv_s = a.adv_tok == 0 && in_bounds(a.err, s, 1, a.S, SITE_POLICY_IN) ? a.adv[s] : 0.0f;
-  const int T = static_cast<int>(a.T);
-  for (int t0 = part * 32 + static_cast<int>(lane_id()); t0 < T; t0 += W * 32 * POL_SUM_TILE) {
-    const long long at = base + t0;
-    bool on[POL_SUM_TILE];
-    float nll[POL_SUM_TILE], old[POL_SUM_TILE], ref[POL_SUM_TILE], adv[POL_SUM_TILE];
+  const long long base = s * a.T;
+  const Side side_s = policy_side(a, !TOK && in_bounds(a.err, s, 1, a.S, SITE_POLICY_IN) ? a.adv[s] : 0.0f);
+  constexpr int GROUPS = POL_SUM_TILE / 4;
+  const int T = static_cast<int>(a.T), first = (part * 32 + static_cast<int>(lane_id())) * (VEC ? 4 : 1);
+  const int step = VEC ? 1 : W * 32, group = W * 32 * 4;                        // between a lane's tokens, and its groups of four
+  for (int t0 = first; t0 < T; t0 += GROUPS * group) {
+    int lab[GROUPS][4];
+    float nll[GROUPS][4], old[GROUPS][4], ref[GROUPS][4], adv[GROUPS][4];
 #pragma unroll
-    for (int i = 0; i < POL_SUM_TILE; ++i) {
-      on[i] = false;
-      nll[i] = old[i] = ref[i] = 0.0f;
-      adv[i] = adv_s;
-      if (i * W * 32 < T - t0 && in_bounds(a.err, at + i * W * 32, 1, n_el, SITE_POLICY_IN)) {
-        on[i] = a.labels[at + i * W * 32] >= 0;
-        nll[i] = a.nll[at + i * W * 32];
-        old[i] = a.old_nll[at + i * W * 32];
-        if (REF) ref[i] = a.ref_nll[at + i * W * 32];
-        if (a.adv_tok) adv[i] = a.adv[at + i * W * 32];
-      }
+    for (int g = 0; g < GROUPS; ++g) {
+      bool there[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) there[i] = g * group + i * step < T - t0;
+      load4<REF, VEC, TOK>(a, base + t0 + g * group, step, there, lab[g], nll[g], old[g], ref[g], adv[g]);
     }
 #pragma unroll
-    for (int i = 0; i < POL_SUM_TILE; ++i) {
-      const Token k = policy_token<REF>(a, nll[i], old[i], ref[i], adv[i]);
-      r.loss += on[i] ? k.loss : 0.0f;
-      if (REF) r.kl += on[i] ? k.kl : 0.0f;
-      r.clipped += on[i] & k.clipped;
-      r.count += on[i];
+    for (int g = 0; g < GROUPS; ++g) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool on = lab[g][i] >= 0;
+        const Token k = policy_token<REF>(a, TOK ? policy_side(a, adv[g][i]) : side_s, nll[g][i], old[g][i], ref[g][i]);
+        r.loss += on ? k.loss : 0.0f;
+        if (REF) r.kl += on ? k.kl : 0.0f;
+        r.clipped += on & k.clipped;
+        r.count += on;
+      }
     }
   }
   r.loss = warp_sum(r.loss);
@@ -200,26 +250,25 @@ __device__ __forceinline__ float policy_weight(int count, int per_sequence, doub
 }
 
 // W warps a sequence.
-template <int W, bool REF>
-__global__ void __launch_bounds__(POL_THREADS, 4) policy_sum_kernel(const __grid_constant__ PolicyArgs a, int* counts,
+template <bool REF, bool VEC, bool TOK>
+__global__ void __launch_bounds__(POL_THREADS, 4) policy_sum_kernel(const __grid_constant__ PolicyArgs a, int W, int* counts,
                                                                  PolicyPart* part, int parts) {
-  constexpr int TEAMS = POL_WARPS / W;
   __shared__ SeqSum red[POL_WARPS];
-  __shared__ PolicyPart join[TEAMS];
+  __shared__ PolicyPart join[POL_WARPS];
+  const int teams = POL_WARPS / W;
   const int lane = lane_id(), warp = warp_id(), team = warp / W, in_team = warp % W;
   grid_dependency_wait();
   grid_dependents_launch();
   PolicyPart sum = {};
   // all teams of a block make the same number of rounds: there are barriers inside
-  for (long long s0 = static_cast<long long>(blockIdx.x) * TEAMS; s0 < a.S; s0 += static_cast<long long>(gridDim.x) * TEAMS) {
+  for (long long s0 = static_cast<long long>(blockIdx.x) * teams; s0 < a.S; s0 += static_cast<long long>(gridDim.x) * teams) {
     const long long s = s0 + team;
     SeqSum r = {0.0f, 0.0f, 0, 0};
-    if (s < a.S) r = policy_sequence<W, REF>(a, s, in_team);
+    if (s < a.S) r = policy_sequence<REF, VEC, TOK>(a, s, in_team, W);
     if (W > 1) {
       if (lane == 0) red[warp] = r;
       __syncthreads();
       r = red[team * W];
-#pragma unroll
       for (int i = 1; i < W; ++i) {
         r.loss += red[team * W + i].loss;
         r.kl += red[team * W + i].kl;
@@ -237,13 +286,13 @@ __global__ void __launch_bounds__(POL_THREADS, 4) policy_sum_kernel(const __grid
   __syncthreads();
   if (threadIdx.x == 0 && in_bounds(a.err, blockIdx.x, 1, parts, SITE_POLICY_OUT)) {
     PolicyPart all = join[0];
-    for (int i = 1; i < TEAMS; ++i) policy_join(all, join[i]);
+    for (int i = 1; i < teams; ++i) policy_join(all, join[i]);
     part[blockIdx.x] = all;
   }
 }
 
 // All of it in one block: a warp takes every 32nd sequence.
-template <bool REF>
+template <bool REF, bool TOK>
 __global__ void __launch_bounds__(POL_SMALL_THREADS) policy_small_kernel(const __grid_constant__ PolicyArgs a, float* stats,
                                                                          float* weight) {
   constexpr int WARPS = POL_SMALL_THREADS / 32;
@@ -255,7 +304,7 @@ __global__ void __launch_bounds__(POL_SMALL_THREADS) policy_small_kernel(const _
   grid_dependents_launch();
   PolicyPart sum = {};
   for (int s = warp; s < a.S; s += WARPS) {
-    const SeqSum r = policy_sequence<1, REF>(a, s, 0);
+    const SeqSum r = policy_sequence<REF, false, TOK>(a, s, 0, 1);
     if (lane == 0) {
       counts[s] = r.count;
       policy_add(sum, r, a.per_sequence);
@@ -333,39 +382,60 @@ __global__ void __launch_bounds__(POL_THREADS) policy_join_kernel(const PolicyPa
   }
 }
 
-template <bool REF>
-__global__ void __launch_bounds__(POL_THREADS) policy_grad_kernel(const __grid_constant__ PolicyArgs a, const float* dloss,
+// Quotients by T of indexes below 2^31 (Granlund and Montgomery's division by an invariant: shift = ceil(log2 T),
+// mul = floor(2^(31 + shift) / T) + 1).
+struct Divide {
+  uint32_t mul;
+  int shift;                 // 0: T = 1
+};
+__host__ __device__ inline uint32_t quotient(const Divide& d, uint32_t n) {
+  return d.shift ? static_cast<uint32_t>((static_cast<uint64_t>(n) * d.mul >> 32) >> (d.shift - 1)) : n;
+}
+
+template <bool REF, bool VEC, bool TOK>
+__global__ void __launch_bounds__(POL_THREADS) policy_grad_kernel(const __grid_constant__ PolicyArgs a, const Divide by_T, const float* dloss,
                                                                   const float* weight, float* dnll) {
   grid_dependency_wait();
   grid_dependents_launch();
   const long long n_el = a.S * a.T;
   const float dl = *dloss;
   const long long span = static_cast<long long>(POL_THREADS) * POL_TILE;
-  for (long long i0 = blockIdx.x * span + threadIdx.x; i0 < n_el; i0 += gridDim.x * span) {
-    int64_t lab[POL_TILE];
-    float nll[POL_TILE], old[POL_TILE], ref[POL_TILE], adv[POL_TILE], w[POL_TILE];
+  constexpr int STEP = VEC ? 1 : POL_THREADS;
+  // 64-bit division only where 31 bits do not hold the index
+  auto sequence = [&](long long t) -> long long { return n_el <= 0x7fffffff ? quotient(by_T, static_cast<uint32_t>(t)) : t / a.T; };
+  for (long long i0 = blockIdx.x * span + threadIdx.x * (VEC ? POL_TILE : 1); i0 < n_el; i0 += gridDim.x * span) {
+    static_assert(POL_TILE == 4, "load4");
+    int lab[4];
+    float nll[4], old[4], ref[4], adv[4], w[4], grad[4];
+    bool there[4];
 #pragma unroll
-    for (int i = 0; i < POL_TILE; ++i) {
-      const long long t = i0 + i * POL_THREADS;
-      lab[i] = -1;
-      nll[i] = old[i] = ref[i] = adv[i] = w[i] = 0.0f;
-      if (t < n_el && in_bounds(a.err, t, 1, n_el, SITE_POLICY_IN)) {
-        // 64-bit division only where 32 bits do not hold the index
-        const long long s = n_el <= 0x7fffffff ? static_cast<uint32_t>(t) / static_cast<uint32_t>(a.T) : t / a.T;
-        lab[i] = a.labels[t];
-        nll[i] = a.nll[t];
-        old[i] = a.old_nll[t];
-        if (REF) ref[i] = a.ref_nll[t];
-        adv[i] = a.adv[a.adv_tok ? t : s];
-        w[i] = weight[s];
+    for (int i = 0; i < 4; ++i) there[i] = i0 + i * STEP < n_el;
+    load4<REF, VEC, TOK>(a, i0, STEP, there, lab, nll, old, ref, adv);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const long long t = i0 + i * STEP;
+      if (VEC && i > 0) {                                // T is a multiple of 4: one sequence's
+        w[i] = w[0];
+        if (!TOK) adv[i] = adv[0];
+        continue;
       }
+      w[i] = 0.0f;
+      if (!TOK) adv[i] = 0.0f;
+      if (!there[i] || !in_bounds(a.err, t, 1, n_el, SITE_POLICY_IN)) continue;
+      const long long s = sequence(t);
+      if (!TOK) adv[i] = a.adv[s];
+      w[i] = weight[s];
     }
 #pragma unroll
-    for (int i = 0; i < POL_TILE; ++i) {
-      const long long t = i0 + i * POL_THREADS;
-      if (t >= n_el || !in_bounds(a.err, t, 1, n_el, SITE_POLICY_OUT)) continue;
-      dnll[t] = lab[i] < 0 ? 0.0f : policy_token<REF>(a, nll[i], old[i], ref[i], adv[i]).grad * (w[i] * dl);
+    for (int i = 0; i < 4; ++i)
+      grad[i] = lab[i] < 0 ? 0.0f : policy_token<REF>(a, policy_side(a, adv[i]), nll[i], old[i], ref[i]).grad * (w[i] * dl);
+    if (VEC) {
+      if (in_bounds(a.err, i0, 4, n_el, SITE_POLICY_OUT)) *reinterpret_cast<float4*>(dnll + i0) = make_float4(grad[0], grad[1], grad[2], grad[3]);
+      continue;
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (there[i] && in_bounds(a.err, i0 + i * STEP, 1, n_el, SITE_POLICY_OUT)) dnll[i0 + i * STEP] = grad[i];
   }
 }
 
@@ -414,6 +484,22 @@ wb_status policy_args(PolicyArgs& a, const float* nll, const float* old_nll, con
   a.per_sequence = 0;
   a.err = nullptr;
   return WB_OK;
+}
+
+// Four tokens side by side are of one sequence and lie on 16 bytes.
+bool policy_vec(const PolicyArgs& a) {
+  return a.T % 4 == 0 && aligned16(a.nll) && aligned16(a.old_nll) && aligned16(a.ref_nll) && aligned16(a.labels) &&
+         (!a.adv_tok || aligned16(a.adv));
+}
+
+// f(with a reference, vec, an advantage for each token), as types.
+template <typename F>
+cudaError_t choose(const PolicyArgs& a, bool vec, F f) {
+  const std::true_type yes;
+  const std::false_type no;
+  auto tok = [&](auto r, auto v) { return a.adv_tok ? f(r, v, yes) : f(r, v, no); };
+  if (a.ref_nll) return vec ? tok(yes, yes) : tok(yes, no);
+  return vec ? tok(no, yes) : tok(no, no);
 }
 
 bool policy_small(int64_t S, int64_t T) { return S <= POL_SMALL_S && T <= POL_SMALL_T; }
@@ -465,7 +551,9 @@ wb_status wb_policy_loss(const float* nll, const float* old_nll, const float* re
   if (!a.err) return WB_ECUDA;
   if (small) {
     Prof pr(PC_POLICY, s);
-    WB_CUDA(launch_pdl(ref_nll ? policy_small_kernel<true> : policy_small_kernel<false>, dim3(1), dim3(POL_SMALL_THREADS), 0, s, a, stats, weight));
+    WB_CUDA(choose(a, false, [&](auto ref, auto, auto tok) {
+      return launch_pdl(policy_small_kernel<decltype(ref)::value, decltype(tok)::value>, dim3(1), dim3(POL_SMALL_THREADS), 0, s, a, stats, weight);
+    }));
     return WB_OK;
   }
   const PolicyWs w = policy_ws(S);
@@ -475,12 +563,10 @@ wb_status wb_policy_loss(const float* nll, const float* old_nll, const float* re
   const int teams = POL_WARPS / warps;
   const int blocks = policy_blocks((S + teams - 1) / teams);
   Prof pr(PC_POLICY, s, 2);
-  auto pick = [&](auto ref) {
-    constexpr bool REF = decltype(ref)::value;
-    return warps == 1 ? policy_sum_kernel<1, REF> : warps == 2 ? policy_sum_kernel<2, REF> : warps == 4 ? policy_sum_kernel<4, REF> : policy_sum_kernel<8, REF>;
-  };
-  const auto kern = ref_nll ? pick(std::true_type()) : pick(std::false_type());
-  WB_CUDA(launch_pdl(kern, dim3(blocks), dim3(POL_THREADS), 0, s, a, counts, part, blocks));
+  WB_CUDA(choose(a, policy_vec(a), [&](auto ref, auto vec, auto tok) {
+    return launch_pdl(policy_sum_kernel<decltype(ref)::value, decltype(vec)::value, decltype(tok)::value>, dim3(blocks), dim3(POL_THREADS), 0, s, a,
+                      warps, counts, part, blocks);
+  }));
   WB_CUDA(launch_pdl(policy_join_kernel, dim3(static_cast<unsigned>((S + POL_THREADS - 1) / POL_THREADS)), dim3(POL_THREADS), 0, s,
                      static_cast<const PolicyPart*>(part), blocks, static_cast<const int*>(counts), static_cast<long long>(S),
                      a.per_sequence, stats, weight, a.err));
@@ -505,7 +591,13 @@ wb_status wb_policy_loss_backward(const float* dloss, const float* nll, const fl
   const long long span = static_cast<long long>(POL_THREADS) * POL_TILE;
   const long long units = (a.S * a.T + span - 1) / span;
   const int blocks = static_cast<int>(units < 8LL * POL_MAX_BLOCKS ? units : 8LL * POL_MAX_BLOCKS);
-  WB_CUDA(launch_pdl(ref_nll ? policy_grad_kernel<true> : policy_grad_kernel<false>, dim3(blocks), dim3(POL_THREADS), 0, s, a, dloss, weight, dnll));
+  Divide by_T{0, 0};
+  while ((1LL << by_T.shift) < T) ++by_T.shift;
+  by_T.mul = by_T.shift ? static_cast<uint32_t>((1ull << (31 + by_T.shift)) / static_cast<uint64_t>(T) + 1) : 0;
+  WB_CUDA(choose(a, policy_vec(a) && aligned16(dnll), [&](auto ref, auto vec, auto tok) {
+    return launch_pdl(policy_grad_kernel<decltype(ref)::value, decltype(vec)::value, decltype(tok)::value>, dim3(blocks), dim3(POL_THREADS), 0, s, a,
+                      by_T, dloss, weight, dnll);
+  }));
   return WB_OK;
 }
 
