@@ -11,8 +11,9 @@
 // Forward: a team of 1 to 8 warps of a block takes a sequence; a block leaves one partial row, and a second kernel joins those
 // in order, in every one of its blocks, and turns counts into weights.  Up to 128 sequences of 512 tokens are one block's, in
 // one launch (8 x 77 tokens: 5.5 us against 8.2 with two).  No atomics: the same call gives the same bits.
-// 16001 x 448 tokens forward 30 us, 3.8 TB/s: the loads of a warp's next sequence wait for the sums of the last, and with 4 blocks an SM
-// (64 registers; 3 blocks a quarter more time, 6 with half the loads each 5 % more) there are not enough others.  Backward, without sums, 23 us, 6.2 TB/s.
+// 16001 x 448 tokens: forward 27 us, of which the join takes 4 (the sums 5 TB/s), backward 22 (6.5 TB/s).  Four tokens side by side a load where
+// they lie on 16 bytes: one at a time it took 30 and 25, half of the issue slots on addresses.  6 blocks an SM with half the loads each: 26, but
+// 1024 x 448 tokens 8.6 for 8.3; prefetching a warp's next sequence into L2: 28.
 //
 // Numbers.  Whether a token is clipped is decided on d against log1p(hi) and log1p(-lo), both as unevaluated sums of
 // two float32 (the rounding of a difference is exact in float32): one rounding near the border would turn a
