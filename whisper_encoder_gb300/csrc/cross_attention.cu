@@ -207,29 +207,23 @@ wb_status wb_cross_attention_backward(const void* dout, int64_t do_batch, int64_
   if (!out || !aligned16(out) || !lse || !aligned4(lse) || !aligned4(q_lens) || !aligned4(kv_lens)) return WB_EINVAL;
   if (!workspace || !aligned16(workspace) || workspace_bytes < wb_cross_attention_backward_workspace_bytes(batch, Tq, n_heads))
     return WB_EWORKSPACE;
-  CrossStatsParams sp;
-  base(sp.x, batch, Tq, Tk, n_heads, n_kv_heads, scale, q_lens, kv_lens, rq, rk);
-  if (!sp.x.err) return WB_ECUDA;
-  sp.x.out = const_cast<__nv_bfloat16*>(static_cast<const __nv_bfloat16*>(out));
-  sp.x.lse = const_cast<float*>(lse);
-  sp.dout = static_cast<const __nv_bfloat16*>(dout);
-  sp.do_batch = ro.batch;
-  sp.do_row = ro.row;
-  sp.stats = static_cast<float*>(workspace);
-  sp.stats_ld = (Tq + 127) / 128 * 128;
   CrossBwdParams p;
-  p.x = sp.x;
+  base(p.x, batch, Tq, Tk, n_heads, n_kv_heads, scale, q_lens, kv_lens, rq, rk);
+  if (!p.x.err) return WB_ECUDA;
+  p.x.out = const_cast<__nv_bfloat16*>(static_cast<const __nv_bfloat16*>(out));
+  p.x.lse = const_cast<float*>(lse);
+  p.dout = static_cast<const __nv_bfloat16*>(dout);
+  p.do_batch = ro.batch;
+  p.do_row = ro.row;
   p.do_items = ro.items;
-  p.stats = sp.stats;
-  p.stats_ld = sp.stats_ld;
+  p.stats = static_cast<float*>(workspace);
+  p.stats_ld = (Tq + 127) / 128 * 128;
   p.dq = static_cast<__nv_bfloat16*>(dq);
   p.dk = static_cast<__nv_bfloat16*>(dk);
   p.dv = static_cast<__nv_bfloat16*>(dv);
   p.want_dq = dq != nullptr;
-  Prof pr(PC_CROSS_BWD, s, dk ? 3 : 2);
-  const long long blocks = (static_cast<long long>(batch) * n_heads * sp.stats_ld + 31) / 32;
+  Prof pr(PC_CROSS_BWD, s, dk ? 2 : 1);
   const int sms = sm_count();
-  WB_CUDA(launch_pdl(cross_stats_kernel, dim3(static_cast<unsigned>(blocks < sms * 8 ? blocks : sms * 8)), dim3(256), 0, s, sp));
   CUtensorMap qm, dm, km, vm;
   if (!rows_map(&qm, rq, batch, Tq, n_heads, CRB_M) || !rows_map(&dm, ro, batch, Tq, n_heads, CRB_M) ||
       !rows_map(&km, rk, batch, Tk, n_kv_heads, CRB_M) || !rows_map(&vm, rv, batch, Tk, n_kv_heads, CRB_M))

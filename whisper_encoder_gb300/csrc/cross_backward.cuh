@@ -5,7 +5,6 @@
 // No scores are stored: two kernels form P and dP again, each from the side whose sums it keeps, so that every sum runs inside one
 // CTA in a fixed order and nothing is added through memory (one kernel for all three would save two of seven products
 // and add dq of every key tile to float32 memory, in an order that changes).
-//   cross_stats_kernel        -lse / scale and -sum_e dout out of every row, -infinity and 0 for rows that take no part: their P is 0
 //   cross_bwd_kernel<false,.> 128 query rows an item, 128 keys a step: S = Q K^T, dP = dO V^T -> dQ += dS K, M += P K
 //   cross_bwd_kernel<true,.>  128 keys an item, 128 query rows a step: S^T = K Q^T, dP^T = V dO^T (lane = key) ->
 //                             dV += P^T dO, dK += dS^T Q
@@ -19,6 +18,8 @@
 // keys and join dQ, M and b through distributed shared memory (dq of 224 rows of 16 heads over 13501 keys 106 -> 37 us).  128 columns a step: with 64, two buffers of both and a group of
 // warps for each, a product took 48 cycles for half the work and a step 2000 (dk and dv of 32 x 448 x 1500 x 20 heads 526 us; one
 // item a CTA, two CTAs an SM, 419).
+// The dq kernel takes lse and delta of its rows at the start of an item and leaves them for the dkv kernel, -infinity and 0 for rows that take no part,
+// whose P is then 0 (a kernel of their own before both: 514 us against 518 for 32 x 448 x 1500 x 20 heads, but 22.2 against 20.2 for 3 x 77 x 1371 x 6).
 // Warp 0 lane 0 loads, warp 1 issues, warps 2-17 run the softmax: 16 rows of half of the columns each.
 //
 // Numbers.  Sums are float32; P and dS are rounded to bf16 once each, as operands beside bf16 q, k and dout (with 64 rows or keys
@@ -57,9 +58,11 @@ static_assert(CrossBwdSmem::TOTAL <= 227 * 1024, "one CTA an SM");
 static_assert(CRB_M * CrossBwdSmem::SHARE_LD * 4 <= CrossBwdSmem::OFF_STATS - CrossBwdSmem::OFF_STEP, "a share fits the ring");
 
 struct CrossBwdParams {
-  CrossParams x;             // out and lse unused here
+  CrossParams x;             // lse, out: the forward pass's
+  const __nv_bfloat16* dout;
+  long long do_batch, do_row;
   int do_items;              // as q_items, for dout
-  float* stats;              // [batch][H][2][stats_ld]: -lse / scale, -delta
+  float* stats;              // [batch][H][2][stats_ld]: -lse / scale, -delta, from the dq kernel to the dkv kernel
   int stats_ld;              // Tq rounded up to 128
   int want_dq;               // cross_bwd_kernel<false,.>: 0: delta alone
   __nv_bfloat16* dq;         // [batch][Tq][H 64]
@@ -67,37 +70,20 @@ struct CrossBwdParams {
   __nv_bfloat16* dv;
 };
 
-struct CrossStatsParams {
-  CrossParams x;             // lse, out: the forward pass's
-  const __nv_bfloat16* dout;
-  long long do_batch, do_row;
-  float* stats;
-  int stats_ld;
-};
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-// 8 lanes a row of 64 elements, 16 bytes each.
-__global__ void __launch_bounds__(256) cross_stats_kernel(const __grid_constant__ CrossStatsParams p) {
+// -lse / scale and -sum_e dout out of a row of q, by the four threads of a quad; -infinity and 0 for one that takes no part.
+__device__ __forceinline__ float2 cross_row_stats(const CrossBwdParams& p, int b, int h, int row, bool there, int t) {
   const CrossParams& x = p.x;
-  grid_dependency_wait();
-  grid_dependents_launch();
-  const long long rows = static_cast<long long>(x.batch) * x.H * p.stats_ld;
-  const int e = (threadIdx.x & 7) * 8;
-  const float inv_scale = 1.0f / x.scale;
-  for (long long r0 = static_cast<long long>(blockIdx.x) * 32; r0 < rows; r0 += static_cast<long long>(gridDim.x) * 32) {
-    const long long r = r0 + (threadIdx.x >> 3);
-    const bool in = r < rows;
-    // heads fastest: the rows of a position lie side by side in memory
-    const int h = static_cast<int>(r % x.H);
-    const long long bt = r / x.H;
-    const int t = static_cast<int>(bt % p.stats_ld), b = static_cast<int>(bt / p.stats_ld);
-    const bool there = in && t < cross_len(x.q_lens, b, x.batch, x.Tq, x.err);
-    float d = 0.0f;
-    if (there) {
-      const long long oi = (static_cast<long long>(b) * x.Tq + t) * x.H * CRA_HD + h * CRA_HD + e;
-      const long long di = static_cast<long long>(b) * p.do_batch + static_cast<long long>(t) * p.do_row + h * CRA_HD + e;
-      if (in_bounds(x.err, oi, 8, static_cast<long long>(x.batch) * x.Tq * x.H * CRA_HD, SITE_CROSS_OUT) &&
-          in_bounds(x.err, di, 8, (x.batch - 1) * p.do_batch + (x.Tq - 1) * p.do_row + x.H * CRA_HD, SITE_CROSS_Q)) {
-        const uint4 a = *reinterpret_cast<const uint4*>(x.out + oi), c = *reinterpret_cast<const uint4*>(p.dout + di);
+  float d = 0.0f, l = INFINITY;
+  if (there) {
+    const long long oi = (static_cast<long long>(b) * x.Tq + row) * x.H * CRA_HD + h * CRA_HD + 16 * t;
+    const long long di = static_cast<long long>(b) * p.do_batch + static_cast<long long>(row) * p.do_row + h * CRA_HD + 16 * t;
+    if (in_bounds(x.err, oi, 16, static_cast<long long>(x.batch) * x.Tq * x.H * CRA_HD, SITE_CROSS_OUT) &&
+        in_bounds(x.err, di, 16, (x.batch - 1) * p.do_batch + (x.Tq - 1) * p.do_row + x.H * CRA_HD, SITE_CROSS_Q)) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint4 a = *reinterpret_cast<const uint4*>(x.out + oi + 8 * k), c = *reinterpret_cast<const uint4*>(p.dout + di + 8 * k);
         const uint32_t au[4] = {a.x, a.y, a.z, a.w}, cu[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -106,21 +92,12 @@ __global__ void __launch_bounds__(256) cross_stats_kernel(const __grid_constant_
         }
       }
     }
-    d += __shfl_xor_sync(0xffffffffu, d, 1);
-    d += __shfl_xor_sync(0xffffffffu, d, 2);
-    d += __shfl_xor_sync(0xffffffffu, d, 4);
-    if (in && e == 0) {
-      const long long si = (static_cast<long long>(b) * x.H + h) * 2 * p.stats_ld + t;
-      const long long li = (static_cast<long long>(b) * x.H + h) * x.Tq + t;
-      float l = INFINITY;
-      if (there && in_bounds(x.err, li, 1, static_cast<long long>(x.batch) * x.H * x.Tq, SITE_CROSS_LSE))
-        l = x.lse[li] * inv_scale;
-      if (in_bounds(x.err, si, 1 + p.stats_ld, 2 * rows, SITE_CROSS_STATS)) {
-        p.stats[si] = -l;
-        p.stats[si + p.stats_ld] = -d;
-      }
-    }
+    const long long li = (static_cast<long long>(b) * x.H + h) * x.Tq + row;
+    if (in_bounds(x.err, li, 1, static_cast<long long>(x.batch) * x.H * x.Tq, SITE_CROSS_LSE)) l = x.lse[li] / x.scale;
   }
+  d += __shfl_xor_sync(0xffffffffu, d, 1);
+  d += __shfl_xor_sync(0xffffffffu, d, 2);
+  return make_float2(-l, -d);
 }
 
 // own0, own1: K and V (DKV) or Q and dO; step0, step1: Q and dO (DKV) or K and V.  Boxes of 64 x 128 rows.
@@ -377,9 +354,9 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
         }
         if (!DKV && splits == 1) {
           const long long si = (static_cast<long long>(i.b) * x.H + i.h) * 2 * p.stats_ld + p.stats_ld + i.r0 + ra;
-          if (half == 0 && t < 2 && i.r0 + ra + 8 * t < i.own_len &&
+          if (half == 0 && t < 2 &&
               in_bounds(x.err, si, 9, static_cast<long long>(x.batch) * x.H * 2 * p.stats_ld, SITE_CROSS_STATS))
-            p.stats[si + 8 * t] = t ? zb - bb.x : za - ba.x;         // -delta
+            p.stats[si + 8 * t] = i.r0 + ra + 8 * t >= i.own_len ? 0.0f : t ? zb - bb.x : za - ba.x;         // -delta
         }
         if (!wait(acc_full, ci & 1, 52)) return false;
         tc_fence_after();
@@ -443,19 +420,31 @@ __global__ void __launch_bounds__(CRB_THREADS, 1)
     float last_za = 0.0f, last_zb = 0.0f;
     for (int it = it_first; it < n_items && ok; it += it_step) {
       const Item i = item_at(it);
+      float la = 0.0f, lb = 0.0f, za = 0.0f, zb = 0.0f;      // rows' -lse / scale and -delta
+      if (!DKV && i.r0 < i.own_len && i.step_len > 0) {
+        const float2 sa = cross_row_stats(p, i.b, i.h, i.r0 + ra, i.r0 + ra < i.own_len, t);
+        const float2 sb = cross_row_stats(p, i.b, i.h, i.r0 + ra + 8, i.r0 + ra + 8 < i.own_len, t);
+        la = sa.x;
+        lb = sb.x;
+        za = sa.y;
+        zb = sb.y;
+        // every row of a tile has an entry; -delta of one is written when b is known (split: corrected then)
+        const long long si = (static_cast<long long>(i.b) * x.H + i.h) * 2 * p.stats_ld + i.r0 + ra;
+        if (half == 0 && t < 2 && rank == 0 &&
+            in_bounds(x.err, si, p.stats_ld + 9, static_cast<long long>(x.batch) * x.H * 2 * p.stats_ld, SITE_CROSS_STATS)) {
+          p.stats[si + 8 * t] = t ? lb : la;
+          if (splits > 1) p.stats[si + p.stats_ld + 8 * t] = t ? zb : za;
+        }
+      }
+      if (!DKV && half == 0 && it + it_step < n_items) {     // the next item's rows of out, for its statistics
+        const Item next = item_at(it + it_step);
+        const int row = next.r0 + lane_base + lane;
+        if (lane < 16 && row < next.own_len)
+          prefetch_l2(x.out + (static_cast<long long>(next.b) * x.Tq + row) * x.H * CRA_HD + next.h * CRA_HD);
+      }
       if (i.steps == 0) {
         ok = finish(i, 0, 0.0f, 0.0f);
         continue;
-      }
-      float la = 0.0f, lb = 0.0f, za = 0.0f, zb = 0.0f;      // rows' -lse / scale and -delta
-      if (!DKV) {
-        const long long si = (static_cast<long long>(i.b) * x.H + i.h) * 2 * p.stats_ld + i.r0 + ra;   // every row of a tile has an entry
-        if (in_bounds(x.err, si, p.stats_ld + 9, static_cast<long long>(x.batch) * x.H * 2 * p.stats_ld, SITE_CROSS_STATS)) {
-          la = p.stats[si];
-          lb = p.stats[si + 8];
-          za = p.stats[si + p.stats_ld];
-          zb = p.stats[si + p.stats_ld + 8];
-        }
       }
       uint64_t ba2 = 0, bb2 = 0;                     // this thread's share of b of the two rows
       float bra = 0.0f, brb = 0.0f;                  // this thread's share of b'
