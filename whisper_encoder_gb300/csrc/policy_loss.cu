@@ -105,7 +105,7 @@ template <bool REF, bool VEC, bool TOK>
 __device__ __forceinline__ void load4(const PolicyArgs& a, long long at, int step, const bool (&there)[4], int (&lab)[4], float (&nll)[4],
                                       float (&old)[4], float (&ref)[4], float (&adv)[4]) {
   const int* hi = reinterpret_cast<const int*>(a.labels) + 1;
-  if (VEC) {
+  if constexpr (VEC) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       lab[i] = -1;
@@ -126,20 +126,20 @@ __device__ __forceinline__ void load4(const PolicyArgs& a, long long at, int ste
       const float4 v = *reinterpret_cast<const float4*>(a.adv + at);
       adv[0] = v.x; adv[1] = v.y; adv[2] = v.z; adv[3] = v.w;
     }
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const long long t = at + static_cast<long long>(i) * step;
-    lab[i] = -1;
-    nll[i] = old[i] = ref[i] = 0.0f;
-    if (TOK) adv[i] = 0.0f;
-    if (!there[i] || !in_bounds(a.err, t, 1, a.S * a.T, SITE_POLICY_IN)) continue;
-    lab[i] = hi[2 * t];
-    nll[i] = a.nll[t];
-    old[i] = a.old_nll[t];
-    if (REF) ref[i] = a.ref_nll[t];
-    if (TOK) adv[i] = a.adv[t];
+    for (int i = 0; i < 4; ++i) {
+      const long long t = at + static_cast<long long>(i) * step;
+      lab[i] = -1;
+      nll[i] = old[i] = ref[i] = 0.0f;
+      if (TOK) adv[i] = 0.0f;
+      if (!there[i] || !in_bounds(a.err, t, 1, a.S * a.T, SITE_POLICY_IN)) continue;
+      lab[i] = hi[2 * t];
+      nll[i] = a.nll[t];
+      old[i] = a.old_nll[t];
+      if (REF) ref[i] = a.ref_nll[t];
+      if (TOK) adv[i] = a.adv[t];
+    }
   }
 }
 
@@ -430,13 +430,13 @@ __global__ void __launch_bounds__(POL_THREADS) policy_grad_kernel(const __grid_c
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       grad[i] = lab[i] < 0 ? 0.0f : policy_token<REF>(a, policy_side(a, adv[i]), nll[i], old[i], ref[i]).grad * (w[i] * dl);
-    if (VEC) {
+    if constexpr (VEC) {
       if (in_bounds(a.err, i0, 4, n_el, SITE_POLICY_OUT)) *reinterpret_cast<float4*>(dnll + i0) = make_float4(grad[0], grad[1], grad[2], grad[3]);
-      continue;
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (there[i] && in_bounds(a.err, i0 + i * STEP, 1, n_el, SITE_POLICY_OUT)) dnll[i0 + i * STEP] = grad[i];
+      for (int i = 0; i < 4; ++i)
+        if (there[i] && in_bounds(a.err, i0 + i * STEP, 1, n_el, SITE_POLICY_OUT)) dnll[i0 + i * STEP] = grad[i];
+    }
   }
 }
 
