@@ -197,6 +197,31 @@ def test_the_kl_term_over_its_range(wb, x):
     assert bool(((dnll.double() - slope).abs() <= 2.0 ** -21 * abs(slope)).all())
 
 
+@pytest.mark.parametrize("S,T", [(1, 1 << 20), (3, 700001), (1, 1 << 24)])
+@pytest.mark.parametrize("d", [-0.15, 0.03, 0.11])
+@pytest.mark.parametrize("per_token", [False, True])
+def test_long_sequences(wb, S, T, d, per_token):
+    # equal terms, whose roundings in one float32 would all go the same way.  32 at most are added in a row, the rest in pairs of float32
+    # but for the last one of a lane (1), 32 lanes (5) and 8 warps (7): 2^-24 of the sum each
+    nll, old, ref = (torch.full((S, T), c, device=DEV) for c in (1.0, 1.0 + d, 0.7))     # within a factor of 2: differences are exact
+    adv = torch.full((S, T) if per_token else (S,), -1.0, device=DEV)
+    labels = torch.zeros(S, T, dtype=torch.int64, device=DEV)
+    labels[:, T - 5:] = -1
+    ratio, x = math.exp(float(old[0, 0]) - 1.0), 1.0 - float(ref[0, 0])
+    kl = math.expm1(x) - x
+    for per_sequence in (False, True):
+        stats, weight, dnll = _run(wb, (nll, old, ref, adv, labels), per_sequence)
+        off = 2.0 ** -24 * (32 + 1 + 5 + 7) + 2.0 ** -22
+        want = ratio + 0.1 * kl
+        assert abs(float(stats[0]) - want) <= (off + 2.0 ** -20) * want
+        assert abs(float(stats[1]) - kl) <= (off + 2.0 ** -20) * kl
+        assert float(stats[2]) == 0
+        w = 1 / (S * (T - 5))
+        assert bool(((weight.double() - w).abs() <= 2.0 ** -23 * w).all())
+        grad = 1.5 * w * (0.1 * math.expm1(x) - ratio)
+        assert bool(((dnll[:, :T - 5].double() - grad).abs() <= 2.0 ** -19 * abs(grad)).all()) and not dnll[:, T - 5:].any()
+
+
 def test_gradient_against_differences(wb):
     nll, old, ref, adv, labels = _data(7, 60, 4)
     stats, weight, dnll = _run(wb, (nll, old, ref, adv, labels), True, dl=1.0)

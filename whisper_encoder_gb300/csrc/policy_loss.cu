@@ -18,7 +18,8 @@
 // Numbers.  Whether a token is clipped is decided on d against log1p(hi) and log1p(-lo), both as unevaluated sums of
 // two float32 (the rounding of a difference is exact in float32): one rounding near the border would turn a
 // whole gradient on or off.  e^x - x - 1 is x^2 / 2 for small x: below 1/2 its series, above it the
-// difference of expm1, which loses two bits at most.  An advantage of zero gives zero, whatever e^d is.
+// difference of expm1, which loses two bits at most.  An advantage of zero gives zero, whatever e^d is.  A lane adds up to 32 of a
+// sequence's tokens in one float32, the rest of its share (sequences of more than 8192 tokens) as pairs.
 #include <cmath>
 #include <type_traits>
 
@@ -33,6 +34,8 @@ constexpr int POL_THREADS = 256, POL_WARPS = POL_THREADS / 32;
 constexpr int POL_MAX_BLOCKS = 608;       // 4 on each SM
 constexpr int POL_TILE = 4;               // tokens of a thread and step, backward
 constexpr int POL_SUM_TILE = 8;           // forward: its loads in flight
+constexpr int POL_FLUSH = 4;              // forward: steps of them that a lane adds in one float32
+constexpr int POL_LANE_TOKENS = POL_FLUSH * POL_SUM_TILE;
 constexpr int POL_SMALL_S = 128, POL_SMALL_T = 512, POL_SMALL_THREADS = 1024;
 
 struct PolicyArgs {
@@ -163,6 +166,7 @@ struct Sum2 {
     c += v.c;
   }
   // (what an infinite sum's roundings left is no number)
+  __device__ __forceinline__ float value32() const { return isfinite(s) ? s + c : s; }
   __device__ __forceinline__ double value() const { return isfinite(s) ? static_cast<double>(s) + static_cast<double>(c) : static_cast<double>(s); }
 };
 
@@ -179,7 +183,8 @@ struct SeqSum {
 };
 
 // This warp's share of a sequence, in every lane: warp `part` of W.  No branches among the tokens of a step: they overlap.
-template <bool REF, bool VEC, bool TOK>
+// LONG: a lane has more than POL_FLUSH steps (in every call the pairs took 2 to 5 % with a reference: 16001 x 448 tokens 40.3 us for 39.5).
+template <bool REF, bool VEC, bool TOK, bool LONG>
 __device__ __forceinline__ SeqSum policy_sequence(const PolicyArgs& a, long long s, int part, int W) {
   SeqSum r = {0.0f, 0.0f, 0, 0};
   const long long base = s * a.T;
@@ -187,7 +192,16 @@ __device__ __forceinline__ SeqSum policy_sequence(const PolicyArgs& a, long long
   constexpr int GROUPS = POL_SUM_TILE / 4;
   const int T = static_cast<int>(a.T), first = (part * 32 + static_cast<int>(lane_id())) * (VEC ? 4 : 1);
   const int step = VEC ? 1 : W * 32, group = W * 32 * 4;                        // between a lane's tokens, and its groups of four
+  // what a lane of a long sequence has added so far: of 4096 equal losses in one float32 the roundings were 2^-15 of the sum, of 65536 2^-11
+  Sum2 loss = {0.0f, 0.0f}, kl = {0.0f, 0.0f};
+  int steps = 0;
   for (int t0 = first; t0 < T; t0 += GROUPS * group) {
+    if (LONG && steps++ == POL_FLUSH) {
+      loss.add(r.loss);
+      if (REF) kl.add(r.kl);
+      r.loss = r.kl = 0.0f;
+      steps = 1;
+    }
     int lab[GROUPS][4];
     float nll[GROUPS][4], old[GROUPS][4], ref[GROUPS][4], adv[GROUPS][4];
 #pragma unroll
@@ -208,6 +222,14 @@ __device__ __forceinline__ SeqSum policy_sequence(const PolicyArgs& a, long long
         r.clipped += on & k.clipped;
         r.count += on;
       }
+    }
+  }
+  if (LONG) {
+    loss.add(r.loss);
+    r.loss = loss.value32();
+    if (REF) {
+      kl.add(r.kl);
+      r.kl = kl.value32();
     }
   }
   r.loss = warp_sum(r.loss);
@@ -251,7 +273,7 @@ __device__ __forceinline__ float policy_weight(int count, int per_sequence, doub
 }
 
 // W warps a sequence.
-template <bool REF, bool VEC, bool TOK>
+template <bool REF, bool VEC, bool TOK, bool LONG>
 __global__ void __launch_bounds__(POL_THREADS, 4) policy_sum_kernel(const __grid_constant__ PolicyArgs a, int W, int* counts,
                                                                  PolicyPart* part, int parts) {
   __shared__ SeqSum red[POL_WARPS];
@@ -265,7 +287,7 @@ __global__ void __launch_bounds__(POL_THREADS, 4) policy_sum_kernel(const __grid
   for (long long s0 = static_cast<long long>(blockIdx.x) * teams; s0 < a.S; s0 += static_cast<long long>(gridDim.x) * teams) {
     const long long s = s0 + team;
     SeqSum r = {0.0f, 0.0f, 0, 0};
-    if (s < a.S) r = policy_sequence<REF, VEC, TOK>(a, s, in_team, W);
+    if (s < a.S) r = policy_sequence<REF, VEC, TOK, LONG>(a, s, in_team, W);
     if (W > 1) {
       if (lane == 0) red[warp] = r;
       __syncthreads();
@@ -305,7 +327,8 @@ __global__ void __launch_bounds__(POL_SMALL_THREADS) policy_small_kernel(const _
   grid_dependents_launch();
   PolicyPart sum = {};
   for (int s = warp; s < a.S; s += WARPS) {
-    const SeqSum r = policy_sequence<REF, false, TOK>(a, s, 0, 1);
+    static_assert(POL_SMALL_T <= 32 * POL_LANE_TOKENS, "not LONG");
+    const SeqSum r = policy_sequence<REF, false, TOK, false>(a, s, 0, 1);
     if (lane == 0) {
       counts[s] = r.count;
       policy_add(sum, r, a.per_sequence);
@@ -564,9 +587,11 @@ wb_status wb_policy_loss(const float* nll, const float* old_nll, const float* re
   const int teams = POL_WARPS / warps;
   const int blocks = policy_blocks((S + teams - 1) / teams);
   Prof pr(PC_POLICY, s, 2);
+  const bool is_long = T > 32LL * warps * POL_LANE_TOKENS;
   WB_CUDA(choose(a, policy_vec(a), [&](auto ref, auto vec, auto tok) {
-    return launch_pdl(policy_sum_kernel<decltype(ref)::value, decltype(vec)::value, decltype(tok)::value>, dim3(blocks), dim3(POL_THREADS), 0, s, a,
-                      warps, counts, part, blocks);
+    constexpr bool R = decltype(ref)::value, V = decltype(vec)::value, K = decltype(tok)::value;
+    return launch_pdl(is_long ? policy_sum_kernel<R, V, K, true> : policy_sum_kernel<R, V, K, false>, dim3(blocks), dim3(POL_THREADS), 0, s, a, warps,
+                      counts, part, blocks);
   }));
   WB_CUDA(launch_pdl(policy_join_kernel, dim3(static_cast<unsigned>((S + POL_THREADS - 1) / POL_THREADS)), dim3(POL_THREADS), 0, s,
                      static_cast<const PolicyPart*>(part), blocks, static_cast<const int*>(counts), static_cast<long long>(S),
