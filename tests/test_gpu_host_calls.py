@@ -1,5 +1,7 @@
 """The C++ marshalling of the plain calls (wb_host) against the long way through ctypes (GPU): the same bits, and the same answers where a
 call is not plain."""
+import ctypes
+
 import pytest
 import torch
 
@@ -84,3 +86,59 @@ def test_outputs_on_a_side_stream_and_in_a_graph(wb, host):
         quiet = wb.cross_attention(q, k, k)
     for a, b, c, d in zip(want, got, inside, quiet):
         assert torch.equal(a, b) and torch.equal(a, c) and torch.equal(a, d)
+
+
+def test_a_call_that_failed_is_not_made_again(wb, host):
+    # a status other than a refusal may come from behind the call's first launch: gradients scaled once may not be scaled twice
+    from whisper_encoder_gb300 import _lib
+    lib, made = _lib.load(), []
+    kinds = {n: ctypes.CFUNCTYPE(ctypes.c_int, *_lib.SIGNATURES[n][1]) for n in (
+        "wb_cross_attention", "wb_cross_attention_backward", "wb_clip_grad_norm", "wb_policy_loss", "wb_policy_loss_backward")}
+
+    def failing(name, status):
+        return kinds[name](lambda *a: made.append(name) or status)
+
+    q, k = torch.randn(2, 3, 128, device=DEV).bfloat16(), torch.randn(2, 5, 64, device=DEV).bfloat16()
+    out, lse = wb.cross_attention(q, k, k)
+    x, labels = torch.ones(4, 9, device=DEV), torch.zeros(4, 9, dtype=torch.int64, device=DEV)
+    _, weight = wb.policy_loss(x, x, x, labels)
+    calls = [("wb_cross_attention", lambda: wb.cross_attention(q, k, k)),
+             ("wb_cross_attention_backward", lambda: wb.cross_attention_backward(out, q, k, k, out, lse)),
+             ("wb_clip_grad_norm", lambda: wb.clip_grad_norm([x], 0.5)),
+             ("wb_policy_loss", lambda: wb.policy_loss(x, x, x, labels)),
+             ("wb_policy_loss_backward", lambda: wb.policy_loss_backward(x[0, :1], x, x, x, labels, weight))]
+    try:
+        for name, call in calls:
+            for status in (_lib.WB_ECUDA, _lib.WB_ETIMEOUT, _lib.WB_EBOUNDS):
+                fake = failing(name, status)
+                _lib.bind_host(host, lib, {name: fake})
+                made.clear()
+                with pytest.raises(wb.WbError) as e:
+                    call()
+                assert made == [name] and name in str(e.value) and _lib.status_string(status) in str(e.value)
+                assert bool((x == 1).all())
+            # a refusal comes before anything is launched: the long way is taken, with its own checks and messages
+            for status in (_lib.WB_EINVAL, _lib.WB_EUNSUPPORTED, _lib.WB_EWORKSPACE):
+                fake = failing(name, status)
+                _lib.bind_host(host, lib, {name: fake})
+                made.clear()
+                call()
+                assert made == [name]
+                x.fill_(1)
+    finally:
+        _lib.bind_host(host, lib)
+    assert wb.check_device_error() == 0
+
+
+def test_an_allocation_that_fails(wb, host):
+    # a result of 16 GB (its rows are the same 1 GB for all items) in a process that may have 8
+    q, k = torch.zeros(1, 1, 2048, dtype=torch.bfloat16, device=DEV), torch.zeros(1, 5, 64, dtype=torch.bfloat16, device=DEV)
+    torch.cuda.empty_cache()
+    torch.cuda.set_per_process_memory_fraction(8 * 2 ** 30 / torch.cuda.mem_get_info()[1])
+    try:
+        rows = torch.zeros(1, 1 << 18, 2048, dtype=torch.bfloat16, device=DEV)
+        with pytest.raises(torch.OutOfMemoryError):
+            wb.cross_attention(rows.expand(16, -1, -1), k.expand(16, -1, -1), k.expand(16, -1, -1))
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert wb.cross_attention(q, k, k)[0].shape == q.shape and wb.check_device_error() == 0

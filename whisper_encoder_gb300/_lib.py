@@ -160,6 +160,16 @@ def load(path: str | None = None) -> ctypes.CDLL:
 _HOST = None
 
 
+_HOST_ENTRIES = ("wb_cross_attention", "wb_cross_attention_backward", "wb_cross_attention_backward_workspace_bytes", "wb_clip_grad_norm",
+                 "wb_clip_grad_norm_workspace_bytes", "wb_policy_loss", "wb_policy_loss_workspace_bytes", "wb_policy_loss_backward")
+
+
+def bind_host(module, lib, replaced=None) -> None:
+    """Give wb_host the entry points of an opened libwb, or a test's own in place of some."""
+    entry = dict(replaced or {})
+    module.bind(WbError, *[ctypes.cast(entry.get(n, getattr(lib, n)), ctypes.c_void_p).value for n in _HOST_ENTRIES])
+
+
 def host_calls():
     """The C++ marshalling of the plain calls (wb_host.so), bound to the loaded libwb; False where it is not built."""
     global _HOST
@@ -169,9 +179,7 @@ def host_calls():
             spec = importlib.util.spec_from_file_location("wb_host", _build.LIB_HOST)
             module = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(module)
-            module.bind(*[ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
-                "wb_cross_attention", "wb_cross_attention_backward", "wb_cross_attention_backward_workspace_bytes", "wb_clip_grad_norm",
-                "wb_clip_grad_norm_workspace_bytes", "wb_policy_loss", "wb_policy_loss_workspace_bytes", "wb_policy_loss_backward")])
+            bind_host(module, lib)
             _HOST = module
         except (ImportError, OSError):
             _HOST = False

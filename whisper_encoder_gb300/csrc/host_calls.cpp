@@ -5,13 +5,16 @@
 // from Python through ctypes (2 of checks, 4 of allocations, 4 of ctypes, 2 of the launch, the rest the interpreter).
 // Nothing is decided here that api.py does not decide: a call with anything out of the ordinary (a stream, a tensor of another
 // device, type or layout, a refusal by the library) returns None before anything was launched, and api.py goes the long way,
-// with its own checks and messages.  Built beside libwb.so where torch's and Python's headers are; without it every call goes the long way.
+// with its own checks and messages.  Any other failure raises what it raises on the long way (the package's WbError, torch's exceptions): it may
+// come from behind a call's first launch, and a call made twice would scale gradients twice.
+// Built beside libwb.so where torch's and Python's headers are; without it every call goes the long way.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
@@ -31,7 +34,10 @@ decltype(&wb_policy_loss) p_policy = nullptr;
 decltype(&wb_policy_loss_workspace_bytes) p_policy_workspace = nullptr;
 decltype(&wb_policy_loss_backward) p_policy_backward = nullptr;
 
+PyObject* wb_error = nullptr;            // the package's exception
+
 struct LongWay {};                       // not the plain case
+struct Raised {};                        // with Python's exception set
 
 PyObject* none() {
   PyErr_Clear();
@@ -41,7 +47,7 @@ PyObject* none() {
 const at::Tensor& tensor(PyObject* o) {
   if (!THPVariable_CheckExact(o)) throw LongWay();       // a tensor or a parameter; subclasses may be anything
   const at::Tensor& t = THPVariable_Unpack(o);
-  if (!t.defined() || !t.is_cuda()) throw LongWay();
+  if (!t.defined() || !t.is_cuda() || t.layout() != at::kStrided) throw LongWay();
   return t;
 }
 double number(PyObject* o) {
@@ -106,15 +112,28 @@ PyObject* wrap(std::initializer_list<const at::Tensor*> list) {
   return t;
 }
 
-// Every entry: LongWay, an allocation that failed or a status of the library: None.
+// Goes on after a call of the library that launched all it should.
+void check(const char* name, wb_status status) {
+  if (status == WB_OK) return;
+  if (status == WB_EINVAL || status == WB_EUNSUPPORTED || status == WB_EWORKSPACE) throw LongWay();      // refusals: nothing was launched
+  PyObject* e = PyObject_CallFunction(wb_error, "si", name, static_cast<int>(status));
+  if (e) PyErr_SetObject(wb_error, e);
+  Py_XDECREF(e);
+  throw Raised();
+}
+
+// Every entry: None for LongWay, null with Python's exception set for any other one.
 template <typename F>
 PyObject* plain(F f) {
+  HANDLE_TH_ERRORS
   try {
     return f();
   } catch (const LongWay&) {
-  } catch (const std::exception&) {
+    return none();
+  } catch (const Raised&) {
+    return nullptr;
   }
-  return none();
+  END_HANDLE_TH_ERRORS
 }
 
 PyObject* cross_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -126,10 +145,10 @@ PyObject* cross_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const float scale = static_cast<float>(number(a[3]));
     const int32_t *ql = lengths(here, a[4], q.batch), *kl = lengths(here, a[5], q.batch);
     const at::Tensor out = here.empty({q.batch, q.T, q.d}, at::kBFloat16), lse = here.empty({q.batch, q.d / 64, q.T}, at::kFloat);
-    if (p_cross(q.p, q.s0, q.s1, k.p, k.s0, k.s1, v.p, v.s0, v.s1, ql, kl, static_cast<int>(q.batch), static_cast<int>(q.T),
-                static_cast<int>(k.T), static_cast<int>(q.d / 64), static_cast<int>(k.d / 64), scale, out.mutable_data_ptr(),
-                lse.mutable_data_ptr<float>(), here.stream()) != WB_OK)
-      throw LongWay();
+    check("wb_cross_attention",
+          p_cross(q.p, q.s0, q.s1, k.p, k.s0, k.s1, v.p, v.s0, v.s1, ql, kl, static_cast<int>(q.batch), static_cast<int>(q.T),
+                  static_cast<int>(k.T), static_cast<int>(q.d / 64), static_cast<int>(k.d / 64), scale, out.mutable_data_ptr(),
+                  lse.mutable_data_ptr<float>(), here.stream()));
     return wrap({&out, &lse});
   });
 }
@@ -154,11 +173,11 @@ PyObject* cross_attention_backward(PyObject*, PyObject* const* a, Py_ssize_t n) 
     }
     const at::Tensor ws = here.workspace(p_cross_workspace(static_cast<int>(q.batch), static_cast<int>(q.T), H));
     auto at_ = [](const at::Tensor& t) { return t.defined() ? t.mutable_data_ptr() : nullptr; };
-    if (p_cross_backward(g.p, g.s0, g.s1, q.p, q.s0, q.s1, k.p, k.s0, k.s1, v.p, v.s0, v.s1, out.const_data_ptr(),
-                         lse.const_data_ptr<float>(), ql, kl, static_cast<int>(q.batch), static_cast<int>(q.T), static_cast<int>(k.T), H,
-                         static_cast<int>(k.d / 64), scale, at_(dq), at_(dk), at_(dv), ws.mutable_data_ptr(),
-                         static_cast<size_t>(ws.numel()), here.stream()) != WB_OK)
-      throw LongWay();
+    check("wb_cross_attention_backward",
+          p_cross_backward(g.p, g.s0, g.s1, q.p, q.s0, q.s1, k.p, k.s0, k.s1, v.p, v.s0, v.s1, out.const_data_ptr(),
+                           lse.const_data_ptr<float>(), ql, kl, static_cast<int>(q.batch), static_cast<int>(q.T), static_cast<int>(k.T), H,
+                           static_cast<int>(k.d / 64), scale, at_(dq), at_(dk), at_(dv), ws.mutable_data_ptr(),
+                           static_cast<size_t>(ws.numel()), here.stream()));
     return wrap({&dq, &dk, &dv});
   });
 }
@@ -198,10 +217,10 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (out_types[i] != types[i] && out_types[i] != WB_F32) throw LongWay();
     }
     const at::Tensor norm = here.empty({}, at::kFloat), ws = here.workspace(p_clip_workspace(static_cast<int>(count)));
-    if (p_clip(grads.data(), write ? outs.data() : nullptr, numel.data(), types.data(), write ? out_types.data() : nullptr,
-               static_cast<int>(count), static_cast<float>(number(a[1])), norm.mutable_data_ptr<float>(), ws.mutable_data_ptr(),
-               static_cast<size_t>(ws.numel()), here.stream()) != WB_OK)
-      throw LongWay();
+    check("wb_clip_grad_norm",
+          p_clip(grads.data(), write ? outs.data() : nullptr, numel.data(), types.data(), write ? out_types.data() : nullptr,
+                 static_cast<int>(count), static_cast<float>(number(a[1])), norm.mutable_data_ptr<float>(), ws.mutable_data_ptr(),
+                 static_cast<size_t>(ws.numel()), here.stream()));
     return THPVariable_Wrap(norm);
   });
 }
@@ -239,10 +258,10 @@ PyObject* policy_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const size_t bytes = p_policy_workspace(p.S, p.T);
     at::Tensor ws;
     if (bytes) ws = here.workspace(bytes);
-    if (p_policy(p.nll, p.old_nll, p.ref, p.adv, p.per_token, p.labels, p.S, p.T, number(a[5]), number(a[6]),
-                 static_cast<float>(number(a[7])), per_sequence, stats.mutable_data_ptr<float>(), weight.mutable_data_ptr<float>(),
-                 bytes ? ws.mutable_data_ptr() : nullptr, bytes ? static_cast<size_t>(ws.numel()) : 0, here.stream()) != WB_OK)
-      throw LongWay();
+    check("wb_policy_loss",
+          p_policy(p.nll, p.old_nll, p.ref, p.adv, p.per_token, p.labels, p.S, p.T, number(a[5]), number(a[6]),
+                   static_cast<float>(number(a[7])), per_sequence, stats.mutable_data_ptr<float>(), weight.mutable_data_ptr<float>(),
+                   bytes ? ws.mutable_data_ptr() : nullptr, bytes ? static_cast<size_t>(ws.numel()) : 0, here.stream()));
     return wrap({&stats, &weight});
   });
 }
@@ -257,25 +276,28 @@ PyObject* policy_loss_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (dloss.scalar_type() != at::kFloat || dloss.numel() != 1) throw LongWay();
     const at::Tensor& weight = need(here, a[5], at::kFloat, {p.S});
     const at::Tensor dnll = here.empty({p.S, p.T}, at::kFloat);
-    if (p_policy_backward(dloss.const_data_ptr<float>(), p.nll, p.old_nll, p.ref, p.adv, p.per_token, p.labels,
-                          weight.const_data_ptr<float>(), p.S, p.T, number(a[7]), number(a[8]), static_cast<float>(number(a[9])),
-                          dnll.mutable_data_ptr<float>(), here.stream()) != WB_OK)
-      throw LongWay();
+    check("wb_policy_loss_backward",
+          p_policy_backward(dloss.const_data_ptr<float>(), p.nll, p.old_nll, p.ref, p.adv, p.per_token, p.labels,
+                            weight.const_data_ptr<float>(), p.S, p.T, number(a[7]), number(a[8]), static_cast<float>(number(a[9])),
+                            dnll.mutable_data_ptr<float>(), here.stream()));
     return THPVariable_Wrap(dnll);
   });
 }
 
-// Addresses of the entry points, as integers.
+// The package's exception, and addresses of the entry points, as integers.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   void* p[8];
-  if (n != 8) {
-    PyErr_SetString(PyExc_TypeError, "bind: eight addresses expected");
+  if (n != 9 || !PyType_Check(a[0])) {
+    PyErr_SetString(PyExc_TypeError, "bind: an exception and eight addresses expected");
     return nullptr;
   }
   for (int i = 0; i < 8; ++i) {
-    p[i] = PyLong_AsVoidPtr(a[i]);
+    p[i] = PyLong_AsVoidPtr(a[i + 1]);
     if (PyErr_Occurred()) return nullptr;
   }
+  Py_INCREF(a[0]);
+  Py_XDECREF(wb_error);
+  wb_error = a[0];
   p_cross = reinterpret_cast<decltype(p_cross)>(p[0]);
   p_cross_backward = reinterpret_cast<decltype(p_cross_backward)>(p[1]);
   p_cross_workspace = reinterpret_cast<decltype(p_cross_workspace)>(p[2]);
