@@ -508,7 +508,7 @@ wb_status wb_cross_attention_backward(const void* dout, int64_t do_batch, int64_
  *  - Tensors that are written overlap nothing else of the call; a tensor listed twice is refused with outs, and counts
  *    twice without.  Pointers are aligned to their element.
  * Squares are summed in float32 over at most 128 elements, then in float64, in a fixed order, over the whole range of
- * the types (elements whose squares leave float32's range are scaled first).
+ * the types (elements whose squares leave float32's range are scaled first; a factor below float32's normal range is taken in float64).
  * WB_EINVAL for bad pointers, sizes, alignment, overlaps or a max_norm that is negative or NaN, WB_EUNSUPPORTED for
  * other types, WB_EWORKSPACE for a missing, small or unaligned workspace. */
 #define WB_CLIP_MAX_TENSORS 65536

@@ -161,3 +161,17 @@ def test_python_refusals(wb):
         with pytest.raises(wb.WbError):
             bad()
     assert bool((x == 1).all()) and abs(float(wb.grad_norm([x, x])) - math.sqrt(8)) < 1e-5
+
+
+@pytest.mark.parametrize("max_norm", [2.0 ** -6, 2.0 ** -10, 2.0 ** -20, 2.0 ** -27, 2.0 ** -60, 2.0 ** -100, 2.0 ** -149])
+@pytest.mark.parametrize("size", [2.0 ** 119, 2.0 ** 100, 1.7 * 2.0 ** 118])
+def test_factors_that_float32_holds_badly_or_not_at_all(wb, size, max_norm):
+    # a factor of 2^-114 to 2^-276: exact values are ordinary numbers as long as the gradients are large
+    g = torch.Generator(device=DEV).manual_seed(3)
+    buf = (size * (1 + torch.rand(20011, generator=g, device=DEV))).to(torch.bfloat16)
+    grads = [size * (1 + torch.rand(1000, generator=g, device=DEV)), buf[:3], buf[3:20010], torch.randn(500, generator=g, device=DEV),
+             torch.randn(700, generator=g, device=DEV).half(), -size * (1 + torch.rand(9001, generator=g, device=DEV))[1:]]
+    _check(wb, grads, max_norm)
+    grads = [size * (1 + torch.rand(16400, generator=g, device=DEV)).to(torch.bfloat16), torch.randn(9, generator=g, device=DEV).half(),
+             -size * torch.ones(16390, device=DEV)]
+    _check(wb, grads, max_norm, f32_out=True)

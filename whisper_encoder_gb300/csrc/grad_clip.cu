@@ -323,14 +323,36 @@ __device__ __forceinline__ void clip_scale(const ClipEntry& e, uint32_t c, float
 
 // The norm from the partial sums (every block, in the same order) and the factor: below 1 only where a finite
 // norm is above max_norm.
-__device__ __forceinline__ float clip_factor(const ClipScale& s, uint32_t* err) {
+__device__ __forceinline__ float clip_factor(const ClipScale& s, uint32_t* err, double& norm) {
   double v = 0.0;
   for (int i = threadIdx.x; i < s.parts; i += CLIP_THREADS)
     if (in_bounds(err, i, 1, s.parts, SITE_CLIP_PART)) v += s.part[i];
-  const double norm = sqrt(clip_block_sum(v));
+  norm = sqrt(clip_block_sum(v));
   const float n32 = static_cast<float>(norm);
   if (s.norm && blockIdx.x == 0 && threadIdx.x == 0) *s.norm = n32;
   return norm > s.max_norm && isfinite(n32) ? static_cast<float>(s.max_norm / norm) : 1.0f;
+}
+
+// A factor below float32's normal range, in float64: gradients of 2^119 clipped to 2^-27 are ordinary numbers, although the factor would be
+// 0 in float32, or keep few of its digits.
+template <typename T, typename O>
+__device__ __forceinline__ void clip_scale_tiny(const ClipEntry& e, uint32_t c, double f, uint32_t* err) {
+  const T* g = static_cast<const T*>(e.g);
+  O* out = static_cast<O*>(e.out);
+  const ClipSpan s = clip_span<T>(e, c);
+  for (long long i = s.lo + threadIdx.x; i < s.hi; i += CLIP_THREADS)
+    if (in_bounds(err, i, 1, e.n, SITE_CLIP_OUT)) out[i] = from_f32<O>(static_cast<float>(static_cast<double>(to_f32(g[i])) * f));
+}
+template <int N>
+__device__ __forceinline__ void clip_scale_tiny(const ClipTable<N>& t, double f) {
+  for (uint32_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+    const ClipEntry& e = t.e[clip_find(t, c)];
+    const uint32_t j = c - e.chunk0;
+    const bool wide = e.out_type == WB_F32;
+    if (e.type == WB_BF16) wide ? clip_scale_tiny<__nv_bfloat16, float>(e, j, f, t.err) : clip_scale_tiny<__nv_bfloat16, __nv_bfloat16>(e, j, f, t.err);
+    else if (e.type == WB_F16) wide ? clip_scale_tiny<__half, float>(e, j, f, t.err) : clip_scale_tiny<__half, __half>(e, j, f, t.err);
+    else clip_scale_tiny<float, float>(e, j, f, t.err);
+  }
 }
 
 template <int N>
@@ -338,7 +360,12 @@ __global__ void __launch_bounds__(CLIP_THREADS, CLIP_BLOCKS_PER_SM)
     clip_scale_kernel(const __grid_constant__ ClipTable<N> t, const ClipScale s) {
   grid_dependency_wait();
   grid_dependents_launch();
-  const float k = clip_factor(s, t.err);
+  double norm;
+  const float k = clip_factor(s, t.err, norm);
+  if (k < 0x1p-126f && s.max_norm > 0.0f) {
+    clip_scale_tiny(t, s.max_norm / norm);
+    return;
+  }
   for (uint32_t i = blockIdx.x; i < t.chunks; i += gridDim.x) {
     const uint32_t c = t.chunks - 1 - i;
     const ClipEntry& e = t.e[clip_find(t, c)];
@@ -359,7 +386,8 @@ __global__ void __launch_bounds__(CLIP_THREADS, CLIP_BLOCKS_PER_SM)
 __global__ void __launch_bounds__(CLIP_THREADS) clip_finish_kernel(const ClipScale s, uint32_t* err) {
   grid_dependency_wait();
   grid_dependents_launch();
-  clip_factor(s, err);
+  double norm;
+  clip_factor(s, err, norm);
 }
 
 int elem_bytes(int type) { return type == WB_F32 ? 4 : 2; }
