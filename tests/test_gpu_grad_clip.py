@@ -175,3 +175,16 @@ def test_factors_that_float32_holds_badly_or_not_at_all(wb, size, max_norm):
     grads = [size * (1 + torch.rand(16400, generator=g, device=DEV)).to(torch.bfloat16), torch.randn(9, generator=g, device=DEV).half(),
              -size * torch.ones(16390, device=DEV)]
     _check(wb, grads, max_norm, f32_out=True)
+
+
+def test_kernels_counted_of_long_lists(wb):
+    # up to 96 tensors a launch of each pass, or 960
+    for n, launches in ((1, 2), (96, 2), (97, 2), (960, 2), (961, 4), (2000, 6)):
+        grads = [torch.ones(3, device=DEV) for _ in range(n)]
+        for clip in (True, False):
+            wb.profile_begin()
+            try:
+                wb.clip_grad_norm(grads, 1.0) if clip else wb.grad_norm(grads)
+            finally:
+                counts = wb.profile_end()
+            assert counts["train.clip"][1] == (launches if clip else launches // 2 + 1), (n, clip)

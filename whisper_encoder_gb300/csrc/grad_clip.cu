@@ -457,6 +457,9 @@ cudaError_t clip_launches(const ClipCall& a, float max_norm, float* norm, double
   return cudaSuccess;
 }
 
+// Tables, and so launches of a pass, that n tensors take.
+int clip_tables(int n) { return n <= CLIP_TABLE_SMALL ? 1 : (n + CLIP_TABLE - 1) / CLIP_TABLE; }
+
 struct Extent {
   uintptr_t lo, hi;
 };
@@ -472,8 +475,7 @@ extern "C" {
 
 size_t wb_clip_grad_norm_workspace_bytes(int n_tensors) {
   if (n_tensors < 1 || n_tensors > WB_CLIP_MAX_TENSORS) return 0;
-  const int launches = n_tensors <= CLIP_TABLE_SMALL ? 1 : (n_tensors + CLIP_TABLE - 1) / CLIP_TABLE;
-  return static_cast<size_t>(launches) * CLIP_MAX_BLOCKS * sizeof(double);
+  return static_cast<size_t>(clip_tables(n_tensors)) * CLIP_MAX_BLOCKS * sizeof(double);
 }
 
 wb_status wb_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numel, const int32_t* dtypes,
@@ -519,7 +521,7 @@ wb_status wb_clip_grad_norm(const void* const* grads, void* const* outs, const i
   if (!err) return WB_ECUDA;
   const ClipCall a{grads, outs, numel, dtypes, out_dtypes, n_tensors};
   double* part = static_cast<double*>(workspace);
-  Prof pr(PC_CLIP, s, 2);
+  Prof pr(PC_CLIP, s, clip_tables(n_tensors) + (outs ? clip_tables(n_tensors) : 1));
   if (n_tensors <= CLIP_TABLE_SMALL) WB_CUDA(clip_launches<CLIP_TABLE_SMALL>(a, max_norm, norm, part, err, s));
   else WB_CUDA(clip_launches<CLIP_TABLE>(a, max_norm, norm, part, err, s));
   return WB_OK;
