@@ -5,8 +5,8 @@
 // from Python through ctypes (2 of checks, 4 of allocations, 4 of ctypes, 2 of the launch, the rest the interpreter).
 // Nothing is decided here that api.py does not decide: a call with anything out of the ordinary (a stream, a tensor of another
 // device, type or layout, a refusal by the library) returns None before anything was launched, and api.py goes the long way,
-// with its own checks and messages.  Any other failure raises what it raises on the long way (the package's WbError, torch's exceptions): it may
-// come from behind a call's first launch, and a call made twice would scale gradients twice.
+// with its own checks and messages.  A failure that may come from behind a call's first launch raises what it raises on the long way
+// (the package's WbError, torch's exceptions): a call made twice would scale gradients twice.
 // Built beside libwb.so where torch's and Python's headers are; without it every call goes the long way.
 #include <Python.h>
 
@@ -112,8 +112,11 @@ PyObject* wrap(std::initializer_list<const at::Tensor*> list) {
   return t;
 }
 
-// Goes on after a call of the library that launched all it should.
-void check(const char* name, wb_status status) {
+// Makes a call of the library, and goes on if it launched all it should.
+template <typename F>
+void call(bool& launched, const char* name, F f) {
+  launched = true;
+  const wb_status status = f();
   if (status == WB_OK) return;
   if (status == WB_EINVAL || status == WB_EUNSUPPORTED || status == WB_EWORKSPACE) throw LongWay();      // refusals: nothing was launched
   PyObject* e = PyObject_CallFunction(wb_error, "si", name, static_cast<int>(status));
@@ -122,40 +125,46 @@ void check(const char* name, wb_status status) {
   throw Raised();
 }
 
-// Every entry: None for LongWay, null with Python's exception set for any other one.
+// Every entry: None for LongWay and for exceptions before the call of the library (no device, an allocation that failed); null with Python's
+// exception set for those behind it.
 template <typename F>
 PyObject* plain(F f) {
   HANDLE_TH_ERRORS
+  bool launched = false;
   try {
-    return f();
+    return f(launched);
   } catch (const LongWay&) {
     return none();
   } catch (const Raised&) {
     return nullptr;
+  } catch (const std::exception&) {
+    if (launched) throw;
+    return none();
   }
   END_HANDLE_TH_ERRORS
 }
 
 PyObject* cross_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 6 || !p_cross) return none();
-  return plain([&]() -> PyObject* {
+  return plain([&](bool& launched) -> PyObject* {
     const Here here;
     const Rows q = rows(here, a[0]), k = rows(here, a[1]), v = rows(here, a[2]);
     if (k.batch != q.batch || v.batch != q.batch || v.T != k.T || v.d != k.d || q.d % k.d) throw LongWay();
     const float scale = static_cast<float>(number(a[3]));
     const int32_t *ql = lengths(here, a[4], q.batch), *kl = lengths(here, a[5], q.batch);
     const at::Tensor out = here.empty({q.batch, q.T, q.d}, at::kBFloat16), lse = here.empty({q.batch, q.d / 64, q.T}, at::kFloat);
-    check("wb_cross_attention",
-          p_cross(q.p, q.s0, q.s1, k.p, k.s0, k.s1, v.p, v.s0, v.s1, ql, kl, static_cast<int>(q.batch), static_cast<int>(q.T),
-                  static_cast<int>(k.T), static_cast<int>(q.d / 64), static_cast<int>(k.d / 64), scale, out.mutable_data_ptr(),
-                  lse.mutable_data_ptr<float>(), here.stream()));
+    call(launched, "wb_cross_attention", [&] {
+      return p_cross(q.p, q.s0, q.s1, k.p, k.s0, k.s1, v.p, v.s0, v.s1, ql, kl, static_cast<int>(q.batch), static_cast<int>(q.T),
+                     static_cast<int>(k.T), static_cast<int>(q.d / 64), static_cast<int>(k.d / 64), scale, out.mutable_data_ptr(),
+                     lse.mutable_data_ptr<float>(), here.stream());
+    });
     return wrap({&out, &lse});
   });
 }
 
 PyObject* cross_attention_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 11 || !p_cross_backward) return none();
-  return plain([&]() -> PyObject* {
+  return plain([&](bool& launched) -> PyObject* {
     const Here here;
     const Rows g = rows(here, a[0]), q = rows(here, a[1]), k = rows(here, a[2]), v = rows(here, a[3]);
     if (k.batch != q.batch || v.batch != q.batch || v.T != k.T || v.d != k.d || q.d % k.d || g.batch != q.batch || g.T != q.T || g.d != q.d)
@@ -173,11 +182,12 @@ PyObject* cross_attention_backward(PyObject*, PyObject* const* a, Py_ssize_t n) 
     }
     const at::Tensor ws = here.workspace(p_cross_workspace(static_cast<int>(q.batch), static_cast<int>(q.T), H));
     auto at_ = [](const at::Tensor& t) { return t.defined() ? t.mutable_data_ptr() : nullptr; };
-    check("wb_cross_attention_backward",
-          p_cross_backward(g.p, g.s0, g.s1, q.p, q.s0, q.s1, k.p, k.s0, k.s1, v.p, v.s0, v.s1, out.const_data_ptr(),
-                           lse.const_data_ptr<float>(), ql, kl, static_cast<int>(q.batch), static_cast<int>(q.T), static_cast<int>(k.T), H,
-                           static_cast<int>(k.d / 64), scale, at_(dq), at_(dk), at_(dv), ws.mutable_data_ptr(),
-                           static_cast<size_t>(ws.numel()), here.stream()));
+    call(launched, "wb_cross_attention_backward", [&] {
+      return p_cross_backward(g.p, g.s0, g.s1, q.p, q.s0, q.s1, k.p, k.s0, k.s1, v.p, v.s0, v.s1, out.const_data_ptr(),
+                              lse.const_data_ptr<float>(), ql, kl, static_cast<int>(q.batch), static_cast<int>(q.T), static_cast<int>(k.T), H,
+                              static_cast<int>(k.d / 64), scale, at_(dq), at_(dk), at_(dv), ws.mutable_data_ptr(),
+                              static_cast<size_t>(ws.numel()), here.stream());
+    });
     return wrap({&dq, &dk, &dv});
   });
 }
@@ -194,7 +204,7 @@ int32_t element_type(const at::Tensor& t) {
 // (grads, max_norm, out): out None: the norm alone; grads itself: in place
 PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 3 || !p_clip || !PyList_CheckExact(a[0]) || (a[2] != Py_None && !PyList_CheckExact(a[2]))) return none();
-  return plain([&]() -> PyObject* {
+  return plain([&](bool& launched) -> PyObject* {
     const Here here;
     const Py_ssize_t count = PyList_GET_SIZE(a[0]);
     const bool write = a[2] != Py_None;
@@ -217,10 +227,11 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (out_types[i] != types[i] && out_types[i] != WB_F32) throw LongWay();
     }
     const at::Tensor norm = here.empty({}, at::kFloat), ws = here.workspace(p_clip_workspace(static_cast<int>(count)));
-    check("wb_clip_grad_norm",
-          p_clip(grads.data(), write ? outs.data() : nullptr, numel.data(), types.data(), write ? out_types.data() : nullptr,
-                 static_cast<int>(count), static_cast<float>(number(a[1])), norm.mutable_data_ptr<float>(), ws.mutable_data_ptr(),
-                 static_cast<size_t>(ws.numel()), here.stream()));
+    call(launched, "wb_clip_grad_norm", [&] {
+      return p_clip(grads.data(), write ? outs.data() : nullptr, numel.data(), types.data(), write ? out_types.data() : nullptr,
+                    static_cast<int>(count), static_cast<float>(number(a[1])), norm.mutable_data_ptr<float>(), ws.mutable_data_ptr(),
+                    static_cast<size_t>(ws.numel()), here.stream());
+    });
     return THPVariable_Wrap(norm);
   });
 }
@@ -250,7 +261,7 @@ Policy policy(const Here& here, PyObject* nll, PyObject* old_nll, PyObject* adv,
 // (nll, old_nll, advantage, labels, ref_nll, clip_low, clip_high, kl_weight, per_sequence)
 PyObject* policy_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 9 || !p_policy) return none();
-  return plain([&]() -> PyObject* {
+  return plain([&](bool& launched) -> PyObject* {
     const Here here;
     const Policy p = policy(here, a[0], a[1], a[2], a[3], a[4]);
     const int per_sequence = truth(a[8]);
@@ -258,10 +269,11 @@ PyObject* policy_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const size_t bytes = p_policy_workspace(p.S, p.T);
     at::Tensor ws;
     if (bytes) ws = here.workspace(bytes);
-    check("wb_policy_loss",
-          p_policy(p.nll, p.old_nll, p.ref, p.adv, p.per_token, p.labels, p.S, p.T, number(a[5]), number(a[6]),
-                   static_cast<float>(number(a[7])), per_sequence, stats.mutable_data_ptr<float>(), weight.mutable_data_ptr<float>(),
-                   bytes ? ws.mutable_data_ptr() : nullptr, bytes ? static_cast<size_t>(ws.numel()) : 0, here.stream()));
+    call(launched, "wb_policy_loss", [&] {
+      return p_policy(p.nll, p.old_nll, p.ref, p.adv, p.per_token, p.labels, p.S, p.T, number(a[5]), number(a[6]),
+                      static_cast<float>(number(a[7])), per_sequence, stats.mutable_data_ptr<float>(), weight.mutable_data_ptr<float>(),
+                      bytes ? ws.mutable_data_ptr() : nullptr, bytes ? static_cast<size_t>(ws.numel()) : 0, here.stream());
+    });
     return wrap({&stats, &weight});
   });
 }
@@ -269,17 +281,18 @@ PyObject* policy_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // (dloss, nll, old_nll, advantage, labels, weight, ref_nll, clip_low, clip_high, kl_weight)
 PyObject* policy_loss_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 10 || !p_policy_backward) return none();
-  return plain([&]() -> PyObject* {
+  return plain([&](bool& launched) -> PyObject* {
     const Here here;
     const Policy p = policy(here, a[1], a[2], a[3], a[4], a[6]);
     const at::Tensor& dloss = here.on(tensor(a[0]));
     if (dloss.scalar_type() != at::kFloat || dloss.numel() != 1) throw LongWay();
     const at::Tensor& weight = need(here, a[5], at::kFloat, {p.S});
     const at::Tensor dnll = here.empty({p.S, p.T}, at::kFloat);
-    check("wb_policy_loss_backward",
-          p_policy_backward(dloss.const_data_ptr<float>(), p.nll, p.old_nll, p.ref, p.adv, p.per_token, p.labels,
-                            weight.const_data_ptr<float>(), p.S, p.T, number(a[7]), number(a[8]), static_cast<float>(number(a[9])),
-                            dnll.mutable_data_ptr<float>(), here.stream()));
+    call(launched, "wb_policy_loss_backward", [&] {
+      return p_policy_backward(dloss.const_data_ptr<float>(), p.nll, p.old_nll, p.ref, p.adv, p.per_token, p.labels,
+                               weight.const_data_ptr<float>(), p.S, p.T, number(a[7]), number(a[8]), static_cast<float>(number(a[9])),
+                               dnll.mutable_data_ptr<float>(), here.stream());
+    });
     return THPVariable_Wrap(dnll);
   });
 }
