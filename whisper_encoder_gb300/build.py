@@ -30,6 +30,7 @@ LIB_DEBUG = os.path.join(BUILD_DEBUG, "libwb_debug.so")
 SOURCES = ["api.cu", "kernels.cu", "tc_kernels.cu", "static_scratch.cu", "host_pipeline.cu", "layernorm_train.cu", "head_loss.cu",
            "cross_attention.cu", "grad_clip.cu", "policy_loss.cu"]
 HOST_SOURCE = "host_calls.cpp"
+HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-shared"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -69,32 +70,43 @@ def _host_command(out: str) -> list:
     include = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include")]
     libs = os.path.join(torch_dir, "lib")
-    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", *["-I" + d for d in include], os.path.join(CSRC, HOST_SOURCE),
+    return [os.environ.get("CXX", "g++"), *HOST_FLAGS, *["-I" + d for d in include], os.path.join(CSRC, HOST_SOURCE),
             "-o", out, "-L" + libs, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath," + libs]
+
+
+def _host_digest() -> str:
+    """What wb_host.so depends on: its source, wb.h, the torch and Python it is for.  Not where the compilers lie: a machine without them runs
+    a tree that was built."""
+    h = hashlib.sha256("\n".join((importlib.metadata.version("torch"), sys.version, sysconfig.get_platform(), *HOST_FLAGS)).encode())
+    for path in (os.path.join(CSRC, HOST_SOURCE), os.path.join(ROOT, "include", "wb.h")):
+        with open(path, "rb") as fh:
+            h.update(fh.read())
+    return h.hexdigest()
 
 
 def build_host(force: bool = False) -> str | None:
     """Compile wb_host.so against the installed torch (if its source, wb.h or torch changed); None where that fails."""
+    stamp = os.path.join(BUILD, "host_digest.txt")
+    current = False
     try:
-        cmd = _host_command(LIB_HOST + ".tmp")
-        h = hashlib.sha256(" ".join(cmd).encode() + importlib.metadata.version("torch").encode() + sys.version.encode())
-        for path in (os.path.join(CSRC, HOST_SOURCE), os.path.join(ROOT, "include", "wb.h")):
-            with open(path, "rb") as fh:
-                h.update(fh.read())
-        stamp = os.path.join(BUILD, "host_digest.txt")
-        if not force and os.path.exists(LIB_HOST) and os.path.exists(stamp) and open(stamp).read() == h.hexdigest():
+        digest = _host_digest()
+        if os.path.exists(LIB_HOST) and os.path.exists(stamp):
+            with open(stamp) as fh:
+                current = fh.read() == digest
+        if current and not force:
             return LIB_HOST
+        cmd = _host_command(LIB_HOST + ".tmp")
         os.makedirs(BUILD, exist_ok=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(r.stderr[-2000:])
         os.replace(LIB_HOST + ".tmp", LIB_HOST)
         with open(stamp, "w") as fh:
-            fh.write(h.hexdigest())
+            fh.write(digest)
         return LIB_HOST
     except Exception as e:  # noqa: BLE001 - the package works without it, with more host time a call
-        if os.path.exists(LIB_HOST):
-            os.remove(LIB_HOST)          # of another torch or another wb.h
+        if not current and os.path.exists(LIB_HOST):
+            os.remove(LIB_HOST)          # of another torch or another wb.h, as far as is known
         sys.stderr.write(f"wb_host.so is not built: {e}\n")
         return None
 
