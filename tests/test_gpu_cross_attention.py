@@ -381,3 +381,28 @@ def test_python_refusals(wb):
         with pytest.raises(wb.WbError):
             bad()
     assert wb.check_device_error() == 0
+
+
+# few tiles of rows: clusters of 4 and 8 CTAs split the keys, 8 the ones of few rows
+@pytest.mark.parametrize("batch,Tq,Tk,H,Hk", [(5, 130, 1500, 2, 1), (5, 40, 3000, 2, 2), (5, 3, 1500, 2, 2), (5, 256, 2000, 1, 1)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf, 3e38])
+def test_what_lies_behind_the_lengths_of_split_keys(wb, batch, Tq, Tk, H, Hk, bad):
+    # keys that end inside a CTA's last tile, at its border, and in the first tile, so that the other CTAs of a cluster have none
+    q, k, v, dout, g = _data(batch, Tq, Tk, H, Hk, Tk + Tq)
+    q_lens = torch.tensor([Tq, Tq - 1, max(1, Tq // 2), 1, Tq + 3], dtype=torch.int32, device=DEV)
+    for ends in ([Tk // 2 + 3, 100, 1, Tk - 1, 129], [Tk, 128, 0, 127, 640], [383, 257, Tk + 9, 1023, 511]):
+        kv_lens = torch.tensor(ends, dtype=torch.int32, device=DEV)
+        ref = _reference(q, k, v, dout, q_lens=q_lens, kv_lens=kv_lens)
+        q2, k2, v2, d2 = (t.clone() for t in (q, k, v, dout))
+        for i in range(batch):
+            a, b = min(int(q_lens[i]), Tq), min(int(kv_lens[i]), Tk)
+            q2[i, a:], d2[i, a:], k2[i, b:], v2[i, b:] = bad, bad, bad, bad
+        got = _both(wb, q2, k2, v2, d2, q_lens=q_lens, kv_lens=kv_lens)
+        _check(got, ref)
+        kw = dict(q_lens=q_lens, kv_lens=kv_lens)
+        dq, none, _ = wb.cross_attention_backward(d2, q2, k2, v2, got["out"], got["lse"], need_dkv=False, **kw)
+        none2, dk, dv = wb.cross_attention_backward(d2, q2, k2, v2, got["out"], got["lse"], need_dq=False, **kw)
+        assert none is None and none2 is None
+        for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
+            assert torch.equal(t, got[name]), name
+    assert wb.check_device_error() == 0
