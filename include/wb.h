@@ -533,7 +533,8 @@ wb_status wb_clip_grad_norm(const void* const* grads, void* const* outs, const i
  *    w (e^d A where not clipped + kl_weight (e^x - 1)), the dloss of wb_linear_cross_entropy_backward.  On the clip's border the
  *    token is not clipped.  dnll may be the buffer of nll, old_nll or ref_nll.
  * Whether a token is clipped is decided on the exact difference; sums run in float32 over at most 45 terms of a sequence in a row and in
- * pairs of float32 (a sum and what its roundings left) beyond and across sequences, in a fixed order.  0 <= clip_low <= 1, 0 <= clip_high <= 1e30, kl_weight finite; S up to 2^31, T up to 2^30, S T up to 2^40.
+ * pairs of float32 (a sum and what its roundings left) beyond and across sequences, in a fixed order.
+ * 0 <= clip_low <= 1, 0 <= clip_high <= 1e30, kl_weight finite; S up to 2^31, T up to 2^30, S T up to 2^40.
  * Pointers are aligned to their element, the workspace to 16 bytes.
  * WB_EINVAL for bad sizes, values or pointers, WB_EWORKSPACE for a missing, small or unaligned workspace (NULL where the
  * query says 0: up to 128 sequences of 512 tokens). */

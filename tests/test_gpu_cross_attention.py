@@ -101,7 +101,8 @@ def _both(wb, q, k, v, dout, **kw):
     return {"out": out, "lse": lse, "dq": dq, "dk": dk, "dv": dv}
 
 
-# rows of a key head of 1 to 16, 17 to 32 and more take different kernels; tiles are 128 rows and keys, 64 in the backward pass
+# rows of a key head of 1 to 16 and more take different kernels, and sides of up to 64 rows or keys others in the backward pass; tiles are
+# 128 rows and keys
 SHAPES = [(1, 1, 1, 1, 1), (2, 1, 1500, 3, 3), (1, 5, 16, 2, 2), (3, 4, 17, 4, 1), (2, 16, 129, 2, 2), (1, 17, 40, 2, 2), (2, 8, 300, 8, 2),
           (1, 32, 1000, 1, 1), (1, 33, 127, 1, 1), (2, 64, 128, 2, 2), (1, 65, 64, 3, 3), (1, 127, 65, 2, 1), (2, 128, 129, 2, 2),
           (1, 129, 1, 2, 2), (2, 200, 257, 6, 2), (1, 448, 1500, 2, 2), (3, 77, 1371, 2, 2), (1, 300, 63, 4, 4), (40, 1, 50, 4, 4)]

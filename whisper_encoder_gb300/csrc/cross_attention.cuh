@@ -11,7 +11,7 @@
 // tiles of rows for the SMs, a cluster of up to 8 CTAs splits a tile's keys; each leaves its O, maxima and sums in
 // shared memory and joins a share of the rows of all of them, in order (224 rows of 16 heads over 13501 keys: 92 us in
 // 32 CTAs, 24 in 256).
-// Warp 0 lane 0 loads with TMA, warp 1 lane 0 issues the MMAs, warps 2-9 run the softmax: each owns 16 query
+// One lane of warp 0 loads with TMA, one of warp 1 issues the MMAs, warps 2-9 run the softmax: each owns 16 query
 // rows through the 16-lane TMEM shapes, four threads a row.
 //
 // Numbers.  Scores stay float32, and so do the exponent's argument and the exponential: lse is a float32 result

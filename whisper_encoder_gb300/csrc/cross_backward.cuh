@@ -11,24 +11,28 @@
 // P and dS go as packed bf16 over the TMEM columns S came from and are read there as A operands; the step's tiles are read both as
 // K-major and as MN-major B tiles of the same shared memory, so nothing is transposed.
 //
-// Persistent, one CTA an SM over its items in turn.  Bound by the tensor pipe: 16 products of 128 x 128 x 16 and 128 x 64 x 16 a
-// step, 64 and 45 cycles each alone.  What keeps it fed: S is double, dP is given back as soon as the softmax holds it in registers, so
-// the scores of step n + 1 are formed under the softmax of step n, and its sums under the softmax of step n + 1; an item's
-// sums are stored after the next item's first softmax.  Where there are fewer tiles of query rows than SMs, clusters of up to 8 CTAs split their
-// keys and join dQ, M and b through distributed shared memory (dq of 224 rows of 16 heads over 13501 keys 106 -> 37 us).  128 columns a step: with 64, two buffers of both and a group of
-// warps for each, a product took 48 cycles for half the work and a step 2000 (dk and dv of 32 x 448 x 1500 x 20 heads 526 us; one
-// item a CTA, two CTAs an SM, 419).
-// The dq kernel takes lse and delta of its rows at the start of an item and leaves them for the dkv kernel, -infinity and 0 for rows that take no part,
-// whose P is then 0 (a kernel of their own before both: 514 us against 518 for 32 x 448 x 1500 x 20 heads, but 22.2 against 20.2 for 3 x 77 x 1371 x 6).
-// Warp 0 lane 0 loads, warp 1 issues, warps 2-17 run the softmax: 16 rows of half of the columns each.
+// Persistent, one CTA an SM over its items in turn.  Bound by the chain of a step (scores, 16 warps read them, the softmax, P and dS back to
+// TMEM, sums).  Its 24 products, 8 of 128 x 128 x 16 (S and dP) and 16 of 128 x 64 x 16 (the two sums), take 1230 cycles at the rates
+// they have alone (64 and 45 each), a step about 2500 (8 x 448 x 1500 x 20 heads; tensor pipe active 36 to 40 %).
+// What overlaps: S is double, dP is given back as soon as the softmax holds it in registers, so the scores of step n + 1 are formed under the
+// softmax of step n, and its sums under the softmax of step n + 1; an item's sums are stored after the next item's first softmax.
+// Where there are fewer tiles of query rows than SMs, clusters of up to 8 CTAs split their keys and join dQ, M and b through
+// distributed shared memory (dq of 224 rows of 16 heads over 13501 keys 106 -> 37 us).
+// 128 columns a step: with 64, two buffers of both and a group of warps for each, a product took 48 cycles for half the work and a step
+// 2000 (dk and dv of 32 x 448 x 1500 x 20 heads 526 us; one item a CTA, two CTAs an SM, 419).
+// The dq kernel takes lse and delta of its rows at the start of an item and leaves them for the dkv kernel, -infinity and 0 for rows that
+// take no part, whose P is then 0 (a kernel of their own before both: 514 us against 518 for 32 x 448 x 1500 x 20 heads, but 22.2
+// against 20.2 for 3 x 77 x 1371 x 6).
+// One lane of warp 0 loads, one of warp 1 issues, warps 2-17 run the softmax: 16 rows of half of the columns each.  All 16 rows of a warp
+// are computed, also those past the item's length: nothing of theirs is stored.
 //
 // Numbers.  Sums are float32; P and dS are rounded to bf16 once each, as operands beside bf16 q, k and dout (with 64 rows or keys
-// or fewer that side's free half of S takes what that leaves as a second operand: dk and dv of few rows 2.4e-3 -> 1.7e-3 from 64 bits; as a branch in the
-// one kernel it cost 25 % of every size).  delta is sum_e dout out as well,
+// or fewer that side's free half of S takes what that leaves as a second operand: dk and dv of few rows 2.4e-3 -> 1.7e-3 from 64 bits;
+// as a branch in the one kernel it cost 25 % of every size).  delta is sum_e dout out as well,
 // but out is rounded to bf16, and what that leaves is the same for all keys of a row: it does not average out (dq and dk were 3.3e-3 of
 // their norm from 64 bits, 2.4e-3 without it).  With d' that delta, b = sum_k P (dP - d') is what it lacks, since sum_k P = 1: the dq
-// kernel hands delta = d' + b to the dkv kernel, and subtracts b' M from dq, M = sum_k P k and b' the sum of dS as it was rounded: what rounding
-// leaves then adds up along k - M alone, which is small where a row's weight lies on one key (dq of sharp rows 2.6e-3 -> 2.1e-3).
+// kernel hands delta = d' + b to the dkv kernel, and subtracts b' M from dq, M = sum_k P k and b' the sum of dS as it was rounded: what
+// rounding leaves then adds up along k - M alone, which is small where a row's weight lies on one key (dq of sharp rows 2.6e-3 -> 2.1e-3).
 // Rows of one key have P = 1 whatever q and k are: their dq and that key's dk are 0, not what rounding leaves.
 // Rows past their item's lengths may hold anything: a step's are cleared in shared memory before its products, an item's own reach only
 // results that are not stored.

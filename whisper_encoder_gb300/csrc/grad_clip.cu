@@ -6,6 +6,10 @@
 // takes in turn; the table of tensors travels as a kernel argument (up to 32 KB), so that nothing is
 // uploaded and a call can be captured.  The second pass walks the chunks from the end: what the first
 // pass read last is still in L2.
+// 79 M bf16 elements: norm alone 27 us, in place 74, into tensors of the same type 77, into float32 106.  Beside memory there is
+// float64: every thread joins the partial sums and takes the root and the quotient.  Its pipe is busy for 12 % of the scaling pass and
+// 20 % of the norm's over 64 M elements (9 and 5 us), and a small call pays the same before its first store: 3.6 M float32 in 20
+// tensors take 18 us for a floor of 4.
 //
 // Numbers.  A thread adds the squares of at most 128 elements in 32 bits (four or eight chains), the rest of the sum is in
 // 64 bits and in a fixed order: the same call gives the same bits.  Squares of elements above 2^63 are
@@ -285,6 +289,7 @@ __device__ __forceinline__ void clip_scale(const ClipEntry& e, uint32_t c, float
     return;
   }
   if (s.lo + t < s.a) one(s.lo + t);
+  // one load in flight a thread, as g and out may be the same memory to the compiler: 79 M bf16 87 us, 77 scaled
   if (copy) {
     constexpr int W = clip_vec<T>();
     for (long long i = s.a + t * W; i < s.hi; i += CLIP_THREADS * W) {
@@ -349,9 +354,10 @@ __device__ __forceinline__ void clip_scale_tiny(const ClipTable<N>& t, double f)
     const ClipEntry& e = t.e[clip_find(t, c)];
     const uint32_t j = c - e.chunk0;
     const bool wide = e.out_type == WB_F32;
-    if (e.type == WB_BF16) wide ? clip_scale_tiny<__nv_bfloat16, float>(e, j, f, t.err) : clip_scale_tiny<__nv_bfloat16, __nv_bfloat16>(e, j, f, t.err);
+    if (e.type == WB_F32) clip_scale_tiny<float, float>(e, j, f, t.err);
     else if (e.type == WB_F16) wide ? clip_scale_tiny<__half, float>(e, j, f, t.err) : clip_scale_tiny<__half, __half>(e, j, f, t.err);
-    else clip_scale_tiny<float, float>(e, j, f, t.err);
+    else if (wide) clip_scale_tiny<__nv_bfloat16, float>(e, j, f, t.err);
+    else clip_scale_tiny<__nv_bfloat16, __nv_bfloat16>(e, j, f, t.err);
   }
 }
 

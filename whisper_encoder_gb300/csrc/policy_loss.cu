@@ -10,10 +10,12 @@
 // Bound by memory (16 bytes a token forward, 20 backward, 4 more with a reference), below a million tokens by the launches.
 // Forward: a team of 1 to 8 warps of a block takes a sequence; a block leaves one partial row, and a second kernel joins those
 // in order, in every one of its blocks, and turns counts into weights.  Up to 128 sequences of 512 tokens are one block's, in
-// one launch (8 x 77 tokens: 5.5 us against 8.2 with two).  No atomics: the same call gives the same bits.
-// 16001 x 448 tokens: forward 27 us, of which the join takes 4 (the sums 5 TB/s), backward 22 (6.5 TB/s).  Four tokens side by side a load where
-// they lie on 16 bytes: one at a time it took 30 and 25, half of the issue slots on addresses.  6 blocks an SM with half the loads each: 26, but
-// 1024 x 448 tokens 8.6 for 8.3; prefetching a warp's next sequence into L2: 28.
+// one launch: 8 x 77 tokens take 5.5 us against 8.2 with two.  Towards that limit the one block is the slower form: 16 x 448 tokens take it
+// 5.2 us, 64 x 448 10.2 and 128 x 512 18.0, where two launches take 6.5 for 129 x 512 (all among other calls; 8 x 77 so 3.5).
+// No atomics: the same call gives the same bits.
+// 16001 x 448 tokens: forward 28 us, of which the join takes 4 (the sums 5 TB/s), backward 22 (6.5 TB/s).  Four tokens side by side a load
+// where they lie on 16 bytes: one at a time it took 30 and 25, half of the issue slots on addresses.  6 blocks an SM with half the loads
+// each: 26, but 1024 x 448 tokens 8.6 for 8.3; prefetching a warp's next sequence into L2: 28.
 //
 // Numbers.  Whether a token is clipped is decided on d against log1p(hi) and log1p(-lo), both as unevaluated sums of
 // two float32 (the rounding of a difference is exact in float32): one rounding near the border would turn a
@@ -192,7 +194,8 @@ __device__ __forceinline__ SeqSum policy_sequence(const PolicyArgs& a, long long
   constexpr int GROUPS = POL_SUM_TILE / 4;
   const int T = static_cast<int>(a.T), first = (part * 32 + static_cast<int>(lane_id())) * (VEC ? 4 : 1);
   const int step = VEC ? 1 : W * 32, group = W * 32 * 4;                        // between a lane's tokens, and its groups of four
-  // what a lane of a long sequence has added so far: of 4096 equal losses in one float32 the roundings were 2^-15 of the sum, of 65536 2^-11
+  // what a lane of a long sequence has added so far: of 4096 equal losses in one float32 the roundings were 2^-15 of the sum, of 65536
+  // 2^-11
   Sum2 loss = {0.0f, 0.0f}, kl = {0.0f, 0.0f};
   int steps = 0;
   for (int t0 = first; t0 < T; t0 += GROUPS * group) {

@@ -317,9 +317,9 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint6
       : "memory");
 }
 
-// One lane of a converged warp, the same each time.  A warp that stays whole around its MMAs, with this predicate on them alone,
-// keeps their descriptors in uniform registers: 16 MMAs of a step with changing operands took 836 cycles to issue against 1022
-// inside `if (lane == 0)`.
+// One lane of a converged warp, the same each time.  A branch on it around a whole issuing role has one thread as far as the compiler can
+// see, and the descriptors of the MMAs inside go to uniform registers without more: 16 MMAs with changing operands took 836 cycles to
+// issue alone against 1022 inside `if (lane == 0)`, the backward pass of cross attention (32 x 448 x 1500 x 20 heads) 504 us against 697.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));

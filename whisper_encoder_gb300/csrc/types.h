@@ -116,7 +116,8 @@ struct AttnParams {
 
 // Sites (bits 8..15 of the error word) of the debug bounds checks: 0x20-0x3F the SIMT kernels,
 // 0x40-0x4F the GEMM epilogues, 0x50-0x5F the attention epilogue, 0x60-0x67 the LayerNorm of training,
-// 0x68-0x6F the vocabulary losses, 0x70-0x74 gradient clipping and the policy loss, 0x75-0x7A cross attention.
+// 0x68-0x6F the vocabulary losses, 0x70-0x74 gradient clipping and the policy loss, 0x75-0x7A cross attention.  Sites of timed-out waits
+// have numbers of their own, some of them the same: ERR_TIMEOUT and ERR_BOUNDS tell them apart.
 enum : uint32_t {
   SITE_PAD_SPLIT = 0x20, SITE_DFT_BASIS, SITE_MEL_FB, SITE_LOGMEL_POST, SITE_STEM_T_IN, SITE_STEM_T_OUT,
   SITE_ZERO_ROWS, SITE_PACK_CONV, SITE_LN_X, SITE_LN_Y, SITE_LN_GB, SITE_STATS_X, SITE_STATS_OUT,
