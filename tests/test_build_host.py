@@ -91,3 +91,13 @@ def test_a_library_of_another_source_does_not_stay(tree, monkeypatch, capfd, how
     tree.works = True
     monkeypatch.setattr(build, "_nvcc", lambda: "/usr/local/cuda/bin/nvcc")
     assert build.build_host() == str(tree.lib) and tree.lib.exists()
+
+
+def test_an_interpreter_that_cannot_tell_removes_nothing(tree, monkeypatch, capfd):
+    def missing(name):
+        raise build.importlib.metadata.PackageNotFoundError(name)
+
+    build.build_host()
+    monkeypatch.setattr(build.importlib.metadata, "version", missing)
+    assert build.build_host() is None and tree.lib.exists() and len(tree.calls) == 1
+    assert "wb_host.so is not built" in capfd.readouterr().err

@@ -87,12 +87,13 @@ def _host_digest() -> str:
 def build_host(force: bool = False) -> str | None:
     """Compile wb_host.so against the installed torch (if its source, wb.h or torch changed); None where that fails."""
     stamp = os.path.join(BUILD, "host_digest.txt")
-    current = False
+    stale = False
     try:
-        digest = _host_digest()
+        digest, current = _host_digest(), False
         if os.path.exists(LIB_HOST) and os.path.exists(stamp):
             with open(stamp) as fh:
                 current = fh.read() == digest
+        stale = not current
         if current and not force:
             return LIB_HOST
         cmd = _host_command(LIB_HOST + ".tmp")
@@ -105,8 +106,8 @@ def build_host(force: bool = False) -> str | None:
             fh.write(digest)
         return LIB_HOST
     except Exception as e:  # noqa: BLE001 - the package works without it, with more host time a call
-        if not current and os.path.exists(LIB_HOST):
-            os.remove(LIB_HOST)          # of another torch or another wb.h, as far as is known
+        if stale and os.path.exists(LIB_HOST):
+            os.remove(LIB_HOST)          # of another torch or another wb.h
         sys.stderr.write(f"wb_host.so is not built: {e}\n")
         return None
 
