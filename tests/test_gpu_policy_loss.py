@@ -222,6 +222,18 @@ def test_long_sequences(wb, S, T, d, per_token):
         assert bool(((dnll[:, :T - 5].double() - grad).abs() <= 2.0 ** -19 * abs(grad)).all()) and not dnll[:, T - 5:].any()
 
 
+@pytest.mark.parametrize("bad,want", [(math.inf, math.inf), (math.nan, math.nan)])
+@pytest.mark.parametrize("at", [0, 3000, 9999, 20000])
+def test_long_sequences_with_a_loss_that_is_not_finite(wb, bad, want, at):
+    # what an infinite sum's roundings left is no number, and stays out of it; the sequence beside it is as it was
+    nll, old, ref, adv, labels = _data(2, 20001, 8)
+    labels[1, at], adv[:] = 7, -1
+    old[1, at] = bad
+    stats, weight, dnll = _run(wb, (nll, old, ref, adv, labels), True)
+    assert math.isnan(float(stats[0])) if math.isnan(want) else float(stats[0]) == want
+    assert math.isfinite(float(stats[1])) and math.isfinite(float(stats[2])) and bool(torch.isfinite(dnll[0]).all())
+
+
 def test_gradient_against_differences(wb):
     nll, old, ref, adv, labels = _data(7, 60, 4)
     stats, weight, dnll = _run(wb, (nll, old, ref, adv, labels), True, dl=1.0)
